@@ -24,6 +24,7 @@
 #include "../../include/la.h"
 #include "la_internal.h"
 #include "la_sm100.cuh"
+#include "la_views.h"
 
 namespace cg = cooperative_groups;
 
@@ -295,6 +296,205 @@ cudaError_t append_by_d(int D, const void *K, const void *V, int N, void *S, voi
     }
 }
 
+// ---- grouped heads: r query heads share one state ----------------------------------------------------------
+
+struct Strides2 {
+    long long b, h;  // batch and head stride of a token tensor, in elements
+};
+struct GroupedArgs {
+    const void *q, *k, *v;
+    void *o;
+    float *g;
+    void *S, *z, *a;
+    int *n;
+    Strides2 qs, ks, vs, os;
+    int Hkv, r;
+};
+
+// One token for r query heads of each state.  As decode_step_kernel, with R CTAs to a head (ROWS = D / R rows of S
+// each); the slab stays in shared memory while QB query heads at a time are multiplied with it, the first QB in the
+// pass that also updates it, and its bulk store runs beside the other passes.
+template <typename T, typename Acc, int D, int R>
+__global__ void __launch_bounds__(kThreads) decode_grouped_kernel(const __grid_constant__ GroupedArgs P) {
+    constexpr int QB = 2;
+    constexpr int ROWS = D / R, VEC = 16 / (int)sizeof(Acc), CG = D / VEC;
+    constexpr int RG = kThreads / CG < ROWS ? kThreads / CG : ROWS, RR = ROWS / RG;
+    constexpr uint32_t BYTES = (uint32_t)(ROWS * D * sizeof(Acc));
+    static_assert(ROWS * R == D && RR * RG == ROWS, "grouped decode split");
+    extern __shared__ __align__(128) unsigned char slab_raw[];
+    Acc *slab = (Acc *)slab_raw;          // ROWS x D
+    Acc *qs = slab + ROWS * D;            // r x D
+    __shared__ Acc ks[D], an[D];          // k; a with v added
+    __shared__ Acc red[QB][RG][D];
+    __shared__ Acc part[QB][D];
+    __shared__ Acc gs[64];                // 1 / g of each query head (r <= 64)
+    __shared__ uint64_t bar;
+    __shared__ int landed;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = R > 1 ? (int)cluster.block_rank() : 0;
+    const long long head = blockIdx.x / R;
+    const long long b = head / P.Hkv;
+    const int hk = (int)(head - b * P.Hkv);
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const T *q = (const T *)P.q + b * P.qs.b + (long long)hk * P.r * P.qs.h;
+    const T *k = (const T *)P.k + b * P.ks.b + hk * P.ks.h, *v = (const T *)P.v + b * P.vs.b + hk * P.vs.h;
+    T *o = (T *)P.o + b * P.os.b + (long long)hk * P.r * P.os.h;
+    Acc *rows = (Acc *)P.S + head * D * D + (long long)rank * ROWS * D;
+    Acc *z = (Acc *)P.z + head * D, *a = (Acc *)P.a + head * D;
+    if (t == 0) {
+        sm100::mbar_init(&bar, 1);
+        sm100::fence_mbar_init();
+        sm100::mbar_arrive_expect_tx(&bar, BYTES);
+        sm100::bulk_load(slab, rows, BYTES, &bar);
+    }
+    // while the slab is on its way: q, k, a and z of after the token, and every g
+    for (int x = t; x < P.r * D; x += kThreads) qs[x] = load_acc<Acc>(q + (x / D) * P.qs.h + x % D);
+    Acc zn[(D + kThreads - 1) / kThreads];
+    for (int x = t, m = 0; x < D; x += kThreads, ++m) {
+        ks[x] = load_acc<Acc>(k + x);
+        an[x] = a[x] + load_acc<Acc>(v + x);
+        zn[m] = z[x] + ks[x];
+        red[0][0][x] = zn[m];  // z for the sums below; the passes write red behind a barrier
+    }
+    const int nn = P.n[head] + 1;
+    __syncthreads();
+    for (int g = warp; g < P.r; g += kThreads / 32) {
+        Acc dz = 0;
+        for (int x = lane; x < D; x += 32) dz += qs[g * D + x] * red[0][0][x];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) dz += __shfl_xor_sync(0xffffffffu, dz, off);
+        if (lane == 0) gs[g] = (Acc)nn + dz;
+    }
+    if (t == 0) landed = sm100::mbar_wait(&bar, 0, 2000000000ull) ? 1 : 0;
+    __syncthreads();  // the slab has landed (or the wait gave up), and every g is there
+    bool ok = landed != 0;
+    if constexpr (R > 1) {
+        // all CTAs of the head update it, or none; and all have read z, a and n, which rank 0 writes below
+        cluster.sync();
+#pragma unroll
+        for (int x = 0; x < R; ++x) ok = ok && *cluster.map_shared_rank(&landed, x) != 0;
+    }
+    if (ok && rank == 0) {
+        for (int x = t, m = 0; x < D; x += kThreads, ++m) {
+            z[x] = zn[m];
+            a[x] = an[x];
+        }
+        if (t == 0) P.n[head] = nn;
+    }
+    const int col = t % CG, p = t / CG;
+    Acc ve[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) ve[j] = load_acc<Acc>(v + col * VEC + j);
+    for (int g0 = 0; g0 < P.r; g0 += QB) {
+        const int nq = P.r - g0 < QB ? P.r - g0 : QB;
+        if (ok && p < RG) {
+            Acc acc[QB][VEC] = {};
+            const Acc *q0 = qs + g0 * D + rank * ROWS, *q1 = nq > 1 ? q0 + D : q0;
+#pragma unroll 4
+            for (int m = 0; m < RR; ++m) {
+                const int row = p + RG * m;
+                uint4 *cell = (uint4 *)(slab + (long long)row * D + col * VEC);
+                uint4 raw = *cell;
+                Acc *sv = (Acc *)&raw;
+                if (g0 == 0) {
+                    const Acc kd = ks[rank * ROWS + row];
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) sv[j] += kd * ve[j];
+                    *cell = raw;
+                }
+                const Acc x0 = q0[row], x1 = q1[row];
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    acc[0][j] += sv[j] * x0;
+                    acc[1][j] += sv[j] * x1;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                red[0][p][col * VEC + j] = acc[0][j];
+                red[1][p][col * VEC + j] = acc[1][j];
+            }
+        }
+        if (g0 == 0) sm100::fence_proxy_async_smem();  // the slab's new values, before the bulk store reads them
+        __syncthreads();
+        if (g0 == 0 && ok && t == 0) {
+            sm100::bulk_store(rows, slab, BYTES);
+            sm100::bulk_commit();
+        }
+        for (int x = t; x < nq * D; x += kThreads) {
+            const int g = x / D, e = x % D;
+            Acc sum = 0;
+#pragma unroll
+            for (int m = 0; m < RG; ++m) sum += red[g][m][e];
+            if constexpr (R > 1) part[g][e] = sum;
+            else
+                o[(g0 + g) * P.os.h + e] = ok ? store_as<T, Acc>((an[e] + sum) / gs[g0 + g]) : store_as<T, Acc>((Acc)NAN);
+        }
+        if constexpr (R > 1) {
+            cluster.sync();  // every CTA's partial sums are in its shared memory
+            // each CTA finishes its share of the columns
+            for (int x = t; x < nq * ROWS; x += kThreads) {
+                const int g = x / ROWS, e = rank * ROWS + x % ROWS;
+                Acc tot = an[e];
+#pragma unroll
+                for (int y = 0; y < R; ++y) tot += *cluster.map_shared_rank(&part[g][e], y);
+                o[(g0 + g) * P.os.h + e] = ok ? store_as<T, Acc>(tot / gs[g0 + g]) : store_as<T, Acc>((Acc)NAN);
+            }
+            cluster.sync();  // all have read the partial sums
+        } else {
+            __syncthreads();
+        }
+    }
+    if (P.g && rank == 0)
+        for (int x = t; x < P.r; x += kThreads) P.g[b * P.Hkv * P.r + (long long)hk * P.r + x] = (float)gs[x];
+    if (t == 0) {
+        if (ok) sm100::bulk_wait0();                    // the state rows are written back before the CTA exits
+        else sm100::mbar_wait(&bar, 0, 2000000000ull);  // a late copy lands before the slab is released
+    }
+}
+
+template <typename T, typename Acc, int D, int R> cudaError_t launch_grouped(const GroupedArgs &P, long long BH, cudaStream_t s) {
+    constexpr int kSlabBytes = D / R * D * (int)sizeof(Acc);
+    static std::atomic<int> attr_state[kMaxDevices];
+    if (!once_per_device(attr_state, [] {
+            return cudaFuncSetAttribute(decode_grouped_kernel<T, Acc, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        kSlabBytes + 64 * D * (int)sizeof(Acc)) == cudaSuccess;
+        }))
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(BH * R));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)kSlabBytes + (size_t)P.r * D * sizeof(Acc);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = R;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_grouped_kernel<T, Acc, D, R>, P);
+}
+
+// CTAs of a head: as few as its slabs need, or eight while all heads' CTAs then still fit on the GPU at once, where a
+// step's time is that of one slab's way in and out.
+template <typename T, typename Acc, int D> cudaError_t grouped_split(const GroupedArgs &P, long long BH, cudaStream_t s) {
+    constexpr int R = DecSplit<Acc, D>::R;
+    if constexpr (D >= 64 && R < 8)
+        if (BH * 8 <= 304) return launch_grouped<T, Acc, D, 8>(P, BH, s);
+    return launch_grouped<T, Acc, D, R>(P, BH, s);
+}
+
+template <typename T, typename Acc> cudaError_t grouped_by_d(int D, const GroupedArgs &P, long long BH, cudaStream_t s) {
+    switch (D) {
+        case 16: return grouped_split<T, Acc, 16>(P, BH, s);
+        case 32: return grouped_split<T, Acc, 32>(P, BH, s);
+        case 64: return grouped_split<T, Acc, 64>(P, BH, s);
+        case 128: return grouped_split<T, Acc, 128>(P, BH, s);
+        default: return grouped_split<T, Acc, 256>(P, BH, s);
+    }
+}
+
 bool supported_d(int D) { return D == 16 || D == 32 || D == 64 || D == 128 || D == 256; }
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 bool overlap(const void *p, size_t pb, const void *q, size_t qb) {
@@ -353,6 +553,52 @@ int la_decode_step(const void *q, const void *k, const void *v, void *o, float *
                               : step_by_d<float, double>(D, q, k, v, o, normaliser, S, z, a, n, BH, s);
     if (e != cudaSuccess) return LA_ERR_CUDA;
     la::count_launches(1);
+    return LA_OK;
+}
+
+int la_decode_step_grouped(const void *q, const void *k, const void *v, void *o, float *normaliser, void *S, void *z,
+                           void *a, int *n, int B, int Hq, int Hkv, int D, int dtype, const long long *strides,
+                           void *stream) {
+    using namespace la;
+    using namespace la::dec;
+    if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
+    if (B < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || D < 1) return LA_ERR_INVALID_ARG;
+    if (!supported_d(D) || Hq / Hkv > 64) return LA_ERR_UNSUPPORTED;
+    if (B == 0) return LA_OK;
+    const long long BH = (long long)B * Hkv;
+    if ((long long)B * Hq >= (1LL << 31) || BH * 8 >= (1LL << 31)) return LA_ERR_INVALID_ARG;
+    const int elem = dtype == LA_BF16 ? 2 : 4;
+    const void *ptr[4] = {q, k, v, o};
+    View w[4];
+    int rc;
+    for (int x = 0; x < 4; ++x) {  // (q, k, v, o) x (batch, head)
+        const int H = x == 0 || x == 3 ? Hq : Hkv;
+        if (!ptr[x] || !aligned16(ptr[x])) return LA_ERR_INVALID_ARG;
+        w[x] = View{ptr[x], {B, H, 1}, {}, D, elem};
+        const long long dense[3] = {(long long)H * D, D, D};
+        const long long given[3] = {strides ? strides[2 * x] : 0, strides ? strides[2 * x + 1] : 0, D};
+        if ((rc = set_view(w[x], strides ? given : dense, dense))) return rc;
+    }
+    const size_t gb = normaliser ? (size_t)B * Hq * 4 : 0;
+    if ((uintptr_t)normaliser & 3) return LA_ERR_INVALID_ARG;
+    const void *ins[5] = {q, k, v, o, normaliser};
+    const size_t ib[5] = {view_bytes(w[0]), view_bytes(w[1]), view_bytes(w[2]), view_bytes(w[3]), gb};
+    if ((rc = check_state(B, Hkv, D, dtype, S, z, a, n, ins, ib, 5))) return rc;
+    for (int x = 0; x < 3; ++x)
+        if (views_meet(w[3], w[x]) || ranges_meet(normaliser, gb, ptr[x], ib[x])) return LA_ERR_INVALID_ARG;
+    if (ranges_meet(normaliser, gb, o, ib[3])) return LA_ERR_INVALID_ARG;
+    GroupedArgs P = {};
+    P.q = q, P.k = k, P.v = v, P.o = o, P.g = normaliser;
+    P.S = S, P.z = z, P.a = a, P.n = n;
+    Strides2 *st[4] = {&P.qs, &P.ks, &P.vs, &P.os};
+    for (int x = 0; x < 4; ++x) *st[x] = Strides2{w[x].st[0], w[x].st[1]};
+    P.Hkv = Hkv;
+    P.r = Hq / Hkv;
+    cudaStream_t s = (cudaStream_t)stream;
+    const cudaError_t e = dtype == LA_BF16 ? grouped_by_d<__nv_bfloat16, float>(D, P, BH, s)
+                                           : grouped_by_d<float, double>(D, P, BH, s);
+    if (e != cudaSuccess) return LA_ERR_CUDA;
+    count_launches(1);
     return LA_OK;
 }
 

@@ -1,0 +1,332 @@
+// la_prompt.cu -- the causal head over packed prompts with grouped heads (la_prompt): argument checks, and the
+// CUDA-core form, which serves fp32 and the bf16 head sizes without a tensor-core form.
+//
+// Sequences of different lengths lie end to end in T rows; query head h reads key/value head h / r.  Per sequence:
+//   O_i = (a + S^T q_i + sum_{j<=i} W_ij v_j) / (n + q_i . z + sum_{j<=i} W_ij),   W_ij = 1 + q_i . k_j
+// with (S, z, a, n) the state of all rows before the block of rows that i and j lie in; the state at the end is what
+// la_decode_step_grouped continues from.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "la_prompt.h"
+#include "la_views.h"
+
+namespace cg = cooperative_groups;
+
+namespace la {
+namespace prompt {
+
+// ----------------------------------------------------------------------------------------------------------------
+// CUDA-core form.  grid = (sequences x key/value heads, column blocks): a CTA walks one sequence 32 rows at a time
+// with E columns of S; the column blocks of a head are a cluster.  Warp w has rows w, w + 8, ... of a block, one lane per column (and per row j of W), so a
+// query head's rows stay within a warp.
+//
+// fp32 tokens keep an fp64 state, as la_decode_step does, but this GPU has two fp64 multiply-adds per SM and clock;
+// a sum is therefore two floats here (the product's and the sum's rounding errors are exact in fp32 and gathered in
+// the low one), good to 2^-46, and becomes a double once, at the end.  O is formed in fp32 from the high floats.
+// ----------------------------------------------------------------------------------------------------------------
+constexpr int kThreads = 256, kWarps = 8, kRows = 32;
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float *p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+
+// A running sum: a float (bf16 tokens), or a float and the sum of its rounding errors (fp32 tokens).
+template <typename T> struct Sum;
+template <> struct Sum<__nv_bfloat16> {
+    using Acc = float;
+    float hi;
+    __device__ void set(float x) { hi = x; }
+    __device__ void add(float x) { hi += x; }
+    __device__ void fma(float x, float y) { hi = fmaf(x, y, hi); }
+    __device__ void join(const Sum &s) { hi += s.hi; }
+    __device__ float get() const { return hi; }
+};
+template <> struct Sum<float> {
+    using Acc = double;
+    float hi, lo;
+    __device__ void set(double x) {
+        hi = (float)x;
+        lo = (float)(x - (double)hi);
+    }
+    __device__ void add(float x) {
+        const float t = __fadd_rn(hi, x), b = __fsub_rn(t, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(x, b)));
+        hi = t;
+    }
+    __device__ void fma(float x, float y) {
+        const float p = __fmul_rn(x, y), e = __fmaf_rn(x, y, -p);
+        add(p);
+        lo = __fadd_rn(lo, e);
+    }
+    __device__ void join(const Sum &s) {
+        add(s.hi);
+        lo = __fadd_rn(lo, s.lo);
+    }
+    __device__ double get() const { return (double)hi + (double)lo; }
+};
+
+template <typename T, int D> struct Tile {
+    static constexpr int E = D < 32 ? D : 32;       // columns of S in a CTA
+    static constexpr int LD = D + 4;                // row pitch of Q and K: 16-byte loads of 8 rows meet all banks
+    static constexpr int RE = 32 / E;               // rows a warp takes side by side (2 where E = 16)
+    static constexpr int NS = D * E / kThreads;     // elements of S of a thread
+    static constexpr size_t SMEM = sizeof(float) * (2 * kRows * LD + kRows * E + kRows * kRows + D * E + D + E);
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_constant__ Args A) {
+    using C = Tile<T, D>;
+    using Acc = typename Sum<T>::Acc;
+    constexpr int E = C::E, LD = C::LD;
+    extern __shared__ __align__(16) float sm[];
+    float *Ks = sm, *Qs = Ks + kRows * LD, *Vs = Qs + kRows * LD, *Ws = Vs + kRows * E, *Sf = Ws + kRows * kRows;
+    float *zs = Sf + D * E, *as = zs + D;
+    if (!offsets_in_order(A)) return;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int seq = blockIdx.x / A.Hkv, h = blockIdx.x % A.Hkv, e0 = blockIdx.y * E;
+    const long long at = (long long)seq * A.Hkv + h;
+    const int lo = A.off[seq], hi = A.off[seq + 1];
+    const T *K = (const T *)A.k + h * A.kh, *V = (const T *)A.v + h * A.vh + e0;
+    Acc *S = A.S ? (Acc *)A.S + at * D * D : nullptr, *z = (Acc *)A.z + at * D, *a = (Acc *)A.a + at * D;
+    const bool resume = A.resume && S;
+    // this thread's elements of S: column t % E, rows t / E + m (256 / E); thread t < D has z[t], t < E has a[e0 + t]
+    const int e = t % E, d0 = t / E;
+    constexpr int DS = kThreads / E;
+    Sum<T> s[C::NS], zt, at_;
+#pragma unroll
+    for (int m = 0; m < C::NS; ++m) {
+        s[m].set(0);
+        if (resume) s[m].set(S[(long long)(d0 + m * DS) * D + e0 + e]);
+        Sf[(d0 + m * DS) * E + e] = s[m].hi;
+    }
+    zt.set(0);
+    at_.set(0);
+    if (t < D) {
+        if (resume) zt.set(z[t]);
+        zs[t] = zt.hi;
+    }
+    if (t < E) {
+        if (resume) at_.set(a[e0 + t]);
+        as[t] = at_.hi;
+    }
+    const int n0 = resume ? A.n[at] : 0;
+    if (gridDim.y > 1) cg::this_cluster().sync();  // the column blocks share z and n: all have read them
+    for (int row0 = lo; row0 < hi; row0 += kRows) {
+        const int live = min(kRows, hi - row0);
+        __syncthreads();  // the block before is done with K and V, and S, z, a are those after it
+        for (int x = t; x < kRows * D; x += kThreads) {
+            const int j = x / D, d = x % D;
+            Ks[j * LD + d] = j < live ? to_f(K[(long long)(row0 + j) * A.kn + d]) : 0.f;
+        }
+        for (int x = t; x < kRows * E; x += kThreads) {
+            const int j = x / E, c = x % E;
+            Vs[x] = j < live ? to_f(V[(long long)(row0 + j) * A.vn + c]) : 0.f;
+        }
+        __syncthreads();
+        const float nb = (float)(n0 + (row0 - lo));
+        for (int g = 0; g < A.r; ++g) {
+            const int hq = h * A.r + g;
+            const T *Q = (const T *)A.q + hq * A.qh;
+            T *O = (T *)A.o + hq * A.oh + e0;
+            __syncwarp();
+            for (int m = 0; m < kRows / kWarps; ++m) {
+                const int i = warp + kWarps * m;
+                for (int d = lane; d < D; d += 32)
+                    Qs[i * LD + d] = i < live ? to_f(Q[(long long)(row0 + i) * A.qn + d]) : 0.f;
+            }
+            __syncwarp();
+            // W and g: lane j of row i
+            float gi[kRows / kWarps];
+#pragma unroll
+            for (int m = 0; m < kRows / kWarps; ++m) {
+                const int i = warp + kWarps * m;
+                float w = 1.f, qz = 0.f;
+#pragma unroll 4
+                for (int d = 0; d < D; d += 4) {
+                    const float4 q4 = *(const float4 *)(Qs + i * LD + d), k4 = *(const float4 *)(Ks + lane * LD + d);
+                    w = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, w))));
+                }
+                for (int d = lane; d < D; d += 32) qz = fmaf(Qs[i * LD + d], zs[d], qz);
+                w = lane <= i ? w : 0.f;
+                Ws[i * kRows + lane] = w;
+                float sum = w + qz;
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                gi[m] = nb + sum;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int m0 = 0; m0 < kRows / kWarps; ++m0) {
+                const int i = warp + kWarps * m0;
+                const int c = lane % E;
+                const int part = lane / E;  // E = 16: the two half warps take half of the sums each
+                float o = part ? 0.f : as[c];
+#pragma unroll 8
+                for (int d = part * (D / C::RE); d < (part + 1) * (D / C::RE); ++d)
+                    o = fmaf(Qs[i * LD + d], Sf[d * E + c], o);
+                for (int j = part; j <= i; j += C::RE) o = fmaf(Ws[i * kRows + j], Vs[j * E + c], o);
+                if (C::RE == 2) o += __shfl_xor_sync(0xffffffffu, o, 16);
+                if (i < live && part == 0) put(O + (long long)(row0 + i) * A.on + c, o / gi[m0]);
+            }
+        }
+        __syncthreads();  // every warp has read S, z and a of before
+        // the block's own sums first: over a long sequence a sum then passes a rounding for every 32 rows, not for each
+        Sum<T> bs[C::NS], bz, ba;
+#pragma unroll
+        for (int m = 0; m < C::NS; ++m) bs[m].set(0);
+        bz.set(0);
+        ba.set(0);
+        for (int j = 0; j < live; ++j) {
+            const float v = Vs[j * E + e];
+#pragma unroll
+            for (int m = 0; m < C::NS; ++m) bs[m].fma(Ks[j * LD + d0 + m * DS], v);
+            if (t < D) bz.add(Ks[j * LD + t]);
+            if (t < E) ba.add(Vs[j * E + t]);
+        }
+#pragma unroll
+        for (int m = 0; m < C::NS; ++m) s[m].join(bs[m]);
+        zt.join(bz);
+        at_.join(ba);
+#pragma unroll
+        for (int m = 0; m < C::NS; ++m) Sf[(d0 + m * DS) * E + e] = s[m].hi;
+        if (t < D) zs[t] = zt.hi;
+        if (t < E) as[t] = at_.hi;
+    }
+    if (!S) return;
+#pragma unroll
+    for (int m = 0; m < C::NS; ++m) S[(long long)(d0 + m * DS) * D + e0 + e] = s[m].get();
+    if (t < E) a[e0 + t] = at_.get();
+    if (blockIdx.y == 0) {
+        if (t < D) z[t] = zt.get();
+        if (t == 0) A.n[at] = n0 + (hi - lo);
+    }
+}
+
+template <typename T, int D> cudaError_t launch_simt(const Args &A, cudaStream_t s) {
+    using C = Tile<T, D>;
+    static std::atomic<int> attr_state[kMaxDevices];
+    if (!once_per_device(attr_state, [] {
+            return cudaFuncSetAttribute(prompt_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)C::SMEM) == cudaSuccess;
+        }))
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)A.nseq * A.Hkv), D / C::E);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = D / C::E;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prompt_simt_kernel<T, D>, A);
+}
+
+template <typename T> cudaError_t simt_by_d(const Args &A, cudaStream_t s) {
+    switch (A.D) {
+        case 16: return launch_simt<T, 16>(A, s);
+        case 32: return launch_simt<T, 32>(A, s);
+        case 64: return launch_simt<T, 64>(A, s);
+        case 128: return launch_simt<T, 128>(A, s);
+        default: return launch_simt<T, 256>(A, s);
+    }
+}
+
+cudaError_t simt(const Args &A, int dtype, cudaStream_t s) {
+    const cudaError_t e = dtype == LA_BF16 ? simt_by_d<__nv_bfloat16>(A, s) : simt_by_d<float>(A, s);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+bool supported_d(int D) { return D == 16 || D == 32 || D == 64 || D == 128 || D == 256; }
+
+}  // namespace prompt
+}  // namespace la
+
+extern "C" {
+
+size_t la_prompt_workspace_bytes(int T, int nseq, int Hq, int Hkv, int D, int dtype) {
+    if (T < 0 || nseq < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || !la::prompt::supported_d(D) ||
+        (dtype != LA_F32 && dtype != LA_BF16))
+        return 0;
+    return 256;
+}
+
+int la_prompt(const void *Q, const void *K, const void *V, const int *seq_offsets, void *O, void *S, void *z, void *a,
+              int *n, int resume, int T, int nseq, int Hq, int Hkv, int D, int dtype, const long long *strides,
+              void *workspace, size_t workspace_bytes, void *stream) {
+    using namespace la;
+    using namespace la::prompt;
+    if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
+    if (T < 0 || nseq < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || D < 1) return LA_ERR_INVALID_ARG;
+    if (!supported_d(D)) return LA_ERR_UNSUPPORTED;
+    if ((long long)T * Hq >= (1LL << 40) / D || (long long)nseq * Hkv >= (1LL << 31) / 16) return LA_ERR_INVALID_ARG;
+    const int elem = dtype == LA_BF16 ? 2 : 4, acc = dtype == LA_BF16 ? 4 : 8;
+    const bool any = S || z || a || n, all = S && z && a && n;
+    if (any != all || (resume && !all)) return LA_ERR_INVALID_ARG;
+    if (nseq == 0) return LA_OK;
+    const size_t ws_need = la_prompt_workspace_bytes(T, nseq, Hq, Hkv, D, dtype);
+    if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < ws_need) return LA_ERR_WORKSPACE;
+    if (!seq_offsets || ((uintptr_t)seq_offsets & 3)) return LA_ERR_INVALID_ARG;
+    const void *ptr[4] = {Q, K, V, O};
+    View v[4];
+    int rc;
+    for (int k = 0; k < 4; ++k) {  // (Q, K, V, O) x (head, row)
+        const int H = k == 0 || k == 3 ? Hq : Hkv;
+        if (T > 0 && (!ptr[k] || ((uintptr_t)ptr[k] & 15))) return LA_ERR_INVALID_ARG;
+        v[k] = View{ptr[k], {1, H, T}, {}, D, elem};
+        const long long dense[3] = {D, D, (long long)H * D};
+        const long long given[3] = {D, strides ? strides[2 * k] : 0, strides ? strides[2 * k + 1] : 0};
+        if (T > 0 && (rc = set_view(v[k], strides ? given : dense, dense))) return rc;
+    }
+    const long long SH = (long long)nseq * Hkv;
+    const void *st[4] = {S, z, a, n};
+    const size_t sb[4] = {(size_t)SH * D * D * acc, (size_t)SH * D * acc, (size_t)SH * D * acc, (size_t)SH * 4};
+    const size_t ob = (size_t)(nseq + 1) * 4;
+    for (int k = 0; k < 3 && T > 0; ++k)
+        if (views_meet(v[3], v[k])) return LA_ERR_INVALID_ARG;
+    if (ranges_meet(workspace, ws_need, seq_offsets, ob)) return LA_ERR_INVALID_ARG;
+    if (T > 0) {
+        if (ranges_meet(O, view_bytes(v[3]), seq_offsets, ob)) return LA_ERR_INVALID_ARG;
+        for (int k = 0; k < 4; ++k)
+            if (ranges_meet(workspace, ws_need, ptr[k], view_bytes(v[k]))) return LA_ERR_INVALID_ARG;
+    }
+    for (int x = 0; x < 4 && all; ++x) {
+        if ((uintptr_t)st[x] & 15) return LA_ERR_INVALID_ARG;
+        for (int y = x + 1; y < 4; ++y)
+            if (ranges_meet(st[x], sb[x], st[y], sb[y])) return LA_ERR_INVALID_ARG;
+        for (int k = 0; k < 4 && T > 0; ++k)
+            if (ranges_meet(st[x], sb[x], ptr[k], view_bytes(v[k]))) return LA_ERR_INVALID_ARG;
+        if (ranges_meet(st[x], sb[x], seq_offsets, ob) || ranges_meet(st[x], sb[x], workspace, ws_need))
+            return LA_ERR_INVALID_ARG;
+    }
+    Args A = {};
+    A.q = Q;
+    A.k = K;
+    A.v = V;
+    A.o = O;
+    A.off = seq_offsets;
+    A.S = S;
+    A.z = z;
+    A.a = a;
+    A.n = n;
+    A.resume = resume ? 1 : 0;
+    A.T = T;
+    A.nseq = nseq;
+    A.Hq = Hq;
+    A.Hkv = Hkv;
+    A.r = Hq / Hkv;
+    A.D = D;
+    A.qh = v[0].st[1], A.qn = v[0].st[2], A.kh = v[1].st[1], A.kn = v[1].st[2];
+    A.vh = v[2].st[1], A.vn = v[2].st[2], A.oh = v[3].st[1], A.on = v[3].st[2];
+    A.status = (uint32_t *)workspace;
+    return simt(A, dtype, (cudaStream_t)stream) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+}  // extern "C"

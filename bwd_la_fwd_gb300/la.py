@@ -74,6 +74,24 @@ def open_library(path: str):
     lib.la_decode_step.restype = i
     lib.la_state_append.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp]
     lib.la_state_append.restype = i
+    lib.la_decode_step_grouped.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, lp, vp]
+    lib.la_decode_step_grouped.restype = i
+    lib.la_prompt_workspace_bytes.argtypes = [i, i, i, i, i, i]
+    lib.la_prompt_workspace_bytes.restype = sz
+    lib.la_prompt.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, lp, vp, sz, vp]
+    lib.la_prompt.restype = i
+    up, dbl, ll = ctypes.POINTER(ctypes.c_ulonglong), ctypes.c_double, ctypes.c_longlong
+    lib.la_rotary_frequencies.argtypes = [i, dbl, i, dbl, dbl, dbl, dbl, up]
+    lib.la_rotary_frequencies.restype = i
+    for f in (lib.la_rotary, lib.la_rotary_backward):
+        f.argtypes = [vp, vp, vp, vp, up, vp, ll, ll, i, ctypes.c_float, i, i, i, i, i, i, i, lp, vp]
+        f.restype = i
+    lib.la_gated_scan.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, lp, vp]
+    lib.la_gated_scan.restype = i
+    lib.la_gated_scan_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, lp, vp]
+    lib.la_gated_scan_backward.restype = i
+    lib.la_gated_scan_step.argtypes = [vp, vp, vp, vp, i, i, i, i, lp, vp]
+    lib.la_gated_scan_step.restype = i
     lib.la_get_status.argtypes = [vp, vp]
     lib.la_get_status.restype = i
     lib.la_forward_noalloc.argtypes = [vp, vp, vp, i, vp, vp, i, i, i, i, i, vp]
@@ -228,14 +246,23 @@ def la_noalloc_get_status(stream=None) -> int:
 class DecodeState:
     """The carried state of the recurrent (decode) form, per (b, h): S [B,H,D,D], z [B,H,D], a [B,H,D] of
     the accumulator type (float32 for bf16 tokens, float64 for float32 tokens) and the count n (int32
-    [B,H]).  Zero-filled is the empty state; the library updates the tensors in place."""
+    [B,H]).  Zero-filled is the empty state; the library updates the tensors in place.
 
-    def __init__(self, B: int, H: int, D: int, token_dtype, device="cuda"):
+    For grouped heads H is the number of key/value heads.  ``tensors`` = (S, z, a, n) takes the caller's
+    tensors (parts of a larger cache, say) instead of new ones."""
+
+    def __init__(self, B: int, H: int, D: int, token_dtype, device="cuda", tensors=None):
         import torch
         acc = torch.float32 if token_dtype == torch.bfloat16 else torch.float64
         if token_dtype not in (torch.bfloat16, torch.float32):
             raise TypeError(f"unsupported dtype {token_dtype}: use torch.bfloat16 or torch.float32")
         self.B, self.H, self.D, self.token_dtype = B, H, D, token_dtype
+        if tensors is not None:
+            for t, shape, dt in zip(tensors, ((B, H, D, D), (B, H, D), (B, H, D), (B, H)), (acc, acc, acc, torch.int32)):
+                if tuple(t.shape) != shape or t.dtype != dt or not t.is_contiguous() or t.device != tensors[0].device:
+                    raise ValueError(f"expected a contiguous {dt} tensor of shape {shape} on one device")
+            self.S, self.z, self.a, self.n = tensors
+            return
         self.S = torch.zeros((B, H, D, D), dtype=acc, device=device)
         self.z = torch.zeros((B, H, D), dtype=acc, device=device)
         self.a = torch.zeros((B, H, D), dtype=acc, device=device)
@@ -278,3 +305,308 @@ def la_state_append(state: DecodeState, K, V, stream=None):
     if st != 0:
         raise LAError(st, "la_state_append")
     return state
+
+
+def _place(stream, *ts):
+    """The stream that a call on these tensors goes to: `stream`, or the current one of their device."""
+    import torch
+    dev = ts[0].device
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {dev}")
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on one device, got {dev} and {t.device}")
+    if stream is None:
+        return torch.cuda.current_stream(dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return stream
+
+
+class _on:
+    """Makes the stream and its device the current ones for a call: new tensors belong to that stream, and the
+    library launches on that device."""
+
+    __slots__ = ("_ctx",)
+
+    def __init__(self, stream):
+        import torch
+        self._ctx = None if stream == torch.cuda.current_stream() else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def _longs(vals):
+    return (ctypes.c_longlong * len(vals))(*vals)
+
+
+def _row_contiguous(*ts):
+    for t in ts:
+        if t is not None and t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError("the last dimension must be contiguous (stride(-1) == 1)")
+
+
+def _expect(t, shape, dtype, what):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+
+
+def la_decode_step_grouped(state: DecodeState, q, k, v, o=None, normaliser=None, stream=None):
+    """o = la_decode_step_grouped(state, q, k, v): one token for grouped heads, q [B,Hq,D], k and v [B,Hkv,D] with
+    Hkv = state.H and Hq a multiple of it.  The tensors may be strided views (slices of a fused projection) with
+    contiguous D; `normaliser`, if given, is a float32 [B,Hq] tensor that receives g."""
+    import torch
+    B, H, D = state.B, state.H, state.D
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != D or H < 1 or q.shape[1] % H != 0 or q.shape[1] < H:
+        raise ValueError(f"expected [B, r Hkv, D] queries for B, Hkv, D = {(B, H, D)}, got {tuple(q.shape)}")
+    Hq = q.shape[1]
+    if tuple(k.shape) != (B, H, D) or tuple(v.shape) != (B, H, D) or (o is not None and o.shape != q.shape):
+        raise ValueError(f"expected k, v of shape {(B, H, D)} and o like q")
+    for t in (q, k, v, o):
+        if t is not None and t.dtype != state.token_dtype:
+            raise ValueError("token dtype does not match the state")
+    _row_contiguous(q, k, v, o)
+    stream = _place(stream, q, k, v, o, normaliser, state.S, state.z, state.a, state.n)
+    if normaliser is not None:
+        _expect(normaliser, (B, Hq), torch.float32, "normaliser")
+    with _on(stream):
+        if o is None:
+            o = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+        st = load_library().la_decode_step_grouped(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(normaliser), state.S.data_ptr(),
+            state.z.data_ptr(), state.a.data_ptr(), state.n.data_ptr(), B, Hq, H, D, _dtype_code(q),
+            _longs((*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2])), stream.cuda_stream)
+    if st != 0:
+        raise LAError(st, "la_decode_step_grouped")
+    return o
+
+
+def la_prompt_workspace_bytes(T: int, nseq: int, Hq: int, Hkv: int, D: int, dtype: int) -> int:
+    return int(load_library().la_prompt_workspace_bytes(T, nseq, Hq, Hkv, D, int(dtype)))
+
+
+def new_prompt_workspace(T: int, nseq: int, Hq: int, Hkv: int, D: int, dtype: int, device="cuda"):
+    """Zero-filled device workspace of the size la_prompt asks for."""
+    import torch
+    n = la_prompt_workspace_bytes(T, nseq, Hq, Hkv, D, dtype)
+    if n == 0:
+        raise LAError(1, "la_prompt_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def la_prompt(Q, K, V, seq_offsets, state=None, resume: bool = False, O=None, workspace=None, stream=None):
+    """O = la_prompt(Q, K, V, seq_offsets, state): the causal forward over packed prompts with grouped heads.
+
+    Q [T,Hq,D], K and V [T,Hkv,D] (strided views with contiguous D are taken as they are); sequence i has rows
+    seq_offsets[i] ... seq_offsets[i+1] - 1 (int32 on the device).  ``state``, a DecodeState(nseq, Hkv, D), receives
+    each sequence's state, or with ``resume`` continues from it.  Rows outside every sequence keep what O holds (a new
+    O is zero there)."""
+    import torch
+    if Q.dim() != 3 or K.dim() != 3 or seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1:
+        raise ValueError("expected [T, H, D] tensors and [nseq + 1] offsets")
+    T, Hq, D = Q.shape
+    Hkv, nseq = K.shape[1], seq_offsets.shape[0] - 1
+    if K.shape[0] != T or K.shape[2] != D or V.shape != K.shape or (O is not None and O.shape != Q.shape):
+        raise ValueError(f"Q {tuple(Q.shape)}, K {tuple(K.shape)}, V {tuple(V.shape)} do not match")
+    if Hkv < 1 or Hq < Hkv or Hq % Hkv != 0:
+        raise ValueError(f"{Hq} query heads are not a multiple of {Hkv} key/value heads")
+    for t in (K, V, O):
+        if t is not None and t.dtype != Q.dtype:
+            raise ValueError("Q, K, V, O must share their dtype")
+    _expect(seq_offsets, (nseq + 1,), torch.int32, "seq_offsets")
+    _row_contiguous(Q, K, V, O)
+    dt = _dtype_code(Q)
+    if state is not None and ((state.B, state.H, state.D) != (nseq, Hkv, D) or state.token_dtype != Q.dtype):
+        raise ValueError(f"the state is not one of nseq, Hkv, D = {(nseq, Hkv, D)} and {Q.dtype}")
+    if resume and state is None:
+        raise ValueError("resume needs a state")
+    parts = (state.S, state.z, state.a, state.n) if state is not None else (None,) * 4
+    stream = _place(stream, Q, K, V, O, seq_offsets, workspace, *parts)
+    with _on(stream):
+        if O is None:
+            O = torch.zeros((T, Hq, D), dtype=Q.dtype, device=Q.device)
+        if workspace is None:
+            workspace = new_prompt_workspace(T, nseq, Hq, Hkv, D, dt, Q.device)
+        st = load_library().la_prompt(
+            Q.data_ptr(), K.data_ptr(), V.data_ptr(), seq_offsets.data_ptr(), O.data_ptr(), *map(_ptr, parts),
+            int(bool(resume)), T, nseq, Hq, Hkv, D, dt,
+            _longs([s for t in (Q, K, V, O) for s in (t.stride(1), t.stride(0))]), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), stream.cuda_stream)
+    if st != 0:
+        raise LAError(st, "la_prompt")
+    return O
+
+
+class RotaryFrequencies:
+    """The rotation of each channel pair per position, in units of 2^-64 turns (``values``, a host array that the
+    library reads during each call), for heads of which ``rotary_dim`` channels are rotated."""
+
+    def __init__(self, rotary_dim: int, values):
+        self.rotary_dim = int(rotary_dim)
+        self.values = (ctypes.c_ulonglong * (self.rotary_dim // 2))(*values)
+
+
+_ROTARY_SCALING = {"none": 0, "linear": 1, "by_turns": 2}
+
+
+def la_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                          original_length: float = 0.0, low_turns: float = 1.0, high_turns: float = 32.0):
+    """RotaryFrequencies for base^(-2 i / rotary_dim) radians per position: as they are ("none"), divided by `factor`
+    ("linear"), or divided by it only for the pairs of few turns over `original_length` positions ("by_turns")."""
+    if scaling not in _ROTARY_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_ROTARY_SCALING)}")
+    out = (ctypes.c_ulonglong * max(1, int(rotary_dim) // 2))()
+    st = load_library().la_rotary_frequencies(int(rotary_dim), base, _ROTARY_SCALING[scaling], factor, original_length,
+                                              low_turns, high_turns, out)
+    if st != 0:
+        raise LAError(st, "la_rotary_frequencies")
+    return RotaryFrequencies(rotary_dim, out)
+
+
+def _rotary(name, Q, K, freqs, positions, first_position, interleaved, magnitude, Q_out, K_out, stream):
+    import torch
+    B, Hq, N, D = _shape(Q)
+    for t, like in ((K, None), (Q_out, Q), (K_out, K)):
+        if t is None:
+            continue
+        if t.dtype != Q.dtype or t.dim() != 4 or (t.shape[0], t.shape[2], t.shape[3]) != (B, N, D) or (
+                like is not None and t.shape != like.shape):
+            raise ValueError("Q, K and the outputs must be [B, H, N, D] tensors that share B, N, D and dtype")
+    if K is None and K_out is not None:
+        raise ValueError("K_out without K")
+    _row_contiguous(Q, K, Q_out, K_out)
+    dt = _dtype_code(Q)
+    stride = 0
+    if positions is not None:
+        if positions.dtype != torch.int32 or tuple(positions.shape) not in ((N,), (B, N)) or (
+                N > 1 and positions.stride(-1) != 1):
+            raise ValueError(f"positions: expected int32 [N] or [B, N] with contiguous rows, got {positions.dtype} "
+                             f"{tuple(positions.shape)}")
+        # a batch of one is stepped by nothing, whatever its stride
+        stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+        if stride and stride < N:
+            raise ValueError("positions of the batch entries overlap")
+    stream = _place(stream, Q, K, Q_out, K_out, positions)
+    with _on(stream):
+        if Q_out is None:
+            Q_out = torch.empty((B, Hq, N, D), dtype=Q.dtype, device=Q.device)
+        if K is not None and K_out is None:
+            K_out = torch.empty(K.shape, dtype=K.dtype, device=K.device)
+        Hk = 0 if K is None else K.shape[1]
+        sk, sko = (K.stride()[:3], K_out.stride()[:3]) if Hk else ((0, 0, 0), (0, 0, 0))
+        st = getattr(load_library(), name)(
+            Q.data_ptr(), _ptr(K), Q_out.data_ptr(), _ptr(K_out), freqs.values, _ptr(positions), stride, first_position,
+            int(bool(interleaved)), magnitude, B, Hq, Hk, N, D, freqs.rotary_dim, dt,
+            _longs((*Q.stride()[:3], *sk, *Q_out.stride()[:3], *sko)), stream.cuda_stream)
+    if st != 0:
+        raise LAError(st, name)
+    return Q_out, K_out
+
+
+def la_rotary(Q, K, freqs: RotaryFrequencies, positions=None, first_position: int = 0, interleaved: bool = False,
+              magnitude: float = 1.0, Q_out=None, K_out=None, stream=None):
+    """Q', K' = la_rotary(Q, K, freqs): positions rotated into Q [B,Hq,N,D] and K [B,Hk,N,D] (or None), in one launch.
+
+    ``positions`` is an int32 [B,N] or [N] device tensor; without it row i has position first_position + i.  Views
+    with contiguous D are taken as they are; Q_out = Q and K_out = K rotate in place."""
+    return _rotary("la_rotary", Q, K, freqs, positions, first_position, interleaved, magnitude, Q_out, K_out, stream)
+
+
+def la_rotary_backward(dQ, dK, freqs: RotaryFrequencies, positions=None, first_position: int = 0,
+                       interleaved: bool = False, magnitude: float = 1.0, dQ_out=None, dK_out=None, stream=None):
+    """The gradients of la_rotary's inputs from those of its outputs (the other arguments as given to it)."""
+    return _rotary("la_rotary_backward", dQ, dK, freqs, positions, first_position, interleaved, magnitude, dQ_out,
+                   dK_out, stream)
+
+
+_GATES = {"log": 0, "sigmoid": 1}
+
+
+def _gate_code(gate) -> int:
+    if gate not in _GATES:
+        raise ValueError(f"gate must be one of {sorted(_GATES)}")
+    return _GATES[gate]
+
+
+def _scan_operands(dims, first, *others):
+    if first.dim() != dims:
+        raise ValueError(f"expected a {'[B, N, C]' if dims == 3 else '[B, C]'} tensor, got shape {tuple(first.shape)}")
+    for t in others:
+        if t is not None and (t.shape != first.shape or t.dtype != first.dtype):
+            raise ValueError("the tensors must share shape and dtype")
+    _row_contiguous(first, *others)
+
+
+def la_gated_scan(X, W, gate: str, h0=None, H=None, h_last=None, stream=None):
+    """H, h_last = la_gated_scan(X, W, gate): h_t = a_t h_{t-1} + b_t x_t along dimension 1 of [B,N,C] tensors, per
+    channel, with a = e^w, b = 1 (gate "log") or a = sigmoid(w), b = 1 - a (gate "sigmoid").  h0 and h_last are float32
+    [B,C]: the value before the first row (None: 0) and after the last."""
+    import torch
+    _scan_operands(3, X, W, H)
+    B, N, C = X.shape
+    code, dt = _gate_code(gate), _dtype_code(X)
+    for t, what in ((h0, "h0"), (h_last, "h_last")):
+        if t is not None:
+            _expect(t, (B, C), torch.float32, what)
+    stream = _place(stream, X, W, h0, H, h_last)
+    with _on(stream):
+        if H is None:
+            H = torch.empty((B, N, C), dtype=X.dtype, device=X.device)
+        if h_last is None:
+            h_last = torch.empty((B, C), dtype=torch.float32, device=X.device)
+        st = load_library().la_gated_scan(X.data_ptr(), W.data_ptr(), _ptr(h0), H.data_ptr(), h_last.data_ptr(), B, N, C,
+                                          code, dt, _longs((*X.stride()[:2], *W.stride()[:2], *H.stride()[:2])),
+                                          stream.cuda_stream)
+    if st != 0:
+        raise LAError(st, "la_gated_scan")
+    return H, h_last
+
+
+def la_gated_scan_backward(X, W, H, dH, gate: str, h0=None, dh_last=None, dX=None, dW=None, dh0=None, stream=None):
+    """dX, dW, dh0 = la_gated_scan_backward(X, W, H, dH, gate): gradients of sum(dH * H) + sum(dh_last * h_last), H and
+    h0 as the forward had them."""
+    import torch
+    _scan_operands(3, X, W, H, dH, dX, dW)
+    B, N, C = X.shape
+    code, dt = _gate_code(gate), _dtype_code(X)
+    for t, what in ((h0, "h0"), (dh_last, "dh_last"), (dh0, "dh0")):
+        if t is not None:
+            _expect(t, (B, C), torch.float32, what)
+    stream = _place(stream, X, W, H, dH, h0, dh_last, dX, dW, dh0)
+    with _on(stream):
+        dX = torch.empty((B, N, C), dtype=X.dtype, device=X.device) if dX is None else dX
+        dW = torch.empty((B, N, C), dtype=X.dtype, device=X.device) if dW is None else dW
+        dh0 = torch.empty((B, C), dtype=torch.float32, device=X.device) if dh0 is None else dh0
+        st = load_library().la_gated_scan_backward(
+            X.data_ptr(), W.data_ptr(), H.data_ptr(), dH.data_ptr(), _ptr(h0), _ptr(dh_last), dX.data_ptr(),
+            dW.data_ptr(), dh0.data_ptr(), B, N, C, code, dt,
+            _longs([s for t in (X, W, H, dH, dX, dW) for s in t.stride()[:2]]), stream.cuda_stream)
+    if st != 0:
+        raise LAError(st, "la_gated_scan_backward")
+    return dX, dW, dh0
+
+
+def la_gated_scan_step(state, x, w, gate: str, h=None, stream=None):
+    """h = la_gated_scan_step(state, x, w, gate): one row of the recurrence for [B,C] tensors; ``state``, float32 [B,C],
+    is advanced in place."""
+    import torch
+    _scan_operands(2, x, w, h)
+    B, C = x.shape
+    code, dt = _gate_code(gate), _dtype_code(x)
+    _expect(state, (B, C), torch.float32, "state")
+    stream = _place(stream, x, w, h, state)
+    with _on(stream):
+        if h is None:
+            h = torch.empty((B, C), dtype=x.dtype, device=x.device)
+        st = load_library().la_gated_scan_step(x.data_ptr(), w.data_ptr(), h.data_ptr(), state.data_ptr(), B, C, code, dt,
+                                               _longs((x.stride(0), w.stride(0), h.stride(0))), stream.cuda_stream)
+    if st != 0:
+        raise LAError(st, "la_gated_scan_step")
+    return h

@@ -58,8 +58,8 @@ typedef enum {
     LA_ERR_TIMEOUT = 5,     /* device: a bounded barrier wait inside a kernel gave up (reported by la_get_status) */
     LA_ERR_BOUNDS = 6,      /* device: an internal layout check failed -- a kernel's shared-memory window was not
                                1024-byte aligned, so it computed nothing; or, in the index-checked test build
-                               (libla_gb300_checked.so), an index out of its array was skipped (reported by
-                               la_get_status) */
+                               (libla_gb300_checked.so), an index out of its array was skipped; or la_prompt's
+                               offsets are not in order within its rows (reported by la_get_status) */
     LA_ERR_STATE = 7        /* device: la_backward_with_forward_state found no matching forward state */
 } la_status;
 
@@ -227,6 +227,110 @@ int la_decode_step(const void *q, const void *k, const void *v, void *o, float *
  */
 int la_state_append(const void *K, const void *V, void *S, void *z, void *a, int *n, int B, int H, int N, int D,
                     int dtype, void *stream);
+
+/*
+ * One token for grouped heads: Hq = r Hkv query heads (r <= 64), of which heads h r ... h r + r - 1 share the state
+ * of key/value head h.  Appends (k, v) to each state, then g = n + q . z, o = (a + S^T q) / g for each query head:
+ * la_decode_step with the shared state read and written once.
+ *   q, o        in / out: [B,Hq,D];  k, v in: [B,Hkv,D], of `dtype`
+ *   normaliser  out: float [B,Hq], or NULL
+ *   S, z, a, n  in/out: the state arrays above for [B,Hkv]
+ *   strides     in : host array, (batch, head) element strides of q, k, v, o (8 values; the rules of the strided
+ *               passes), or NULL for contiguous tensors
+ */
+int la_decode_step_grouped(const void *q, const void *k, const void *v, void *o, float *normaliser, void *S, void *z,
+                           void *a, int *n, int B, int Hq, int Hkv, int D, int dtype, const long long *strides,
+                           void *stream);
+
+/*
+ * The causal forward over packed prompts with grouped heads, for serving: nseq sequences of different lengths lie end
+ * to end in T rows, and each leaves the state that la_decode_step_grouped continues from.
+ *   Q, O         in / out: [T,Hq,D] of `dtype`;  K, V in: [T,Hkv,D];  Hq = r Hkv, query head h with key/value head h / r
+ *   seq_offsets  in : device int [nseq + 1]; sequence i has rows seq_offsets[i] ... seq_offsets[i + 1] - 1 (none is
+ *                fine).  Rows outside every sequence are neither read into a result nor written.  Offsets that are
+ *                not in order within [0, T] are found on the device: nothing is computed, LA_ERR_BOUNDS is reported.
+ *   S, z, a, n   in/out: the state arrays above for [nseq,Hkv], or all NULL (sequences start empty and leave nothing)
+ *   resume       in : nonzero continues each sequence from its state (a prompt in parts); 0 starts it empty, and the
+ *                state arrays are written only
+ *   strides      in : host array, (head, row) element strides of Q, K, V, O (8 values; the rules of the strided
+ *                passes), or NULL for contiguous [T,H,D]
+ *   workspace    in/out: workspace_bytes >= la_prompt_workspace_bytes(), under the workspace rules above
+ * A sequence's rows do not depend on other sequences, nor on the rows around them, whatever those hold (infinities
+ * and NaN included).  A NaN or an infinity of its own K or V may reach every row of the sequence.
+ */
+size_t la_prompt_workspace_bytes(int T, int nseq, int Hq, int Hkv, int D, int dtype);
+int la_prompt(const void *Q, const void *K, const void *V, const int *seq_offsets, void *O, void *S, void *z, void *a,
+              int *n, int resume, int T, int nseq, int Hq, int Hkv, int D, int dtype, const long long *strides,
+              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rotary positions.  Pair i of a row at position p is turned by p f_i and scaled by `magnitude` m:
+ *   y1 = m (x1 cos - x2 sin),  y2 = m (x1 sin + x2 cos)
+ * A pair is channels (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with `interleaved`; channels from rotary_dim on are
+ * copied.  Q [B,Hq,N,D] and K [B,Hk,N,D] (Hk = 0: none, K and Kr unused) go in one launch.
+ *   frequencies      in : HOST array [rotary_dim / 2], f_i / 2 pi in units of 2^-64 turns per position, read during the
+ *                    call; la_rotary_frequencies fills one.  The phase p f_i is then exact for every position.
+ *   positions        in : device int, the position of (b, i) at positions[b position_stride + i] (position_stride 0:
+ *                    shared by the batch), or NULL for first_position + i
+ *   rotary_dim       in : even, 2 ... D;  D <= 256 and a whole number of 16-byte vectors
+ *   strides          in : host array, (batch, head, row) element strides of Q, K, Qr, Kr (12 values; the rules of the
+ *                    strided passes), or NULL for contiguous tensors
+ * An output may be its own input (same pointer and strides: in place, the channels from rotary_dim on untouched); else
+ * outputs meet neither inputs nor each other.  B = 0 or N = 0 does nothing.
+ * la_rotary_backward turns the gradients of the outputs into those of the inputs (turned back, by -p f_i, with the
+ * same m); its arguments are those of la_rotary.
+ */
+typedef enum {
+    LA_ROTARY_NONE = 0,    /* f_i = base^(-2 i / rotary_dim) */
+    LA_ROTARY_LINEAR = 1,  /* f_i / factor */
+    LA_ROTARY_BY_TURNS = 2 /* by the turns n_i = original_length f_i / 2 pi of the pair over the original length:
+                              f_i / factor up to low_turns, f_i from high_turns on, blended linearly between */
+} la_rotary_scaling;
+int la_rotary_frequencies(int rotary_dim, double base, int scaling, double factor, double original_length,
+                          double low_turns, double high_turns, unsigned long long *frequencies);
+int la_rotary(const void *Q, const void *K, void *Qr, void *Kr, const unsigned long long *frequencies,
+              const int *positions, long long position_stride, long long first_position, int interleaved,
+              float magnitude, int B, int Hq, int Hk, int N, int D, int rotary_dim, int dtype,
+              const long long *strides, void *stream);
+int la_rotary_backward(const void *dQr, const void *dKr, void *dQ, void *dK, const unsigned long long *frequencies,
+                       const int *positions, long long position_stride, long long first_position, int interleaved,
+                       float magnitude, int B, int Hq, int Hk, int N, int D, int rotary_dim, int dtype,
+                       const long long *strides, void *stream);
+
+/*
+ * Gated linear recurrence over N rows of C channels, each channel by itself:
+ *   h_t = a_t h_{t-1} + b_t x_t,   LA_GATE_LOG: a = e^w, b = 1;   LA_GATE_SIGMOID: a = 1 / (1 + e^-w), b = 1 - a
+ * A gate whose a is 0 in fp32 (w = -inf) cuts: what came before, infinities and NaN included, has no part in what
+ * follows, so packed sequences restart with it; an input whose b is 0 has none either.
+ *   X, W, H   in, in, out: [B,N,C] of `dtype`
+ *   h0        in : float [B,C], the value before the first row, or NULL for 0
+ *   h_last    out: float [B,C], the value after the last row (h0 when N = 0), or NULL
+ *   strides   in : host array, (batch, row) element strides of X, W, H (6 values; the rules of the strided passes), or
+ *             NULL for contiguous tensors
+ * The recurrence is held in fp32 and needs no workspace.
+ */
+typedef enum { LA_GATE_LOG = 0, LA_GATE_SIGMOID = 1 } la_gate;
+int la_gated_scan(const void *X, const void *W, const float *h0, void *H, float *h_last, int B, int N, int C, int gate,
+                  int dtype, const long long *strides, void *stream);
+
+/*
+ * Gradients of sum dH . H + sum dh_last . h_last: with G_t = dH_t + a_{t+1} G_{t+1} (dh_last behind the last row),
+ *   dX_t = b_t G_t,  dW_t = a_t h_{t-1} G_t (log) or a_t b_t (h_{t-1} - x_t) G_t (sigmoid),  dh0 = a_0 G_0
+ *   H         in : la_gated_scan's output (h_{t-1} is taken from it, as rounded to `dtype`)
+ *   dh_last   in : float [B,C] or NULL for 0;  dh0 out: float [B,C] or NULL
+ *   strides   in : (batch, row) of X, W, H, dH, dX, dW (12 values), or NULL
+ */
+int la_gated_scan_backward(const void *X, const void *W, const void *H, const void *dH, const float *h0,
+                           const float *dh_last, void *dX, void *dW, float *dh0, int B, int N, int C, int gate,
+                           int dtype, const long long *strides, void *stream);
+
+/*
+ * One row: state = a state + b x in place, h = state rounded to `dtype`.
+ *   x, w, h   in, in, out: [B,C] of `dtype`;  state in/out: float [B,C], 16-byte aligned
+ *   strides   in : the row strides of x, w, h (3 values), or NULL
+ */
+int la_gated_scan_step(const void *x, const void *w, void *h, float *state, int B, int C, int gate, int dtype,
+                       const long long *strides, void *stream);
 
 /*
  * Synchronises `stream`, then returns and clears the sticky device status recorded in `workspace`
