@@ -255,7 +255,7 @@ size_t la_prompt_workspace_bytes(int T, int nseq, int Hq, int Hkv, int D, int dt
     if (T < 0 || nseq < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || !la::prompt::supported_d(D) ||
         (dtype != LA_F32 && dtype != LA_BF16))
         return 0;
-    return 256;
+    return la::prompt::tc_supported(D, dtype) ? la::prompt::tc_workspace_bytes(T, nseq, Hkv, Hq / Hkv, D) : 256;
 }
 
 int la_prompt(const void *Q, const void *K, const void *V, const int *seq_offsets, void *O, void *S, void *z, void *a,
@@ -326,7 +326,11 @@ int la_prompt(const void *Q, const void *K, const void *V, const int *seq_offset
     A.qh = v[0].st[1], A.qn = v[0].st[2], A.kh = v[1].st[1], A.kn = v[1].st[2];
     A.vh = v[2].st[1], A.vn = v[2].st[2], A.oh = v[3].st[1], A.on = v[3].st[2];
     A.status = (uint32_t *)workspace;
-    return simt(A, dtype, (cudaStream_t)stream) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+    // without rows there is nothing to map for the tensor-core form; the other one leaves the states as they should be
+    const cudaError_t e = tc_supported(D, dtype) && T > 0
+                              ? tensor_cores(A, (unsigned char *)workspace, (cudaStream_t)stream)
+                              : simt(A, dtype, (cudaStream_t)stream);
+    return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 
 }  // extern "C"

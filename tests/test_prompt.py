@@ -146,6 +146,30 @@ def test_prompt_matches_explicit_weights(kind, D, Hq, Hkv, lens):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("ctas", [1, 2, 3, 7, 40])
+@pytest.mark.parametrize("D,Hq,Hkv,resume", [(128, 6, 2, False), (128, 2, 2, True), (64, 4, 1, True), (32, 5, 5, False)])
+def test_slices_of_any_number_of_ctas(monkeypatch, D, Hq, Hkv, resume, ctas):
+    """The tensor-core form's work split: heads that straddle CTAs, CTAs with many heads, CTAs with nothing."""
+    from bwd_la_fwd_gb300 import la
+    monkeypatch.setenv("LA_TC_MAX_CTAS", str(ctas))
+    lens = [300, 0, 1, 900, 128, 256, 77]
+    off = _offsets(lens)
+    q, k, v = _tokens(off[-1], Hq, Hkv, D, "bf16", seed=ctas)
+    state = _state(len(lens), Hkv, D, "bf16")
+    start = R.empty_state(len(lens), Hkv, D)
+    if resume:  # a state that some other tokens left
+        pq, pk, pv = _tokens(50 * len(lens), Hq, Hkv, D, "bf16", seed=99)
+        po = _offsets([50] * len(lens))
+        la.la_prompt(pq, pk, pv, torch.tensor(po, dtype=torch.int32, device="cuda"), state)
+        start = tuple(t.double().cpu() for t in (state.S, state.z, state.a)) + (state.n.cpu().long(),)
+    ws = la.new_prompt_workspace(off[-1], len(lens), Hq, Hkv, D, la.LA_BF16)
+    O = la.la_prompt(q, k, v, torch.tensor(off, dtype=torch.int32, device="cuda"), state, resume=resume, workspace=ws)
+    assert la.la_get_status(ws) == 0
+    ref, tol = R.prompt(q, k, v, off, start, "bf16", True)
+    _check(O, state, ref, tol, off)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind,D,Hq,Hkv", [("bf16", 128, 4, 1), ("bf16", 64, 4, 2), ("bf16", 256, 1, 1), ("f32", 64, 4, 2),
                                            ("f32", 128, 2, 2)])
 def test_prompts_in_parts(kind, D, Hq, Hkv):
