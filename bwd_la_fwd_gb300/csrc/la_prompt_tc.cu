@@ -1,10 +1,11 @@
 // la_prompt_tc.cu -- tcgen05 / TMA form of la_prompt (bf16, D = 32, 64, 128).
 //
 // Per key/value head and chunk of 128 rows, with S, z, a, n those of the rows before the chunk, for each query head:
-//   T = Q K^T,  P = [j <= i](1 + T) in bf16,  O = (Q Sb + P V + a) / (n + q . z + row sums of P)
-// and once per chunk  S += K^T V,  z += K^T 1,  a += V^T 1.  Sb is S rounded to bf16; z goes through the tensor cores
-// as two bf16 parts (16 bits).  S itself lives in fp32 registers of the epilogue: a chunk's K^T V is summed by itself in
-// TMEM and added there, so that a long sequence's sums are rounded to nearest once a chunk.
+//   T = Q K^T,  P = [j <= i](1 + T),  O = (Q Sb + P V + a) / (n + q . z + row sums of P)
+// and once per chunk  S += K^T V,  z += K^T 1,  a += V^T 1.  The tensor cores take S rounded to bf16 (Sb) and P as bf16,
+// in two parts (16 bits) where P's rounding would show beside the output's.  S itself lives in fp32 registers of the
+// epilogue: a chunk's K^T V is summed by itself in TMEM and added there, so that a long sequence's sums are rounded to
+// nearest once a chunk.
 //
 // Work split.  All (sequence, head, chunk) items are laid end to end in that order and cut into G equal slices, one per
 // CTA; the part of a slice in one head is a piece.  A piece that stops short of its head's end is always its CTA's last
@@ -12,9 +13,7 @@
 // into the state each CTA's first piece starts from; prompt_kernel walks.  Only heads that straddle CTAs have their K
 // and V read twice.
 //
-// Bound by HBM: for r query heads to a key/value head a chunk moves (2 r + 2) tiles of 32 KB (D = 128) and costs 3 r + 1
-// products of 128^3, at the measured rates a quarter of the time of its bytes.  Q, K and V come by TMA through rings of
-// tiles that different threads fill, and O leaves by TMA from the tile its Q came in.
+// Bound by HBM: for r query heads to a key/value head a chunk moves (2 r + 2) tiles of 32 KB (D = 128).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <stdlib.h>
@@ -61,51 +60,56 @@ template <int NB> __device__ __forceinline__ int slot_at(int d, int hf, int q) {
 
 __device__ __forceinline__ int chunks_of(int len) { return len > kC ? (len + kC - 1) / kC : 1; }
 
-// The (chunk, query head) units of a slice in order.
+// The (chunk, query head) units of CTA blockIdx.x's slice in order.
 struct Units {
-    const Args *A;
-    int VH, r;
-    long long left;      // items from this one on
-    int seq, vh, c, j;   // j: query head within vh
-    int a, e, nch;       // chunks of the piece, of the head
-    int lo, len;         // the sequence's rows
-    __device__ __forceinline__ void enter() {
-        lo = A->off[seq];
-        len = A->off[seq + 1] - lo;
+    int left;               // items from this one on
+    int seq, vh, c, j;      // j: query head within vh
+    int nch, lo, len;       // the head's chunks, the sequence's rows
+    __device__ __forceinline__ void enter(const TcArgs &P) {
+        lo = P.A.off[seq];
+        len = P.A.off[seq + 1] - lo;
         nch = chunks_of(len);
     }
-    __device__ __forceinline__ void piece() {
-        a = c;
-        e = left < nch - c ? c + (int)left : nch;
-    }
-    __device__ __forceinline__ Units(const TcArgs &P, const Slice &s)
-        : A(&P.A), VH(P.A.Hkv * P.gs), r(P.r), left(s.left), seq(s.seq), vh(s.vh), c(s.c), j(0) {
-        if (left > 0) {
-            enter();
-            piece();
-        }
+    __device__ __forceinline__ explicit Units(const TcArgs &P) {
+        const Slice &s = P.slices[blockIdx.x];
+        left = (int)s.left, seq = s.seq, vh = s.vh, c = s.c, j = 0;
+        nch = lo = len = 0;
+        if (left > 0) enter(P);
     }
     __device__ __forceinline__ bool valid() const { return left > 0; }
-    __device__ __forceinline__ bool last_head() const { return j == r - 1; }
-    __device__ __forceinline__ bool last_chunk() const { return c + 1 == e; }
+    // of the piece in this slice; the head's
+    __device__ __forceinline__ bool last_chunk() const { return left == 1 || c + 1 == nch; }
     __device__ __forceinline__ bool ends_head() const { return c + 1 == nch; }
     __device__ __forceinline__ int live() const { return min(kC, len - c * kC); }
-    // whether the chunk's sums are needed: by the next chunk, or as the head's final state
-    __device__ __forceinline__ bool sums_wanted(int gs) const {
-        return !last_chunk() || (ends_head() && A->S != nullptr && vh % gs == 0);
-    }
-    __device__ __forceinline__ void next() {
+    // whether the CTA writes the head's state behind this chunk
+    __device__ __forceinline__ bool saves(const TcArgs &P) const { return ends_head() && P.A.S && vh % P.gs == 0; }
+    // whether the chunk's sums are needed: by the next chunk, or for the head's state
+    __device__ __forceinline__ bool sums_wanted(const TcArgs &P) const { return !last_chunk() || saves(P); }
+    // the unit after this one, for r query heads of each of VH heads
+    __device__ __forceinline__ void next(const TcArgs &P, int r, int VH) {
         if (++j < r) return;
         j = 0;
         ++c;
-        if (--left == 0 || c < e) return;
+        if (--left == 0 || c < nch) return;
         c = 0;
         if (++vh == VH) {
             vh = 0;
             ++seq;
-            enter();
+            enter(P);
         }
-        piece();
+    }
+    // At the first unit of a piece: the slot that holds what it starts from, null if that is the caller's state (or
+    // nothing); where the head's state is; the rows before the first of this call.
+    template <int NB> __device__ __forceinline__ const float *slot(const TcArgs &P) const {
+        if (c > 0) return P.carry + (long long)blockIdx.x * kSlot<NB>;                       // carried on from others
+        if (P.A.resume && left < nch) return P.sums + (long long)blockIdx.x * kSlot<NB>;     // others carry it on
+        return nullptr;
+    }
+    __device__ __forceinline__ long long state(const TcArgs &P) const { return (long long)seq * P.A.Hkv + vh / P.gs; }
+    template <int NB> __device__ __forceinline__ int rows_before(const TcArgs &P) const {
+        const float *f = slot<NB>(P);
+        if (f) return *(const int *)(f + kSlotS<NB> + 256);
+        return P.A.resume ? P.A.n[state(P)] : 0;
     }
 };
 
@@ -299,37 +303,16 @@ __global__ void __launch_bounds__(kSumThreads, 1) sums_kernel(const __grid_const
 }
 
 // ----------------------------------------------------------------------------------------------------------------
-// Carries.  grid = (float4s of a slot / 256, G): the blocks of the CTA b in which a straddling head begins walk that
-// head's CTAs in order and leave in each later one's carry the sum of all before it.  b's own sums are replaced by what
-// the head starts from (resumed), because the CTA that ends the head writes the state while b may not have read it.
+// Carries.  A chain is the CTAs of one head that straddles CTAs; it begins with the CTA b0 whose last piece is the head's
+// first and open.  Blocks (x, y) walk chains y, y + kChains, ... and leave in each later CTA's carry the sum of all
+// before it, each thread one float4 of the slots.  b0's own sums are replaced by what the head starts from (resumed),
+// because the CTA that ends the head writes the state while b0 may not have read it.
 // ----------------------------------------------------------------------------------------------------------------
-template <int NB> __global__ void __launch_bounds__(256) carry_kernel(const __grid_constant__ TcArgs P) {
+constexpr int kChains = 32;
+
+template <int NB>
+__device__ void walk_chain(const TcArgs &P, const Slice &s, int b0, int x, const int *chain, int length) {
     constexpr int S4 = kSlotS<NB> / 4, N4 = S4 + 64;
-    __shared__ int chain[tc::kMaxCtas + 1];  // the head's CTAs after b0, in order
-    __shared__ int length;
-    griddep_wait();
-    griddep_launch_dependents();
-    const int b0 = blockIdx.y, x = blockIdx.x * 256 + threadIdx.x;
-    const Slice s = P.slices[b0];
-    if (!s.open || s.la != 0) return;  // the same for the whole block
-    if (threadIdx.x < 32) {  // a CTA carries the head on while its last piece is of that head and open
-        int n = 0;
-        bool more = true;
-        for (int b = b0 + 1; b < P.G && more; b += 32) {
-            const int mine = b + threadIdx.x;
-            Slice c = {};
-            if (mine < P.G) c = P.slices[mine];
-            const unsigned any = __ballot_sync(0xffffffffu, c.left > 0);
-            const unsigned on = __ballot_sync(0xffffffffu, c.left > 0 && c.open && c.lseq == s.lseq && c.lvh == s.lvh);
-            const unsigned stop = any & ~on;                       // the first CTA that does not ends the head
-            const unsigned take = stop ? any & (2u * (stop & -stop) - 1u) : any;
-            if (take >> threadIdx.x & 1u) chain[n + __popc(take & ((1u << threadIdx.x) - 1u))] = mine;
-            n += __popc(take);
-            more = !stop;
-        }
-        if (threadIdx.x == 0) length = n;
-    }
-    __syncthreads();
     if (x > N4) return;
     const int D = P.A.D, h = s.lvh / P.gs;
     const long long at = (long long)s.lseq * P.A.Hkv + h;
@@ -371,70 +354,243 @@ template <int NB> __global__ void __launch_bounds__(256) carry_kernel(const __gr
     ((float4 *)first)[x] = start;
 }
 
+template <int NB> __global__ void __launch_bounds__(256) carry_kernel(const __grid_constant__ TcArgs P) {
+    __shared__ int chain[tc::kMaxCtas + 1];  // the head's CTAs after b0, in order
+    __shared__ int begin, length;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int x = blockIdx.x * 256 + threadIdx.x;
+    int skip = blockIdx.y;  // chains that other blocks take before this one's next
+    for (int b0 = 0; b0 < P.G;) {
+        __syncthreads();  // the chain before has been read
+        if (threadIdx.x < 32) {
+            int at = P.G;  // where the chain after `skip` others begins
+            for (int b = b0; b < P.G && at == P.G; b += 32) {
+                const int mine = b + threadIdx.x;
+                bool begins = false;
+                if (mine < P.G) {
+                    const Slice c = P.slices[mine];
+                    begins = c.left > 0 && c.open && c.la == 0;
+                }
+                unsigned on = __ballot_sync(0xffffffffu, begins);
+                for (; skip > 0 && on; --skip) on &= on - 1;
+                if (on) at = b + __ffs(on) - 1;
+            }
+            int n = 0;
+            if (at < P.G) {  // a CTA carries the head on while its last piece is of that head and open
+                const Slice s = P.slices[at];
+                bool more = true;
+                for (int b = at + 1; b < P.G && more; b += 32) {
+                    const int mine = b + threadIdx.x;
+                    Slice c = {};
+                    if (mine < P.G) c = P.slices[mine];
+                    const unsigned any = __ballot_sync(0xffffffffu, c.left > 0);
+                    const unsigned on = __ballot_sync(0xffffffffu, c.left > 0 && c.open && c.lseq == s.lseq && c.lvh == s.lvh);
+                    const unsigned stop = any & ~on;                       // the first CTA that does not ends the head
+                    const unsigned take = stop ? any & (2u * (stop & -stop) - 1u) : any;
+                    if (take >> threadIdx.x & 1u) chain[n + __popc(take & ((1u << threadIdx.x) - 1u))] = mine;
+                    n += __popc(take);
+                    more = !stop;
+                }
+            }
+            if (threadIdx.x == 0) {
+                begin = at;
+                length = n;
+            }
+        }
+        __syncthreads();
+        const int cb = begin;
+        if (cb >= P.G) return;
+        b0 = cb + 1;
+        skip = kChains - 1;
+        walk_chain<NB>(P, P.slices[cb], cb, x, chain, length);
+    }
+}
+
 // ----------------------------------------------------------------------------------------------------------------
-// The walk.  Warp 0 loads K and V, warp 10 loads Q, warp 1 issues MMAs, warps 2-9 (two per TMEM lane quarter, each half
-// of the columns) are the epilogue.  A unit u is one query head of one chunk; three epilogue steps
-//   A(u)  T -> P (TMEM), row sums              B(u)  O -> out              C  (a chunk's last unit)  S, Sb, z, a
-// run as A(u + 1), B(u) [, C]: while A(u + 1) works, the tensor cores form O of u, and while B(u) works, T of u + 2.
-// A does not need the state, so the order holds across chunks and across heads.
-// TMEM columns: T 0, P 128 (even heads) and 320 (odd), O 192, K^T V 320, z and a sums 448, 464, q . z 480, row sums 496.
-// The odd P and K^T V share columns: K^T V is formed behind the last unit's P V and read in C, before the next chunk's
-// A(1).
+// The walk.  A unit u is one query head of one chunk.  Warp 0 loads K and V, warp 2 loads Q, warp 1 issues MMAs; the
+// epilogue is two groups of eight warps (two per TMEM lane quarter, each half of the columns):
+//   A(u)  T -> P (TMEM), row sums        B(u)  O -> out, and after a chunk's last unit  C  S, Sb, z, a
+// A works on u + 1 while B writes u and the tensor cores form Q S of u + 1.  O is staged in the tile its Q came in and
+// leaves by TMA.
+// K and V have one tile each: K is free behind the last T and K^T V (formed while the last A works), V behind the last
+// P V, and each has about a unit's time to be filled again; four Q tiles, because one is held from its load to its O's
+// store, some 2 units and a load's latency.  (With two K, V tiles and three Q tiles every unit waited for its Q.)
+// An MMA of 128 x 128 x 16 reads 8 KB of shared memory, 64 clocks: T, Q S and P V take 1.5 k, the N = 16 products
+// (q . z; K^T 1 and V^T 1 once a chunk) 0.4 k of the 3.4 k clocks that a unit's bytes take (D = 128, r = 4).  CUDA cores
+// did those sums in twice the epilogue's time.
+// Two things cost the epilogue more than its arithmetic: code that does not come round again within a unit (the warps
+// then wait for instructions), hence loops that are not unrolled and one group per step; and spilled registers, which
+// with this much shared memory are L2 accesses, hence 32-bit shared addresses and registers split by role.
+// P's low part: with n rows before the chunk, P's rounding enters a row's O as sqrt(rows / n) of the output's own, so it
+// is kept for a sequence's first kLowChunks chunks, beyond which it adds less than a tenth to the output's rounding.
+// TMEM columns: T 0, P 128, O 192, K^T V 320, z and a sums 448, 464, q . z 480.  P's low parts share the columns of
+// K^T V, which in those chunks is formed behind the last P V, and A waits for C before the next chunk's.
 // ----------------------------------------------------------------------------------------------------------------
-constexpr int kThreads = 352;
-template <int NB> constexpr int kKV = NB == 2 ? 3 : 6;  // K and V tiles, alternating
-template <int NB> constexpr int kQ = NB == 2 ? 3 : 5;   // Q tiles
-template <int NB> constexpr size_t kSmemWalk = (kKV<NB> + kQ<NB> + 1) * (size_t)kTileB<NB> + 2048 + 512 + 512;
-static_assert(kSmemWalk<2> <= 232448, "shared-memory limit");
+
+// Two fp32 operations at a time.
+__device__ __forceinline__ unsigned long long bits2(float2 a) { return *reinterpret_cast<unsigned long long *>(&a); }
+__device__ __forceinline__ float2 pair2(unsigned long long x) { return *reinterpret_cast<float2 *>(&x); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return pair2(r);
+}
+
+// Shared memory by 32-bit address.
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts_f4(uint32_t a, float4 v) {
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts_f(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity), "r"(20000u)  // asleep for up to 20 us a try: the CTA's other warps have work
+                 : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int row, int head) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            dst),
+        "l"(m), "r"(bar), "r"(x), "r"(row), "r"(head)
+        : "memory");
+}
+__device__ __forceinline__ void store_box(const CUtensorMap *m, uint32_t src, int x, int row, int head) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m), "r"(src),
+                 "r"(x), "r"(row), "r"(head)
+                 : "memory");
+}
+// As tc::wait_or_abort: bounded in time, and over early once a role has given up.  `ab`: the CTA's AbortState.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, uint32_t ab, uint32_t *status, uint32_t where) {
+    if (try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        if (try_wait(bar, parity)) return true;
+        uint32_t gone;
+        uint64_t limit;
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(gone) : "r"(ab) : "memory");
+        if (gone) return false;
+        asm volatile("ld.volatile.shared.u64 %0, [%1];" : "=l"(limit) : "r"(ab + 8) : "memory");
+        if (globaltimer_ns() - t0 > limit) {
+            asm volatile("st.volatile.shared.u32 [%0], 1;" ::"r"(ab) : "memory");
+            tc::report(status, kDevTimeout, where);
+            return false;
+        }
+    }
+}
+// A last wait for something that is on its way, in a CTA that gives up.
+__device__ __forceinline__ void wait_briefly(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!try_wait(bar, parity) && globaltimer_ns() - t0 < 50000000ull) {
+    }
+}
+
+constexpr int kThreads = 640;
+// Registers: 640 threads start with 96 each; B, which holds S, takes what the others leave.
+constexpr int kRegsFew = 64, kRegsA = 72, kRegsB = 128;
+static_assert(128 * kRegsFew + 256 * kRegsA + 256 * kRegsB <= 640 * 96, "more registers than the block is launched with");
+constexpr int kLowChunks = 4;
+
+// Shared memory of the walk, from its base.
+template <int NB> struct Walk {
+    static constexpr uint32_t TILE = kTileB<NB>;
+    static constexpr int NQ = NB == 2 ? 4 : 6;      // Q tiles
+    static constexpr uint32_t K = 0, V = TILE, Q = 2 * TILE;
+    static constexpr uint32_t SB = Q + NQ * TILE;   // bf16 S, [d][e]
+    // N = 16 operand, two boxes of 8 rows of 128 bytes: rows z (two bf16 parts) and ones; the products with the other
+    // rows are not used, so rows 3-6 hold a (first box) and the first half's row sums (second box)
+    static constexpr uint32_t ZT = SB + TILE;
+    static constexpr uint32_t A = ZT + 384, R0 = ZT + 1024 + 384;
+    static constexpr uint32_t R1 = ZT + 2048;       // the second half's row sums
+    static constexpr uint32_t BARS = R1 + 512;
+    // barriers, 8 bytes each
+    static constexpr uint32_t KFULL = BARS, KEMPTY = KFULL + 8, VFULL = KEMPTY + 8, VEMPTY = VFULL + 8;
+    static constexpr uint32_t QFULL = VEMPTY + 8, QEMPTY = QFULL + 8 * NQ, T = QEMPTY + 8 * NQ, PREADY = T + 8;
+    static constexpr uint32_t O = PREADY + 8, OFREE = O + 8, S = OFREE + 8, SREADY = S + 8, ADONE = SREADY + 8;
+    static constexpr uint32_t HALF = ADONE + 8, DRAIN = HALF + 16, TSLOT = DRAIN + 8, ABORT = TSLOT + 8;
+    static constexpr size_t BYTES = ABORT + 16;
+    static_assert(BYTES <= 232448, "shared-memory limit");
+};
 
 template <int NB>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ TcArgs P) {
-    constexpr uint32_t TILE = kTileB<NB>;
-    constexpr int NKV = kKV<NB>, NQ = kQ<NB>, CH = 32 * NB;  // CH: columns of O or S that an epilogue thread has
+    using W = Walk<NB>;
+    constexpr uint32_t TILE = W::TILE;
+    constexpr int NQ = W::NQ, CH = 32 * NB;  // CH: columns of O or S that an epilogue thread has
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     bool aligned;
-    unsigned char *kv = tc::smem_base(smem_raw, P.A.status, &aligned);
+    const uint32_t sm = smem_u32(tc::smem_base(smem_raw, P.A.status, &aligned)), ab = sm + W::ABORT;
     if (!aligned) return;
-    unsigned char *qt = kv + NKV * TILE;
-    unsigned char *Sb = qt + NQ * TILE;   // bf16 S, [d][e]
-    unsigned char *zt = Sb + TILE;        // N = 16 operand: rows z (two bf16 parts) and ones
-    float *as = (float *)(zt + 2048);     // a
-    uint64_t *kvfull = (uint64_t *)(as + 128), *kvempty = kvfull + NKV, *qfull = kvempty + NKV, *qempty = qfull + NQ;
-    uint64_t *barT = qempty + NQ, *pready = barT + 1, *barO = pready + 1, *ofree = barO + 1, *barS = ofree + 1;
-    uint64_t *sready = barS + 1, *epi = sready + 1, *half = epi + 1, *drain = half + 2;
-    uint32_t *tslot = (uint32_t *)(drain + 1);
-    AbortState *abst = (AbortState *)(tslot + 2);
-    volatile int *abort_flag = &abst->flag;
-    uint32_t *status = P.A.status;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int k = 0; k < NKV; ++k) {
-            mbar_init(&kvfull[k], 1);
-            mbar_init(&kvempty[k], 1);
-        }
+        auto init = [&](uint32_t at, uint32_t count) { mbar_init((uint64_t *)(smem_raw + at), count); };
+        init(W::KFULL, 1);
+        init(W::KEMPTY, 1);
+        init(W::VFULL, 1);
+        init(W::VEMPTY, 1);
         for (int k = 0; k < NQ; ++k) {
-            mbar_init(&qfull[k], 1);
-            mbar_init(&qempty[k], NB);
+            init(W::QFULL + 8 * k, 1);
+            init(W::QEMPTY + 8 * k, NB);
         }
-        mbar_init(barT, 1);
-        mbar_init(pready, 256);
-        mbar_init(barO, 1);
-        mbar_init(ofree, 256);
-        mbar_init(barS, 1);
-        mbar_init(sready, 256);
-        mbar_init(epi, 256);
-        mbar_init(&half[0], 128);
-        mbar_init(&half[1], 128);
-        mbar_init(drain, 1);
-        *abort_flag = 0;
-        abst->limit_ns = P.wait_ns ? P.wait_ns : tc::kWaitNs;
+        init(W::T, 1);
+        init(W::PREADY, 256);
+        init(W::O, 1);
+        init(W::OFREE, 256);
+        init(W::S, 1);
+        init(W::SREADY, 256);
+        init(W::ADONE, 256);
+        init(W::HALF, 128);
+        init(W::HALF + 8, 128);
+        init(W::DRAIN, 1);
+        AbortState *st = (AbortState *)(smem_raw + W::ABORT);
+        st->flag = 0;
+        st->limit_ns = P.wait_ns ? P.wait_ns : tc::kWaitNs;
         fence_mbar_init();
     }
-    for (int i = threadIdx.x; i < 512; i += blockDim.x)  // row 2 of each box ones, the rest zero
-        ((uint32_t *)zt)[i] = (i % 256) / 32 == 2 ? 0x3F803F80u : 0u;
+    for (int k = threadIdx.x; k < 512; k += kThreads)
+        ((uint32_t *)(smem_raw + W::ZT))[k] = (k % 256) / 32 == 2 ? 0x3F803F80u : 0u;
     fence_proxy_async_smem();
     if (warp == 1) {
-        tmem_alloc(tslot, 512);
+        tmem_alloc((uint32_t *)(smem_raw + W::TSLOT), 512);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -442,377 +598,356 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     tc_fence_after();
     griddep_wait();
     griddep_launch_dependents();
-    const uint32_t tmem = *tslot;
-    const uint32_t tT = tmem, tO = tmem + 192, tS = tmem + 320, tZA = tmem + 448, tQZ = tmem + 480, tR = tmem + 496;
-    const Slice s = P.slices[blockIdx.x];
-
-    if (warp == 0 && lane == 0) {
-        // ---- K and V: tile 2 n is K, 2 n + 1 V of the slice's chunk n
-        prefetch_tmap(&P.tmK);
-        prefetch_tmap(&P.tmV);
-        int t = 0;
-        bool ok = true;
-        Units u(P, s);
-        u.r = 1;
-        for (; u.valid() && ok; u.next()) {
-            const int row = u.lo + u.c * kC, h = u.vh / P.gs;
-            for (int k = 0; k < 2; ++k, ++t) {
-                const int x = t % NKV;
-                if (t >= NKV && !wait_or_abort(&kvempty[x], ((t / NKV) - 1) & 1, abort_flag, status, 0x801)) {
-                    ok = false;
-                    break;
-                }
-                mbar_arrive_expect_tx(&kvfull[x], TILE);
+    const uint32_t tmem = *(const uint32_t *)(smem_raw + W::TSLOT);
+    const uint32_t tT = tmem, tP = tmem + 128, tO = tmem + 192, tS = tmem + 320, tL = tS, tZA = tmem + 448, tQZ = tmem + 480;
+    uint32_t *status = P.A.status;
+    const int VH = P.A.Hkv * P.gs;
+    auto wait1 = [&](uint32_t bar, uint32_t parity, uint32_t where) { return wait_for(sm + bar, parity & 1, ab, status, where); };
+    auto wait = [&](uint32_t bar, uint32_t parity, uint32_t where) {  // a warp gives up together
+        return __all_sync(0xffffffffu, wait_for(sm + bar, parity & 1, ab, status, where)) != 0;
+    };
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+        if (warp == 0 && lane == 0) {
+            // ---- K and V of the slice's chunk n
+            prefetch_tmap(&P.tmK);
+            prefetch_tmap(&P.tmV);
+            int n = 0, kn = 0, vn = 0;  // chunks whose K, V have been asked for
+            for (Units u(P); u.valid(); u.next(P, 1, VH), ++n) {
+                const int row = u.lo + u.c * kC, h = u.vh / P.gs;
+                if (n > 0 && !wait1(W::KEMPTY, n - 1, 0x801)) break;
+                expect_bytes(sm + W::KFULL, TILE);
+                for (int b = 0; b < NB; ++b) load_box(sm + W::K + b * kBox, &P.tmK, sm + W::KFULL, 64 * b, row, h);
+                ++kn;
+                if (n > 0 && !wait1(W::VEMPTY, n - 1, 0x802)) break;
+                expect_bytes(sm + W::VFULL, TILE);
+                for (int b = 0; b < NB; ++b) load_box(sm + W::V + b * kBox, &P.tmV, sm + W::VFULL, 64 * b, row, h);
+                ++vn;
+            }
+            // copies already issued land before the CTA exits
+            if (kn > 0) wait_briefly(sm + W::KFULL, (kn - 1) & 1);
+            if (vn > 0) wait_briefly(sm + W::VFULL, (vn - 1) & 1);
+        } else if (warp == 2 && lane == 0) {
+            // ---- Q: one tile a unit
+            prefetch_tmap(&P.tmQ);
+            int t = 0;
+            for (Units u(P); u.valid(); u.next(P, P.r, VH), ++t) {
+                const uint32_t x = t % NQ;
+                if (t >= NQ && !wait1(W::QEMPTY + 8 * x, t / NQ - 1, 0x803)) break;
+                expect_bytes(sm + W::QFULL + 8 * x, TILE);
                 for (int b = 0; b < NB; ++b)
-                    tma_load_3d(kv + x * TILE + b * kBox, k ? &P.tmV : &P.tmK, &kvfull[x], 64 * b, row, h);
+                    load_box(sm + W::Q + x * TILE + b * kBox, &P.tmQ, sm + W::QFULL + 8 * x, 64 * b, u.lo + u.c * kC,
+                             u.vh * P.r + u.j);
             }
-        }
-        if (!ok)  // let the copies already issued land before the CTA exits
-            for (int k = t > NKV ? t - NKV : 0; k < t; ++k) mbar_wait(&kvfull[k % NKV], (k / NKV) & 1, 50000000ull);
-    } else if (warp == 10 && lane == 0) {
-        // ---- Q: one tile a unit
-        prefetch_tmap(&P.tmQ);
-        int t = 0;
-        bool ok = true;
-        for (Units u(P, s); u.valid(); u.next(), ++t) {
-            const int x = t % NQ;
-            if (t >= NQ && !wait_or_abort(&qempty[x], ((t / NQ) - 1) & 1, abort_flag, status, 0x802)) {
-                ok = false;
-                break;
-            }
-            mbar_arrive_expect_tx(&qfull[x], TILE);
-            for (int b = 0; b < NB; ++b)
-                tma_load_3d(qt + x * TILE + b * kBox, &P.tmQ, &qfull[x], 64 * b, u.lo + u.c * kC, u.vh * P.r + u.j);
-        }
-        if (!ok)
-            for (int k = t > NQ ? t - NQ : 0; k < t; ++k) mbar_wait(&qfull[k % NQ], (k / NQ) & 1, 50000000ull);
-    } else if (warp == 1 && lane == 0) {
-        // ---- MMA
-        const uint32_t idT = idesc_bf16(128, 128, false, false), idO = idesc_bf16(128, 64 * NB, false, true);
-        const uint32_t idS = idesc_bf16(128, 64 * NB, true, true), idZ = idesc_bf16(128, 16, true, false);
-        const uint32_t idQZ = idesc_bf16(128, 16, false, false);
-        const uint32_t lbo = NB == 2 ? kBox : 0;
-        const uint32_t zb = smem_u32(zt), sb = smem_u32(Sb), kv0 = smem_u32(kv), q0 = smem_u32(qt);
-        int n = 0;  // chunk of unit u
-        int un = 0;
-        // T of unit x (its number) in chunk m
-        auto issue_t = [&](const Units &w, int x, int m) {
-            if (w.j == 0 && !wait_or_abort(&kvfull[(2 * m) % NKV], ((2 * m) / NKV) & 1, abort_flag, status, 0x803)) return false;
-            if (!wait_or_abort(&qfull[x % NQ], (x / NQ) & 1, abort_flag, status, 0x804)) return false;
-            tc_fence_after();
-            const uint32_t qb = q0 + (x % NQ) * TILE, kb = kv0 + ((2 * m) % NKV) * TILE;
+            for (int k = t > NQ ? t - NQ : 0; k < t; ++k) wait_briefly(sm + W::QFULL + 8 * (k % NQ), (k / NQ) & 1);
+        } else if (warp == 1 && lane == 0) {
+            // ---- MMA
+            constexpr uint32_t idT = idesc_bf16(128, 128, false, false), idO = idesc_bf16(128, 64 * NB, false, true);
+            constexpr uint32_t idS = idesc_bf16(128, 64 * NB, true, true), idZ = idesc_bf16(128, 16, true, false);
+            constexpr uint32_t idQZ = idesc_bf16(128, 16, false, false);
+            constexpr uint32_t lbo = NB == 2 ? kBox : 0;  // D <= 64: rows 64-127 of S repeat rows 0-63 and are not read
+            int n = 0, un = 0;                            // chunk and number of unit u
+            uint32_t sx = sm;
+            // T of unit x in chunk m
+            auto issue_t = [&](bool fresh, int x, int m) {
+                if (fresh && !wait1(W::KFULL, m, 0x804)) return false;
+                if (!wait1(W::QFULL + 8 * (x % NQ), x / NQ, 0x805)) return false;
+                tc_fence_after();
+                const uint32_t qb = sx + W::Q + (x % NQ) * TILE;
 #pragma unroll
-            for (int k = 0; k < 4 * NB; ++k)
-                mma_ss(tT, sdesc_sw128(qb + (k >> 2) * kBox + 32 * (k & 3), 16, 1024),
-                       sdesc_sw128(kb + (k >> 2) * kBox + 32 * (k & 3), 16, 1024), idT, k > 0);
-            mma_commit(barT);
-            return true;
-        };
-        Units u(P, s);
-        bool ok = u.valid() && issue_t(u, 0, 0);
-        while (ok) {
-            Units w = u;
-            w.next();
-            if (!wait_or_abort(pready, un & 1, abort_flag, status, 0x805)) break;  // P(u) is there, T may be overwritten
-            tc_fence_after();
-            if (w.valid() && !issue_t(w, un + 1, u.last_head() ? n + 1 : n)) break;
-            if (un > 0 && !wait_or_abort(ofree, (un - 1) & 1, abort_flag, status, 0x806)) break;
-            const int kx = (2 * n) % NKV, vx = (2 * n + 1) % NKV;
-            if (u.j == 0) {
-                if (!wait_or_abort(&kvfull[vx], ((2 * n + 1) / NKV) & 1, abort_flag, status, 0x807)) break;
-                if (!wait_or_abort(sready, n & 1, abort_flag, status, 0x808)) break;
-            }
-            tc_fence_after();
-            const uint32_t qb = q0 + (un % NQ) * TILE, kb = kv0 + kx * TILE, vb = kv0 + vx * TILE;
-            const uint32_t tP = tmem + (u.j & 1 ? 320 : 128);
-#pragma unroll
-            for (int k = 0; k < 4 * NB; ++k) {
-                const uint64_t qd = sdesc_sw128(qb + (k >> 2) * kBox + 32 * (k & 3), 16, 1024);
-                mma_ss(tO, qd, sdesc_sw128(sb + 2048 * k, lbo, 1024), idO, k > 0);
-                mma_ss(tQZ, qd, sdesc_sw128(zb + (k >> 2) * 1024 + 32 * (k & 3), 16, 0), idQZ, k > 0);
-            }
-#pragma unroll
-            for (int k = 0; k < kC / 16; ++k) mma_ts(tO, tP + 8 * k, sdesc_sw128(vb + 2048 * k, lbo, 1024), idO, 1u);
-            mma_commit(barO);
-            if (u.last_head()) {
-                if (u.sums_wanted(P.gs)) {
+                for (int k = 0; k < 4 * NB; ++k)
+                    mma_ss(tT, sdesc_sw128(qb + (k >> 2) * kBox + 32 * (k & 3), 16, 1024),
+                           sdesc_sw128(sx + W::K + (k >> 2) * kBox + 32 * (k & 3), 16, 1024), idT, k > 0);
+                commit(sm + W::T);
+                return true;
+            };
+            // the chunk's K^T V; K is then done with
+            auto issue_s = [&](bool wanted) {
+                if (wanted) {
 #pragma unroll
                     for (int k = 0; k < kC / 16; ++k) {
-                        const uint64_t kt = sdesc_sw128(kb + 2048 * k, lbo, 1024), vt = sdesc_sw128(vb + 2048 * k, lbo, 1024);
-                        const uint64_t on = sdesc_sw128(zb + (k >> 2) * 1024 + 32 * (k & 3), 16, 0);
-                        mma_ss(tS, kt, vt, idS, k > 0);
-                        mma_ss(tZA, kt, on, idZ, k > 0);
-                        mma_ss(tZA + 16, vt, on, idZ, k > 0);
+                        const uint64_t kd = sdesc_sw128(sx + W::K + 2048 * k, lbo, 1024);
+                        const uint64_t vd = sdesc_sw128(sx + W::V + 2048 * k, lbo, 1024);
+                        const uint64_t on = sdesc_sw128(sx + W::ZT + (k >> 2) * 1024 + 32 * (k & 3), 16, 0);
+                        mma_ss(tS, kd, vd, idS, k > 0);
+                        mma_ss(tZA, kd, on, idZ, k > 0);
+                        mma_ss(tZA + 16, vd, on, idZ, k > 0);
                     }
-                    mma_commit(barS);
+                    commit(sm + W::S);
                 }
-                mma_commit(&kvempty[kx]);
-                mma_commit(&kvempty[vx]);
-                ++n;
+                commit(sm + W::KEMPTY);
+            };
+            Units u(P);
+            bool ok = u.valid() && issue_t(true, 0, 0);
+            while (ok) {
+                asm volatile("" : "+r"(sx));  // descriptors are formed where they are used, not kept in registers
+                const bool last = u.j == P.r - 1, first = u.j == 0, wanted = u.sums_wanted(P), parts = u.c < kLowChunks;
+                u.next(P, P.r, VH);
+                if (first) {
+                    if (!wait1(W::VFULL, n, 0x806)) break;
+                    if (!wait1(W::SREADY, n, 0x807)) break;  // Sb is there, K^T V has been read
+                    tc_fence_after();
+                }
+                if (last && !first && !parts) issue_s(wanted);
+                if (un > 0 && !wait1(W::OFREE, un - 1, 0x809)) break;
+                tc_fence_after();
+                const uint32_t qb = sx + W::Q + (un % NQ) * TILE;
+#pragma unroll
+                for (int k = 0; k < 4 * NB; ++k) {
+                    const uint64_t qd = sdesc_sw128(qb + (k >> 2) * kBox + 32 * (k & 3), 16, 1024);
+                    mma_ss(tO, qd, sdesc_sw128(sx + W::SB + 2048 * k, lbo, 1024), idO, k > 0);
+                    mma_ss(tQZ, qd, sdesc_sw128(sx + W::ZT + (k >> 2) * 1024 + 32 * (k & 3), 16, 0), idQZ, k > 0);
+                }
+                if (!wait1(W::PREADY, un, 0x808)) break;  // P is there, T may be overwritten
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < kC / 16; ++k)
+                    mma_ts(tO, tP + 8 * k, sdesc_sw128(sx + W::V + 2048 * k, lbo, 1024), idO, 1u);
+                if (parts) {
+#pragma unroll
+                    for (int k = 0; k < kC / 16; ++k)
+                        mma_ts(tO, tL + 8 * k, sdesc_sw128(sx + W::V + 2048 * k, lbo, 1024), idO, 1u);
+                }
+                commit(sm + W::O);
+                // behind A, which clears rows that are not the sequence's, and behind the low parts
+                if (last && (first || parts)) issue_s(wanted);
+                if (!last && !issue_t(false, un + 1, n)) break;
+                if (last) {
+                    commit(sm + W::VEMPTY);
+                    ++n;
+                    if (u.valid() && !issue_t(true, un + 1, n)) break;
+                }
+                if (!u.valid()) break;
+                ++un;
             }
-            if (!w.valid()) break;
-            u = w;
-            ++un;
+            commit(sm + W::DRAIN);
+            wait_briefly(sm + W::DRAIN, 0);
         }
-        mma_commit(drain);
-        mbar_wait(drain, 0, 50000000ull);
-    } else if (warp >= 2 && warp < 10) {
-        // ---- epilogue: thread <-> row i of a chunk (of S: row d = i) and half hf of the columns
-        const int q4 = warp & 3, hf = (warp - 2) >> 2, i = 32 * q4 + lane;
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsA));
+        // ---- A: P and row sums.  Thread <-> row i of a chunk and half hf of the columns.
+        const int q4 = warp & 3, hf = (warp - 4) >> 2, i = 32 * q4 + lane;
+        const uint32_t lo = (uint32_t)(32 * q4) << 16;
+        int m = 0, x = 0;  // chunk, unit
+        for (Units u(P); u.valid(); ++x) {
+            const bool parts = u.c < kLowChunks;
+            if (!wait(W::T, x, 0x811)) break;
+            if (u.j == 0) {  // (behind T, which was formed behind the chunk before: no phase is missed)
+                if (parts && !wait(W::SREADY, m, 0x810)) break;  // K^T V of the chunk before has been read
+                ++m;
+            }
+            tc_fence_after();
+            if (x > 0) {  // P V of the unit before has read its P
+                if (!wait(W::O, x - 1, 0x812)) break;
+                tc_fence_after();
+            }
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                const int blk = 2 * hf + b;
+                uint32_t hi[16];
+                if (blk > q4) {  // above the diagonal
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) hi[k] = 0u;
+                    tmem_st16(tP + lo + 16 * blk, hi);
+                    if (parts) tmem_st16(tL + lo + 16 * blk, hi);
+                    continue;
+                }
+                uint32_t v[32];
+                tmem_ld32(tT + lo + 32 * blk, v);
+                tmem_wait_ld(v);
+                if (blk == q4) {  // -1 where P is to be 0
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = k <= lane ? v[k] : 0xbf800000u;
+                }
+                float2 p[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    p[k] = add2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), make_float2(1.f, 1.f));
+                    hi[k] = pack_bf16(p[k].x, p[k].y);
+                    sum = add2(sum, p[k]);
+                }
+                tmem_st16(tP + lo + 16 * blk, hi);
+                if (parts) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) hi[k] = pack_bf16(p[k].x - tc::bf16lo(hi[k]), p[k].y - tc::bf16hi(hi[k]));
+                    tmem_st16(tL + lo + 16 * blk, hi);
+                }
+            }
+            if (u.j == 0 && u.live() < kC) {
+                // the chunk reaches past its sequence: rows that are not its own must not enter P V and K^T V, where
+                // a zero weight would not keep an infinity out
+                if (!wait(W::VFULL, m - 1, 0x815)) break;
+                if (!wait(W::KFULL, m - 1, 0x816)) break;
+                const int none = u.live() > 0 ? u.live() : 0;
+                for (int y = threadIdx.x - 128; y < (kC - none) * 8 * NB; y += 256) {
+                    const int row = none + y / (8 * NB), g = y % (8 * NB);
+                    const uint32_t at = sm + (g >> 3) * kBox + row * 128 + (g & 7) * 16;
+                    sts128(at + W::K, make_uint4(0u, 0u, 0u, 0u));
+                    sts128(at + W::V, make_uint4(0u, 0u, 0u, 0u));
+                }
+                fence_proxy_async_smem();
+            }
+            if (x > 0 && !wait(W::OFREE, x - 1, 0x817)) break;  // B has read the row sums of the unit before
+            sts_f(sm + (hf ? W::R1 : W::R0) + 4 * i, sum.x + sum.y);
+            tmem_st_wait();
+            tc_fence_before();
+            arrive(sm + W::PREADY);
+            u.next(P, P.r, VH);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsB));
+        // ---- B: O -> out, and C: the state.  Thread <-> row i of a chunk (of S: row d = i) and half hf of the columns.
+        const int q4 = warp & 3, hf = (warp - 12) >> 2, i = 32 * q4 + lane;
         const uint32_t lo = (uint32_t)(32 * q4) << 16;
         const int D = P.A.D, col0 = CH * hf;
         const bool has_row = NB == 2 || q4 < 2;          // rows of S there are
         const bool storer = lane == 0 && q4 == 0 && (NB == 2 || hf == 0);
-        float S[CH], za = 0.f;                           // S[i][col0 ...]; z[i] (half 0), a[i] (half 1)
-        int n0 = 0;                                      // n before the head's first row
+        float2 S[CH / 2];                                // S[i][col0 ...]
+        float za = 0.f;                                  // z[i] (first half) or a[i] (second half)
+        int n0 = 0;                                      // rows of the sequence before the first of this call
         int pending = -1;                                // Q tile whose O is on its way out (storer)
-        int epis = 0, halves = 0, ks = 0;
-        // A warp gives up together: its TMEM accesses are the whole warp's.
-        auto wait = [&](uint64_t *bar, uint32_t parity, uint32_t where) {
-            return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, status, where)) != 0;
-        };
-
-        // The state a piece starts from, into registers, Sb, z and a (shared).
-        auto put_state = [&]() {
-            if (has_row) {
-                unsigned char *tile = Sb + (NB == 2 ? hf * kBox : 0);
+        int halves = 0, ks = 0, m = 0, x = 0;
+        for (Units u(P); u.valid(); ++x) {
+            if (u.j == 0 && (x == 0 || u.c == 0)) {  // the state a piece starts from
 #pragma unroll
-                for (int g = 0; g < CH / 8; ++g) {
-                    uint4 w;
-                    w.x = pack_bf16(S[8 * g], S[8 * g + 1]);
-                    w.y = pack_bf16(S[8 * g + 2], S[8 * g + 3]);
-                    w.z = pack_bf16(S[8 * g + 4], S[8 * g + 5]);
-                    w.w = pack_bf16(S[8 * g + 6], S[8 * g + 7]);
-                    *(uint4 *)(tile + tc::sw128_off(i, (NB == 2 ? 0 : 4 * hf) + g)) = w;
-                }
-                if (hf == 0) tc::split_tile_put(zt, i, za);
-                else as[i] = za;
-            }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            mbar_arrive(sready);
-        };
-        auto load_state = [&](const Units &u) {
-            const long long at = (long long)u.seq * P.A.Hkv + u.vh / P.gs;
-            const bool carried = u.a > 0, open = u.e < u.nch;
-            const bool slot = carried || (open && P.A.resume);
-            n0 = 0;
-            za = 0.f;
-#pragma unroll
-            for (int m = 0; m < CH; ++m) S[m] = 0.f;
-            if (slot) {
-                const float *f = (carried ? P.carry : P.sums) + (long long)blockIdx.x * kSlot<NB>;
-                if (has_row) {
+                for (int k = 0; k < CH / 2; ++k) S[k] = make_float2(0.f, 0.f);
+                const float *f = u.slot<NB>(P);
+                n0 = u.rows_before<NB>(P);
+                za = 0.f;
+                if (f) za = f[kSlotS<NB> + 128 * hf + i];
+                else if (P.A.resume && i < D) za = (hf ? (const float *)P.A.a : (const float *)P.A.z)[u.state(P) * D + i];
+                if (f && has_row) {
 #pragma unroll
                     for (int q = 0; q < 8 * NB; ++q) {
                         const float4 v = ((const float4 *)f)[slot_at<NB>(i, hf, q)];
-                        S[4 * q] = v.x, S[4 * q + 1] = v.y, S[4 * q + 2] = v.z, S[4 * q + 3] = v.w;
+                        S[2 * q] = make_float2(v.x, v.y), S[2 * q + 1] = make_float2(v.z, v.w);
                     }
-                    za = f[kSlotS<NB> + 128 * hf + i];
-                }
-                n0 = *(const int *)(f + kSlotS<NB> + 256);
-            } else if (P.A.resume) {
-                if (i < D && col0 < D) {
-                    const float4 *src = (const float4 *)((const float *)P.A.S + (at * D + i) * D + col0);
+                } else if (!f && P.A.resume && i < D && col0 < D) {
+                    const float4 *src = (const float4 *)((const float *)P.A.S + (u.state(P) * D + i) * D + col0);
 #pragma unroll
                     for (int q = 0; q < CH / 4; ++q) {
                         const float4 v = src[q];
-                        S[4 * q] = v.x, S[4 * q + 1] = v.y, S[4 * q + 2] = v.z, S[4 * q + 3] = v.w;
-                    }
-                }
-                if (i < D) za = (hf == 0 ? (const float *)P.A.z : (const float *)P.A.a)[at * D + i];
-                n0 = P.A.n[at];
-            }
-        };
-        auto save_state = [&](const Units &u) {
-            const long long at = (long long)u.seq * P.A.Hkv + u.vh / P.gs;
-            if (i < D && col0 < D) {
-                float4 *dst = (float4 *)((float *)P.A.S + (at * D + i) * D + col0);
-#pragma unroll
-                for (int q = 0; q < CH / 4; ++q) dst[q] = make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
-            }
-            if (i < D) (hf == 0 ? (float *)P.A.z : (float *)P.A.a)[at * D + i] = za;
-            if (hf == 0 && i == 0) P.A.n[at] = n0 + u.len;
-        };
-        // A: P and row sums of unit x in chunk m
-        auto step_a = [&](const Units &u, int x, int m) {
-            if (!wait(barT, x & 1, 0x810)) return false;
-            tc_fence_after();
-            uint32_t pk[2][16];
-            float sum = 0.f;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int j0 = 64 * hf + 32 * b, blk = 2 * hf + b;
-                if (blk > q4) {  // above the diagonal
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) pk[b][k] = 0u;
-                } else {
-                    uint32_t v[32];
-                    tmem_ld32(tT + lo + j0, v);
-                    tmem_wait_ld(v);
-                    if (blk < q4) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float p0 = 1.f + __uint_as_float(v[2 * k]), p1 = 1.f + __uint_as_float(v[2 * k + 1]);
-                            pk[b][k] = pack_bf16(p0, p1);
-                            sum += p0 + p1;
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float p0 = 2 * k <= lane ? 1.f + __uint_as_float(v[2 * k]) : 0.f;
-                            const float p1 = 2 * k + 1 <= lane ? 1.f + __uint_as_float(v[2 * k + 1]) : 0.f;
-                            pk[b][k] = pack_bf16(p0, p1);
-                            sum += p0 + p1;
-                        }
+                        S[2 * q] = make_float2(v.x, v.y), S[2 * q + 1] = make_float2(v.z, v.w);
                     }
                 }
             }
-            if (u.j == 0 && x > 0 && (u.r & 1)) {  // the unit before has its P in the same columns
-                if (!wait(barO, (x - 1) & 1, 0x811)) return false;
-                tc_fence_after();
-            }
-            if (u.j == 1 && !wait(sready, m & 1, 0x818)) return false;  // all have read K^T V
-            const uint32_t tP = tmem + (u.j & 1 ? 320 : 128) + lo + 32 * hf;
-            tmem_st16(tP, pk[0]);
-            tmem_st16(tP + 16, pk[1]);
-            tmem_st1(tR + lo + 2 * (x & 1) + hf, __float_as_uint(sum));
-            tmem_st_wait();
-            if (u.j == 0 && u.live() < kC) {
-                // the chunk reaches past its sequence: rows that are not its own must not enter P V and K^T V, where
-                // a zero weight would not keep an infinity out
-                for (int k = 0; k < 2; ++k) {
-                    const int t = 2 * m + k;
-                    if (!wait(&kvfull[t % NKV], (t / NKV) & 1, 0x812)) return false;
-                    unsigned char *tile = kv + (t % NKV) * TILE;
-                    const int first = u.live() > 0 ? u.live() : 0, e = threadIdx.x - 64;
-                    for (int y = e; y < (kC - first) * 8 * NB; y += 256) {
-                        const int row = first + y / (8 * NB), g = y % (8 * NB);
-                        *(uint4 *)(tile + (g >> 3) * kBox + row * 128 + (g & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
+            if (u.j == 0) {
+                if (has_row) {
+                    const uint32_t tile = sm + W::SB + (NB == 2 ? hf * kBox : 0);
+#pragma unroll
+                    for (int g = 0; g < CH / 8; ++g)
+                        sts128(tile + tc::sw128_off(i, (NB == 2 ? 0 : 4 * hf) + g),
+                               make_uint4(pack_bf16(S[4 * g].x, S[4 * g].y), pack_bf16(S[4 * g + 1].x, S[4 * g + 1].y),
+                                          pack_bf16(S[4 * g + 2].x, S[4 * g + 2].y), pack_bf16(S[4 * g + 3].x, S[4 * g + 3].y)));
+                }
+                if (has_row) {
+                    if (hf == 0) tc::split_tile_put(smem_raw + W::ZT, i, za);
+                    else sts_f(sm + W::A + 4 * i, za);
                 }
                 fence_proxy_async_smem();
+                tc_fence_before();
+                arrive(sm + W::SREADY);
+                ++m;
             }
-            tc_fence_before();
-            mbar_arrive(pready);
-            return true;
-        };
-        auto release = [&]() {
-            if (pending >= 0) {
+            if (pending >= 0) {  // the last unit's O has been read out of its Q tile, which may be filled again
                 bulk_wait_read0();
-                mbar_arrive(&qempty[pending]);
+                arrive(sm + W::QEMPTY + 8 * pending);
                 pending = -1;
             }
-        };
-        // B: output of unit x
-        auto step_b = [&](const Units &u, int x) {
-            if (!wait(barO, x & 1, 0x813)) return false;
+            __syncwarp();
+            if (!wait(W::O, x, 0x821)) break;
             tc_fence_after();
-            uint32_t z0, z1, r0, r1;
-            tmem_ld2(tQZ + lo, z0, z1);
-            tmem_ld2(tR + lo + 2 * (x & 1), r0, r1);
-            tmem_wait_ld(z0, z1);
-            tmem_wait_ld(r0, r1);
-            const float g = (float)(n0 + u.c * kC) + (__uint_as_float(z0) + __uint_as_float(z1)) +
-                            (__uint_as_float(r0) + __uint_as_float(r1));
-            const float inv = 1.f / g;
-            const int live = u.live(), hq = u.vh * P.r + u.j;
-            unsigned char *tile = qt + (x % NQ) * TILE + (NB == 2 ? hf * kBox : 0);
-            __nv_bfloat16 *out = (__nv_bfloat16 *)P.A.o + hq * P.A.oh + (long long)(u.lo + u.c * kC + i) * P.A.on + col0;
-#pragma unroll
+            uint32_t qz0, qz1;
+            tmem_ld2(tQZ + lo, qz0, qz1);
+            tmem_wait_ld(qz0, qz1);
+            const float sc = 1.f / ((float)(n0 + u.c * kC) + (__uint_as_float(qz0) + __uint_as_float(qz1)) +
+                                    (lds_f(sm + W::R0 + 4 * i) + lds_f(sm + W::R1 + 4 * i)));
+            const int live = u.live();
+            const uint32_t tile = sm + W::Q + (x % NQ) * TILE + (NB == 2 ? hf * kBox : 0);
+#pragma unroll 1
             for (int b = 0; b < NB; ++b) {
                 uint32_t v[32];
                 tmem_ld32(tO + lo + col0 + 32 * b, v);
                 tmem_wait_ld(v);
-                const float4 *a4 = (const float4 *)(as + col0 + 32 * b);
+                if (b == NB - 1) {  // O, q . z and the row sums have been read
+                    tc_fence_before();
+                    arrive(sm + W::OFREE);
+                }
+                const uint32_t acol = sm + W::A + 4 * (col0 + 32 * b);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const float4 c0 = a4[2 * y], c1 = a4[2 * y + 1];
-                    uint4 w;
-                    w.x = pack_bf16((__uint_as_float(v[8 * y]) + c0.x) * inv, (__uint_as_float(v[8 * y + 1]) + c0.y) * inv);
-                    w.y = pack_bf16((__uint_as_float(v[8 * y + 2]) + c0.z) * inv, (__uint_as_float(v[8 * y + 3]) + c0.w) * inv);
-                    w.z = pack_bf16((__uint_as_float(v[8 * y + 4]) + c1.x) * inv, (__uint_as_float(v[8 * y + 5]) + c1.y) * inv);
-                    w.w = pack_bf16((__uint_as_float(v[8 * y + 6]) + c1.z) * inv, (__uint_as_float(v[8 * y + 7]) + c1.w) * inv);
+                    uint32_t w[4];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float4 a = lds_f4(acol + 32 * y + 16 * c);
+                        const uint32_t *o = v + 8 * y + 4 * c;
+                        const float2 s0 = mul2(add2(make_float2(__uint_as_float(o[0]), __uint_as_float(o[1])), make_float2(a.x, a.y)),
+                                               make_float2(sc, sc));
+                        const float2 s1 = mul2(add2(make_float2(__uint_as_float(o[2]), __uint_as_float(o[3])), make_float2(a.z, a.w)),
+                                               make_float2(sc, sc));
+                        w[2 * c] = pack_bf16(s0.x, s0.y);
+                        w[2 * c + 1] = pack_bf16(s1.x, s1.y);
+                    }
+                    const uint4 w4 = make_uint4(w[0], w[1], w[2], w[3]);
                     const int e = 32 * b + 8 * y;  // column within the thread's
-                    if (live == kC) *(uint4 *)(tile + tc::sw128_off(i, (NB == 2 ? 0 : 4 * hf) + (e >> 3))) = w;
-                    else if (i < live && col0 + e < D) *(uint4 *)(out + e) = w;  // rows of others stay as they are
+                    if (live == kC) sts128(tile + tc::sw128_off(i, (NB == 2 ? 0 : 4 * hf) + (e >> 3)), w4);
+                    else if (i < live && col0 + e < D)  // rows of others stay as they are
+                        *(uint4 *)((__nv_bfloat16 *)P.A.o + (u.vh * P.r + u.j) * P.A.oh +
+                                   (long long)(u.lo + u.c * kC + i) * P.A.on + col0 + e) = w4;
                 }
             }
-            tc_fence_before();
-            mbar_arrive(ofree);
+            const bool last = u.j == P.r - 1;
+            if (last) arrive(sm + W::ADONE);  // a of this chunk has been read
             if (live == kC) {
                 fence_proxy_async_smem();
-                uint64_t *bar = NB == 2 ? &half[hf] : &half[0];
-                if (NB == 2 || hf == 0) mbar_arrive(bar);
-                else mbar_arrive(&half[1]);
-                if (storer && wait_or_abort(bar, halves & 1, abort_flag, status, 0x814) &&
-                    (NB == 2 || wait_or_abort(&half[1], halves & 1, abort_flag, status, 0x815))) {
-                    tma_store_3d(&P.tmO, tile, NB == 2 ? col0 : 0, u.lo + u.c * kC, hq);
+                arrive(sm + W::HALF + 8 * hf);
+                if (storer && wait1(W::HALF + 8 * hf, halves, 0x822) && (NB == 2 || wait1(W::HALF + 8, halves, 0x823))) {
+                    store_box(&P.tmO, tile, NB == 2 ? col0 : 0, u.lo + u.c * kC, u.vh * P.r + u.j);
                     bulk_commit();
                     pending = x % NQ;
                 }
                 __syncwarp();
                 ++halves;
             } else if (storer) {
-                mbar_arrive(&qempty[x % NQ]);
+                arrive(sm + W::QEMPTY + 8 * (x % NQ));
             }
-            return true;
-        };
-        // C: the state after unit x's chunk; then what the next chunk (w) starts from
-        auto step_c = [&](const Units &u, const Units &w) {
-            // everyone has read a
-            mbar_arrive(epi);
-            if (!wait(epi, epis & 1, 0x816)) return false;
-            ++epis;
-            if (u.sums_wanted(P.gs)) {
-                if (!wait(barS, ks & 1, 0x817)) return false;
-                ++ks;
-                tc_fence_after();
-                if (has_row) {
-                    uint32_t z0, z1;
-                    tmem_ld2(tZA + lo + 16 * hf + 2, z0, z1);  // column 2: the ones
+            if (last) {
+                // C: the state after the chunk
+                if (!wait(W::ADONE, m - 1, 0x825)) break;
+                if (u.sums_wanted(P)) {
+                    if (!wait(W::S, ks, 0x824)) break;
+                    ++ks;
+                    tc_fence_after();
+                    if (has_row) {
+                        uint32_t s0, s1;
+                        tmem_ld2(tZA + lo + 16 * hf + 2, s0, s1);  // column 2: the ones
+                        tmem_wait_ld(s0, s1);
+                        za += __uint_as_float(s0);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        uint32_t v[32];
-                        tmem_ld32(tS + lo + col0 + 32 * b, v);
-                        tmem_wait_ld(v);
+                        for (int b = 0; b < NB; ++b) {
+                            uint32_t v[32];
+                            tmem_ld32(tS + lo + col0 + 32 * b, v);
+                            tmem_wait_ld(v);
 #pragma unroll
-                        for (int m = 0; m < 32; ++m) S[32 * b + m] += __uint_as_float(v[m]);
+                            for (int k = 0; k < 16; ++k)
+                                S[16 * b + k] = add2(S[16 * b + k], make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])));
+                        }
                     }
-                    tmem_wait_ld(z0, z1);
-                    za += __uint_as_float(z0);
+                    tc_fence_before();
                 }
-                tc_fence_before();
+                if (u.saves(P) && i < D) {
+                    (hf ? (float *)P.A.a : (float *)P.A.z)[u.state(P) * D + i] = za;
+                    if (hf == 0 && i == 0) P.A.n[u.state(P)] = n0 + u.len;
+                }
+                if (u.saves(P) && i < D && col0 < D) {
+                    float4 *dst = (float4 *)((float *)P.A.S + (u.state(P) * D + i) * D + col0);
+#pragma unroll
+                    for (int q = 0; q < CH / 4; ++q)
+                        dst[q] = make_float4(S[2 * q].x, S[2 * q].y, S[2 * q + 1].x, S[2 * q + 1].y);
+                }
             }
-            if (u.last_chunk()) {
-                if (u.ends_head() && P.A.S && u.vh % P.gs == 0) save_state(u);
-                if (w.valid()) load_state(w);
-            }
-            if (w.valid()) put_state();
-            return true;
-        };
-
-        Units u(P, s);
-        int x = 0, m = 0;
-        bool ok = u.valid();
-        if (ok) {
-            load_state(u);
-            put_state();
-            ok = step_a(u, 0, 0);
-        }
-        while (ok) {
-            Units w = u;
-            w.next();
-            if (w.valid() && !step_a(w, x + 1, u.last_head() ? m + 1 : m)) break;
-            release();
-            if (!step_b(u, x)) break;
-            if (u.last_head()) {
-                if (!step_c(u, w)) break;
-                ++m;
-            }
-            if (!w.valid()) break;
-            u = w;
-            ++x;
+            u.next(P, P.r, VH);
         }
         if (storer) bulk_wait0();  // output stores complete before the CTA exits
     }
@@ -871,7 +1006,7 @@ template <int NB> static cudaError_t run(TcArgs &P, unsigned char *ws, cudaStrea
     if (!once_per_device(state, [] {
             const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
             return cudaFuncSetAttribute(sums_kernel<NB>, a, (int)kSmemSums<NB>) == cudaSuccess &&
-                   cudaFuncSetAttribute(prompt_kernel<NB>, a, (int)kSmemWalk<NB>) == cudaSuccess;
+                   cudaFuncSetAttribute(prompt_kernel<NB>, a, (int)Walk<NB>::BYTES) == cudaSuccess;
         }))
         return cudaErrorInvalidValue;
     P.slices = (Slice *)(ws + 256);
@@ -879,8 +1014,8 @@ template <int NB> static cudaError_t run(TcArgs &P, unsigned char *ws, cudaStrea
     P.carry = P.sums + (size_t)P.G * kSlot<NB>;
     cudaError_t e = launch(sums_kernel<NB>, dim3(P.G), kSumThreads, kSmemSums<NB>, s, P);
     if (e == cudaSuccess && P.G > 1)
-        e = launch(carry_kernel<NB>, dim3((kSlotS<NB> / 4 + 64 + 256) / 256, P.G), 256, 0, s, P);
-    if (e == cudaSuccess) e = launch(prompt_kernel<NB>, dim3(P.G), kThreads, kSmemWalk<NB>, s, P);
+        e = launch(carry_kernel<NB>, dim3((kSlotS<NB> / 4 + 64 + 256) / 256, P.G < kChains ? P.G : kChains), 256, 0, s, P);
+    if (e == cudaSuccess) e = launch(prompt_kernel<NB>, dim3(P.G), kThreads, Walk<NB>::BYTES, s, P);
     return e;
 }
 
