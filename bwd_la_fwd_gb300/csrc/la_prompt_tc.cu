@@ -19,6 +19,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include "la_f32x2.cuh"
 #include "la_prompt.h"
 #include "la_tc_host.h"
 #include "la_tc_kern.cuh"
@@ -427,25 +428,6 @@ template <int NB> __global__ void __launch_bounds__(256) carry_kernel(const __gr
 // TMEM columns: T 0, P 128, O 192, K^T V 320, z and a sums 448, 464, q . z 480.  P's low parts share the columns of
 // K^T V, which in those chunks is formed behind the last P V, and A waits for C before the next chunk's.
 // ----------------------------------------------------------------------------------------------------------------
-
-// Two fp32 operations at a time.
-__device__ __forceinline__ unsigned long long bits2(float2 a) { return *reinterpret_cast<unsigned long long *>(&a); }
-__device__ __forceinline__ float2 pair2(unsigned long long x) { return *reinterpret_cast<float2 *>(&x); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-    return pair2(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-    return pair2(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-    return pair2(r);
-}
 
 // Shared memory by 32-bit address.
 __device__ __forceinline__ uint4 lds128(uint32_t a) {

@@ -8,8 +8,9 @@
 // instead as a 64-bit fixed-point fraction F of a turn: p F mod 2^64 is the phase, exact in its 64 bits for every
 // p (negative ones too) but for F's own rounding (p 2^-54 turns), in two integer multiplies.
 //
-// Bound by HBM: every element is read and written once.  One thread turns the same V pairs of one token in several
-// heads of Q and K, so that a sine and a cosine serve up to kHeads rows.
+// Bound by HBM: every element is read and written once.  A block takes a few rows (tokens) in all heads of Q and K, or in
+// some: its threads form each sine and cosine once, into shared memory, and then turn one vector of pairs each in every
+// kth head.  (With the sines formed by each thread for the 8 heads it turned, they took as long as the copying.)
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -23,12 +24,13 @@ namespace rot {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 128;  // D <= 256
+constexpr int kTable = 2048;    // sines of a block
 
 struct Side {  // Q or K: from, to, their (batch, head, row) strides in elements
     const void *x;
     void *y;
     long long xs[3], ys[3];
-    int H;     // heads
+    int H;     // heads (K: possibly none)
     int copy;  // the channels past R are copied (not in place)
 };
 
@@ -40,14 +42,14 @@ struct Params {
     long long rows;        // B N
     int N, R, D;
     int units;             // vectors a row is cut into
-    int heads;             // heads of each thread
-    int groups_q, groups;  // head groups of Q; of Q and K together
+    int tile;              // rows of a block
+    int par;               // heads turned side by side
+    int heads, groups;     // heads of a block, blocks that a row's heads are spread over
     float magnitude;
     int inverse;
     unsigned long long freq[kMaxPairs];
 };
 
-template <typename T> struct alignas(16) Vec16 { T e[16 / sizeof(T)]; };
 template <typename T, int V> struct alignas(V * sizeof(T)) VecN { T e[V]; };
 
 __device__ __forceinline__ float load_f(float x) { return x; }
@@ -66,78 +68,102 @@ __device__ __forceinline__ void turn(const Params &P, long long p, int i, float 
 
 // INTER: unit u is the 16-byte vector u of the row, V / 2 pairs, the last ones copied.  Otherwise unit u < R / 2 / V
 // holds pairs u V ... as a vector of the first and one of the second half, and the units after those are the copied
-// vectors.  Threads run over units, then rows, so that a warp's accesses are whole row pieces.
+// vectors.  Threads run over units, then rows, then heads, so that a warp's accesses are whole row pieces.
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const __grid_constant__ Params P) {
     constexpr int NP = INTER ? V / 2 : V;  // pairs per unit
     constexpr int BATCH = 4;               // heads in flight
-    const unsigned group = blockIdx.x % (unsigned)P.groups;
-    const long long f = (long long)(blockIdx.x / (unsigned)P.groups) * kThreads + threadIdx.x;
-    const long long row = f / P.units;
-    const int u = (int)(f - row * P.units);
-    if (row >= P.rows) return;
-    const bool is_k = (int)group >= P.groups_q;
-    const Side &S = P.side[is_k ? 1 : 0];
-    const int h0 = ((int)group - (is_k ? P.groups_q : 0)) * P.heads;
-    const int h1 = min(h0 + P.heads, S.H);
+    __shared__ float2 turns[kTable];       // [row of the block][pair]: cos, sin
+    const long long row0 = (long long)(blockIdx.x / (unsigned)P.groups) * P.tile;
+    const int head0 = (int)(blockIdx.x % (unsigned)P.groups) * P.heads, H = P.side[0].H + P.side[1].H;
+    const int head1 = min(head0 + P.heads, H);
+    const int t = threadIdx.x, u = t % P.units, r = t / P.units % P.tile, lane = t / (P.units * P.tile);
+    const long long row = row0 + r;
+    const bool live = lane < P.par && row < P.rows;
     const long long b = row / P.N, n = row - b * P.N;
-    const T *x = (const T *)S.x + b * S.xs[0] + n * S.xs[2];
-    T *y = (T *)S.y + b * S.ys[0] + n * S.ys[2];
     const int half_units = P.R / 2 / V;
-    if (INTER ? u * V >= P.R : u >= half_units) {  // nothing but copied channels
-        if (!S.copy) return;
-        const int at = INTER ? u * V : P.R + (u - half_units) * V;
-        for (int h = h0; h < h1; ++h)
-            *(VecN<T, V> *)(y + h * S.ys[1] + at) = *(const VecN<T, V> *)(x + h * S.xs[1] + at);
-        return;
-    }
-    const long long pos = P.positions ? (long long)P.positions[b * P.pos_stride + n] : P.first + n;
-    float c[NP], s[NP];
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-        const int i = u * NP + j;
-        if (!INTER || 2 * i < P.R) turn(P, pos, i, c[j], s[j]);
-        else c[j] = 1.f, s[j] = 0.f;
-    }
-    const int at1 = u * V, at2 = INTER ? u * V : P.R / 2 + u * V;
-    for (int h = h0; h < h1; h += BATCH) {
-        VecN<T, V> v1[BATCH], v2[BATCH];
+    const bool turned = INTER ? u * V < P.R : u < half_units;
+    const int at1 = INTER || turned ? u * V : P.R + (u - half_units) * V, at2 = INTER ? 0 : P.R / 2 + u * V;
+    // this thread's vectors in head h of Q and K together
+    auto from = [&](int h) {
+        const bool k = h >= P.side[0].H;
+        const Side &S = P.side[k];
+        return (const T *)S.x + b * S.xs[0] + n * S.xs[2] + (k ? h - P.side[0].H : h) * S.xs[1];
+    };
+    VecN<T, V> v1[BATCH], v2[BATCH];
+    auto load = [&](int h) {
 #pragma unroll
         for (int k = 0; k < BATCH; ++k)
-            if (h + k < h1) {
-                v1[k] = *(const VecN<T, V> *)(x + (h + k) * S.xs[1] + at1);
-                if (!INTER) v2[k] = *(const VecN<T, V> *)(x + (h + k) * S.xs[1] + at2);
+            if (live && h + k * P.par < head1) {
+                const T *x = from(h + k * P.par);
+                v1[k] = *(const VecN<T, V> *)(x + at1);
+                if (!INTER && turned) v2[k] = *(const VecN<T, V> *)(x + at2);
             }
+    };
+    load(head0 + lane);  // on their way while the sines are formed
+    const int pairs = P.R / 2;
+    for (int i = t; i < P.tile * pairs; i += kThreads) {
+        const long long at = row0 + i / pairs;
+        if (at >= P.rows) break;
+        const long long ab = at / P.N, an = at - ab * P.N;
+        const long long pos = P.positions ? (long long)P.positions[ab * P.pos_stride + an] : P.first + an;
+        float2 cs;
+        turn(P, pos, i % pairs, cs.x, cs.y);
+        turns[i] = cs;
+    }
+    __syncthreads();
+    float c[NP], s[NP];
+    if (turned && live) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            const int i = u * NP + j;
+            const float2 cs = turns[r * pairs + (INTER ? min(i, pairs - 1) : i)];
+            c[j] = cs.x, s[j] = cs.y;
+        }
+    }
+    for (int h = head0 + lane; h < head1; h += BATCH * P.par) {
+        if (h != head0 + lane) load(h);
+        if (!live) continue;
 #pragma unroll
         for (int k = 0; k < BATCH; ++k)
-            if (h + k < h1) {
+            if (h + k * P.par < head1) {
+                const int hh = h + k * P.par;
+                const bool is_k = hh >= P.side[0].H;
+                const Side &S = P.side[is_k];
+                T *y = (T *)S.y + b * S.ys[0] + n * S.ys[2] + (is_k ? hh - P.side[0].H : hh) * S.ys[1];
+                if (!turned) {
+                    if (S.copy) *(VecN<T, V> *)(y + at1) = v1[k];
+                    continue;
+                }
 #pragma unroll
                 for (int j = 0; j < NP; ++j) {
                     T &e1 = INTER ? v1[k].e[2 * j] : v1[k].e[j];
                     T &e2 = INTER ? v1[k].e[2 * j + 1] : v2[k].e[j];
                     if (INTER && 2 * (u * NP + j) >= P.R) continue;  // copied as it is (no product with 1: NaN payloads, -0)
-                    const float a = load_f(e1), d = load_f(e2);
-                    e1 = round_to<T>(a * c[j] - d * s[j]);
-                    e2 = round_to<T>(a * s[j] + d * c[j]);
+                    const float x1 = load_f(e1), x2 = load_f(e2);
+                    e1 = round_to<T>(x1 * c[j] - x2 * s[j]);
+                    e2 = round_to<T>(x1 * s[j] + x2 * c[j]);
                 }
-                *(VecN<T, V> *)(y + (h + k) * S.ys[1] + at1) = v1[k];
-                if (!INTER) *(VecN<T, V> *)(y + (h + k) * S.ys[1] + at2) = v2[k];
+                *(VecN<T, V> *)(y + at1) = v1[k];
+                if (!INTER) *(VecN<T, V> *)(y + at2) = v2[k];
             }
     }
 }
 
 template <typename T, int V, bool INTER> cudaError_t launch(Params &P, cudaStream_t s) {
     P.units = INTER ? P.D / V : P.R / 2 / V + (P.D - P.R) / V;
-    const long long threads = P.rows * P.units;
-    const long long blocks = (threads + kThreads - 1) / kThreads;
-    // Heads per thread: up to 8, so that a sine serves 8 rows, fewer while that leaves the GPU without some 1024
-    // threads on each SM: a token of a small batch is then one load, one turn and one store deep.
-    const int sms = 152;
-    P.heads = 8;
-    auto groups = [&](int H) { return (H + P.heads - 1) / P.heads; };
-    while (P.heads > 1 && threads * (groups(P.side[0].H) + groups(P.side[1].H)) < (long long)sms * 1024) P.heads /= 2;
-    P.groups_q = groups(P.side[0].H);
-    P.groups = P.groups_q + groups(P.side[1].H);
+    // Rows of a block: as many as its threads take of one head (contiguous pieces of 8 KB and more: with 1 KB, 4 rows of 8
+    // heads at a time, DRAM gave 2.9 instead of 3.6 TB/s), as the table holds, and so that every SM has two blocks.
+    // Units fit into a block: V = 1 only where R / 2 is odd, and then there are at most D - R / 2 < 256 of them.
+    P.tile = kThreads / P.units;
+    while (P.tile > 1 && (P.tile * (P.R / 2) > kTable || (P.rows + P.tile - 1) / P.tile < 304)) P.tile = (P.tile + 1) / 2;
+    P.par = kThreads / (P.units * P.tile);
+    // Heads of a block: all of them, or fewer while that leaves the GPU without two blocks on each SM.
+    const int H = P.side[0].H + P.side[1].H;
+    const long long blocks = (P.rows + P.tile - 1) / P.tile;
+    P.heads = H;
+    while (P.heads > P.par && blocks * ((H + P.heads - 1) / P.heads) < 304) P.heads = (P.heads + 1) / 2;
+    P.groups = (H + P.heads - 1) / P.heads;
     if (blocks * P.groups >= (1LL << 31)) return cudaErrorInvalidConfiguration;
     rotary_kernel<T, V, INTER><<<(unsigned)(blocks * P.groups), kThreads, 0, s>>>(P);
     return cudaGetLastError();

@@ -82,7 +82,7 @@ inline bool views_meet(const View &a, const View &b) {
         hi[n] = a.ext[k] - 1;
         ++n;
     }
-    for (int x = 0; x < n; ++x)  // by decreasing stride
+    for (int x = 0; x + 1 < n && n <= 3; ++x)  // by decreasing stride
         for (int y = x + 1; y < n; ++y)
             if (st[y] > st[x]) {
                 long long t;

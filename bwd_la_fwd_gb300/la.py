@@ -35,6 +35,8 @@ def library_path() -> str:
 def load_library():
     """Load the compiled CUDA library (built by ``bwd_la_fwd_gb300.build``); raise if it is absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -307,31 +309,14 @@ def la_state_append(state: DecodeState, K, V, stream=None):
     return state
 
 
-def _place(stream, *ts):
-    """The stream that a call on these tensors goes to: `stream`, or the current one of their device."""
-    import torch
-    dev = ts[0].device
-    if dev.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got {dev}")
-    for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on one device, got {dev} and {t.device}")
-    if stream is None:
-        return torch.cuda.current_stream(dev)
-    if stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    return stream
-
-
 class _on:
-    """Makes the stream and its device the current ones for a call: new tensors belong to that stream, and the
-    library launches on that device."""
+    """Makes a stream and its device the current ones for a call: new tensors belong to that stream, and the library
+    launches on that device."""
 
     __slots__ = ("_ctx",)
 
-    def __init__(self, stream):
-        import torch
-        self._ctx = None if stream == torch.cuda.current_stream() else torch.cuda.stream(stream)
+    def __init__(self, ctx):
+        self._ctx = ctx
 
     def __enter__(self):
         if self._ctx is not None:
@@ -342,8 +327,32 @@ class _on:
             self._ctx.__exit__(*exc)
 
 
-def _longs(vals):
-    return (ctypes.c_longlong * len(vals))(*vals)
+_HERE_ALREADY = _on(None)
+
+
+def _place(stream, first, *ts):
+    """(context, stream pointer) of a call on these tensors, all of one CUDA device: on `stream`, or on the current
+    stream of their device."""
+    import torch
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {dev}")
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on one device, got {dev} and {t.device}")
+    if stream is None:
+        current = torch.cuda.current_device() == dev.index
+        return _HERE_ALREADY if current else _on(torch.cuda.device(dev)), torch._C._cuda_getCurrentRawStream(dev.index)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return _on(torch.cuda.stream(stream)), stream.cuda_stream
+
+
+_ARRAYS = {n: ctypes.c_longlong * n for n in (3, 6, 8, 12)}
+
+
+def _longs(*vals):
+    return _ARRAYS[len(vals)](*vals)
 
 
 def _row_contiguous(*ts):
@@ -373,16 +382,16 @@ def la_decode_step_grouped(state: DecodeState, q, k, v, o=None, normaliser=None,
         if t is not None and t.dtype != state.token_dtype:
             raise ValueError("token dtype does not match the state")
     _row_contiguous(q, k, v, o)
-    stream = _place(stream, q, k, v, o, normaliser, state.S, state.z, state.a, state.n)
+    on, sp = _place(stream, q, k, v, o, normaliser, state.S, state.z, state.a, state.n)
     if normaliser is not None:
         _expect(normaliser, (B, Hq), torch.float32, "normaliser")
-    with _on(stream):
+    with on:
         if o is None:
             o = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
         st = load_library().la_decode_step_grouped(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(normaliser), state.S.data_ptr(),
             state.z.data_ptr(), state.a.data_ptr(), state.n.data_ptr(), B, Hq, H, D, _dtype_code(q),
-            _longs((*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2])), stream.cuda_stream)
+            _longs(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2]), sp)
     if st != 0:
         raise LAError(st, "la_decode_step_grouped")
     return o
@@ -428,8 +437,8 @@ def la_prompt(Q, K, V, seq_offsets, state=None, resume: bool = False, O=None, wo
     if resume and state is None:
         raise ValueError("resume needs a state")
     parts = (state.S, state.z, state.a, state.n) if state is not None else (None,) * 4
-    stream = _place(stream, Q, K, V, O, seq_offsets, workspace, *parts)
-    with _on(stream):
+    on, sp = _place(stream, Q, K, V, O, seq_offsets, workspace, *parts)
+    with on:
         if O is None:
             O = torch.zeros((T, Hq, D), dtype=Q.dtype, device=Q.device)
         if workspace is None:
@@ -437,8 +446,8 @@ def la_prompt(Q, K, V, seq_offsets, state=None, resume: bool = False, O=None, wo
         st = load_library().la_prompt(
             Q.data_ptr(), K.data_ptr(), V.data_ptr(), seq_offsets.data_ptr(), O.data_ptr(), *map(_ptr, parts),
             int(bool(resume)), T, nseq, Hq, Hkv, D, dt,
-            _longs([s for t in (Q, K, V, O) for s in (t.stride(1), t.stride(0))]), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), stream.cuda_stream)
+            _longs(*[s for t in (Q, K, V, O) for s in (t.stride(1), t.stride(0))]), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), sp)
     if st != 0:
         raise LAError(st, "la_prompt")
     return O
@@ -493,8 +502,8 @@ def _rotary(name, Q, K, freqs, positions, first_position, interleaved, magnitude
         stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
         if stride and stride < N:
             raise ValueError("positions of the batch entries overlap")
-    stream = _place(stream, Q, K, Q_out, K_out, positions)
-    with _on(stream):
+    on, sp = _place(stream, Q, K, Q_out, K_out, positions)
+    with on:
         if Q_out is None:
             Q_out = torch.empty((B, Hq, N, D), dtype=Q.dtype, device=Q.device)
         if K is not None and K_out is None:
@@ -504,7 +513,7 @@ def _rotary(name, Q, K, freqs, positions, first_position, interleaved, magnitude
         st = getattr(load_library(), name)(
             Q.data_ptr(), _ptr(K), Q_out.data_ptr(), _ptr(K_out), freqs.values, _ptr(positions), stride, first_position,
             int(bool(interleaved)), magnitude, B, Hq, Hk, N, D, freqs.rotary_dim, dt,
-            _longs((*Q.stride()[:3], *sk, *Q_out.stride()[:3], *sko)), stream.cuda_stream)
+            _longs(*Q.stride()[:3], *sk, *Q_out.stride()[:3], *sko), sp)
     if st != 0:
         raise LAError(st, name)
     return Q_out, K_out
@@ -555,15 +564,15 @@ def la_gated_scan(X, W, gate: str, h0=None, H=None, h_last=None, stream=None):
     for t, what in ((h0, "h0"), (h_last, "h_last")):
         if t is not None:
             _expect(t, (B, C), torch.float32, what)
-    stream = _place(stream, X, W, h0, H, h_last)
-    with _on(stream):
+    on, sp = _place(stream, X, W, h0, H, h_last)
+    with on:
         if H is None:
             H = torch.empty((B, N, C), dtype=X.dtype, device=X.device)
         if h_last is None:
             h_last = torch.empty((B, C), dtype=torch.float32, device=X.device)
         st = load_library().la_gated_scan(X.data_ptr(), W.data_ptr(), _ptr(h0), H.data_ptr(), h_last.data_ptr(), B, N, C,
-                                          code, dt, _longs((*X.stride()[:2], *W.stride()[:2], *H.stride()[:2])),
-                                          stream.cuda_stream)
+                                          code, dt, _longs(*X.stride()[:2], *W.stride()[:2], *H.stride()[:2]),
+                                          sp)
     if st != 0:
         raise LAError(st, "la_gated_scan")
     return H, h_last
@@ -579,15 +588,15 @@ def la_gated_scan_backward(X, W, H, dH, gate: str, h0=None, dh_last=None, dX=Non
     for t, what in ((h0, "h0"), (dh_last, "dh_last"), (dh0, "dh0")):
         if t is not None:
             _expect(t, (B, C), torch.float32, what)
-    stream = _place(stream, X, W, H, dH, h0, dh_last, dX, dW, dh0)
-    with _on(stream):
+    on, sp = _place(stream, X, W, H, dH, h0, dh_last, dX, dW, dh0)
+    with on:
         dX = torch.empty((B, N, C), dtype=X.dtype, device=X.device) if dX is None else dX
         dW = torch.empty((B, N, C), dtype=X.dtype, device=X.device) if dW is None else dW
         dh0 = torch.empty((B, C), dtype=torch.float32, device=X.device) if dh0 is None else dh0
         st = load_library().la_gated_scan_backward(
             X.data_ptr(), W.data_ptr(), H.data_ptr(), dH.data_ptr(), _ptr(h0), _ptr(dh_last), dX.data_ptr(),
             dW.data_ptr(), dh0.data_ptr(), B, N, C, code, dt,
-            _longs([s for t in (X, W, H, dH, dX, dW) for s in t.stride()[:2]]), stream.cuda_stream)
+            _longs(*[s for t in (X, W, H, dH, dX, dW) for s in t.stride()[:2]]), sp)
     if st != 0:
         raise LAError(st, "la_gated_scan_backward")
     return dX, dW, dh0
@@ -601,12 +610,12 @@ def la_gated_scan_step(state, x, w, gate: str, h=None, stream=None):
     B, C = x.shape
     code, dt = _gate_code(gate), _dtype_code(x)
     _expect(state, (B, C), torch.float32, "state")
-    stream = _place(stream, x, w, h, state)
-    with _on(stream):
+    on, sp = _place(stream, x, w, h, state)
+    with on:
         if h is None:
             h = torch.empty((B, C), dtype=x.dtype, device=x.device)
         st = load_library().la_gated_scan_step(x.data_ptr(), w.data_ptr(), h.data_ptr(), state.data_ptr(), B, C, code, dt,
-                                               _longs((x.stride(0), w.stride(0), h.stride(0))), stream.cuda_stream)
+                                               _longs(x.stride(0), w.stride(0), h.stride(0)), sp)
     if st != 0:
         raise LAError(st, "la_gated_scan_step")
     return h
