@@ -8,14 +8,16 @@
 // instead as a 64-bit fixed-point fraction F of a turn: p F mod 2^64 is the phase, exact in its 64 bits for every
 // p (negative ones too) but for F's own rounding (p 2^-54 turns), in two integer multiplies.
 //
-// Bound by HBM: every element is read and written once.  A block takes a few rows (tokens) in all heads of Q and K, or in
-// some: its threads form each sine and cosine once, into shared memory, and then turn one vector of pairs each in every
-// kth head.  (With the sines formed by each thread for the 8 heads it turned, they took as long as the copying.)
+// Bound by HBM: every element is read and written once.  A block takes a few rows of one batch entry in all heads of Q and
+// K, or in some: its threads form each sine and cosine once, into shared memory, and then turn one vector of pairs each in
+// every kth head.  Thread and block indices are the coordinates themselves: with rows counted through and divided out
+// again (64-bit divisions), a block's beginning took longer than its copying.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
 
+#include "la_f32x2.cuh"
 #include "la_internal.h"
 #include "la_views.h"
 
@@ -24,7 +26,8 @@ namespace rot {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 128;  // D <= 256
-constexpr int kTable = 2048;    // sines of a block
+constexpr int kTable = 1024;    // sines of a block
+constexpr int kAhead = 4;       // heads of a thread on their way
 
 struct Side {  // Q or K: from, to, their (batch, head, row) strides in elements
     const void *x;
@@ -39,12 +42,8 @@ struct Params {
     const int *positions;  // nullptr: first + row
     long long pos_stride;  // between batch entries
     long long first;
-    long long rows;        // B N
-    int N, R, D;
-    int units;             // vectors a row is cut into
-    int tile;              // rows of a block
-    int par;               // heads turned side by side
-    int heads, groups;     // heads of a block, blocks that a row's heads are spread over
+    int B, N, R, D;
+    int heads;             // heads of a block
     float magnitude;
     int inverse;
     unsigned long long freq[kMaxPairs];
@@ -66,106 +65,148 @@ __device__ __forceinline__ void turn(const Params &P, long long p, int i, float 
     s *= P.inverse ? -P.magnitude : P.magnitude;
 }
 
+// A vector of 4, 8 or 16 bytes, global -> shared.
+template <typename T, int V> __device__ __forceinline__ void copy_async(VecN<T, V> *dst, const T *src) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if constexpr (sizeof(VecN<T, V>) == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"((int)sizeof(VecN<T, V>)) : "memory");
+}
+
+// (y1, y2) of two pairs side by side: x1 c - x2 s and x1 s + x2 c.
+__device__ __forceinline__ void turn2(float2 &x1, float2 &x2, float2 c, float2 s) {
+    const float2 m = mul2(x2, s), y1 = fma2(x1, c, make_float2(-m.x, -m.y));
+    x2 = fma2(x1, s, mul2(x2, c));
+    x1 = y1;
+}
+
+// Block (units, rows, heads side by side), grid (row tiles, head groups, batch).
 // INTER: unit u is the 16-byte vector u of the row, V / 2 pairs, the last ones copied.  Otherwise unit u < R / 2 / V
 // holds pairs u V ... as a vector of the first and one of the second half, and the units after those are the copied
-// vectors.  Threads run over units, then rows, then heads, so that a warp's accesses are whole row pieces.
+// vectors.
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ Params P) {
     constexpr int NP = INTER ? V / 2 : V;  // pairs per unit
-    constexpr int BATCH = 4;               // heads in flight
-    __shared__ float2 turns[kTable];       // [row of the block][pair]: cos, sin
-    const long long row0 = (long long)(blockIdx.x / (unsigned)P.groups) * P.tile;
-    const int head0 = (int)(blockIdx.x % (unsigned)P.groups) * P.heads, H = P.side[0].H + P.side[1].H;
-    const int head1 = min(head0 + P.heads, H);
-    const int t = threadIdx.x, u = t % P.units, r = t / P.units % P.tile, lane = t / (P.units * P.tile);
-    const long long row = row0 + r;
-    const bool live = lane < P.par && row < P.rows;
-    const long long b = row / P.N, n = row - b * P.N;
-    const int half_units = P.R / 2 / V;
-    const bool turned = INTER ? u * V < P.R : u < half_units;
-    const int at1 = INTER || turned ? u * V : P.R + (u - half_units) * V, at2 = INTER ? 0 : P.R / 2 + u * V;
-    // this thread's vectors in head h of Q and K together
-    auto from = [&](int h) {
-        const bool k = h >= P.side[0].H;
-        const Side &S = P.side[k];
-        return (const T *)S.x + b * S.xs[0] + n * S.xs[2] + (k ? h - P.side[0].H : h) * S.xs[1];
-    };
-    VecN<T, V> v1[BATCH], v2[BATCH];
-    auto load = [&](int h) {
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k)
-            if (live && h + k * P.par < head1) {
-                const T *x = from(h + k * P.par);
-                v1[k] = *(const VecN<T, V> *)(x + at1);
-                if (!INTER && turned) v2[k] = *(const VecN<T, V> *)(x + at2);
+    constexpr bool ASYNC = V * sizeof(T) >= 4;  // vectors that cp.async can copy
+    __shared__ float2 turns[kTable];            // [row of the block][pair]: cos, sin
+    // each thread's own ring of vectors on their way: only so do enough bytes fly (with the next head's vectors in
+    // registers 4.0 TB/s, so 5.8)
+    __shared__ VecN<T, V> ring[ASYNC ? kAhead : 1][INTER ? 1 : 2][kThreads];
+    const int me = threadIdx.x + blockDim.x * (threadIdx.y + blockDim.y * threadIdx.z);
+    const int u = threadIdx.x, r = threadIdx.y, n = blockIdx.x * blockDim.y + r;
+    const int Hq = P.side[0].H, H = Hq + P.side[1].H;
+    const int head0 = blockIdx.y * P.heads + threadIdx.z, head1 = min((int)(blockIdx.y + 1) * P.heads, H);
+    const int step = blockDim.z, pairs = P.R / 2, half_units = pairs / V;
+    const bool live = n < P.N, turned = INTER ? u * V < P.R : u < half_units;
+    const int at1 = INTER || turned ? u * V : P.R + (u - half_units) * V, at2 = pairs + u * V;
+    for (int b = blockIdx.z; b < P.B; b += gridDim.z) {
+        // the row's vector in head h of Q and K together
+        const T *xq = (const T *)P.side[0].x + b * P.side[0].xs[0] + n * P.side[0].xs[2] + at1;
+        const T *xk = (const T *)P.side[1].x + b * P.side[1].xs[0] + n * P.side[1].xs[2] + at1 - Hq * P.side[1].xs[1];
+        T *yq = (T *)P.side[0].y + b * P.side[0].ys[0] + n * P.side[0].ys[2] + at1;
+        T *yk = (T *)P.side[1].y + b * P.side[1].ys[0] + n * P.side[1].ys[2] + at1 - Hq * P.side[1].ys[1];
+        VecN<T, V> va, vb;
+        auto fetch = [&](int h, int slot) {
+            if (live && h < head1) {
+                const T *x = h < Hq ? xq + h * P.side[0].xs[1] : xk + h * P.side[1].xs[1];
+                if constexpr (ASYNC) {
+                    copy_async(&ring[slot][0][me], x);
+                    if (!INTER && turned) copy_async(&ring[slot][INTER ? 0 : 1][me], x + at2 - at1);
+                } else {
+                    va = *(const VecN<T, V> *)x;
+                    if (!INTER && turned) vb = *(const VecN<T, V> *)(x + at2 - at1);
+                }
             }
-    };
-    load(head0 + lane);  // on their way while the sines are formed
-    const int pairs = P.R / 2;
-    for (int i = t; i < P.tile * pairs; i += kThreads) {
-        const long long at = row0 + i / pairs;
-        if (at >= P.rows) break;
-        const long long ab = at / P.N, an = at - ab * P.N;
-        const long long pos = P.positions ? (long long)P.positions[ab * P.pos_stride + an] : P.first + an;
-        float2 cs;
-        turn(P, pos, i % pairs, cs.x, cs.y);
-        turns[i] = cs;
-    }
-    __syncthreads();
-    float c[NP], s[NP];
-    if (turned && live) {
+            if constexpr (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        if constexpr (ASYNC) {  // on their way while the sines are formed
 #pragma unroll
-        for (int j = 0; j < NP; ++j) {
-            const int i = u * NP + j;
-            const float2 cs = turns[r * pairs + (INTER ? min(i, pairs - 1) : i)];
-            c[j] = cs.x, s[j] = cs.y;
+            for (int k = 0; k < kAhead; ++k) fetch(head0 + k * step, k);
         }
-    }
-    for (int h = head0 + lane; h < head1; h += BATCH * P.par) {
-        if (h != head0 + lane) load(h);
-        if (!live) continue;
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k)
-            if (h + k * P.par < head1) {
-                const int hh = h + k * P.par;
-                const bool is_k = hh >= P.side[0].H;
-                const Side &S = P.side[is_k];
-                T *y = (T *)S.y + b * S.ys[0] + n * S.ys[2] + (is_k ? hh - P.side[0].H : hh) * S.ys[1];
-                if (!turned) {
-                    if (S.copy) *(VecN<T, V> *)(y + at1) = v1[k];
-                    continue;
-                }
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    T &e1 = INTER ? v1[k].e[2 * j] : v1[k].e[j];
-                    T &e2 = INTER ? v1[k].e[2 * j + 1] : v2[k].e[j];
-                    if (INTER && 2 * (u * NP + j) >= P.R) continue;  // copied as it is (no product with 1: NaN payloads, -0)
-                    const float x1 = load_f(e1), x2 = load_f(e2);
-                    e1 = round_to<T>(x1 * c[j] - x2 * s[j]);
-                    e2 = round_to<T>(x1 * s[j] + x2 * c[j]);
-                }
-                *(VecN<T, V> *)(y + at1) = v1[k];
-                if (!INTER) *(VecN<T, V> *)(y + at2) = v2[k];
+        if (live) {
+            const long long pos = P.positions ? (long long)P.positions[b * P.pos_stride + n] : P.first + n;
+            for (int i = u + blockDim.x * threadIdx.z; i < pairs; i += blockDim.x * blockDim.z) {
+                float2 cs;
+                turn(P, pos, i, cs.x, cs.y);
+                turns[r * pairs + i] = cs;
             }
+        }
+        __syncthreads();
+        float c[NP], s[NP];
+        if (live && turned) {
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+                const float2 cs = turns[r * pairs + (INTER ? min(u * NP + j, pairs - 1) : u * NP + j)];
+                c[j] = cs.x, s[j] = cs.y;
+            }
+        }
+        int slot = 0;
+        for (int h = head0; h < head1; h += step) {
+            if constexpr (ASYNC) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+                va = ring[slot][0][me];
+                if (!INTER) vb = ring[slot][INTER ? 0 : 1][me];
+            } else {
+                fetch(h, 0);
+            }
+            if (!live) continue;
+            T *y = h < Hq ? yq + h * P.side[0].ys[1] : yk + h * P.side[1].ys[1];
+            if (!turned) {  // copied, unless in place
+                if (P.side[h >= Hq].copy) *(VecN<T, V> *)y = va;
+            } else {
+                if constexpr (INTER) {
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) {
+                        if (2 * (u * NP + j) >= P.R) continue;  // copied as it is (no product with 1: NaN payloads, -0)
+                        const float x1 = load_f(va.e[2 * j]), x2 = load_f(va.e[2 * j + 1]);
+                        const float2 z = fma2(make_float2(x1, x2), both(c[j]), mul2(make_float2(x2, x1), make_float2(-s[j], s[j])));
+                        va.e[2 * j] = round_to<T>(z.x);
+                        va.e[2 * j + 1] = round_to<T>(z.y);
+                    }
+                } else if constexpr (V == 1) {
+                    const float x1 = load_f(va.e[0]), x2 = load_f(vb.e[0]);
+                    va.e[0] = round_to<T>(x1 * c[0] - x2 * s[0]);
+                    vb.e[0] = round_to<T>(x1 * s[0] + x2 * c[0]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; j += 2) {
+                        float2 x1 = make_float2(load_f(va.e[j]), load_f(va.e[j + 1]));
+                        float2 x2 = make_float2(load_f(vb.e[j]), load_f(vb.e[j + 1]));
+                        turn2(x1, x2, make_float2(c[j], c[j + 1]), make_float2(s[j], s[j + 1]));
+                        va.e[j] = round_to<T>(x1.x), va.e[j + 1] = round_to<T>(x1.y);
+                        vb.e[j] = round_to<T>(x2.x), vb.e[j + 1] = round_to<T>(x2.y);
+                    }
+                }
+                *(VecN<T, V> *)y = va;
+                if (!INTER) *(VecN<T, V> *)(y + at2 - at1) = vb;
+            }
+            if constexpr (ASYNC) {
+                fetch(h + kAhead * step, slot);
+                slot = (slot + 1) % kAhead;
+            }
+        }
+        __syncthreads();  // the sines have been read
     }
 }
 
 template <typename T, int V, bool INTER> cudaError_t launch(Params &P, cudaStream_t s) {
-    P.units = INTER ? P.D / V : P.R / 2 / V + (P.D - P.R) / V;
-    // Rows of a block: as many as its threads take of one head (contiguous pieces of 8 KB and more: with 1 KB, 4 rows of 8
-    // heads at a time, DRAM gave 2.9 instead of 3.6 TB/s), as the table holds, and so that every SM has two blocks.
     // Units fit into a block: V = 1 only where R / 2 is odd, and then there are at most D - R / 2 < 256 of them.
-    P.tile = kThreads / P.units;
-    while (P.tile > 1 && (P.tile * (P.R / 2) > kTable || (P.rows + P.tile - 1) / P.tile < 304)) P.tile = (P.tile + 1) / 2;
-    P.par = kThreads / (P.units * P.tile);
-    // Heads of a block: all of them, or fewer while that leaves the GPU without two blocks on each SM.
-    const int H = P.side[0].H + P.side[1].H;
-    const long long blocks = (P.rows + P.tile - 1) / P.tile;
+    const int units = INTER ? P.D / V : P.R / 2 / V + (P.D - P.R) / V, H = P.side[0].H + P.side[1].H;
+    auto ceil = [](long long a, long long b) { return (a + b - 1) / b; };
+    // Rows of a block: two warps' worth of vectors of one head (8 rows of 8: 47 us at 4 x 4096 x 32 heads of 128 in bf16, 4
+    // rows 48, one row 74), and what the table holds; the rest of its threads take heads.
+    int tile = units < 64 ? 64 / units : 1;
+    if (tile > P.N) tile = P.N;
+    while (tile > 1 && tile * (P.R / 2) > kTable) --tile;
+    int par = kThreads / (units * tile);
+    if (par > H) par = H;
+    if (par > 64) par = 64;
+    // Heads of a block: all of them, or fewer while that leaves the GPU without four blocks on each SM.
     P.heads = H;
-    while (P.heads > P.par && blocks * ((H + P.heads - 1) / P.heads) < 304) P.heads = (P.heads + 1) / 2;
-    P.groups = (H + P.heads - 1) / P.heads;
-    if (blocks * P.groups >= (1LL << 31)) return cudaErrorInvalidConfiguration;
-    rotary_kernel<T, V, INTER><<<(unsigned)(blocks * P.groups), kThreads, 0, s>>>(P);
+    while (P.heads > par && ceil(P.N, tile) * P.B * ceil(H, P.heads) < 608) P.heads = (P.heads + 1) / 2;
+    const long long gx = ceil(P.N, tile), gy = ceil(H, P.heads);
+    if (gy > 65535) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)gx, (unsigned)gy, P.B < 65535 ? P.B : 65535);
+    rotary_kernel<T, V, INTER><<<grid, dim3(units, tile, par), 0, s>>>(P);
     return cudaGetLastError();
 }
 
@@ -233,7 +274,7 @@ int rotary(const void *Q, const void *K, void *Qr, void *Kr, const unsigned long
     P.positions = positions;
     P.pos_stride = position_stride;
     P.first = first;
-    P.rows = rows;
+    P.B = B;
     P.N = N;
     P.R = R;
     P.D = D;

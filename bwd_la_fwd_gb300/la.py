@@ -335,14 +335,15 @@ def _place(stream, first, *ts):
     stream of their device."""
     import torch
     dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got {dev}")
     for t in ts:
         if t is not None and t.device != dev:
             raise ValueError(f"all tensors must be on one device, got {dev} and {t.device}")
+    index = dev.index
+    if index is None or dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {dev}")
     if stream is None:
-        current = torch.cuda.current_device() == dev.index
-        return _HERE_ALREADY if current else _on(torch.cuda.device(dev)), torch._C._cuda_getCurrentRawStream(dev.index)
+        here = torch._C._cuda_getDevice() == index
+        return _HERE_ALREADY if here else _on(torch.cuda.device(dev)), torch._C._cuda_getCurrentRawStream(index)
     if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
     return _on(torch.cuda.stream(stream)), stream.cuda_stream
@@ -351,14 +352,12 @@ def _place(stream, first, *ts):
 _ARRAYS = {n: ctypes.c_longlong * n for n in (3, 6, 8, 12)}
 
 
-def _longs(*vals):
-    return _ARRAYS[len(vals)](*vals)
-
-
-def _row_contiguous(*ts):
-    for t in ts:
-        if t is not None and t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise ValueError("the last dimension must be contiguous (stride(-1) == 1)")
+def _rows(t):
+    """A tensor's strides; its last dimension has to be contiguous."""
+    s = t.stride()
+    if s[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError("the last dimension must be contiguous (stride(-1) == 1)")
+    return s
 
 
 def _expect(t, shape, dtype, what):
@@ -373,25 +372,26 @@ def la_decode_step_grouped(state: DecodeState, q, k, v, o=None, normaliser=None,
     contiguous D; `normaliser`, if given, is a float32 [B,Hq] tensor that receives g."""
     import torch
     B, H, D = state.B, state.H, state.D
-    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != D or H < 1 or q.shape[1] % H != 0 or q.shape[1] < H:
-        raise ValueError(f"expected [B, r Hkv, D] queries for B, Hkv, D = {(B, H, D)}, got {tuple(q.shape)}")
-    Hq = q.shape[1]
-    if tuple(k.shape) != (B, H, D) or tuple(v.shape) != (B, H, D) or (o is not None and o.shape != q.shape):
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3 or shape[0] != B or shape[2] != D or H < 1 or shape[1] % H != 0 or shape[1] < H:
+        raise ValueError(f"expected [B, r Hkv, D] queries for B, Hkv, D = {(B, H, D)}, got {tuple(shape)}")
+    Hq = shape[1]
+    if k.shape != (B, H, D) or v.shape != (B, H, D) or (o is not None and o.shape != shape):
         raise ValueError(f"expected k, v of shape {(B, H, D)} and o like q")
-    for t in (q, k, v, o):
-        if t is not None and t.dtype != state.token_dtype:
-            raise ValueError("token dtype does not match the state")
-    _row_contiguous(q, k, v, o)
-    on, sp = _place(stream, q, k, v, o, normaliser, state.S, state.z, state.a, state.n)
+    if dtype != state.token_dtype or k.dtype != dtype or v.dtype != dtype or (o is not None and o.dtype != dtype):
+        raise ValueError("token dtype does not match the state")
     if normaliser is not None:
         _expect(normaliser, (B, Hq), torch.float32, "normaliser")
+    sq, sk, sv = _rows(q), _rows(k), _rows(v)
+    so = (Hq * D, D) if o is None else _rows(o)
+    on, sp = _place(stream, q, k, v, o, normaliser, state.S, state.z, state.a, state.n)
     with on:
         if o is None:
-            o = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+            o = torch.empty(shape, dtype=dtype, device=q.device)
         st = load_library().la_decode_step_grouped(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(normaliser), state.S.data_ptr(),
-            state.z.data_ptr(), state.a.data_ptr(), state.n.data_ptr(), B, Hq, H, D, _dtype_code(q),
-            _longs(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2]), sp)
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), 0 if normaliser is None else normaliser.data_ptr(),
+            state.S.data_ptr(), state.z.data_ptr(), state.a.data_ptr(), state.n.data_ptr(), B, Hq, H, D, _dtype_code(q),
+            _ARRAYS[8](sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1]), sp)
     if st != 0:
         raise LAError(st, "la_decode_step_grouped")
     return o
@@ -430,7 +430,6 @@ def la_prompt(Q, K, V, seq_offsets, state=None, resume: bool = False, O=None, wo
         if t is not None and t.dtype != Q.dtype:
             raise ValueError("Q, K, V, O must share their dtype")
     _expect(seq_offsets, (nseq + 1,), torch.int32, "seq_offsets")
-    _row_contiguous(Q, K, V, O)
     dt = _dtype_code(Q)
     if state is not None and ((state.B, state.H, state.D) != (nseq, Hkv, D) or state.token_dtype != Q.dtype):
         raise ValueError(f"the state is not one of nseq, Hkv, D = {(nseq, Hkv, D)} and {Q.dtype}")
@@ -441,12 +440,13 @@ def la_prompt(Q, K, V, seq_offsets, state=None, resume: bool = False, O=None, wo
     with on:
         if O is None:
             O = torch.zeros((T, Hq, D), dtype=Q.dtype, device=Q.device)
+        strides = [s for t in (Q, K, V, O) for s in _rows(t)[1::-1]]  # (head, row)
         if workspace is None:
             workspace = new_prompt_workspace(T, nseq, Hq, Hkv, D, dt, Q.device)
         st = load_library().la_prompt(
             Q.data_ptr(), K.data_ptr(), V.data_ptr(), seq_offsets.data_ptr(), O.data_ptr(), *map(_ptr, parts),
             int(bool(resume)), T, nseq, Hq, Hkv, D, dt,
-            _longs(*[s for t in (Q, K, V, O) for s in (t.stride(1), t.stride(0))]), workspace.data_ptr(),
+            _ARRAYS[8](*strides), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), sp)
     if st != 0:
         raise LAError(st, "la_prompt")
@@ -481,39 +481,45 @@ def la_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str =
 
 def _rotary(name, Q, K, freqs, positions, first_position, interleaved, magnitude, Q_out, K_out, stream):
     import torch
-    B, Hq, N, D = _shape(Q)
-    for t, like in ((K, None), (Q_out, Q), (K_out, K)):
-        if t is None:
-            continue
-        if t.dtype != Q.dtype or t.dim() != 4 or (t.shape[0], t.shape[2], t.shape[3]) != (B, N, D) or (
-                like is not None and t.shape != like.shape):
-            raise ValueError("Q, K and the outputs must be [B, H, N, D] tensors that share B, N, D and dtype")
-    if K is None and K_out is not None:
+    shape, dtype, Hk = Q.shape, Q.dtype, 0
+    if len(shape) != 4:
+        raise ValueError(f"expected a [B, H, N, D] tensor, got shape {tuple(shape)}")
+    B, Hq, N, D = shape
+    if K is not None:
+        ks = K.shape
+        if len(ks) != 4 or ks[0] != B or ks[2] != N or ks[3] != D or K.dtype != dtype:
+            raise ValueError("Q and K must be [B, H, N, D] tensors that share B, N, D and dtype")
+        Hk = ks[1]
+    elif K_out is not None:
         raise ValueError("K_out without K")
-    _row_contiguous(Q, K, Q_out, K_out)
-    dt = _dtype_code(Q)
-    stride = 0
+    for out, like in ((Q_out, Q), (K_out, K)):
+        if out is not None and (out.shape != like.shape or out.dtype != dtype):
+            raise ValueError("the outputs must share their inputs' shape and dtype")
+    dt, ps = _dtype_code(Q), 0
     if positions is not None:
-        if positions.dtype != torch.int32 or tuple(positions.shape) not in ((N,), (B, N)) or (
-                N > 1 and positions.stride(-1) != 1):
+        ext = positions.shape
+        if positions.dtype != torch.int32 or (ext != (B, N) and ext != (N,)) or (N > 1 and positions.stride(-1) != 1):
             raise ValueError(f"positions: expected int32 [N] or [B, N] with contiguous rows, got {positions.dtype} "
-                             f"{tuple(positions.shape)}")
+                             f"{tuple(ext)}")
         # a batch of one is stepped by nothing, whatever its stride
-        stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
-        if stride and stride < N:
+        ps = positions.stride(0) if len(ext) == 2 and B > 1 else 0
+        if ps and ps < N:
             raise ValueError("positions of the batch entries overlap")
+    sq = _rows(Q)
+    sk = _rows(K) if Hk else (0, 0, 0)
+    sqo = (Hq * N * D, N * D, D) if Q_out is None else _rows(Q_out)
+    sko = (Hk * N * D, N * D, D) if K_out is None else _rows(K_out)
     on, sp = _place(stream, Q, K, Q_out, K_out, positions)
     with on:
         if Q_out is None:
-            Q_out = torch.empty((B, Hq, N, D), dtype=Q.dtype, device=Q.device)
+            Q_out = torch.empty(shape, dtype=dtype, device=Q.device)
         if K is not None and K_out is None:
-            K_out = torch.empty(K.shape, dtype=K.dtype, device=K.device)
-        Hk = 0 if K is None else K.shape[1]
-        sk, sko = (K.stride()[:3], K_out.stride()[:3]) if Hk else ((0, 0, 0), (0, 0, 0))
+            K_out = torch.empty(ks, dtype=dtype, device=Q.device)
         st = getattr(load_library(), name)(
-            Q.data_ptr(), _ptr(K), Q_out.data_ptr(), _ptr(K_out), freqs.values, _ptr(positions), stride, first_position,
-            int(bool(interleaved)), magnitude, B, Hq, Hk, N, D, freqs.rotary_dim, dt,
-            _longs(*Q.stride()[:3], *sk, *Q_out.stride()[:3], *sko), sp)
+            Q.data_ptr(), K.data_ptr() if Hk else 0, Q_out.data_ptr(), K_out.data_ptr() if Hk else 0, freqs.values,
+            0 if positions is None else positions.data_ptr(), ps, first_position, 1 if interleaved else 0, magnitude, B, Hq,
+            Hk, N, D, freqs.rotary_dim, dt,
+            _ARRAYS[12](sq[0], sq[1], sq[2], sk[0], sk[1], sk[2], sqo[0], sqo[1], sqo[2], sko[0], sko[1], sko[2]), sp)
     if st != 0:
         raise LAError(st, name)
     return Q_out, K_out
@@ -545,12 +551,20 @@ def _gate_code(gate) -> int:
 
 
 def _scan_operands(dims, first, *others):
-    if first.dim() != dims:
-        raise ValueError(f"expected a {'[B, N, C]' if dims == 3 else '[B, C]'} tensor, got shape {tuple(first.shape)}")
+    """The operands' row strides ((batch, row) each); None, an output that the call makes, is contiguous."""
+    shape, dtype = first.shape, first.dtype
+    if len(shape) != dims:
+        raise ValueError(f"expected a {'[B, N, C]' if dims == 3 else '[B, C]'} tensor, got shape {tuple(shape)}")
+    strides = list(_rows(first)[:-1])
+    dense = (shape[1] * shape[2], shape[2]) if dims == 3 else (shape[1],)
     for t in others:
-        if t is not None and (t.shape != first.shape or t.dtype != first.dtype):
+        if t is None:
+            strides += dense
+            continue
+        if t.shape != shape or t.dtype != dtype:
             raise ValueError("the tensors must share shape and dtype")
-    _row_contiguous(first, *others)
+        strides += _rows(t)[:-1]
+    return strides
 
 
 def la_gated_scan(X, W, gate: str, h0=None, H=None, h_last=None, stream=None):
@@ -558,7 +572,7 @@ def la_gated_scan(X, W, gate: str, h0=None, H=None, h_last=None, stream=None):
     channel, with a = e^w, b = 1 (gate "log") or a = sigmoid(w), b = 1 - a (gate "sigmoid").  h0 and h_last are float32
     [B,C]: the value before the first row (None: 0) and after the last."""
     import torch
-    _scan_operands(3, X, W, H)
+    strides = _scan_operands(3, X, W, H)
     B, N, C = X.shape
     code, dt = _gate_code(gate), _dtype_code(X)
     for t, what in ((h0, "h0"), (h_last, "h_last")):
@@ -571,7 +585,7 @@ def la_gated_scan(X, W, gate: str, h0=None, H=None, h_last=None, stream=None):
         if h_last is None:
             h_last = torch.empty((B, C), dtype=torch.float32, device=X.device)
         st = load_library().la_gated_scan(X.data_ptr(), W.data_ptr(), _ptr(h0), H.data_ptr(), h_last.data_ptr(), B, N, C,
-                                          code, dt, _longs(*X.stride()[:2], *W.stride()[:2], *H.stride()[:2]),
+                                          code, dt, _ARRAYS[6](*strides),
                                           sp)
     if st != 0:
         raise LAError(st, "la_gated_scan")
@@ -582,7 +596,7 @@ def la_gated_scan_backward(X, W, H, dH, gate: str, h0=None, dh_last=None, dX=Non
     """dX, dW, dh0 = la_gated_scan_backward(X, W, H, dH, gate): gradients of sum(dH * H) + sum(dh_last * h_last), H and
     h0 as the forward had them."""
     import torch
-    _scan_operands(3, X, W, H, dH, dX, dW)
+    strides = _scan_operands(3, X, W, H, dH, dX, dW)
     B, N, C = X.shape
     code, dt = _gate_code(gate), _dtype_code(X)
     for t, what in ((h0, "h0"), (dh_last, "dh_last"), (dh0, "dh0")):
@@ -596,7 +610,7 @@ def la_gated_scan_backward(X, W, H, dH, gate: str, h0=None, dh_last=None, dX=Non
         st = load_library().la_gated_scan_backward(
             X.data_ptr(), W.data_ptr(), H.data_ptr(), dH.data_ptr(), _ptr(h0), _ptr(dh_last), dX.data_ptr(),
             dW.data_ptr(), dh0.data_ptr(), B, N, C, code, dt,
-            _longs(*[s for t in (X, W, H, dH, dX, dW) for s in t.stride()[:2]]), sp)
+            _ARRAYS[12](*strides), sp)
     if st != 0:
         raise LAError(st, "la_gated_scan_backward")
     return dX, dW, dh0
@@ -606,16 +620,16 @@ def la_gated_scan_step(state, x, w, gate: str, h=None, stream=None):
     """h = la_gated_scan_step(state, x, w, gate): one row of the recurrence for [B,C] tensors; ``state``, float32 [B,C],
     is advanced in place."""
     import torch
-    _scan_operands(2, x, w, h)
+    strides = _scan_operands(2, x, w, h)
     B, C = x.shape
     code, dt = _gate_code(gate), _dtype_code(x)
     _expect(state, (B, C), torch.float32, "state")
     on, sp = _place(stream, x, w, h, state)
     with on:
         if h is None:
-            h = torch.empty((B, C), dtype=x.dtype, device=x.device)
+            h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         st = load_library().la_gated_scan_step(x.data_ptr(), w.data_ptr(), h.data_ptr(), state.data_ptr(), B, C, code, dt,
-                                               _longs(x.stride(0), w.stride(0), h.stride(0)), sp)
+                                               _ARRAYS[3](*strides), sp)
     if st != 0:
         raise LAError(st, "la_gated_scan_step")
     return h
