@@ -18,13 +18,18 @@ namespace la {
 namespace prompt {
 
 // ----------------------------------------------------------------------------------------------------------------
-// CUDA-core form.  grid = (sequences x key/value heads, column blocks): a CTA walks one sequence 32 rows at a time
-// with E columns of S; the column blocks of a head are a cluster.  Warp w has rows w, w + 8, ... of a block, one lane per column (and per row j of W), so a
-// query head's rows stay within a warp.
+// CUDA-core form.  grid = (sequences x key/value heads, column blocks, parts): a cluster has one head of one sequence, its
+// CTAs E columns of S each and a part of the rows each, which they walk 32 rows at a time.  First every CTA sums its
+// part; the parts' sums are exchanged through distributed shared memory, and every CTA then walks its rows again, for O,
+// from the state of all before it.  In a block of rows warp w has rows w, w + 8, ..., one lane per column (and per row j
+// of W), so a query head's rows stay within a warp.
 //
 // fp32 tokens keep an fp64 state, as la_decode_step does, but this GPU has two fp64 multiply-adds per SM and clock;
 // a sum is therefore two floats here (the product's and the sum's rounding errors are exact in fp32 and gathered in
-// the low one), good to 2^-46, and becomes a double once, at the end.  O is formed in fp32 from the high floats.
+// the low one), good to 2^-46, and becomes a double once, at the end.  O is formed in fp32 from the high floats, so the
+// second walk sums in plain fp32.  1,500 tokens in 7 sequences, 8 query and 4 key/value heads of 64, fp32: 162 us (one walk
+// for both, one CTA to a sequence: 405 us).  What bounds it is the longest sequence: a block of rows after another, each
+// some fp32 instructions of 256 threads behind a barrier.
 // ----------------------------------------------------------------------------------------------------------------
 constexpr int kThreads = 256, kWarps = 8, kRows = 32;
 
@@ -71,138 +76,232 @@ template <> struct Sum<float> {
 template <typename T, int D> struct Tile {
     static constexpr int E = D < 32 ? D : 32;       // columns of S in a CTA
     static constexpr int LD = D + 4;                // row pitch of Q and K: 16-byte loads of 8 rows meet all banks
-    static constexpr int RE = 32 / E;               // rows a warp takes side by side (2 where E = 16)
-    static constexpr int NS = D * E / kThreads;     // elements of S of a thread
-    static constexpr size_t SMEM = sizeof(float) * (2 * kRows * LD + kRows * E + kRows * kRows + D * E + D + E);
+    static constexpr int RE = 32 / E;               // halves of a warp that share the sums of O (2 where E = 16)
+    static constexpr int NS = D * E / kThreads;     // elements of S of a thread: column t % E, rows from t / E * NS
+    static constexpr int PER = kRows / kWarps;      // rows of a block of a warp
+    static constexpr size_t FLOATS = 2 * kRows * LD + kRows * E + kRows * kRows + D * E + D + E;
+    static constexpr size_t SMEM = sizeof(float) * FLOATS + sizeof(Sum<T>) * (D * E + D + E);
 };
+
+// `rows` rows of 32 (the others zero) of W elements each, global -> shared floats, 16 bytes at a time.
+template <typename T, int W>
+__device__ __forceinline__ void load_rows(float *dst, int pitch, const T *src, long long stride, int rows, int first, int step) {
+    constexpr int V = 16 / (int)sizeof(T);
+    for (int x = first; x < kRows * W / V; x += step) {
+        const int j = x / (W / V), c = x % (W / V) * V;
+        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+        if (j < rows) raw = *(const uint4 *)(src + j * stride + c);
+        const T *e = (const T *)&raw;
+#pragma unroll
+        for (int k = 0; k < V; ++k) dst[j * pitch + c + k] = to_f(e[k]);
+    }
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_constant__ Args A) {
     using C = Tile<T, D>;
     using Acc = typename Sum<T>::Acc;
-    constexpr int E = C::E, LD = C::LD;
+    constexpr int E = C::E, LD = C::LD, NS = C::NS, PER = C::PER;
     extern __shared__ __align__(16) float sm[];
     float *Ks = sm, *Qs = Ks + kRows * LD, *Vs = Qs + kRows * LD, *Ws = Vs + kRows * E, *Sf = Ws + kRows * kRows;
     float *zs = Sf + D * E, *as = zs + D;
-    if (!offsets_in_order(A)) return;
+    Sum<T> *of_part = (Sum<T> *)(sm + C::FLOATS);  // the part's sums: S, z, a
+    if (!offsets_in_order(A)) return;               // the same for the whole grid
+    cg::cluster_group cluster = cg::this_cluster();
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int seq = blockIdx.x / A.Hkv, h = blockIdx.x % A.Hkv, e0 = blockIdx.y * E;
+    const int parts = gridDim.z, part = blockIdx.z;
     const long long at = (long long)seq * A.Hkv + h;
-    const int lo = A.off[seq], hi = A.off[seq + 1];
-    const T *K = (const T *)A.k + h * A.kh, *V = (const T *)A.v + h * A.vh + e0;
+    const int first = A.off[seq], len = A.off[seq + 1] - first;
+    const int share = ((len + kRows - 1) / kRows + parts - 1) / parts * kRows;  // rows of a part
+    const int lo = min(part * share, len), hi = min(lo + share, len);
+    const T *K = (const T *)A.k + h * A.kh + first * A.kn, *V = (const T *)A.v + h * A.vh + first * A.vn + e0;
     Acc *S = A.S ? (Acc *)A.S + at * D * D : nullptr, *z = (Acc *)A.z + at * D, *a = (Acc *)A.a + at * D;
     const bool resume = A.resume && S;
-    // this thread's elements of S: column t % E, rows t / E + m (256 / E); thread t < D has z[t], t < E has a[e0 + t]
-    const int e = t % E, d0 = t / E;
-    constexpr int DS = kThreads / E;
-    Sum<T> s[C::NS], zt, at_;
+    // this thread's elements of S: column t % E, rows d0 ...; thread t < D has z[t], t < E has a[e0 + t]
+    const int e = t % E, d0 = t / E * NS;
+    // ---- the part's sums
+    {
+        Sum<T> s[NS], zt, at_;
 #pragma unroll
-    for (int m = 0; m < C::NS; ++m) {
+        for (int m = 0; m < NS; ++m) s[m].set(0);
+        zt.set(0);
+        at_.set(0);
+        for (int row0 = lo; row0 < hi; row0 += kRows) {
+            const int live = min(kRows, hi - row0);
+            __syncthreads();
+            load_rows<T, D>(Ks, LD, K + (long long)row0 * A.kn, A.kn, live, t, kThreads);
+            load_rows<T, E>(Vs, E, V + (long long)row0 * A.vn, A.vn, live, t, kThreads);
+            __syncthreads();
+            // the block's own sums first: over a long sequence a sum then passes a rounding for every 32 rows
+            Sum<T> bs[NS], bz, ba;
+#pragma unroll
+            for (int m = 0; m < NS; ++m) bs[m].set(0);
+            bz.set(0);
+            ba.set(0);
+            for (int j = 0; j < live; ++j) {
+                const float v = Vs[j * E + e];
+                if constexpr (NS % 4 == 0) {
+#pragma unroll
+                    for (int m = 0; m < NS; m += 4) {
+                        const float4 k4 = *(const float4 *)(Ks + j * LD + d0 + m);
+                        bs[m].fma(k4.x, v), bs[m + 1].fma(k4.y, v), bs[m + 2].fma(k4.z, v), bs[m + 3].fma(k4.w, v);
+                    }
+                } else {
+#pragma unroll
+                    for (int m = 0; m < NS; ++m) bs[m].fma(Ks[j * LD + d0 + m], v);
+                }
+                if (t < D) bz.add(Ks[j * LD + t]);
+                if (t < E) ba.add(Vs[j * E + t]);
+            }
+#pragma unroll
+            for (int m = 0; m < NS; ++m) s[m].join(bs[m]);
+            zt.join(bz);
+            at_.join(ba);
+        }
+#pragma unroll
+        for (int m = 0; m < NS; ++m) of_part[(d0 + m) * E + e] = s[m];
+        if (t < D) of_part[D * E + t] = zt;
+        if (t < E) of_part[D * E + D + t] = at_;
+    }
+    // ---- the state before the part, and behind the last one
+    Sum<T> s[NS], zt, at_;
+#pragma unroll
+    for (int m = 0; m < NS; ++m) {
         s[m].set(0);
-        if (resume) s[m].set(S[(long long)(d0 + m * DS) * D + e0 + e]);
-        Sf[(d0 + m * DS) * E + e] = s[m].hi;
+        if (resume) s[m].set(S[(long long)(d0 + m) * D + e0 + e]);
     }
     zt.set(0);
     at_.set(0);
-    if (t < D) {
-        if (resume) zt.set(z[t]);
-        zs[t] = zt.hi;
-    }
-    if (t < E) {
-        if (resume) at_.set(a[e0 + t]);
-        as[t] = at_.hi;
-    }
+    if (resume && t < D) zt.set(z[t]);
+    if (resume && t < E) at_.set(a[e0 + t]);
     const int n0 = resume ? A.n[at] : 0;
-    if (gridDim.y > 1) cg::this_cluster().sync();  // the column blocks share z and n: all have read them
+    cluster.sync();  // every part's sums are there, and all have read the state
+    for (int p = 0; p <= parts; ++p) {
+        if (p == part) {
+#pragma unroll
+            for (int m = 0; m < NS; ++m) Sf[(d0 + m) * E + e] = s[m].hi;
+            if (t < D) zs[t] = zt.hi;
+            if (t < E) as[t] = at_.hi;
+            if (part != 0 || !S) break;  // the first part's CTAs write the state
+        }
+        if (p == parts) break;
+        const Sum<T> *other = cluster.map_shared_rank(of_part, p * gridDim.y + blockIdx.y);
+#pragma unroll
+        for (int m = 0; m < NS; ++m) s[m].join(other[(d0 + m) * E + e]);
+        if (t < D) zt.join(other[D * E + t]);
+        if (t < E) at_.join(other[D * E + D + t]);
+    }
+    if (part == 0 && S) {
+#pragma unroll
+        for (int m = 0; m < NS; ++m) S[(long long)(d0 + m) * D + e0 + e] = s[m].get();
+        if (t < E) a[e0 + t] = at_.get();
+        if (blockIdx.y == 0) {
+            if (t < D) z[t] = zt.get();
+            if (t == 0) A.n[at] = n0 + len;
+        }
+    }
+    // ---- O
     for (int row0 = lo; row0 < hi; row0 += kRows) {
         const int live = min(kRows, hi - row0);
         __syncthreads();  // the block before is done with K and V, and S, z, a are those after it
-        for (int x = t; x < kRows * D; x += kThreads) {
-            const int j = x / D, d = x % D;
-            Ks[j * LD + d] = j < live ? to_f(K[(long long)(row0 + j) * A.kn + d]) : 0.f;
-        }
-        for (int x = t; x < kRows * E; x += kThreads) {
-            const int j = x / E, c = x % E;
-            Vs[x] = j < live ? to_f(V[(long long)(row0 + j) * A.vn + c]) : 0.f;
-        }
+        load_rows<T, D>(Ks, LD, K + (long long)row0 * A.kn, A.kn, live, t, kThreads);
+        load_rows<T, E>(Vs, E, V + (long long)row0 * A.vn, A.vn, live, t, kThreads);
         __syncthreads();
-        const float nb = (float)(n0 + (row0 - lo));
+        const float nb = (float)(n0 + row0);
         for (int g = 0; g < A.r; ++g) {
             const int hq = h * A.r + g;
-            const T *Q = (const T *)A.q + hq * A.qh;
-            T *O = (T *)A.o + hq * A.oh + e0;
+            const T *Q = (const T *)A.q + hq * A.qh + (first + (long long)row0) * A.qn;
+            T *O = (T *)A.o + hq * A.oh + (first + (long long)row0) * A.on + e0;
             __syncwarp();
-            for (int m = 0; m < kRows / kWarps; ++m) {
-                const int i = warp + kWarps * m;
-                for (int d = lane; d < D; d += 32)
-                    Qs[i * LD + d] = i < live ? to_f(Q[(long long)(row0 + i) * A.qn + d]) : 0.f;
+            // the warp's rows warp, warp + 8, ... stand one behind another in Qs
+            float *Qw = Qs + warp * PER * LD;
+            {
+                constexpr int VW = 16 / (int)sizeof(T);
+                for (int x = lane; x < PER * D / VW; x += 32) {
+                    const int m = x / (D / VW), c = x % (D / VW) * VW, i = warp + kWarps * m;
+                    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                    if (i < live) raw = *(const uint4 *)(Q + i * A.qn + c);
+                    const T *el = (const T *)&raw;
+#pragma unroll
+                    for (int k = 0; k < VW; ++k) Qw[m * LD + c + k] = to_f(el[k]);
+                }
             }
             __syncwarp();
             // W and g: lane j of row i
-            float gi[kRows / kWarps];
+            float w[PER], gi[PER];
 #pragma unroll
-            for (int m = 0; m < kRows / kWarps; ++m) {
-                const int i = warp + kWarps * m;
-                float w = 1.f, qz = 0.f;
+            for (int m = 0; m < PER; ++m) w[m] = 1.f, gi[m] = 0.f;
 #pragma unroll 4
-                for (int d = 0; d < D; d += 4) {
-                    const float4 q4 = *(const float4 *)(Qs + i * LD + d), k4 = *(const float4 *)(Ks + lane * LD + d);
-                    w = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, w))));
-                }
-                for (int d = lane; d < D; d += 32) qz = fmaf(Qs[i * LD + d], zs[d], qz);
-                w = lane <= i ? w : 0.f;
-                Ws[i * kRows + lane] = w;
-                float sum = w + qz;
+            for (int d = 0; d < D; d += 4) {
+                const float4 k4 = *(const float4 *)(Ks + lane * LD + d);
 #pragma unroll
-                for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-                gi[m] = nb + sum;
+                for (int m = 0; m < PER; ++m) {
+                    const float4 q4 = *(const float4 *)(Qw + m * LD + d);
+                    w[m] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, w[m]))));
+                }
+            }
+            for (int d = lane; d < D; d += 32) {
+                const float zd = zs[d];
+#pragma unroll
+                for (int m = 0; m < PER; ++m) gi[m] = fmaf(Qw[m * LD + d], zd, gi[m]);
+            }
+#pragma unroll
+            for (int m = 0; m < PER; ++m) {
+                w[m] = lane <= warp + kWarps * m ? w[m] : 0.f;
+                Ws[(warp * PER + m) * kRows + lane] = w[m];
+                gi[m] += w[m];
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1) gi[m] += __shfl_xor_sync(0xffffffffu, gi[m], x);
             }
             __syncwarp();
+            const int c = lane % E, half = lane / E;  // E = 16: the two half warps take half of the sums each
+            float o[PER];
 #pragma unroll
-            for (int m0 = 0; m0 < kRows / kWarps; ++m0) {
-                const int i = warp + kWarps * m0;
-                const int c = lane % E;
-                const int part = lane / E;  // E = 16: the two half warps take half of the sums each
-                float o = part ? 0.f : as[c];
-#pragma unroll 8
-                for (int d = part * (D / C::RE); d < (part + 1) * (D / C::RE); ++d)
-                    o = fmaf(Qs[i * LD + d], Sf[d * E + c], o);
-                for (int j = part; j <= i; j += C::RE) o = fmaf(Ws[i * kRows + j], Vs[j * E + c], o);
-                if (C::RE == 2) o += __shfl_xor_sync(0xffffffffu, o, 16);
-                if (i < live && part == 0) put(O + (long long)(row0 + i) * A.on + c, o / gi[m0]);
+            for (int m = 0; m < PER; ++m) o[m] = half ? 0.f : as[c];
+#pragma unroll 4
+            for (int d = half * (D / C::RE); d < (half + 1) * (D / C::RE); d += 4) {
+                const float s0 = Sf[d * E + c], s1 = Sf[(d + 1) * E + c], s2 = Sf[(d + 2) * E + c], s3 = Sf[(d + 3) * E + c];
+#pragma unroll
+                for (int m = 0; m < PER; ++m) {
+                    const float4 q4 = *(const float4 *)(Qw + m * LD + d);
+                    o[m] = fmaf(q4.x, s0, fmaf(q4.y, s1, fmaf(q4.z, s2, fmaf(q4.w, s3, o[m]))));
+                }
+            }
+#pragma unroll 4
+            for (int j = half * 4; j < kRows; j += 4 * C::RE) {
+                const float v0 = Vs[j * E + c], v1 = Vs[(j + 1) * E + c], v2 = Vs[(j + 2) * E + c], v3 = Vs[(j + 3) * E + c];
+#pragma unroll
+                for (int m = 0; m < PER; ++m) {
+                    const float4 w4 = *(const float4 *)(Ws + (warp * PER + m) * kRows + j);
+                    o[m] = fmaf(w4.x, v0, fmaf(w4.y, v1, fmaf(w4.z, v2, fmaf(w4.w, v3, o[m]))));
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < PER; ++m) {
+                const int i = warp + kWarps * m;
+                if (C::RE == 2) o[m] += __shfl_xor_sync(0xffffffffu, o[m], 16);
+                if (i < live && half == 0) put(O + (long long)i * A.on + c, o[m] / (nb + gi[m]));
             }
         }
+        if (row0 + kRows >= hi) break;
         __syncthreads();  // every warp has read S, z and a of before
-        // the block's own sums first: over a long sequence a sum then passes a rounding for every 32 rows, not for each
-        Sum<T> bs[C::NS], bz, ba;
+        float bs[NS], bz = 0.f, ba = 0.f;
 #pragma unroll
-        for (int m = 0; m < C::NS; ++m) bs[m].set(0);
-        bz.set(0);
-        ba.set(0);
+        for (int m = 0; m < NS; ++m) bs[m] = 0.f;
         for (int j = 0; j < live; ++j) {
             const float v = Vs[j * E + e];
 #pragma unroll
-            for (int m = 0; m < C::NS; ++m) bs[m].fma(Ks[j * LD + d0 + m * DS], v);
-            if (t < D) bz.add(Ks[j * LD + t]);
-            if (t < E) ba.add(Vs[j * E + t]);
+            for (int m = 0; m < NS; ++m) bs[m] = fmaf(Ks[j * LD + d0 + m], v, bs[m]);
+            if (t < D) bz += Ks[j * LD + t];
+            if (t < E) ba += Vs[j * E + t];
         }
 #pragma unroll
-        for (int m = 0; m < C::NS; ++m) s[m].join(bs[m]);
-        zt.join(bz);
-        at_.join(ba);
-#pragma unroll
-        for (int m = 0; m < C::NS; ++m) Sf[(d0 + m * DS) * E + e] = s[m].hi;
-        if (t < D) zs[t] = zt.hi;
-        if (t < E) as[t] = at_.hi;
+        for (int m = 0; m < NS; ++m) Sf[(d0 + m) * E + e] += bs[m];
+        if (t < D) zs[t] += bz;
+        if (t < E) as[t] += ba;
     }
-    if (!S) return;
-#pragma unroll
-    for (int m = 0; m < C::NS; ++m) S[(long long)(d0 + m * DS) * D + e0 + e] = s[m].get();
-    if (t < E) a[e0 + t] = at_.get();
-    if (blockIdx.y == 0) {
-        if (t < D) z[t] = zt.get();
-        if (t == 0) A.n[at] = n0 + (hi - lo);
-    }
+    cluster.sync();  // no CTA leaves while another may still read its sums
 }
 
 template <typename T, int D> cudaError_t launch_simt(const Args &A, cudaStream_t s) {
@@ -210,19 +309,27 @@ template <typename T, int D> cudaError_t launch_simt(const Args &A, cudaStream_t
     static std::atomic<int> attr_state[kMaxDevices];
     if (!once_per_device(attr_state, [] {
             return cudaFuncSetAttribute(prompt_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (int)C::SMEM) == cudaSuccess;
+                                        (int)C::SMEM) == cudaSuccess &&
+                   cudaFuncSetAttribute(prompt_simt_kernel<T, D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                       cudaSuccess;
         }))
         return cudaErrorInvalidValue;
+    // Parts: up to what a cluster holds, while that does not make more than three CTAs for each SM and leaves sequences
+    // of the mean length two blocks of rows in a part.
+    constexpr int cols = D / C::E;
+    const long long heads = (long long)A.nseq * A.Hkv;
+    int parts = 1;
+    while (2 * parts * cols <= 16 && 2 * parts * cols * heads <= 456 && (long long)A.T >= 4LL * parts * kRows * A.nseq) parts *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)A.nseq * A.Hkv), D / C::E);
+    cfg.gridDim = dim3((unsigned)heads, cols, parts);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 1;
-    attr[0].val.clusterDim.y = D / C::E;
-    attr[0].val.clusterDim.z = 1;
+    attr[0].val.clusterDim.y = cols;
+    attr[0].val.clusterDim.z = parts;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, prompt_simt_kernel<T, D>, A);
