@@ -71,25 +71,25 @@ inline bool steps_meet(long long delta, const long long *st, const long long *lo
 inline bool views_meet(const View &a, const View &b) {
     if (!ranges_meet(a.p, view_bytes(a), b.p, view_bytes(b))) return false;
     if (a.elem != b.elem || a.width != b.width) return true;
-    // the stride of a dimension that only one of them steps is that one's
-    long long st[3], lo[3], hi[3];
+    // the stride of a dimension that only one of them steps is that one's; of one that neither does, 0
+    long long st[3] = {}, lo[3] = {}, hi[3] = {};
     int n = 0;
     for (int k = 0; k < 3; ++k) {
         if (a.ext[k] == 1 && b.ext[k] == 1) continue;
         if (a.ext[k] > 1 && b.ext[k] > 1 && a.st[k] != b.st[k]) return true;
-        st[n] = a.ext[k] > 1 ? a.st[k] : b.st[k];
-        lo[n] = -(b.ext[k] - 1);
-        hi[n] = a.ext[k] - 1;
+        st[k] = a.ext[k] > 1 ? a.st[k] : b.st[k];
+        lo[k] = -(b.ext[k] - 1);
+        hi[k] = a.ext[k] - 1;
         ++n;
     }
-    for (int x = 0; x + 1 < n && n <= 3; ++x)  // by decreasing stride
-        for (int y = x + 1; y < n; ++y)
-            if (st[y] > st[x]) {
-                long long t;
-                t = st[x], st[x] = st[y], st[y] = t;
-                t = lo[x], lo[x] = lo[y], lo[y] = t;
-                t = hi[x], hi[x] = hi[y], hi[y] = t;
-            }
+    auto order = [&](int x, int y) {
+        if (st[y] <= st[x]) return;
+        long long t;
+        t = st[x], st[x] = st[y], st[y] = t;
+        t = lo[x], lo[x] = lo[y], lo[y] = t;
+        t = hi[x], hi[x] = hi[y], hi[y] = t;
+    };
+    order(0, 1), order(1, 2), order(0, 1);  // by decreasing stride
     for (int x = 0; x < n; ++x) {  // the two together have to nest for the search below; else refuse
         long long inner = a.width;
         if (x + 1 < n) inner = st[x + 1] * ((hi[x + 1] > -lo[x + 1] ? hi[x + 1] : -lo[x + 1]) + 1);
