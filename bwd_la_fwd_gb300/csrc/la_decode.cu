@@ -313,23 +313,30 @@ struct GroupedArgs {
 
 // One token for r query heads of each state.  As decode_step_kernel, with R CTAs to a head (ROWS = D / R rows of S
 // each); the slab stays in shared memory while QB query heads at a time are multiplied with it, the first QB in the
-// pass that also updates it, and its bulk store runs beside the other passes.
-template <typename T, typename Acc, int D, int R>
+// pass that also updates it, and its bulk store runs beside the other passes.  Bound by the state's way in and out: 2,048
+// bf16 heads of 128, r = 4, take 52 us (5.2 TB/s), of which a launch is some 8; 4,096 heads take 40 us more than 2,048.
+template <typename T, typename Acc, int D, int R, int QB>
 __global__ void __launch_bounds__(kThreads) decode_grouped_kernel(const __grid_constant__ GroupedArgs P) {
-    constexpr int QB = 2;
+    // q and k in shared memory: as they are, but for the fp64 state, where a conversion costs as much as a multiply-add
+    using Tok = typename std::conditional<sizeof(Acc) == 8, Acc, T>::type;
+    struct alignas(sizeof(Tok) * QB < 16 ? sizeof(Tok) * QB : 16) Group {
+        Tok x[QB];
+    };
+    auto as_acc = [](Tok x) { return (Acc)x; };
+    constexpr int RB = QB < 2 ? QB : 2;   // query heads whose sums are joined at a time
     constexpr int ROWS = D / R, VEC = 16 / (int)sizeof(Acc), CG = D / VEC;
     constexpr int RG = kThreads / CG < ROWS ? kThreads / CG : ROWS, RR = ROWS / RG;
     constexpr uint32_t BYTES = (uint32_t)(ROWS * D * sizeof(Acc));
     static_assert(ROWS * R == D && RR * RG == ROWS, "grouped decode split");
     extern __shared__ __align__(128) unsigned char slab_raw[];
-    // Kept small, so that three CTAs with a 64 KB slab fit on an SM: 4.8 TB/s over 2,048 heads of 128, two 4.3 TB/s.
+    // Kept small, so that three CTAs with a 64 KB slab fit on an SM: with two, 2,048 heads of 128 moved 4.3 TB/s.
     Acc *slab = (Acc *)slab_raw;          // ROWS x D
     Acc *gs = slab + ROWS * D;            // g of each query head
-    T *qs = (T *)(gs + (P.r + 3) / 4 * 4);  // r x D
-    __shared__ T ks[D];
+    Tok *qs = (Tok *)(gs + (P.r + 3) / 4 * 4);  // r / QB groups x D x QB, the last group filled up with zeros
+    __shared__ Tok ks[D];
     __shared__ Acc an[D];                 // a with v added
-    __shared__ Acc red[QB][RG][D];
-    __shared__ Acc part[R > 1 ? QB : 1][R > 1 ? D : 1];
+    __shared__ Acc red[RB][RG][D];
+    __shared__ Acc part[R > 1 ? RB : 1][R > 1 ? D : 1];
     __shared__ uint64_t bar;
     __shared__ int landed;
     cg::cluster_group cluster = cg::this_cluster();
@@ -350,10 +357,13 @@ __global__ void __launch_bounds__(kThreads) decode_grouped_kernel(const __grid_c
         sm100::bulk_load(slab, rows, BYTES, &bar);
     }
     // while the slab is on its way: q, k, a and z of after the token, and every g
-    for (int x = t; x < P.r * D; x += kThreads) qs[x] = q[(x / D) * P.qs.h + x % D];
+    for (int x = t; x < (P.r + QB - 1) / QB * QB * D; x += kThreads) {
+        const int g = x / D, d = x % D;
+        qs[(g / QB * D + d) * QB + g % QB] = g < P.r ? Tok(q[g * P.qs.h + d]) : Tok(0.f);
+    }
     Acc zn[(D + kThreads - 1) / kThreads];
     for (int x = t, m = 0; x < D; x += kThreads, ++m) {
-        ks[x] = k[x];
+        ks[x] = Tok(k[x]);
         an[x] = a[x] + load_acc<Acc>(v + x);
         zn[m] = z[x] + load_acc<Acc>(k + x);
         red[0][0][x] = zn[m];  // z for the sums below; the passes write red behind a barrier
@@ -362,7 +372,7 @@ __global__ void __launch_bounds__(kThreads) decode_grouped_kernel(const __grid_c
     __syncthreads();
     for (int g = warp; g < P.r; g += kThreads / 32) {
         Acc dz = 0;
-        for (int x = lane; x < D; x += 32) dz += load_acc<Acc>(qs + g * D + x) * red[0][0][x];
+        for (int x = lane; x < D; x += 32) dz += as_acc(qs[(g / QB * D + x) * QB + g % QB]) * red[0][0][x];
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) dz += __shfl_xor_sync(0xffffffffu, dz, off);
         if (lane == 0) gs[g] = (Acc)nn + dz;
@@ -388,10 +398,9 @@ __global__ void __launch_bounds__(kThreads) decode_grouped_kernel(const __grid_c
 #pragma unroll
     for (int j = 0; j < VEC; ++j) ve[j] = load_acc<Acc>(v + col * VEC + j);
     for (int g0 = 0; g0 < P.r; g0 += QB) {
-        const int nq = P.r - g0 < QB ? P.r - g0 : QB;
+        Acc acc[QB][VEC] = {};
         if (ok && p < RG) {
-            Acc acc[QB][VEC] = {};
-            const T *q0 = qs + g0 * D + rank * ROWS, *q1 = nq > 1 ? q0 + D : q0;
+            const Group *qg = (const Group *)(qs + (g0 * D + rank * ROWS * QB));
 #pragma unroll 4
             for (int m = 0; m < RR; ++m) {
                 const int row = p + RG * m;
@@ -399,52 +408,58 @@ __global__ void __launch_bounds__(kThreads) decode_grouped_kernel(const __grid_c
                 uint4 raw = *cell;
                 Acc *sv = (Acc *)&raw;
                 if (g0 == 0) {
-                    const Acc kd = load_acc<Acc>(ks + rank * ROWS + row);
+                    const Acc kd = as_acc(ks[rank * ROWS + row]);
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) sv[j] += kd * ve[j];
                     *cell = raw;
                 }
-                const Acc x0 = load_acc<Acc>(q0 + row), x1 = load_acc<Acc>(q1 + row);
+                const Group x = qg[row];
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    acc[0][j] += sv[j] * x0;
-                    acc[1][j] += sv[j] * x1;
+                for (int g = 0; g < QB; ++g) {
+                    const Acc xd = as_acc(x.x[g]);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) acc[g][j] += sv[j] * xd;
                 }
-            }
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                red[0][p][col * VEC + j] = acc[0][j];
-                red[1][p][col * VEC + j] = acc[1][j];
             }
         }
         if (g0 == 0) sm100::fence_proxy_async_smem();  // the slab's new values, before the bulk store reads them
-        __syncthreads();
-        if (g0 == 0 && ok && t == 0) {
-            sm100::bulk_store(rows, slab, BYTES);
-            sm100::bulk_commit();
-        }
-        for (int x = t; x < nq * D; x += kThreads) {
-            const int g = x / D, e = x % D;
-            Acc sum = 0;
 #pragma unroll
-            for (int m = 0; m < RG; ++m) sum += red[g][m][e];
-            if constexpr (R > 1) part[g][e] = sum;
-            else
-                o[(g0 + g) * P.os.h + e] = ok ? store_as<T, Acc>((an[e] + sum) / gs[g0 + g]) : store_as<T, Acc>((Acc)NAN);
-        }
-        if constexpr (R > 1) {
-            cluster.sync();  // every CTA's partial sums are in its shared memory
-            // each CTA finishes its share of the columns
-            for (int x = t; x < nq * ROWS; x += kThreads) {
-                const int g = x / ROWS, e = rank * ROWS + x % ROWS;
-                Acc tot = an[e];
+        for (int q0 = 0; q0 < QB; q0 += RB) {
+            const int gb = g0 + q0, nq = P.r - gb < RB ? P.r - gb : RB;
+            if (p < RG) {
 #pragma unroll
-                for (int y = 0; y < R; ++y) tot += *cluster.map_shared_rank(&part[g][e], y);
-                o[(g0 + g) * P.os.h + e] = ok ? store_as<T, Acc>(tot / gs[g0 + g]) : store_as<T, Acc>((Acc)NAN);
+                for (int g = 0; g < RB; ++g)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) red[g][p][col * VEC + j] = acc[q0 + g][j];
             }
-            cluster.sync();  // all have read the partial sums
-        } else {
             __syncthreads();
+            if (gb == 0 && ok && t == 0) {
+                sm100::bulk_store(rows, slab, BYTES);
+                sm100::bulk_commit();
+            }
+            for (int x = t; x < nq * D; x += kThreads) {
+                const int g = x / D, e = x % D;
+                Acc sum = 0;
+#pragma unroll
+                for (int m = 0; m < RG; ++m) sum += red[g][m][e];
+                if constexpr (R > 1) part[g][e] = sum;
+                else
+                    o[(gb + g) * P.os.h + e] = ok ? store_as<T, Acc>((an[e] + sum) / gs[gb + g]) : store_as<T, Acc>((Acc)NAN);
+            }
+            if constexpr (R > 1) {
+                cluster.sync();  // every CTA's partial sums are in its shared memory
+                // each CTA finishes its share of the columns
+                for (int x = t; x < nq * ROWS; x += kThreads) {
+                    const int g = x / ROWS, e = rank * ROWS + x % ROWS;
+                    Acc tot = an[e];
+#pragma unroll
+                    for (int y = 0; y < R; ++y) tot += *cluster.map_shared_rank(&part[g][e], y);
+                    o[(gb + g) * P.os.h + e] = ok ? store_as<T, Acc>(tot / gs[gb + g]) : store_as<T, Acc>((Acc)NAN);
+                }
+                cluster.sync();  // all have read the partial sums
+            } else {
+                __syncthreads();
+            }
         }
     }
     if (P.g && rank == 0)
@@ -455,18 +470,18 @@ __global__ void __launch_bounds__(kThreads) decode_grouped_kernel(const __grid_c
     }
 }
 
-template <typename T, typename Acc, int D, int R> cudaError_t launch_grouped(const GroupedArgs &P, long long BH, cudaStream_t s) {
-    constexpr int kSlabBytes = D / R * D * (int)sizeof(Acc), kPerHead = (int)sizeof(Acc) + D * (int)sizeof(T);
+template <typename T, typename Acc, int D, int R, int QB> cudaError_t launch_grouped(const GroupedArgs &P, long long BH, cudaStream_t s) {
+    constexpr int kSlabBytes = D / R * D * (int)sizeof(Acc), kTok = sizeof(Acc) == 8 ? 8 : (int)sizeof(T);
     static std::atomic<int> attr_state[kMaxDevices];
     if (!once_per_device(attr_state, [] {
-            return cudaFuncSetAttribute(decode_grouped_kernel<T, Acc, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kSlabBytes + 64 * kPerHead) == cudaSuccess;
+            return cudaFuncSetAttribute(decode_grouped_kernel<T, Acc, D, R, QB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        kSlabBytes + 64 * ((int)sizeof(Acc) + D * kTok)) == cudaSuccess;
         }))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(BH * R));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)kSlabBytes + (P.r + 3) / 4 * 4 * sizeof(Acc) + (size_t)P.r * D * sizeof(T);
+    cfg.dynamicSmemBytes = (size_t)kSlabBytes + (P.r + 3) / 4 * 4 * sizeof(Acc) + (size_t)(P.r + QB - 1) / QB * QB * D * kTok;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -475,7 +490,15 @@ template <typename T, typename Acc, int D, int R> cudaError_t launch_grouped(con
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_grouped_kernel<T, Acc, D, R>, P);
+    return cudaLaunchKernelEx(&cfg, decode_grouped_kernel<T, Acc, D, R, QB>, P);
+}
+
+// Query heads in a pass over the slab: four where they divide r (2,048 states of 128 x 128, r = 4: 52 us, in
+// pairs 58), else two; one where r is one, since an fp64 state's passes are bound by its multiply-adds.
+template <typename T, typename Acc, int D, int R> cudaError_t grouped_pass(const GroupedArgs &P, long long BH, cudaStream_t s) {
+    if (P.r % 4 == 0) return launch_grouped<T, Acc, D, R, 4>(P, BH, s);
+    if (P.r == 1) return launch_grouped<T, Acc, D, R, 1>(P, BH, s);
+    return launch_grouped<T, Acc, D, R, 2>(P, BH, s);
 }
 
 // CTAs of a head: as few as its slabs need, or eight while all heads' CTAs then still fit on the GPU at once, where a
@@ -483,8 +506,8 @@ template <typename T, typename Acc, int D, int R> cudaError_t launch_grouped(con
 template <typename T, typename Acc, int D> cudaError_t grouped_split(const GroupedArgs &P, long long BH, cudaStream_t s) {
     constexpr int R = DecSplit<Acc, D>::R;
     if constexpr (D >= 64 && R < 8)
-        if (BH * 8 <= 304) return launch_grouped<T, Acc, D, 8>(P, BH, s);
-    return launch_grouped<T, Acc, D, R>(P, BH, s);
+        if (BH * 8 <= 304) return grouped_pass<T, Acc, D, 8>(P, BH, s);
+    return grouped_pass<T, Acc, D, R>(P, BH, s);
 }
 
 template <typename T, typename Acc> cudaError_t grouped_by_d(int D, const GroupedArgs &P, long long BH, cudaStream_t s) {
