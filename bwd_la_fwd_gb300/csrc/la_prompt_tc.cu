@@ -411,22 +411,25 @@ template <int NB> __global__ void __launch_bounds__(256) carry_kernel(const __gr
 // ----------------------------------------------------------------------------------------------------------------
 // The walk.  A unit u is one query head of one chunk.  Warp 0 loads K and V, warp 2 loads Q, warp 1 issues MMAs; the
 // epilogue is two groups of eight warps (two per TMEM lane quarter, each half of the columns):
-//   A(u)  T -> P (TMEM), row sums        B(u)  O -> out, and after a chunk's last unit  C  S, Sb, z, a
-// A works on u + 1 while B writes u and the tensor cores form Q S of u + 1.  O is staged in the tile its Q came in and
-// leaves by TMA.
-// K and V have one tile each: K is free behind the last T and K^T V (formed while the last A works), V behind the last
-// P V, and each has about a unit's time to be filled again; four Q tiles, because one is held from its load to its O's
-// store, some 2 units and a load's latency.  (With two K, V tiles and three Q tiles every unit waited for its Q.)
-// An MMA of 128 x 128 x 16 reads 8 KB of shared memory, 64 clocks: T, Q S and P V take 1.5 k, the N = 16 products
-// (q . z; K^T 1 and V^T 1 once a chunk) 0.4 k of the 3.4 k clocks that a unit's bytes take (D = 128, r = 4).  CUDA cores
-// did those sums in twice the epilogue's time.
+//   A(u)  T -> P (TMEM), row sums; after a chunk's last unit  C  S, Sb, z, a        B(u)  O -> out
+// The tensor cores form Q S of u + 1 and A works on u + 1 while B writes u: O has two buffers, and K^T V is formed in
+// the one that the next unit will take.  O is staged in the tile its Q came in and leaves by TMA.
+// K and V have one tile each: K is free behind the last T and K^T V, V behind the last P V; four Q tiles, because one is
+// held from its load to its O's store, some 2 units and a load's latency.  (With two K, V tiles and three Q tiles every
+// unit waited for its Q.)
+// What bounds it are the MMAs of a CTA, one behind another: T 0.7 k clocks, Q S and P V 0.7 k each (8 of 128 x 128 x 16,
+// 64 clocks of shared memory each at best), once a chunk K^T V with the sums of K and V 1.7 k; HBM would take 3.4 k for a
+// unit's bytes (D = 128, r = 4).  An N = 16 MMA takes more than an N = 128 one: z stands behind K's rows, so that T
+// brings q . z along (N = 144), and only a chunk's first unit, whose T is formed before the chunk's z is known, has
+// products of its own for it.  (Such products in each unit: 204 us where this takes 191.)  The sums of K and V on the
+// CUDA cores took twice the epilogue's time.
 // Two things cost the epilogue more than its arithmetic: code that does not come round again within a unit (the warps
 // then wait for instructions), hence loops that are not unrolled and one group per step; and spilled registers, which
 // with this much shared memory are L2 accesses, hence 32-bit shared addresses and registers split by role.
 // P's low part: with n rows before the chunk, P's rounding enters a row's O as sqrt(rows / n) of the output's own, so it
-// is kept for a sequence's first kLowChunks chunks, beyond which it adds less than a tenth to the output's rounding.
-// TMEM columns: T 0, P 128, O 192, K^T V 320, z and a sums 448, 464, q . z 480.  P's low parts share the columns of
-// K^T V, which in those chunks is formed behind the last P V, and A waits for C before the next chunk's.
+// is kept for a sequence's first kLowChunks chunks, beyond which it adds less than a tenth to the output's rounding.  It
+// stands in the columns of the T it comes from.
+// TMEM columns: O 0 and 128 (K^T V), T 256, its q . z 384, P 400, sums of K and V 464 and 480, a first unit's q . z 496.
 // ----------------------------------------------------------------------------------------------------------------
 
 // Shared memory by 32-bit address.
@@ -506,9 +509,16 @@ __device__ __forceinline__ void wait_briefly(uint32_t bar, uint32_t parity) {
     }
 }
 
+// As sdesc_sw128, at `off` bytes behind 16-byte unit s4 of shared memory: one addition.
+__device__ __forceinline__ uint64_t desc_at(uint32_t s4, uint32_t off, uint32_t lbo, uint32_t sbo) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(s4 + (off >> 4) + (lbo >> 4 << 16)), "r"((sbo >> 4) | 1u << 14 | 2u << 29));
+    return d;
+}
+
 constexpr int kThreads = 640;
-// Registers: 640 threads start with 96 each; B, which holds S, takes what the others leave.
-constexpr int kRegsFew = 64, kRegsA = 72, kRegsB = 128;
+// Registers: 640 threads start with 96 each; A, which holds S, takes what the others leave.
+constexpr int kRegsFew = 72, kRegsA = 128, kRegsB = 72;
 static_assert(128 * kRegsFew + 256 * kRegsA + 256 * kRegsB <= 640 * 96, "more registers than the block is launched with");
 constexpr int kLowChunks = 4;
 
@@ -516,18 +526,19 @@ constexpr int kLowChunks = 4;
 template <int NB> struct Walk {
     static constexpr uint32_t TILE = kTileB<NB>;
     static constexpr int NQ = NB == 2 ? 4 : 6;      // Q tiles
-    static constexpr uint32_t K = 0, V = TILE, Q = 2 * TILE;
+    // K's boxes, each followed by 8 rows of 128 bytes: rows z (two bf16 parts) and ones.  As rows 128 and 129 of K they
+    // give T two columns of q . z; by themselves they are an N = 16 operand.  The products with the other rows are not
+    // used, so rows 3-6 hold a (first box) and the first half's row sums (second box).
+    static constexpr uint32_t KBOX = NB == 2 ? kBox + 1024 : kBox, ZT = kBox, ZBOX = NB == 2 ? KBOX : 1024;
+    static constexpr uint32_t K = 0, V = TILE + 2048, Q = V + TILE;
     static constexpr uint32_t SB = Q + NQ * TILE;   // bf16 S, [d][e]
-    // N = 16 operand, two boxes of 8 rows of 128 bytes: rows z (two bf16 parts) and ones; the products with the other
-    // rows are not used, so rows 3-6 hold a (first box) and the first half's row sums (second box)
-    static constexpr uint32_t ZT = SB + TILE;
-    static constexpr uint32_t A = ZT + 384, R0 = ZT + 1024 + 384;
-    static constexpr uint32_t R1 = ZT + 2048;       // the second half's row sums
+    static constexpr uint32_t A = ZT + 384, R0 = ZT + ZBOX + 384;
+    static constexpr uint32_t R1 = SB + TILE;       // the second half's row sums
     static constexpr uint32_t BARS = R1 + 512;
     // barriers, 8 bytes each
     static constexpr uint32_t KFULL = BARS, KEMPTY = KFULL + 8, VFULL = KEMPTY + 8, VEMPTY = VFULL + 8;
     static constexpr uint32_t QFULL = VEMPTY + 8, QEMPTY = QFULL + 8 * NQ, T = QEMPTY + 8 * NQ, PREADY = T + 8;
-    static constexpr uint32_t O = PREADY + 8, OFREE = O + 8, S = OFREE + 8, SREADY = S + 8, ADONE = SREADY + 8;
+    static constexpr uint32_t O = PREADY + 8, OFREE = O + 8, RFREE = OFREE + 16, S = RFREE + 8, SREADY = S + 8, ADONE = SREADY + 8;
     static constexpr uint32_t HALF = ADONE + 8, DRAIN = HALF + 16, TSLOT = DRAIN + 8, ABORT = TSLOT + 8;
     static constexpr size_t BYTES = ABORT + 16;
     static_assert(BYTES <= 232448, "shared-memory limit");
@@ -557,6 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         init(W::PREADY, 256);
         init(W::O, 1);
         init(W::OFREE, 256);
+        init(W::OFREE + 8, 256);
+        init(W::RFREE, 256);
         init(W::S, 1);
         init(W::SREADY, 256);
         init(W::ADONE, 256);
@@ -569,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         fence_mbar_init();
     }
     for (int k = threadIdx.x; k < 512; k += kThreads)
-        ((uint32_t *)(smem_raw + W::ZT))[k] = (k % 256) / 32 == 2 ? 0x3F803F80u : 0u;
+        ((uint32_t *)(smem_raw + W::ZT + k / 256 * W::ZBOX))[k % 256] = (k % 256) / 32 == 2 ? 0x3F803F80u : 0u;
     fence_proxy_async_smem();
     if (warp == 1) {
         tmem_alloc((uint32_t *)(smem_raw + W::TSLOT), 512);
@@ -581,7 +594,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     griddep_wait();
     griddep_launch_dependents();
     const uint32_t tmem = *(const uint32_t *)(smem_raw + W::TSLOT);
-    const uint32_t tT = tmem, tP = tmem + 128, tO = tmem + 192, tS = tmem + 320, tL = tS, tZA = tmem + 448, tQZ = tmem + 480;
+    const uint32_t tO = tmem, tT = tmem + 256, tX = tmem + 384, tP = tmem + 400, tZA = tmem + 464;
+    // q . z of a chunk's first unit x
+    auto tQZ = [&](int x) { return P.r == 1 && (x & 1) ? tX : tmem + 496; };
     uint32_t *status = P.A.status;
     const int VH = P.A.Hkv * P.gs;
     auto wait1 = [&](uint32_t bar, uint32_t parity, uint32_t where) { return wait_for(sm + bar, parity & 1, ab, status, where); };
@@ -599,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 const int row = u.lo + u.c * kC, h = u.vh / P.gs;
                 if (n > 0 && !wait1(W::KEMPTY, n - 1, 0x801)) break;
                 expect_bytes(sm + W::KFULL, TILE);
-                for (int b = 0; b < NB; ++b) load_box(sm + W::K + b * kBox, &P.tmK, sm + W::KFULL, 64 * b, row, h);
+                for (int b = 0; b < NB; ++b) load_box(sm + W::K + b * W::KBOX, &P.tmK, sm + W::KFULL, 64 * b, row, h);
                 ++kn;
                 if (n > 0 && !wait1(W::VEMPTY, n - 1, 0x802)) break;
                 expect_bytes(sm + W::VFULL, TILE);
@@ -624,33 +639,37 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             for (int k = t > NQ ? t - NQ : 0; k < t; ++k) wait_briefly(sm + W::QFULL + 8 * (k % NQ), (k / NQ) & 1);
         } else if (warp == 1 && lane == 0) {
             // ---- MMA
-            constexpr uint32_t idT = idesc_bf16(128, 128, false, false), idO = idesc_bf16(128, 64 * NB, false, true);
-            constexpr uint32_t idS = idesc_bf16(128, 64 * NB, true, true), idZ = idesc_bf16(128, 16, true, false);
-            constexpr uint32_t idQZ = idesc_bf16(128, 16, false, false);
-            constexpr uint32_t lbo = NB == 2 ? kBox : 0;  // D <= 64: rows 64-127 of S repeat rows 0-63 and are not read
+            constexpr uint32_t idT = idesc_bf16(128, 128, false, false), idTX = idesc_bf16(128, 144, false, false);
+            constexpr uint32_t idO = idesc_bf16(128, 64 * NB, false, true), idS = idesc_bf16(128, 64 * NB, true, true);
+            constexpr uint32_t idZ = idesc_bf16(128, 16, true, false), idQZ = idesc_bf16(128, 16, false, false);
+            // D <= 64: rows 64-127 of S repeat rows 0-63 and are not read
+            constexpr uint32_t lbo = NB == 2 ? kBox : 0, lboK = NB == 2 ? W::KBOX : 0;
             int n = 0, un = 0;                            // chunk and number of unit u
-            uint32_t sx = sm;
+            uint32_t sx = sm >> 4;
             // T of unit x in chunk m
             auto issue_t = [&](bool fresh, int x, int m) {
                 if (fresh && !wait1(W::KFULL, m, 0x804)) return false;
                 if (!wait1(W::QFULL + 8 * (x % NQ), x / NQ, 0x805)) return false;
                 tc_fence_after();
-                const uint32_t qb = sx + W::Q + (x % NQ) * TILE;
+                const uint32_t qb = sx + (x % NQ) * (TILE >> 4), id = fresh ? idT : idTX;
 #pragma unroll
                 for (int k = 0; k < 4 * NB; ++k)
-                    mma_ss(tT, sdesc_sw128(qb + (k >> 2) * kBox + 32 * (k & 3), 16, 1024),
-                           sdesc_sw128(sx + W::K + (k >> 2) * kBox + 32 * (k & 3), 16, 1024), idT, k > 0);
+                    mma_ss(tT, desc_at(qb, W::Q + (k >> 2) * kBox + 32 * (k & 3), 16, 1024),
+                           desc_at(sx, W::K + (k >> 2) * W::KBOX + 32 * (k & 3), 16, 1024), id, k > 0);
                 commit(sm + W::T);
                 return true;
             };
-            // the chunk's K^T V; K is then done with
-            auto issue_s = [&](bool wanted) {
+            // the chunk's K^T V, behind its last unit x, where O of x + 1 is going to be; K is then done with
+            auto issue_s = [&](bool wanted, int x) {
                 if (wanted) {
+                    if (x > 0 && !wait1(W::OFREE + 8 * ((x - 1) & 1), (x - 1) >> 1, 0x80a)) return false;
+                    tc_fence_after();
+                    const uint32_t tS = tO + 128 * ((x + 1) & 1);
 #pragma unroll
                     for (int k = 0; k < kC / 16; ++k) {
-                        const uint64_t kd = sdesc_sw128(sx + W::K + 2048 * k, lbo, 1024);
-                        const uint64_t vd = sdesc_sw128(sx + W::V + 2048 * k, lbo, 1024);
-                        const uint64_t on = sdesc_sw128(sx + W::ZT + (k >> 2) * 1024 + 32 * (k & 3), 16, 0);
+                        const uint64_t kd = desc_at(sx, W::K + 2048 * k, lboK, 1024);
+                        const uint64_t vd = desc_at(sx, W::V + 2048 * k, lbo, 1024);
+                        const uint64_t on = desc_at(sx, W::ZT + (k >> 2) * W::ZBOX + 32 * (k & 3), 16, 0);
                         mma_ss(tS, kd, vd, idS, k > 0);
                         mma_ss(tZA, kd, on, idZ, k > 0);
                         mma_ss(tZA + 16, vd, on, idZ, k > 0);
@@ -658,41 +677,48 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     commit(sm + W::S);
                 }
                 commit(sm + W::KEMPTY);
+                return true;
             };
             Units u(P);
-            bool ok = u.valid() && issue_t(true, 0, 0);
+            bool ok = u.valid() && issue_t(true, 0, 0), parts = false;
             while (ok) {
                 asm volatile("" : "+r"(sx));  // descriptors are formed where they are used, not kept in registers
-                const bool last = u.j == P.r - 1, first = u.j == 0, wanted = u.sums_wanted(P), parts = u.c < kLowChunks;
-                u.next(P, P.r, VH);
+                const bool last = u.j == P.r - 1, first = u.j == 0, wanted = last && u.sums_wanted(P);
+                const uint32_t ob = un & 1, tOu = tO + 128 * ob;
                 if (first) {
+                    parts = u.c < kLowChunks;
                     if (!wait1(W::VFULL, n, 0x806)) break;
                     if (!wait1(W::SREADY, n, 0x807)) break;  // Sb is there, K^T V has been read
-                    tc_fence_after();
                 }
-                if (last && !first && !parts) issue_s(wanted);
-                if (un > 0 && !wait1(W::OFREE, un - 1, 0x809)) break;
+                if (un > 1 && !wait1(W::OFREE + 8 * ob, (un >> 1) - 1, 0x809)) break;
                 tc_fence_after();
-                const uint32_t qb = sx + W::Q + (un % NQ) * TILE;
+                const uint32_t qb = sx + (un % NQ) * (TILE >> 4);
 #pragma unroll
-                for (int k = 0; k < 4 * NB; ++k) {
-                    const uint64_t qd = sdesc_sw128(qb + (k >> 2) * kBox + 32 * (k & 3), 16, 1024);
-                    mma_ss(tO, qd, sdesc_sw128(sx + W::SB + 2048 * k, lbo, 1024), idO, k > 0);
-                    mma_ss(tQZ, qd, sdesc_sw128(sx + W::ZT + (k >> 2) * 1024 + 32 * (k & 3), 16, 0), idQZ, k > 0);
+                for (int k = 0; k < 4 * NB; ++k)
+                    mma_ss(tOu, desc_at(qb, W::Q + (k >> 2) * kBox + 32 * (k & 3), 16, 1024),
+                           desc_at(sx, W::SB + 2048 * k, lbo, 1024), idO, k > 0);
+                if (first) {
+                    const uint32_t tQ = tQZ(un);
+#pragma unroll
+                    for (int k = 0; k < 4 * NB; ++k)
+                        mma_ss(tQ, desc_at(qb, W::Q + (k >> 2) * kBox + 32 * (k & 3), 16, 1024),
+                               desc_at(sx, W::ZT + (k >> 2) * W::ZBOX + 32 * (k & 3), 16, 0), idQZ, k > 0);
                 }
+                if (last && !first && !issue_s(wanted, un)) break;
+                u.next(P, P.r, VH);
                 if (!wait1(W::PREADY, un, 0x808)) break;  // P is there, T may be overwritten
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < kC / 16; ++k)
-                    mma_ts(tO, tP + 8 * k, sdesc_sw128(sx + W::V + 2048 * k, lbo, 1024), idO, 1u);
+                    mma_ts(tOu, tP + 8 * k, desc_at(sx, W::V + 2048 * k, lbo, 1024), idO, 1u);
                 if (parts) {
 #pragma unroll
                     for (int k = 0; k < kC / 16; ++k)
-                        mma_ts(tO, tL + 8 * k, sdesc_sw128(sx + W::V + 2048 * k, lbo, 1024), idO, 1u);
+                        mma_ts(tOu, tT + 32 * (k >> 1) + 8 * (k & 1), desc_at(sx, W::V + 2048 * k, lbo, 1024), idO, 1u);
                 }
                 commit(sm + W::O);
-                // behind A, which clears rows that are not the sequence's, and behind the low parts
-                if (last && (first || parts)) issue_s(wanted);
+                // behind A, which clears rows that are not the sequence's
+                if (last && first && !issue_s(wanted, un)) break;
                 if (!last && !issue_t(false, un + 1, n)) break;
                 if (last) {
                     commit(sm + W::VEMPTY);
@@ -706,24 +732,64 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             wait_briefly(sm + W::DRAIN, 0);
         }
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsA));
-        // ---- A: P and row sums.  Thread <-> row i of a chunk and half hf of the columns.
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsA));
+        // ---- A: P and row sums, and C: the state.  Thread <-> row i of a chunk (of S: row d = i) and half hf of the
+        // columns.
         const int q4 = warp & 3, hf = (warp - 4) >> 2, i = 32 * q4 + lane;
         const uint32_t lo = (uint32_t)(32 * q4) << 16;
-        int m = 0, x = 0;  // chunk, unit
+        const int D = P.A.D, col0 = CH * hf;
+        const bool has_row = NB == 2 || q4 < 2;          // rows of S there are
+        float2 S[CH / 2];                                // S[i][col0 ...]
+        float za = 0.f;                                  // z[i] (first half) or a[i] (second half)
+        int ks = 0, m = 0, x = 0;                        // K^T V read, chunk, unit
         for (Units u(P); u.valid(); ++x) {
             const bool parts = u.c < kLowChunks;
-            if (!wait(W::T, x, 0x811)) break;
-            if (u.j == 0) {  // (behind T, which was formed behind the chunk before: no phase is missed)
-                if (parts && !wait(W::SREADY, m, 0x810)) break;  // K^T V of the chunk before has been read
+            if (u.j == 0 && (x == 0 || u.c == 0)) {  // the state a piece starts from
+#pragma unroll
+                for (int k = 0; k < CH / 2; ++k) S[k] = make_float2(0.f, 0.f);
+                const float *f = u.slot<NB>(P);
+                za = 0.f;
+                if (f) za = f[kSlotS<NB> + 128 * hf + i];
+                else if (P.A.resume && i < D) za = (hf ? (const float *)P.A.a : (const float *)P.A.z)[u.state(P) * D + i];
+                if (f && has_row) {
+#pragma unroll
+                    for (int q = 0; q < 8 * NB; ++q) {
+                        const float4 v = ((const float4 *)f)[slot_at<NB>(i, hf, q)];
+                        S[2 * q] = make_float2(v.x, v.y), S[2 * q + 1] = make_float2(v.z, v.w);
+                    }
+                } else if (!f && P.A.resume && i < D && col0 < D) {
+                    const float4 *src = (const float4 *)((const float *)P.A.S + (u.state(P) * D + i) * D + col0);
+#pragma unroll
+                    for (int q = 0; q < CH / 4; ++q) {
+                        const float4 v = src[q];
+                        S[2 * q] = make_float2(v.x, v.y), S[2 * q + 1] = make_float2(v.z, v.w);
+                    }
+                }
+            }
+            if (x > 0 && !wait(W::O, x - 1, 0x812)) break;  // Q S and P V of the unit before have read Sb and P
+            if (u.j == 0) {
+                if (has_row) {
+                    const uint32_t tile = sm + W::SB + (NB == 2 ? hf * kBox : 0);
+#pragma unroll
+                    for (int g = 0; g < CH / 8; ++g)
+                        sts128(tile + tc::sw128_off(i, (NB == 2 ? 0 : 4 * hf) + g),
+                               make_uint4(pack_bf16(S[4 * g].x, S[4 * g].y), pack_bf16(S[4 * g + 1].x, S[4 * g + 1].y),
+                                          pack_bf16(S[4 * g + 2].x, S[4 * g + 2].y), pack_bf16(S[4 * g + 3].x, S[4 * g + 3].y)));
+                }
+                if (has_row && hf == 0) tc::split_tile_put(smem_raw + W::ZT + (i >> 6) * W::ZBOX, i & 63, za);
+                fence_proxy_async_smem();
+                tc_fence_before();
+                arrive(sm + W::SREADY);
                 ++m;
             }
+            if (!wait(W::T, x, 0x811)) break;
             tc_fence_after();
-            if (x > 0) {  // P V of the unit before has read its P
-                if (!wait(W::O, x - 1, 0x812)) break;
-                tc_fence_after();
-            }
             float2 sum = make_float2(0.f, 0.f);
+            uint32_t qz0 = 0u, qz1 = 0u;  // q . z, but for the first unit, whose T was formed before z was known
+            if (u.j > 0 && hf == 0) {
+                tmem_ld2(tX + lo, qz0, qz1);
+                tmem_wait_ld(qz0, qz1);
+            }
 #pragma unroll 1
             for (int b = 0; b < 2; ++b) {
                 const int blk = 2 * hf + b;
@@ -732,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
                     for (int k = 0; k < 16; ++k) hi[k] = 0u;
                     tmem_st16(tP + lo + 16 * blk, hi);
-                    if (parts) tmem_st16(tL + lo + 16 * blk, hi);
+                    if (parts) tmem_st16(tT + lo + 32 * blk, hi);
                     continue;
                 }
                 uint32_t v[32];
@@ -753,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 if (parts) {
 #pragma unroll
                     for (int k = 0; k < 16; ++k) hi[k] = pack_bf16(p[k].x - tc::bf16lo(hi[k]), p[k].y - tc::bf16hi(hi[k]));
-                    tmem_st16(tL + lo + 16 * blk, hi);
+                    tmem_st16(tT + lo + 32 * blk, hi);  // over the T it came from
                 }
             }
             if (u.j == 0 && u.live() < kC) {
@@ -764,74 +830,66 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 const int none = u.live() > 0 ? u.live() : 0;
                 for (int y = threadIdx.x - 128; y < (kC - none) * 8 * NB; y += 256) {
                     const int row = none + y / (8 * NB), g = y % (8 * NB);
-                    const uint32_t at = sm + (g >> 3) * kBox + row * 128 + (g & 7) * 16;
-                    sts128(at + W::K, make_uint4(0u, 0u, 0u, 0u));
-                    sts128(at + W::V, make_uint4(0u, 0u, 0u, 0u));
+                    const uint32_t at = sm + row * 128 + (g & 7) * 16;
+                    sts128(at + W::K + (g >> 3) * W::KBOX, make_uint4(0u, 0u, 0u, 0u));
+                    sts128(at + W::V + (g >> 3) * kBox, make_uint4(0u, 0u, 0u, 0u));
                 }
                 fence_proxy_async_smem();
             }
-            if (x > 0 && !wait(W::OFREE, x - 1, 0x817)) break;  // B has read the row sums of the unit before
-            sts_f(sm + (hf ? W::R1 : W::R0) + 4 * i, sum.x + sum.y);
+            if (x > 0 && !wait(W::RFREE, x - 1, 0x817)) break;  // B has read the row sums of the unit before
+            if (u.j == 0) {
+                if (m > 1 && !wait(W::ADONE, m - 2, 0x825)) break;  // and a of the chunk before
+                if (hf && has_row) sts_f(sm + W::A + 4 * i, za);
+            }
+            sts_f(sm + (hf ? W::R1 : W::R0) + 4 * i, (sum.x + sum.y) + (__uint_as_float(qz0) + __uint_as_float(qz1)));
             tmem_st_wait();
             tc_fence_before();
             arrive(sm + W::PREADY);
+            if (u.j == P.r - 1) {
+                // C: the state after the chunk
+                if (u.sums_wanted(P)) {
+                    if (!wait(W::S, ks, 0x824)) break;
+                    ++ks;
+                    tc_fence_after();
+                    if (has_row) {
+                        uint32_t s0, s1;
+                        tmem_ld2(tZA + lo + 16 * hf + 2, s0, s1);  // column 2: the ones
+                        tmem_wait_ld(s0, s1);
+                        za += __uint_as_float(s0);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            uint32_t v[32];
+                            tmem_ld32(tO + 128 * ((x + 1) & 1) + lo + col0 + 32 * b, v);
+                            tmem_wait_ld(v);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                S[16 * b + k] = add2(S[16 * b + k], make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])));
+                        }
+                    }
+                    tc_fence_before();
+                }
+                if (u.saves(P) && i < D) (hf ? (float *)P.A.a : (float *)P.A.z)[u.state(P) * D + i] = za;
+                if (u.saves(P) && i < D && col0 < D) {
+                    float4 *dst = (float4 *)((float *)P.A.S + (u.state(P) * D + i) * D + col0);
+#pragma unroll
+                    for (int q = 0; q < CH / 4; ++q)
+                        dst[q] = make_float4(S[2 * q].x, S[2 * q].y, S[2 * q + 1].x, S[2 * q + 1].y);
+                }
+            }
             u.next(P, P.r, VH);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsB));
-        // ---- B: O -> out, and C: the state.  Thread <-> row i of a chunk (of S: row d = i) and half hf of the columns.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsB));
+        // ---- B: O -> out.  Thread <-> row i of a chunk and half hf of the columns.
         const int q4 = warp & 3, hf = (warp - 12) >> 2, i = 32 * q4 + lane;
         const uint32_t lo = (uint32_t)(32 * q4) << 16;
         const int D = P.A.D, col0 = CH * hf;
-        const bool has_row = NB == 2 || q4 < 2;          // rows of S there are
         const bool storer = lane == 0 && q4 == 0 && (NB == 2 || hf == 0);
-        float2 S[CH / 2];                                // S[i][col0 ...]
-        float za = 0.f;                                  // z[i] (first half) or a[i] (second half)
         int n0 = 0;                                      // rows of the sequence before the first of this call
         int pending = -1;                                // Q tile whose O is on its way out (storer)
-        int halves = 0, ks = 0, m = 0, x = 0;
+        int halves = 0, m = 0, x = 0;                    // m: chunk
         for (Units u(P); u.valid(); ++x) {
-            if (u.j == 0 && (x == 0 || u.c == 0)) {  // the state a piece starts from
-#pragma unroll
-                for (int k = 0; k < CH / 2; ++k) S[k] = make_float2(0.f, 0.f);
-                const float *f = u.slot<NB>(P);
-                n0 = u.rows_before<NB>(P);
-                za = 0.f;
-                if (f) za = f[kSlotS<NB> + 128 * hf + i];
-                else if (P.A.resume && i < D) za = (hf ? (const float *)P.A.a : (const float *)P.A.z)[u.state(P) * D + i];
-                if (f && has_row) {
-#pragma unroll
-                    for (int q = 0; q < 8 * NB; ++q) {
-                        const float4 v = ((const float4 *)f)[slot_at<NB>(i, hf, q)];
-                        S[2 * q] = make_float2(v.x, v.y), S[2 * q + 1] = make_float2(v.z, v.w);
-                    }
-                } else if (!f && P.A.resume && i < D && col0 < D) {
-                    const float4 *src = (const float4 *)((const float *)P.A.S + (u.state(P) * D + i) * D + col0);
-#pragma unroll
-                    for (int q = 0; q < CH / 4; ++q) {
-                        const float4 v = src[q];
-                        S[2 * q] = make_float2(v.x, v.y), S[2 * q + 1] = make_float2(v.z, v.w);
-                    }
-                }
-            }
-            if (u.j == 0) {
-                if (has_row) {
-                    const uint32_t tile = sm + W::SB + (NB == 2 ? hf * kBox : 0);
-#pragma unroll
-                    for (int g = 0; g < CH / 8; ++g)
-                        sts128(tile + tc::sw128_off(i, (NB == 2 ? 0 : 4 * hf) + g),
-                               make_uint4(pack_bf16(S[4 * g].x, S[4 * g].y), pack_bf16(S[4 * g + 1].x, S[4 * g + 1].y),
-                                          pack_bf16(S[4 * g + 2].x, S[4 * g + 2].y), pack_bf16(S[4 * g + 3].x, S[4 * g + 3].y)));
-                }
-                if (has_row) {
-                    if (hf == 0) tc::split_tile_put(smem_raw + W::ZT, i, za);
-                    else sts_f(sm + W::A + 4 * i, za);
-                }
-                fence_proxy_async_smem();
-                tc_fence_before();
-                arrive(sm + W::SREADY);
-                ++m;
-            }
+            if (u.j == 0 && (x == 0 || u.c == 0)) n0 = u.rows_before<NB>(P);
             if (pending >= 0) {  // the last unit's O has been read out of its Q tile, which may be filled again
                 bulk_wait_read0();
                 arrive(sm + W::QEMPTY + 8 * pending);
@@ -840,21 +898,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             __syncwarp();
             if (!wait(W::O, x, 0x821)) break;
             tc_fence_after();
-            uint32_t qz0, qz1;
-            tmem_ld2(tQZ + lo, qz0, qz1);
-            tmem_wait_ld(qz0, qz1);
+            uint32_t qz0 = 0u, qz1 = 0u;
+            if (u.j == 0) {
+                tmem_ld2(tQZ(x) + lo, qz0, qz1);
+                tmem_wait_ld(qz0, qz1);
+            }
             const float sc = 1.f / ((float)(n0 + u.c * kC) + (__uint_as_float(qz0) + __uint_as_float(qz1)) +
                                     (lds_f(sm + W::R0 + 4 * i) + lds_f(sm + W::R1 + 4 * i)));
+            arrive(sm + W::RFREE);
             const int live = u.live();
             const uint32_t tile = sm + W::Q + (x % NQ) * TILE + (NB == 2 ? hf * kBox : 0);
 #pragma unroll 1
             for (int b = 0; b < NB; ++b) {
                 uint32_t v[32];
-                tmem_ld32(tO + lo + col0 + 32 * b, v);
+                tmem_ld32(tO + 128 * (x & 1) + lo + col0 + 32 * b, v);
                 tmem_wait_ld(v);
-                if (b == NB - 1) {  // O, q . z and the row sums have been read
+                if (b == NB - 1) {  // O and q . z have been read
                     tc_fence_before();
-                    arrive(sm + W::OFREE);
+                    arrive(sm + W::OFREE + 8 * (x & 1));
                 }
                 const uint32_t acol = sm + W::A + 4 * (col0 + 32 * b);
 #pragma unroll
@@ -895,39 +956,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 arrive(sm + W::QEMPTY + 8 * (x % NQ));
             }
             if (last) {
-                // C: the state after the chunk
-                if (!wait(W::ADONE, m - 1, 0x825)) break;
-                if (u.sums_wanted(P)) {
-                    if (!wait(W::S, ks, 0x824)) break;
-                    ++ks;
-                    tc_fence_after();
-                    if (has_row) {
-                        uint32_t s0, s1;
-                        tmem_ld2(tZA + lo + 16 * hf + 2, s0, s1);  // column 2: the ones
-                        tmem_wait_ld(s0, s1);
-                        za += __uint_as_float(s0);
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            uint32_t v[32];
-                            tmem_ld32(tS + lo + col0 + 32 * b, v);
-                            tmem_wait_ld(v);
-#pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                S[16 * b + k] = add2(S[16 * b + k], make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])));
-                        }
-                    }
-                    tc_fence_before();
-                }
-                if (u.saves(P) && i < D) {
-                    (hf ? (float *)P.A.a : (float *)P.A.z)[u.state(P) * D + i] = za;
+                // the head's n, which every thread of B has read
+                if (u.saves(P)) {
+                    if (!wait(W::ADONE, m, 0x825)) break;
                     if (hf == 0 && i == 0) P.A.n[u.state(P)] = n0 + u.len;
                 }
-                if (u.saves(P) && i < D && col0 < D) {
-                    float4 *dst = (float4 *)((float *)P.A.S + (u.state(P) * D + i) * D + col0);
-#pragma unroll
-                    for (int q = 0; q < CH / 4; ++q)
-                        dst[q] = make_float4(S[2 * q].x, S[2 * q].y, S[2 * q + 1].x, S[2 * q + 1].y);
-                }
+                ++m;
             }
             u.next(P, P.r, VH);
         }
