@@ -67,13 +67,13 @@ struct Units {
     int seq, vh, c, j;      // j: query head within vh
     int nch, lo, len;       // the head's chunks, the sequence's rows
     __device__ __forceinline__ void enter(const TcArgs &P) {
-        lo = P.A.off[seq];
-        len = P.A.off[seq + 1] - lo;
+        lo = __ldcg(P.A.off + seq);
+        len = __ldcg(P.A.off + seq + 1) - lo;
         nch = chunks_of(len);
     }
     __device__ __forceinline__ explicit Units(const TcArgs &P) {
-        const Slice &s = P.slices[blockIdx.x];
-        left = (int)s.left, seq = s.seq, vh = s.vh, c = s.c, j = 0;
+        const Slice *s = P.slices + blockIdx.x;
+        left = (int)__ldcg(&s->left), seq = __ldcg(&s->seq), vh = __ldcg(&s->vh), c = __ldcg(&s->c), j = 0;
         nch = lo = len = 0;
         if (left > 0) enter(P);
     }
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sums_kernel(const __grid_const
 // before it, each thread one float4 of the slots.  b0's own sums are replaced by what the head starts from (resumed),
 // because the CTA that ends the head writes the state while b0 may not have read it.
 // ----------------------------------------------------------------------------------------------------------------
-constexpr int kChains = 32;
+constexpr int kChains = 32, kCarryThreads = 128;
 
 template <int NB>
 __device__ void walk_chain(const TcArgs &P, const Slice &s, int b0, int x, const int *chain, int length) {
@@ -339,14 +339,15 @@ __device__ void walk_chain(const TcArgs &P, const Slice &s, int b0, int x, const
         }
     }
     const float4 start = run;
-    for (int k0 = 0; k0 < length; k0 += 8) {  // eight loads in flight
-        float4 v[8];
+    constexpr int kAhead = 16;
+    for (int k0 = 0; k0 < length; k0 += kAhead) {  // that many loads in flight
+        float4 v[kAhead];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < kAhead; ++k)
             if (k0 + k < length)
                 v[k] = ((const float4 *)(P.sums + (long long)(k0 + k ? chain[k0 + k - 1] : b0) * kSlot<NB>))[x];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < kAhead; ++k)
             if (k0 + k < length) {
                 run.x += v[k].x, run.y += v[k].y, run.z += v[k].z, run.w += v[k].w;
                 ((float4 *)(P.carry + (long long)chain[k0 + k] * kSlot<NB>))[x] = run;
@@ -355,12 +356,14 @@ __device__ void walk_chain(const TcArgs &P, const Slice &s, int b0, int x, const
     ((float4 *)first)[x] = start;
 }
 
-template <int NB> __global__ void __launch_bounds__(256) carry_kernel(const __grid_constant__ TcArgs P) {
+template <int NB> __global__ void __launch_bounds__(kCarryThreads) carry_kernel(const __grid_constant__ TcArgs P) {
+    __shared__ Slice slices[tc::kMaxCtas];
     __shared__ int chain[tc::kMaxCtas + 1];  // the head's CTAs after b0, in order
     __shared__ int begin, length;
     griddep_wait();
     griddep_launch_dependents();
-    const int x = blockIdx.x * 256 + threadIdx.x;
+    const int x = blockIdx.x * kCarryThreads + threadIdx.x;
+    for (int b = threadIdx.x; b < P.G; b += kCarryThreads) slices[b] = P.slices[b];
     int skip = blockIdx.y;  // chains that other blocks take before this one's next
     for (int b0 = 0; b0 < P.G;) {
         __syncthreads();  // the chain before has been read
@@ -370,7 +373,7 @@ template <int NB> __global__ void __launch_bounds__(256) carry_kernel(const __gr
                 const int mine = b + threadIdx.x;
                 bool begins = false;
                 if (mine < P.G) {
-                    const Slice c = P.slices[mine];
+                    const Slice c = slices[mine];
                     begins = c.left > 0 && c.open && c.la == 0;
                 }
                 unsigned on = __ballot_sync(0xffffffffu, begins);
@@ -379,12 +382,12 @@ template <int NB> __global__ void __launch_bounds__(256) carry_kernel(const __gr
             }
             int n = 0;
             if (at < P.G) {  // a CTA carries the head on while its last piece is of that head and open
-                const Slice s = P.slices[at];
+                const Slice s = slices[at];
                 bool more = true;
                 for (int b = at + 1; b < P.G && more; b += 32) {
                     const int mine = b + threadIdx.x;
                     Slice c = {};
-                    if (mine < P.G) c = P.slices[mine];
+                    if (mine < P.G) c = slices[mine];
                     const unsigned any = __ballot_sync(0xffffffffu, c.left > 0);
                     const unsigned on = __ballot_sync(0xffffffffu, c.left > 0 && c.open && c.lseq == s.lseq && c.lvh == s.lvh);
                     const unsigned stop = any & ~on;                       // the first CTA that does not ends the head
@@ -404,7 +407,7 @@ template <int NB> __global__ void __launch_bounds__(256) carry_kernel(const __gr
         if (cb >= P.G) return;
         b0 = cb + 1;
         skip = kChains - 1;
-        walk_chain<NB>(P, P.slices[cb], cb, x, chain, length);
+        walk_chain<NB>(P, slices[cb], cb, x, chain, length);
     }
 }
 
@@ -591,7 +594,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    griddep_wait();
+    // Before the carries are there: a kernel that waits for the sums has let this one start, so that the slices, and all
+    // that was there before the sums, are.  Only A and B wait for it, A for its state and B before it writes.
+    if (P.G == 1) griddep_wait();  // no carries: this one follows the sums
     griddep_launch_dependents();
     const uint32_t tmem = *(const uint32_t *)(smem_raw + W::TSLOT);
     const uint32_t tO = tmem, tT = tmem + 256, tX = tmem + 384, tP = tmem + 400, tZA = tmem + 464;
@@ -659,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 commit(sm + W::T);
                 return true;
             };
-            // the chunk's K^T V, behind its last unit x, where O of x + 1 is going to be; K is then done with
+            // the chunk's K^T V, at its last unit x, where O of x + 1 is going to be; K is then done with
             auto issue_s = [&](bool wanted, int x) {
                 if (wanted) {
                     if (x > 0 && !wait1(W::OFREE + 8 * ((x - 1) & 1), (x - 1) >> 1, 0x80a)) return false;
@@ -687,9 +692,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 const uint32_t ob = un & 1, tOu = tO + 128 * ob;
                 if (first) {
                     parts = u.c < kLowChunks;
-                    if (!wait1(W::VFULL, n, 0x806)) break;
                     if (!wait1(W::SREADY, n, 0x807)) break;  // Sb is there, K^T V has been read
                 }
+                if (last && !first && !issue_s(wanted, un)) break;  // early, so that K is filled again in time
                 if (un > 1 && !wait1(W::OFREE + 8 * ob, (un >> 1) - 1, 0x809)) break;
                 tc_fence_after();
                 const uint32_t qb = sx + (un % NQ) * (TILE >> 4);
@@ -704,8 +709,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                         mma_ss(tQ, desc_at(qb, W::Q + (k >> 2) * kBox + 32 * (k & 3), 16, 1024),
                                desc_at(sx, W::ZT + (k >> 2) * W::ZBOX + 32 * (k & 3), 16, 0), idQZ, k > 0);
                 }
-                if (last && !first && !issue_s(wanted, un)) break;
                 u.next(P, P.r, VH);
+                if (first && !wait1(W::VFULL, n, 0x806)) break;
                 if (!wait1(W::PREADY, un, 0x808)) break;  // P is there, T may be overwritten
                 tc_fence_after();
 #pragma unroll
@@ -742,7 +747,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         float2 S[CH / 2];                                // S[i][col0 ...]
         float za = 0.f;                                  // z[i] (first half) or a[i] (second half)
         int ks = 0, m = 0, x = 0;                        // K^T V read, chunk, unit
-        for (Units u(P); u.valid(); ++x) {
+        Units u(P);
+        griddep_wait();
+        for (; u.valid(); ++x) {
             const bool parts = u.c < kLowChunks;
             if (u.j == 0 && (x == 0 || u.c == 0)) {  // the state a piece starts from
 #pragma unroll
@@ -888,7 +895,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         int n0 = 0;                                      // rows of the sequence before the first of this call
         int pending = -1;                                // Q tile whose O is on its way out (storer)
         int halves = 0, m = 0, x = 0;                    // m: chunk
-        for (Units u(P); u.valid(); ++x) {
+        Units u(P);
+        griddep_wait();
+        for (; u.valid(); ++x) {
             if (u.j == 0 && (x == 0 || u.c == 0)) n0 = u.rows_before<NB>(P);
             if (pending >= 0) {  // the last unit's O has been read out of its Q tile, which may be filled again
                 bulk_wait_read0();
@@ -1030,7 +1039,8 @@ template <int NB> static cudaError_t run(TcArgs &P, unsigned char *ws, cudaStrea
     P.carry = P.sums + (size_t)P.G * kSlot<NB>;
     cudaError_t e = launch(sums_kernel<NB>, dim3(P.G), kSumThreads, kSmemSums<NB>, s, P);
     if (e == cudaSuccess && P.G > 1)
-        e = launch(carry_kernel<NB>, dim3((kSlotS<NB> / 4 + 64 + 256) / 256, P.G < kChains ? P.G : kChains), 256, 0, s, P);
+        e = launch(carry_kernel<NB>, dim3((kSlotS<NB> / 4 + 64 + kCarryThreads) / kCarryThreads, P.G < kChains ? P.G : kChains),
+                   kCarryThreads, 0, s, P);
     if (e == cudaSuccess) e = launch(prompt_kernel<NB>, dim3(P.G), kThreads, Walk<NB>::BYTES, s, P);
     return e;
 }
