@@ -304,110 +304,131 @@ __global__ void __launch_bounds__(kSumThreads, 1) sums_kernel(const __grid_const
 }
 
 // ----------------------------------------------------------------------------------------------------------------
-// Carries.  A chain is the CTAs of one head that straddles CTAs; it begins with the CTA b0 whose last piece is the head's
-// first and open.  Blocks (x, y) walk chains y, y + kChains, ... and leave in each later CTA's carry the sum of all
-// before it, each thread one float4 of the slots.  b0's own sums are replaced by what the head starts from (resumed),
-// because the CTA that ends the head writes the state while b0 may not have read it.
+// Carries.  A chain is the CTAs of one head that straddles CTAs: b0, whose last piece is the head's first and open, those
+// that only have a piece of the same head's middle, and the one that ends it.  Every later CTA's carry is the sum of all
+// pieces before it.  b0's own sums are replaced by what the head starts from (resumed), because the CTA that ends the
+// head writes the state while b0 may not have read it.
+// A float4 of the slots goes along a chain in up to 32 segments of at most 5 CTAs, one thread each, which first add up
+// their own: with one thread to a whole chain of 38 CTAs (65,536 tokens, 4 heads) the loads came in five rounds of 3 us.
+// A chain in m segments is the work of m blocks for each kCarryThreads float4s, so that all chains together keep about as
+// many blocks busy whether they are few and long or many and short.
 // ----------------------------------------------------------------------------------------------------------------
-constexpr int kChains = 32, kCarryThreads = 128;
-
-template <int NB>
-__device__ void walk_chain(const TcArgs &P, const Slice &s, int b0, int x, const int *chain, int length) {
-    constexpr int S4 = kSlotS<NB> / 4, N4 = S4 + 64;
-    if (x > N4) return;
-    const int D = P.A.D, h = s.lvh / P.gs;
-    const long long at = (long long)s.lseq * P.A.Hkv + h;
-    float *first = P.sums + (long long)b0 * kSlot<NB>;
-    const bool resume = P.A.resume;
-    if (x == N4) {  // n before the sequence's first row
-        const int n0 = resume ? P.A.n[at] : 0;
-        *(int *)(first + kSlotS<NB> + 256) = n0;
-        for (int k = 0; k < length; ++k) *(int *)(P.carry + (long long)chain[k] * kSlot<NB> + kSlotS<NB> + 256) = n0;
-        return;
-    }
-    float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (resume) {
-        float *r = &run.x;
-        for (int m = 0; m < 4; ++m) {
-            if (x < S4) {
-                const int d = x % 128, e = 4 * (x / 128) + m;
-                if (d < D && e < D) r[m] = ((const float *)P.A.S)[(at * D + d) * D + e];
-            } else {
-                const int i = 4 * (x - S4) + m, d = i % 128;
-                if (d < D) r[m] = (i < 128 ? (const float *)P.A.z : (const float *)P.A.a)[at * D + d];
-            }
-        }
-    }
-    const float4 start = run;
-    constexpr int kAhead = 16;
-    for (int k0 = 0; k0 < length; k0 += kAhead) {  // that many loads in flight
-        float4 v[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (k0 + k < length)
-                v[k] = ((const float4 *)(P.sums + (long long)(k0 + k ? chain[k0 + k - 1] : b0) * kSlot<NB>))[x];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (k0 + k < length) {
-                run.x += v[k].x, run.y += v[k].y, run.z += v[k].z, run.w += v[k].w;
-                ((float4 *)(P.carry + (long long)chain[k0 + k] * kSlot<NB>))[x] = run;
-            }
-    }
-    ((float4 *)first)[x] = start;
+constexpr int kCarryThreads = 256, kCarryBlocks = 44;  // 17 x 44 blocks, five on an SM, are all there at once
+constexpr int kSegment = 5, kWords = tc::kMaxCtas / 32;
+static_assert(tc::kMaxCtas <= kCarryThreads && tc::kMaxCtas % 32 == 0 && tc::kMaxCtas <= 32 * kSegment, "slices in a chain");
+__device__ __forceinline__ int segments(int length) {
+    int m = 1;
+    while (m < 32 && length > kSegment * m) m *= 2;
+    return m;
 }
 
-template <int NB> __global__ void __launch_bounds__(kCarryThreads) carry_kernel(const __grid_constant__ TcArgs P) {
-    __shared__ Slice slices[tc::kMaxCtas];
-    __shared__ int chain[tc::kMaxCtas + 1];  // the head's CTAs after b0, in order
-    __shared__ int begin, length;
+template <int NB> __global__ void __launch_bounds__(kCarryThreads, 5) carry_kernel(const __grid_constant__ TcArgs P) {
+    constexpr int S4 = kSlotS<NB> / 4, N4 = S4 + 64;
+    __shared__ uint32_t any[kWords], ends[kWords];     // CTAs with items; of those, the ones that no chain passes through
+    __shared__ int before[kWords + 1];                 // blocks' worth of the chains that begin in the words before
+    __shared__ int begin, length, share, chain[tc::kMaxCtas];
+    __shared__ float4 total[kCarryThreads];
     griddep_wait();
     griddep_launch_dependents();
-    const int x = blockIdx.x * kCarryThreads + threadIdx.x;
-    for (int b = threadIdx.x; b < P.G; b += kCarryThreads) slices[b] = P.slices[b];
-    int skip = blockIdx.y;  // chains that other blocks take before this one's next
-    for (int b0 = 0; b0 < P.G;) {
-        __syncthreads();  // the chain before has been read
-        if (threadIdx.x < 32) {
-            int at = P.G;  // where the chain after `skip` others begins
-            for (int b = b0; b < P.G && at == P.G; b += 32) {
-                const int mine = b + threadIdx.x;
-                bool begins = false;
-                if (mine < P.G) {
-                    const Slice c = slices[mine];
-                    begins = c.left > 0 && c.open && c.la == 0;
-                }
-                unsigned on = __ballot_sync(0xffffffffu, begins);
-                for (; skip > 0 && on; --skip) on &= on - 1;
-                if (on) at = b + __ffs(on) - 1;
-            }
-            int n = 0;
-            if (at < P.G) {  // a CTA carries the head on while its last piece is of that head and open
-                const Slice s = slices[at];
-                bool more = true;
-                for (int b = at + 1; b < P.G && more; b += 32) {
-                    const int mine = b + threadIdx.x;
-                    Slice c = {};
-                    if (mine < P.G) c = slices[mine];
-                    const unsigned any = __ballot_sync(0xffffffffu, c.left > 0);
-                    const unsigned on = __ballot_sync(0xffffffffu, c.left > 0 && c.open && c.lseq == s.lseq && c.lvh == s.lvh);
-                    const unsigned stop = any & ~on;                       // the first CTA that does not ends the head
-                    const unsigned take = stop ? any & (2u * (stop & -stop) - 1u) : any;
-                    if (take >> threadIdx.x & 1u) chain[n + __popc(take & ((1u << threadIdx.x) - 1u))] = mine;
-                    n += __popc(take);
-                    more = !stop;
-                }
-            }
-            if (threadIdx.x == 0) {
-                begin = at;
-                length = n;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    Slice s = {};
+    if (t < P.G) s = P.slices[t];
+    const uint32_t on = __ballot_sync(0xffffffffu, s.left > 0);
+    const uint32_t stop = __ballot_sync(0xffffffffu, s.left > 0 && !(s.open && s.la > 0));
+    if (lane == 0 && warp < kWords) any[warp] = on, ends[warp] = stop;
+    __syncthreads();
+    // of a chain that begins at CTA t: its last CTA and its length
+    int last = t, len = 0;
+    if (s.left > 0 && s.open && s.la == 0) {
+        for (int w = warp; w < kWords; ++w) {
+            const uint32_t from = w == warp ? ~1u << lane : ~0u, e = ends[w] & from;  // (lane 31: none left of this word)
+            const uint32_t to = e ? 2u * (e & -e) - 1u : ~0u;
+            len += __popc(any[w] & from & to);
+            if (e) {
+                last = 32 * w + __ffs(e) - 1;
+                break;
             }
         }
+    }
+    const int blocks = len > 0 ? segments(len) : 0;
+    int upto = blocks;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, x);
+        if (lane >= x) upto += v;
+    }
+    if (lane == 31 && warp < kWords) before[warp + 1] = upto;
+    __syncthreads();
+    if (t == 0) {
+        before[0] = 0;
+        for (int w = 0; w < kWords; ++w) before[w + 1] += before[w];
+    }
+    __syncthreads();
+    for (int y = blockIdx.y; y < before[kWords]; y += gridDim.y) {
+        if (warp < kWords && y >= before[warp] + upto - blocks && y < before[warp] + upto) {
+            begin = t;
+            length = len;
+            share = y - (before[warp] + upto - blocks);
+            int n = 0;
+            for (int w = warp; w <= last >> 5; ++w)
+                for (uint32_t m = any[w] & (w == warp ? ~1u << lane : ~0u) & (w == last >> 5 ? 2u * (1u << (last & 31)) - 1u : ~0u); m; m &= m - 1)
+                    chain[n++] = 32 * w + __ffs(m) - 1;
+        }
         __syncthreads();
-        const int cb = begin;
-        if (cb >= P.G) return;
-        b0 = cb + 1;
-        skip = kChains - 1;
-        walk_chain<NB>(P, slices[cb], cb, x, chain, length);
+        const int L = length, b0 = begin, m = segments(L), wide = kCarryThreads / m, seg = t / wide, col = t % wide;
+        const int x = blockIdx.x * kCarryThreads + share * wide + col;
+        const int k0 = L * seg / m, count = L * (seg + 1) / m - k0;  // <= kSegment
+        const Slice h = P.slices[b0];
+        const long long at = (long long)h.lseq * P.A.Hkv + h.lvh / P.gs;
+        float *first = P.sums + (long long)b0 * kSlot<NB>;
+        float4 v[kSegment];
+        if (x < N4) {
+#pragma unroll
+            for (int k = 0; k < kSegment; ++k)
+                if (k < count) {
+                    const int from = k0 + k ? chain[k0 + k - 1] : b0;
+                    v[k] = ((const float4 *)(P.sums + (long long)from * kSlot<NB>))[x];
+                }
+        }
+        float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (x < N4 && P.A.resume) {
+            float *r = &run.x;
+            for (int k = 0; k < 4; ++k) {
+                const int D = P.A.D;
+                if (x < S4) {
+                    const int d = x % 128, e = 4 * (x / 128) + k;
+                    if (d < D && e < D) r[k] = ((const float *)P.A.S)[(at * D + d) * D + e];
+                } else {
+                    const int i = 4 * (x - S4) + k, d = i % 128;
+                    if (d < D) r[k] = (i < 128 ? (const float *)P.A.z : (const float *)P.A.a)[at * D + d];
+                }
+            }
+        }
+        const float4 start = run;
+        auto add = [](float4 &r, const float4 &y) { r.x += y.x, r.y += y.y, r.z += y.z, r.w += y.w; };
+        if (m > 1) {
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kSegment; ++k)
+                if (x < N4 && k < count) add(sum, v[k]);
+            total[t] = sum;
+            __syncthreads();
+            for (int y2 = 0; y2 < seg; ++y2) add(run, total[y2 * wide + col]);
+        }
+        if (x < N4) {
+#pragma unroll
+            for (int k = 0; k < kSegment; ++k)
+                if (k < count) {
+                    add(run, v[k]);
+                    ((float4 *)(P.carry + (long long)chain[k0 + k] * kSlot<NB>))[x] = run;
+                }
+            if (seg == 0) ((float4 *)first)[x] = start;
+        } else if (x == N4 && seg == 0) {  // n before the sequence's first row
+            const int n0 = P.A.resume ? P.A.n[at] : 0;
+            *(int *)(first + kSlotS<NB> + 256) = n0;
+            for (int k = 0; k < L; ++k) *(int *)(P.carry + (long long)chain[k] * kSlot<NB> + kSlotS<NB> + 256) = n0;
+        }
+        __syncthreads();  // chain and total have been read
     }
 }
 
@@ -1039,7 +1060,7 @@ template <int NB> static cudaError_t run(TcArgs &P, unsigned char *ws, cudaStrea
     P.carry = P.sums + (size_t)P.G * kSlot<NB>;
     cudaError_t e = launch(sums_kernel<NB>, dim3(P.G), kSumThreads, kSmemSums<NB>, s, P);
     if (e == cudaSuccess && P.G > 1)
-        e = launch(carry_kernel<NB>, dim3((kSlotS<NB> / 4 + 64 + kCarryThreads) / kCarryThreads, P.G < kChains ? P.G : kChains),
+        e = launch(carry_kernel<NB>, dim3((kSlotS<NB> / 4 + 64 + kCarryThreads) / kCarryThreads, P.G < kCarryBlocks ? P.G : kCarryBlocks),
                    kCarryThreads, 0, s, P);
     if (e == cudaSuccess) e = launch(prompt_kernel<NB>, dim3(P.G), kThreads, Walk<NB>::BYTES, s, P);
     return e;
