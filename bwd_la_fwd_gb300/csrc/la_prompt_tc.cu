@@ -964,27 +964,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     }
                     const uint4 w4 = make_uint4(w[0], w[1], w[2], w[3]);
                     const int e = 32 * b + 8 * y;  // column within the thread's
-                    if (live == kC) sts128(tile + tc::sw128_off(i, (NB == 2 ? 0 : 4 * hf) + (e >> 3)), w4);
-                    else if (i < live && col0 + e < D)  // rows of others stay as they are
-                        *(uint4 *)((__nv_bfloat16 *)P.A.o + (u.vh * P.r + u.j) * P.A.oh +
-                                   (long long)(u.lo + u.c * kC + i) * P.A.on + col0 + e) = w4;
+                    sts128(tile + tc::sw128_off(i, (NB == 2 ? 0 : 4 * hf) + (e >> 3)), w4);
                 }
             }
             const bool last = u.j == P.r - 1;
             if (last) arrive(sm + W::ADONE);  // a of this chunk has been read
-            if (live == kC) {
-                fence_proxy_async_smem();
-                arrive(sm + W::HALF + 8 * hf);
-                if (storer && wait1(W::HALF + 8 * hf, halves, 0x822) && (NB == 2 || wait1(W::HALF + 8, halves, 0x823))) {
+            if (live < kC) {
+                // rows of others stay as they are: the warp copies its own, a row's columns by neighbouring lanes
+                constexpr int PER = CH / 8;
+                __nv_bfloat16 *out = (__nv_bfloat16 *)P.A.o + (u.vh * P.r + u.j) * P.A.oh + (long long)(u.lo + u.c * kC) * P.A.on + col0;
+                __syncwarp();
+#pragma unroll 1
+                for (int y = lane; y < 32 * PER; y += 32) {
+                    const int row = 32 * q4 + y / PER, g = y % PER;
+                    if (row < live && col0 + 8 * g < D)
+                        *(uint4 *)(out + (long long)row * P.A.on + 8 * g) = lds128(tile + tc::sw128_off(row, (NB == 2 ? 0 : 4 * hf) + g));
+                }
+            }
+            fence_proxy_async_smem();
+            arrive(sm + W::HALF + 8 * hf);
+            if (storer && wait1(W::HALF + 8 * hf, halves, 0x822) && (NB == 2 || wait1(W::HALF + 8, halves, 0x823))) {
+                if (live == kC) {
                     store_box(&P.tmO, tile, NB == 2 ? col0 : 0, u.lo + u.c * kC, u.vh * P.r + u.j);
                     bulk_commit();
                     pending = x % NQ;
+                } else {
+                    arrive(sm + W::QEMPTY + 8 * (x % NQ));
                 }
-                __syncwarp();
-                ++halves;
-            } else if (storer) {
-                arrive(sm + W::QEMPTY + 8 * (x % NQ));
             }
+            __syncwarp();
+            ++halves;
             if (last) {
                 // the head's n, which every thread of B has read
                 if (u.saves(P)) {
