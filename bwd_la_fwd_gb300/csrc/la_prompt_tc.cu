@@ -768,10 +768,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         float2 S[CH / 2];                                // S[i][col0 ...]
         float za = 0.f;                                  // z[i] (first half) or a[i] (second half)
         int ks = 0, m = 0, x = 0;                        // K^T V read, chunk, unit
+        // The caller's S is loaded and stored by way of the warp's own part of Sb, half of its columns at a time, so
+        // that neighbouring lanes have neighbouring columns.  (A lane to a row took 6 k clocks.)
+        constexpr int GP = 4 * NB;                       // float4s of a row in a half
+        auto staged = [&](int r, int g) {
+            return sm + W::SB + (NB == 2 ? hf * kBox : 0) + tc::sw128_off(32 * q4 + r, (NB == 2 ? 0 : 4 * hf) + g);
+        };
         Units u(P);
         griddep_wait();
         for (; u.valid(); ++x) {
             const bool parts = u.c < kLowChunks;
+            if (x > 0 && !wait(W::O, x - 1, 0x812)) break;  // Q S and P V of the unit before have read Sb and P
             if (u.j == 0 && (x == 0 || u.c == 0)) {  // the state a piece starts from
 #pragma unroll
                 for (int k = 0; k < CH / 2; ++k) S[k] = make_float2(0.f, 0.f);
@@ -785,16 +792,27 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                         const float4 v = ((const float4 *)f)[slot_at<NB>(i, hf, q)];
                         S[2 * q] = make_float2(v.x, v.y), S[2 * q + 1] = make_float2(v.z, v.w);
                     }
-                } else if (!f && P.A.resume && i < D && col0 < D) {
-                    const float4 *src = (const float4 *)((const float *)P.A.S + (u.state(P) * D + i) * D + col0);
+                } else if (!f && P.A.resume && has_row) {
+                    const float *src = (const float *)P.A.S + (u.state(P) * D + 32 * q4) * D + col0;
 #pragma unroll
-                    for (int q = 0; q < CH / 4; ++q) {
-                        const float4 v = src[q];
-                        S[2 * q] = make_float2(v.x, v.y), S[2 * q + 1] = make_float2(v.z, v.w);
+                    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                        for (int y = lane; y < 32 * GP; y += 32) {
+                            const int r = y / GP, g = y % GP, e = 4 * (GP * b + g);
+                            if (32 * q4 + r < D && col0 + e < D) sts128(staged(r, g), *(const uint4 *)(src + r * D + e));
+                        }
+                        __syncwarp();
+                        if (i < D && col0 + 4 * GP * b < D) {
+#pragma unroll
+                            for (int g = 0; g < GP; ++g) {
+                                const float4 v = lds_f4(staged(lane, g));
+                                S[2 * (GP * b + g)] = make_float2(v.x, v.y), S[2 * (GP * b + g) + 1] = make_float2(v.z, v.w);
+                            }
+                        }
+                        __syncwarp();
                     }
                 }
             }
-            if (x > 0 && !wait(W::O, x - 1, 0x812)) break;  // Q S and P V of the unit before have read Sb and P
             if (u.j == 0) {
                 if (has_row) {
                     const uint32_t tile = sm + W::SB + (NB == 2 ? hf * kBox : 0);
@@ -896,12 +914,27 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     }
                     tc_fence_before();
                 }
-                if (u.saves(P) && i < D) (hf ? (float *)P.A.a : (float *)P.A.z)[u.state(P) * D + i] = za;
-                if (u.saves(P) && i < D && col0 < D) {
-                    float4 *dst = (float4 *)((float *)P.A.S + (u.state(P) * D + i) * D + col0);
+                if (u.saves(P)) {
+                    if (i < D) (hf ? (float *)P.A.a : (float *)P.A.z)[u.state(P) * D + i] = za;
+                    if (!wait(W::O, x, 0x826)) break;  // Q S has read Sb
+                    float *dst = (float *)P.A.S + (u.state(P) * D + 32 * q4) * D + col0;
 #pragma unroll
-                    for (int q = 0; q < CH / 4; ++q)
-                        dst[q] = make_float4(S[2 * q].x, S[2 * q].y, S[2 * q + 1].x, S[2 * q + 1].y);
+                    for (int b = 0; b < 2; ++b) {
+                        if (!has_row) break;
+#pragma unroll
+                        for (int g = 0; g < GP; ++g) {
+                            const float2 s0 = S[2 * (GP * b + g)], s1 = S[2 * (GP * b + g) + 1];
+                            sts128(staged(lane, g), make_uint4(__float_as_uint(s0.x), __float_as_uint(s0.y), __float_as_uint(s1.x),
+                                                               __float_as_uint(s1.y)));
+                        }
+                        __syncwarp();
+#pragma unroll 1
+                        for (int y = lane; y < 32 * GP; y += 32) {
+                            const int r = y / GP, g = y % GP, e = 4 * (GP * b + g);
+                            if (32 * q4 + r < D && col0 + e < D) *(uint4 *)(dst + r * D + e) = lds128(staged(r, g));
+                        }
+                        __syncwarp();
+                    }
                 }
             }
             u.next(P, P.r, VH);
