@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "la_f32x2.cuh"
 #include "la_prompt.h"
 #include "la_views.h"
 
@@ -18,18 +19,19 @@ namespace la {
 namespace prompt {
 
 // ----------------------------------------------------------------------------------------------------------------
-// CUDA-core form.  grid = (sequences x key/value heads, column blocks, parts): a cluster has one head of one sequence, its
-// CTAs E columns of S each and a part of the rows each, which they walk 32 rows at a time.  First every CTA sums its
-// part; the parts' sums are exchanged through distributed shared memory, and every CTA then walks its rows again, for O,
-// from the state of all before it.  In a block of rows warp w has rows w, w + 8, ..., one lane per column (and per row j
-// of W), so a query head's rows stay within a warp.
+// CUDA-core form.  grid = (sequences x key/value heads, column blocks, parts): a cluster has one head of one sequence,
+// its CTAs E columns of S each and a part of the rows each, which they walk 32 rows at a time.  First every CTA sums its
+// part; the parts' sums are added up through distributed shared memory, each CTA a share of the elements over all parts;
+// and every CTA then walks its rows again, for O, from the state before them.  In a block of rows warp w has rows w,
+// w + 8, ..., one lane per column (and per row j of W), so a query head's rows stay within a warp.
 //
 // fp32 tokens keep an fp64 state, as la_decode_step does, but this GPU has two fp64 multiply-adds per SM and clock;
 // a sum is therefore two floats here (the product's and the sum's rounding errors are exact in fp32 and gathered in
 // the low one), good to 2^-46, and becomes a double once, at the end.  O is formed in fp32 from the high floats, so the
-// second walk sums in plain fp32.  1,500 tokens in 7 sequences, 8 query and 4 key/value heads of 64, fp32: 162 us (one walk
-// for both, one CTA to a sequence: 405 us).  What bounds it is the longest sequence: a block of rows after another, each
-// some fp32 instructions of 256 threads behind a barrier.
+// second walk sums in plain fp32.  1,500 tokens in 7 sequences, 8 query and 4 key/value heads of 64, fp32: 96 us (one
+// walk for both, one CTA to a sequence: 405 us; the whole exchange in every CTA and scalar multiply-adds: 130 us).
+// Bound by fp32 arithmetic, ten operations for a product of the sums, in the SMs that have the longest sequence's
+// cluster: a block of 32 rows takes a CTA 4 us for the sums and 5 us for O, and up to three share an SM.
 // ----------------------------------------------------------------------------------------------------------------
 constexpr int kThreads = 256, kWarps = 8, kRows = 32;
 
@@ -40,7 +42,7 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bf
 
 // A running sum: a float (bf16 tokens), or a float and the sum of its rounding errors (fp32 tokens).
 template <typename T> struct Sum;
-template <> struct Sum<__nv_bfloat16> {
+template <> struct Sum<__nv_bfloat16> {  // (one float)
     using Acc = float;
     float hi;
     __device__ void set(float x) { hi = x; }
@@ -73,6 +75,21 @@ template <> struct Sum<float> {
     __device__ double get() const { return (double)hi + (double)lo; }
 };
 
+// a += x.x y, b += x.y y; the two floats of each in ten packed operations.  -p is formed as x (-y), and differences as
+// multiply-adds with -1, which are exact products.
+__device__ __forceinline__ void fma_pair(Sum<__nv_bfloat16> &a, Sum<__nv_bfloat16> &b, float2 x, float y) {
+    const float2 r = fma2(x, both(y), make_float2(a.hi, b.hi));
+    a.hi = r.x, b.hi = r.y;
+}
+__device__ __forceinline__ void fma_pair(Sum<float> &a, Sum<float> &b, float2 x, float y) {
+    const float2 hi = make_float2(a.hi, b.hi), minus = both(-1.f);
+    const float2 np = mul2(x, both(-y)), e = fma2(x, both(y), np);
+    const float2 s = fma2(np, minus, hi), d = fma2(hi, minus, s);  // hi + p, and what of it p brought
+    const float2 lost = fma2(add2(np, d), minus, fma2(fma2(d, minus, s), minus, hi));
+    const float2 lo = add2(add2(make_float2(a.lo, b.lo), lost), e);
+    a.hi = s.x, b.hi = s.y, a.lo = lo.x, b.lo = lo.y;
+}
+
 template <typename T, int D> struct Tile {
     static constexpr int E = D < 32 ? D : 32;       // columns of S in a CTA
     static constexpr int LD = D + 4;                // row pitch of Q and K: 16-byte loads of 8 rows meet all banks
@@ -80,7 +97,9 @@ template <typename T, int D> struct Tile {
     static constexpr int NS = D * E / kThreads;     // elements of S of a thread: column t % E, rows from t / E * NS
     static constexpr int PER = kRows / kWarps;      // rows of a block of a warp
     static constexpr size_t FLOATS = 2 * kRows * LD + kRows * E + kRows * kRows + D * E + D + E;
-    static constexpr size_t SMEM = sizeof(float) * FLOATS + sizeof(Sum<T>) * (D * E + D + E);
+    static constexpr int SUMS = D * E + D + E;      // S, z and a of a CTA
+    static constexpr size_t SMEM = sizeof(float) * FLOATS + sizeof(Sum<T>) * SUMS + sizeof(typename Sum<T>::Acc) * D;
+    static_assert(FLOATS % 4 == 0 && SUMS % 2 == 0, "alignment of the sums and of z");
 };
 
 // `rows` rows of 32 (the others zero) of W elements each, global -> shared floats, 16 bytes at a time.
@@ -106,6 +125,7 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
     float *Ks = sm, *Qs = Ks + kRows * LD, *Vs = Qs + kRows * LD, *Ws = Vs + kRows * E, *Sf = Ws + kRows * kRows;
     float *zs = Sf + D * E, *as = zs + D;
     Sum<T> *of_part = (Sum<T> *)(sm + C::FLOATS);  // the part's sums: S, z, a
+    Acc *z0 = (Acc *)(of_part + C::SUMS);          // z before the first row of this call
     if (!offsets_in_order(A)) return;               // the same for the whole grid
     cg::cluster_group cluster = cg::this_cluster();
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -145,7 +165,8 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
 #pragma unroll
                     for (int m = 0; m < NS; m += 4) {
                         const float4 k4 = *(const float4 *)(Ks + j * LD + d0 + m);
-                        bs[m].fma(k4.x, v), bs[m + 1].fma(k4.y, v), bs[m + 2].fma(k4.z, v), bs[m + 3].fma(k4.w, v);
+                        fma_pair(bs[m], bs[m + 1], make_float2(k4.x, k4.y), v);
+                        fma_pair(bs[m + 2], bs[m + 3], make_float2(k4.z, k4.w), v);
                     }
                 } else {
 #pragma unroll
@@ -164,43 +185,36 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
         if (t < D) of_part[D * E + t] = zt;
         if (t < E) of_part[D * E + D + t] = at_;
     }
-    // ---- the state before the part, and behind the last one
-    Sum<T> s[NS], zt, at_;
-#pragma unroll
-    for (int m = 0; m < NS; ++m) {
-        s[m].set(0);
-        if (resume) s[m].set(S[(long long)(d0 + m) * D + e0 + e]);
-    }
-    zt.set(0);
-    at_.set(0);
-    if (resume && t < D) zt.set(z[t]);
-    if (resume && t < E) at_.set(a[e0 + t]);
+    // ---- the state before each part, and behind the last one.  Each CTA adds up its share of the elements over all parts
+    // and leaves them in the parts' shared memory.
     const int n0 = resume ? A.n[at] : 0;
-    cluster.sync();  // every part's sums are there, and all have read the state
-    for (int p = 0; p <= parts; ++p) {
-        if (p == part) {
+    if (resume && t < D) z0[t] = z[t];
+    cluster.sync();  // every part's sums are there, and all have read z and n
+    {
+        const int per = (C::SUMS + parts - 1) / parts;
+        for (int x = part * per + t; x < min((part + 1) * per, C::SUMS); x += kThreads) {
+            const bool of_z = x >= D * E && x < D * E + D;
+            Acc *state = x < D * E ? S + (long long)(x / E) * D + e0 + x % E : of_z ? z + (x - D * E) : a + e0 + (x - D * E - D);
+            Sum<T> run;
+            run.set(resume ? of_z ? z0[x - D * E] : *state : (Acc)0);
+            constexpr int kAhead = 8;
+            for (int p0 = 0; p0 < parts; p0 += kAhead) {
+                Sum<T> v[kAhead];
 #pragma unroll
-            for (int m = 0; m < NS; ++m) Sf[(d0 + m) * E + e] = s[m].hi;
-            if (t < D) zs[t] = zt.hi;
-            if (t < E) as[t] = at_.hi;
-            if (part != 0 || !S) break;  // the first part's CTAs write the state
+                for (int p = 0; p < kAhead; ++p)
+                    if (p0 + p < parts) v[p] = *cluster.map_shared_rank(of_part + x, (p0 + p) * gridDim.y + blockIdx.y);
+#pragma unroll
+                for (int p = 0; p < kAhead; ++p)
+                    if (p0 + p < parts) {
+                        *cluster.map_shared_rank(Sf + x, (p0 + p) * gridDim.y + blockIdx.y) = run.hi;  // Sf, zs, as in a row
+                        run.join(v[p]);
+                    }
+            }
+            if (S && (!of_z || blockIdx.y == 0)) *state = run.get();
         }
-        if (p == parts) break;
-        const Sum<T> *other = cluster.map_shared_rank(of_part, p * gridDim.y + blockIdx.y);
-#pragma unroll
-        for (int m = 0; m < NS; ++m) s[m].join(other[(d0 + m) * E + e]);
-        if (t < D) zt.join(other[D * E + t]);
-        if (t < E) at_.join(other[D * E + D + t]);
+        if (S && part == 0 && blockIdx.y == 0 && t == 0) A.n[at] = n0 + len;
     }
-    if (part == 0 && S) {
-#pragma unroll
-        for (int m = 0; m < NS; ++m) S[(long long)(d0 + m) * D + e0 + e] = s[m].get();
-        if (t < E) a[e0 + t] = at_.get();
-        if (blockIdx.y == 0) {
-            if (t < D) z[t] = zt.get();
-            if (t == 0) A.n[at] = n0 + len;
-        }
-    }
+    cluster.sync();  // the parts have their states, and none is read any more
     // ---- O
     for (int row0 = lo; row0 < hi; row0 += kRows) {
         const int live = min(kRows, hi - row0);
@@ -229,16 +243,18 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
             }
             __syncwarp();
             // W and g: lane j of row i
+            float2 w2[PER];
             float w[PER], gi[PER];
 #pragma unroll
-            for (int m = 0; m < PER; ++m) w[m] = 1.f, gi[m] = 0.f;
+            for (int m = 0; m < PER; ++m) w2[m] = make_float2(1.f, 0.f), gi[m] = 0.f;
 #pragma unroll 4
             for (int d = 0; d < D; d += 4) {
                 const float4 k4 = *(const float4 *)(Ks + lane * LD + d);
 #pragma unroll
                 for (int m = 0; m < PER; ++m) {
                     const float4 q4 = *(const float4 *)(Qw + m * LD + d);
-                    w[m] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, w[m]))));
+                    w2[m] = fma2(make_float2(q4.x, q4.y), make_float2(k4.x, k4.y), w2[m]);
+                    w2[m] = fma2(make_float2(q4.z, q4.w), make_float2(k4.z, k4.w), w2[m]);
                 }
             }
             for (int d = lane; d < D; d += 32) {
@@ -248,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
             }
 #pragma unroll
             for (int m = 0; m < PER; ++m) {
-                w[m] = lane <= warp + kWarps * m ? w[m] : 0.f;
+                w[m] = lane <= warp + kWarps * m ? w2[m].x + w2[m].y : 0.f;
                 Ws[(warp * PER + m) * kRows + lane] = w[m];
                 gi[m] += w[m];
 #pragma unroll
@@ -256,16 +272,17 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
             }
             __syncwarp();
             const int c = lane % E, half = lane / E;  // E = 16: the two half warps take half of the sums each
-            float o[PER];
+            float2 o2[PER];
 #pragma unroll
-            for (int m = 0; m < PER; ++m) o[m] = half ? 0.f : as[c];
+            for (int m = 0; m < PER; ++m) o2[m] = make_float2(half ? 0.f : as[c], 0.f);
 #pragma unroll 4
             for (int d = half * (D / C::RE); d < (half + 1) * (D / C::RE); d += 4) {
                 const float s0 = Sf[d * E + c], s1 = Sf[(d + 1) * E + c], s2 = Sf[(d + 2) * E + c], s3 = Sf[(d + 3) * E + c];
 #pragma unroll
                 for (int m = 0; m < PER; ++m) {
                     const float4 q4 = *(const float4 *)(Qw + m * LD + d);
-                    o[m] = fmaf(q4.x, s0, fmaf(q4.y, s1, fmaf(q4.z, s2, fmaf(q4.w, s3, o[m]))));
+                    o2[m] = fma2(make_float2(q4.x, q4.y), make_float2(s0, s1), o2[m]);
+                    o2[m] = fma2(make_float2(q4.z, q4.w), make_float2(s2, s3), o2[m]);
                 }
             }
 #pragma unroll 4
@@ -274,34 +291,45 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
 #pragma unroll
                 for (int m = 0; m < PER; ++m) {
                     const float4 w4 = *(const float4 *)(Ws + (warp * PER + m) * kRows + j);
-                    o[m] = fmaf(w4.x, v0, fmaf(w4.y, v1, fmaf(w4.z, v2, fmaf(w4.w, v3, o[m]))));
+                    o2[m] = fma2(make_float2(w4.x, w4.y), make_float2(v0, v1), o2[m]);
+                    o2[m] = fma2(make_float2(w4.z, w4.w), make_float2(v2, v3), o2[m]);
                 }
             }
 #pragma unroll
             for (int m = 0; m < PER; ++m) {
                 const int i = warp + kWarps * m;
-                if (C::RE == 2) o[m] += __shfl_xor_sync(0xffffffffu, o[m], 16);
-                if (i < live && half == 0) put(O + (long long)i * A.on + c, o[m] / (nb + gi[m]));
+                float o = o2[m].x + o2[m].y;
+                if (C::RE == 2) o += __shfl_xor_sync(0xffffffffu, o, 16);
+                if (i < live && half == 0) put(O + (long long)i * A.on + c, o / (nb + gi[m]));
             }
         }
         if (row0 + kRows >= hi) break;
         __syncthreads();  // every warp has read S, z and a of before
-        float bs[NS], bz = 0.f, ba = 0.f;
+        Sum<__nv_bfloat16> bs[NS];
+        float bz = 0.f, ba = 0.f;
 #pragma unroll
-        for (int m = 0; m < NS; ++m) bs[m] = 0.f;
+        for (int m = 0; m < NS; ++m) bs[m].set(0);
         for (int j = 0; j < live; ++j) {
             const float v = Vs[j * E + e];
+            if constexpr (NS % 4 == 0) {
 #pragma unroll
-            for (int m = 0; m < NS; ++m) bs[m] = fmaf(Ks[j * LD + d0 + m], v, bs[m]);
+                for (int m = 0; m < NS; m += 4) {
+                    const float4 k4 = *(const float4 *)(Ks + j * LD + d0 + m);
+                    fma_pair(bs[m], bs[m + 1], make_float2(k4.x, k4.y), v);
+                    fma_pair(bs[m + 2], bs[m + 3], make_float2(k4.z, k4.w), v);
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < NS; ++m) bs[m].fma(Ks[j * LD + d0 + m], v);
+            }
             if (t < D) bz += Ks[j * LD + t];
             if (t < E) ba += Vs[j * E + t];
         }
 #pragma unroll
-        for (int m = 0; m < NS; ++m) Sf[(d0 + m) * E + e] += bs[m];
+        for (int m = 0; m < NS; ++m) Sf[(d0 + m) * E + e] += bs[m].hi;
         if (t < D) zs[t] += bz;
         if (t < E) as[t] += ba;
     }
-    cluster.sync();  // no CTA leaves while another may still read its sums
 }
 
 template <typename T, int D> cudaError_t launch_simt(const Args &A, cudaStream_t s) {
@@ -315,11 +343,12 @@ template <typename T, int D> cudaError_t launch_simt(const Args &A, cudaStream_t
         }))
         return cudaErrorInvalidValue;
     // Parts: up to what a cluster holds, while that does not make more than three CTAs for each SM and leaves sequences
-    // of the mean length two blocks of rows in a part.
+    // of the mean length a block of rows in a part.  (The case above: eight parts 106 us, four 116, two 179, before the
+    // exchange was shared out; no more than two CTAs for each SM: 112 where three take 82.)
     constexpr int cols = D / C::E;
     const long long heads = (long long)A.nseq * A.Hkv;
     int parts = 1;
-    while (2 * parts * cols <= 16 && 2 * parts * cols * heads <= 456 && (long long)A.T >= 4LL * parts * kRows * A.nseq) parts *= 2;
+    while (2 * parts * cols <= 16 && 2 * parts * cols * heads <= 456 && (long long)A.T >= (long long)parts * kRows * A.nseq) parts *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)heads, cols, parts);
     cfg.blockDim = dim3(kThreads);
