@@ -28,11 +28,12 @@ namespace prompt {
 // fp32 tokens keep an fp64 state, as la_decode_step does, but this GPU has two fp64 multiply-adds per SM and clock;
 // a sum is therefore two floats here (the product's and the sum's rounding errors are exact in fp32 and gathered in
 // the low one), good to 2^-46, and becomes a double once, at the end.  O is formed in fp32 from the high floats, so the
-// second walk sums in plain fp32.  1,500 tokens in 7 sequences, 8 query and 4 key/value heads of 64, fp32: 96 us (one
-// walk for both, one CTA to a sequence: 405 us; the whole exchange in every CTA and scalar multiply-adds: 130 us).
+// second walk sums in plain fp32.  1,500 tokens in 7 sequences, 8 query and 4 key/value heads of 64, fp32: 68 us (one
+// walk for both, one CTA to a sequence: 405 us; the whole exchange in every CTA and scalar multiply-adds: 92 us).
 // Bound by fp32 arithmetic, ten operations for a product of the sums, in the SMs that have the longest sequence's
 // cluster: a block of 32 rows takes a CTA 4 us for the sums and 5 us for O, and up to three share an SM.
 // ----------------------------------------------------------------------------------------------------------------
+constexpr int kMaxRows = 0x7fffffff - 256;  // a chunk that begins at a row ends at an int
 constexpr int kThreads = 256, kWarps = 8, kRows = 32;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -388,7 +389,7 @@ bool supported_d(int D) { return D == 16 || D == 32 || D == 64 || D == 128 || D 
 extern "C" {
 
 size_t la_prompt_workspace_bytes(int T, int nseq, int Hq, int Hkv, int D, int dtype) {
-    if (T < 0 || nseq < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || !la::prompt::supported_d(D) ||
+    if (T < 0 || T > la::prompt::kMaxRows || nseq < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || !la::prompt::supported_d(D) ||
         (dtype != LA_F32 && dtype != LA_BF16))
         return 0;
     return la::prompt::tc_supported(D, dtype) ? la::prompt::tc_workspace_bytes(T, nseq, Hkv, Hq / Hkv, D) : 256;
@@ -400,7 +401,7 @@ int la_prompt(const void *Q, const void *K, const void *V, const int *seq_offset
     using namespace la;
     using namespace la::prompt;
     if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
-    if (T < 0 || nseq < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || D < 1) return LA_ERR_INVALID_ARG;
+    if (T < 0 || T > kMaxRows || nseq < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || D < 1) return LA_ERR_INVALID_ARG;
     if (!supported_d(D)) return LA_ERR_UNSUPPORTED;
     if ((long long)T * Hq >= (1LL << 40) / D || (long long)nseq * Hkv >= (1LL << 31) / 16) return LA_ERR_INVALID_ARG;
     const int elem = dtype == LA_BF16 ? 2 : 4, acc = dtype == LA_BF16 ? 4 : 8;

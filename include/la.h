@@ -245,7 +245,8 @@ int la_decode_step_grouped(const void *q, const void *k, const void *v, void *o,
 /*
  * The causal forward over packed prompts with grouped heads, for serving: nseq sequences of different lengths lie end
  * to end in T rows, and each leaves the state that la_decode_step_grouped continues from.
- *   Q, O         in / out: [T,Hq,D] of `dtype`;  K, V in: [T,Hkv,D];  Hq = r Hkv, query head h with key/value head h / r
+ *   Q, O         in / out: [T,Hq,D] of `dtype`;  K, V in: [T,Hkv,D];  Hq = r Hkv, query head h with key/value head h / r;
+ *                T < 2^31 - 256
  *   seq_offsets  in : device int [nseq + 1]; sequence i has rows seq_offsets[i] ... seq_offsets[i + 1] - 1 (none is
  *                fine).  Rows outside every sequence are neither read into a result nor written.  Offsets that are
  *                not in order within [0, T] are found on the device: nothing is computed, LA_ERR_BOUNDS is reported.

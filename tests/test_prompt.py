@@ -75,6 +75,15 @@ def test_prompt_refuses_on_the_host():
         assert lib.la_prompt_workspace_bytes(*bad) == 0
 
 
+def test_prompt_refuses_more_rows_than_an_int_numbers():
+    from bwd_la_fwd_gb300 import la
+    lib = la.load_library()
+    for T, fine in ((2 ** 31 - 1 - 256, True), (2 ** 31 - 256, False), (2 ** 31 - 1, False)):
+        assert (lib.la_prompt_workspace_bytes(T, 1, 1, 1, 32, 1) > 0) == fine
+    assert lib.la_prompt(0x100000, 0x200000, 0x300000, 0x400000, 0x500000, None, None, None, None, 0, 2 ** 31 - 100, 1, 1, 1,
+                         32, 1, None, 0xA00000, 1 << 50, None) == 1
+
+
 def test_grouped_decode_refuses_on_the_host():
     from bwd_la_fwd_gb300 import la
     lib = la.load_library()
@@ -167,6 +176,49 @@ def test_slices_of_any_number_of_ctas(monkeypatch, D, Hq, Hkv, resume, ctas):
     assert la.la_get_status(ws) == 0
     ref, tol = R.prompt(q, k, v, off, start, "bf16", True)
     _check(O, state, ref, tol, off)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,D,Hq,Hkv,resume", [([6000], 64, 3, 3, True), ([6000], 128, 2, 1, False),
+                                                  ([3000] + [130] * 20, 64, 6, 3, True), ([257] * 60, 32, 2, 2, False),
+                                                  ([1500, 1, 0, 1500, 700], 128, 4, 2, True)], ids=str)
+def test_heads_that_straddle_many_ctas(lens, D, Hq, Hkv, resume):
+    """The tensor-core form's carries: few long chains of CTAs, many short ones, both together; a state to start from."""
+    from bwd_la_fwd_gb300 import la
+    off = _offsets(lens)
+    q, k, v = _tokens(off[-1], Hq, Hkv, D, "bf16", seed=len(lens))
+    state = _state(len(lens), Hkv, D, "bf16")
+    start = R.empty_state(len(lens), Hkv, D)
+    if resume:
+        pq, pk, pv = _tokens(40 * len(lens), Hq, Hkv, D, "bf16", seed=98)
+        la.la_prompt(pq, pk, pv, torch.tensor(_offsets([40] * len(lens)), dtype=torch.int32, device="cuda"), state)
+        start = tuple(t.double().cpu() for t in (state.S, state.z, state.a)) + (state.n.cpu().long(),)
+    ws = la.new_prompt_workspace(off[-1], len(lens), Hq, Hkv, D, la.LA_BF16)
+    ws[256:].fill_(255)  # what earlier calls left is not read
+    O = la.la_prompt(q, k, v, torch.tensor(off, dtype=torch.int32, device="cuda"), state, resume=resume, workspace=ws)
+    assert la.la_get_status(ws) == 0
+    ref, tol = R.prompt(q, k, v, off, start, "bf16", True)
+    _check(O, state, ref, tol, off)
+
+
+@pytest.mark.gpu
+def test_prompts_on_two_streams_at_once():
+    """Calls that overlap, each with a workspace of its own, give the bits of calls one after another."""
+    from bwd_la_fwd_gb300 import la
+    D, Hq, Hkv, T = 128, 4, 2, 2000
+    off = torch.tensor([0, 900, T], dtype=torch.int32, device="cuda")
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    toks = [_tokens(T, Hq, Hkv, D, "bf16", seed=s) for s in (1, 2)]
+    ws = [la.new_prompt_workspace(T, 2, Hq, Hkv, D, la.LA_BF16) for _ in streams]
+    alone = [la.la_prompt(*t, off, workspace=w) for t, w in zip(toks, ws)]
+    outs = [torch.zeros_like(o) for o in alone]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for s, t, w, o in zip(streams, toks, ws, outs):
+            la.la_prompt(*t, off, O=o, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    assert all(la.la_get_status(w) == 0 for w in ws)
+    assert all(torch.equal(a, b) for a, b in zip(alone, outs))
 
 
 @pytest.mark.gpu
