@@ -13,7 +13,10 @@
 // into the state each CTA's first piece starts from; prompt_kernel walks.  Only heads that straddle CTAs have their K
 // and V read twice.
 //
-// Bound by HBM: for r query heads to a key/value head a chunk moves (2 r + 2) tiles of 32 KB (D = 128).
+// For r query heads to a key/value head a chunk has to move (2 r + 2) tiles of 32 KB (D = 128).  65,536 tokens, 16 query
+// and 4 key/value heads of 128 (671 MB): 175 us, about 30 for the sums (which read K and V once more), 10 for the carries
+// and 128 for the walk (5.2 TB/s).  12 prompts of 12,000 tokens together: 59 us; a CTA has three chunks there, and what
+// it waits for at each kernel's and each piece's beginning counts for as much as they do.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <stdlib.h>
@@ -445,8 +448,9 @@ template <int NB> __global__ void __launch_bounds__(kCarryThreads, 5) carry_kern
 // 64 clocks of shared memory each at best), once a chunk K^T V with the sums of K and V 1.7 k; HBM would take 3.4 k for a
 // unit's bytes (D = 128, r = 4).  An N = 16 MMA takes more than an N = 128 one: z stands behind K's rows, so that T
 // brings q . z along (N = 144), and only a chunk's first unit, whose T is formed before the chunk's z is known, has
-// products of its own for it.  (Such products in each unit: 204 us where this takes 191.)  The sums of K and V on the
-// CUDA cores took twice the epilogue's time.
+// products of its own for it.  (Such products in each unit: 204 us for the first case where this took 191.)  The sums of
+// K and V on the CUDA cores took twice the epilogue's time.  Two threads that issue MMAs side by side (T, and the rest):
+// 191 us where one takes 182.
 // Two things cost the epilogue more than its arithmetic: code that does not come round again within a unit (the warps
 // then wait for instructions), hence loops that are not unrolled and one group per step; and spilled registers, which
 // with this much shared memory are L2 accesses, hence 32-bit shared addresses and registers split by role.
