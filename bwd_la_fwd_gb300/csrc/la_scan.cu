@@ -38,7 +38,7 @@ namespace scan {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 16;  // parts that time is cut into
-constexpr int kEnough = 228;     // CTAs: three for two SMs
+constexpr int kEnough = 228, kFew = 76;  // CTAs: three for two SMs, one for two SMs
 
 struct Op {
     const void *p;
@@ -430,14 +430,16 @@ template <typename T, int GATE, bool BACK, int CH> cudaError_t launch(Params P, 
                                         1) == cudaSuccess;
         }))
         return cudaErrorInvalidValue;
-    // Parts of time, which are read twice: none where the channel blocks make three CTAs for two SMs, else doubled until
-    // they do, as long as each has two rounds.  (1 x 65536 x 512, fp32, 32 blocks: 341, 154, 129, 159 us for 1, 4, 8, 16
-    // parts.)
+    // Parts of time, which are read twice: none where the channel blocks make a CTA for every other SM, else doubled until
+    // there are three for two SMs, as long as each has two rounds.  (For 1, 2, 4, 8, 16 parts: 1 x 65536 x 512, fp32, 32
+    // blocks: 339, 270, 151, 129, 157 us; 1 x 8192 x 1024, bf16, backward, 64 blocks: 76, 60, 52, 57, 81; 2 x 30000 x 640,
+    // fp32, 80 blocks: 188, 223, 195, 169, 199; 1 x 8192 x 2048, bf16, 128 blocks: 50, 66, 71, 72, 109.)
     P.cblocks = (P.C + CH - 1) / CH;
     const long long blocks = (long long)B * P.cblocks;
     const int round = kWarps * Sh::RUNS * Sh::SEG, all = (P.N + round - 1) / round;
     int ncta = 1;
-    while (ncta < kMaxCluster && blocks * ncta < kEnough && 4 * ncta <= all) ncta *= 2;
+    if (blocks < kFew)
+        while (ncta < kMaxCluster && blocks * ncta < kEnough && 4 * ncta <= all) ncta *= 2;
     P.rounds = (all + ncta - 1) / ncta;
     if (blocks * ncta >= (1LL << 31)) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
