@@ -14,8 +14,8 @@
 // and V read twice.
 //
 // For r query heads to a key/value head a chunk has to move (2 r + 2) tiles of 32 KB (D = 128).  65,536 tokens, 16 query
-// and 4 key/value heads of 128 (671 MB): 175 us, about 30 for the sums (which read K and V once more), 10 for the carries
-// and 128 for the walk (5.2 TB/s).  12 prompts of 12,000 tokens together: 59 us; a CTA has three chunks there, and what
+// and 4 key/value heads of 128 (671 MB): 171 us, about 30 for the sums (which read K and V once more), 10 for the carries
+// and 124 for the walk (5.4 TB/s).  12 prompts of 12,000 tokens together: 57 us; a CTA has three chunks there, and what
 // it waits for at each kernel's and each piece's beginning counts for as much as they do.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -489,11 +489,12 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 __device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t n) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
+// (No suspend time: with one of 20 us the waiting threads wake later, 65,536 tokens taking 176 us where they take 171.)
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(ok)
-                 : "r"(bar), "r"(parity), "r"(20000u)  // asleep for up to 20 us a try: the CTA's other warps have work
+                 : "r"(bar), "r"(parity)
                  : "memory");
     return ok != 0;
 }
