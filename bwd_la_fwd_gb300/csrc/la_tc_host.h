@@ -118,7 +118,7 @@ __device__ inline volatile uint32_t *fwd_terms_kept(const TcParams &P) {
 
 // Host helpers shared by the forward and backward launchers (la_tc_fwd.cu).
 namespace tc_host {
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // the driver's tensor-map encoder, null on error
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // CUDA's tensor-map encoder, null on error
 int sm_count();  // multiprocessors of the current device (cached per device), 0 on error
 bool make_map(CUtensorMap *m, const void *ptr, const Plan &p, int op, bool flat);
 bool flat_heads(const Plan &p, const int *ops, int n);
