@@ -202,6 +202,24 @@ def test_heads_that_straddle_many_ctas(lens, D, Hq, Hkv, resume):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind,D", [("bf16", 128), ("bf16", 256), ("f32", 64)])
+def test_prompts_without_rows(kind, D):
+    """T = 0: sequences start empty and stay so, or keep the state that they continue from."""
+    from bwd_la_fwd_gb300 import la
+    q, k = torch.empty(0, 4, D, dtype=R.TYPES[kind], device="cuda"), torch.empty(0, 2, D, dtype=R.TYPES[kind], device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    ws = la.new_prompt_workspace(0, 2, 4, 2, D, la.LA_BF16 if kind == "bf16" else la.LA_F32)
+    state = _state(2, 2, D, kind)
+    parts = (state.S, state.z, state.a, state.n)
+    for t in parts:
+        t.fill_(5)
+    assert la.la_prompt(q, k, k, off, state, resume=True, workspace=ws).shape == (0, 4, D)
+    assert all(bool((t == 5).all()) for t in parts)
+    la.la_prompt(q, k, k, off, state, workspace=ws)
+    assert all(not bool(t.any()) for t in parts) and la.la_get_status(ws) == 0
+
+
+@pytest.mark.gpu
 def test_prompts_on_two_streams_at_once():
     """Calls that overlap, each with a workspace of its own, give the bits of calls one after another."""
     from bwd_la_fwd_gb300 import la

@@ -202,3 +202,12 @@ def test_copied_channels_keep_their_bits():
     for inter in (False, True):
         y, _ = la.la_rotary(q, None, la.la_rotary_frequencies(16), interleaved=inter)
         assert torch.equal(y.view(torch.int16)[..., 16:], q.view(torch.int16)[..., 16:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,N", [(0, 3), (2, 0)])
+def test_rotary_of_nothing(B, N):
+    from bwd_la_fwd_gb300 import la
+    f = la.la_rotary_frequencies(64)
+    Q, K = la.la_rotary(torch.empty(B, 4, N, 64, device="cuda"), torch.empty(B, 2, N, 64, device="cuda"), f)
+    assert Q.shape == (B, 4, N, 64) and K.shape == (B, 2, N, 64)
