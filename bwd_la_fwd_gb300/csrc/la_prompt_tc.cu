@@ -54,6 +54,7 @@ struct TcArgs {
     Slice *slices;       // [G]
     float *sums, *carry; // [G] slots
     uint64_t wait_ns;
+    int drop;            // test hook: the unit whose Q CTA 0 of the walk does not load; -1: none
 };
 
 // A slot: S as float4s in (column group, row) order, then z, a (128 each) and n.
@@ -662,6 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             for (Units u(P); u.valid(); u.next(P, P.r, VH), ++t) {
                 const uint32_t x = t % NQ;
                 if (t >= NQ && !wait1(W::QEMPTY + 8 * x, t / NQ - 1, 0x803)) break;
+                if (t == P.drop && blockIdx.x == 0) continue;
                 expect_bytes(sm + W::QFULL + 8 * x, TILE);
                 for (int b = 0; b < NB; ++b)
                     load_box(sm + W::Q + x * TILE + b * kBox, &P.tmQ, sm + W::QFULL + 8 * x, 64 * b, u.lo + u.c * kC,
@@ -1140,6 +1142,8 @@ cudaError_t tensor_cores(const Args &A, unsigned char *ws, cudaStream_t s) {
         const long long ns = atoll(env);
         if (ns >= 1000000) P.wait_ns = (uint64_t)ns;
     }
+    P.drop = -1;
+    if (const char *env = getenv("LA_TEST_DROP_LOAD")) P.drop = atoi(env);
     if (A.T > 0 && (!head_map(&P.tmQ, enc, A.q, A.D, A.T, A.Hq, A.qh, A.qn) ||
                     !head_map(&P.tmK, enc, A.k, A.D, A.T, A.Hkv, A.kh, A.kn) ||
                     !head_map(&P.tmV, enc, A.v, A.D, A.T, A.Hkv, A.vh, A.vn) ||

@@ -220,6 +220,31 @@ def test_prompts_without_rows(kind, D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,unit", [(128, 0), (128, 9), (64, 6)])
+def test_a_wait_that_runs_out_is_reported_and_leaves_the_next_call_exact(monkeypatch, D, unit):
+    """A tile of Q that the walk's first CTA does not ask for (no copy and no arrival): its wait ends after 20 ms, every
+    role stops, and the next call on the same workspace has the bits of one that never saw it."""
+    from bwd_la_fwd_gb300 import la
+    T, Hq, Hkv = 2048, 4, 2
+    q, k, v = _tokens(T, Hq, Hkv, D, "bf16", seed=unit)
+    off = torch.tensor([0, 900, T], dtype=torch.int32, device="cuda")
+    monkeypatch.setenv("LA_TC_MAX_CTAS", "4")
+    ws = la.new_prompt_workspace(T, 2, Hq, Hkv, D, la.LA_BF16)
+    state = _state(2, Hkv, D, "bf16")
+    want = la.la_prompt(q, k, v, off, state, workspace=ws)
+    parts = [t.clone() for t in (state.S, state.z, state.a, state.n)]
+    assert la.la_get_status(ws) == 0
+    monkeypatch.setenv("LA_TEST_WAIT_NS", "20000000")
+    monkeypatch.setenv("LA_TEST_DROP_LOAD", str(unit))
+    la.la_prompt(q, k, v, off, state, workspace=ws)
+    assert la.la_get_status(ws) == 5  # LA_ERR_TIMEOUT
+    monkeypatch.delenv("LA_TEST_WAIT_NS")
+    monkeypatch.delenv("LA_TEST_DROP_LOAD")
+    assert torch.equal(la.la_prompt(q, k, v, off, state, workspace=ws), want) and la.la_get_status(ws) == 0
+    assert all(torch.equal(a, b) for a, b in zip(parts, (state.S, state.z, state.a, state.n)))
+
+
+@pytest.mark.gpu
 def test_prompts_on_two_streams_at_once():
     """Calls that overlap, each with a workspace of its own, give the bits of calls one after another."""
     from bwd_la_fwd_gb300 import la
