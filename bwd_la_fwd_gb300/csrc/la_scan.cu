@@ -144,6 +144,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
     __shared__ __align__(16) Map2 of_cta[kMaxCluster][LANES];
     cg::cluster_group cluster = cg::this_cluster();
     const int ncta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    // A CTA's shared memory may be written by others once it has begun: said here, waited for before the first such write.
+    if (ncta > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int block = (int)(blockIdx.x / (unsigned)ncta);
     const long long b = block / P.cblocks;
@@ -279,12 +281,13 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
         copy_wait<0>();
         if (run == 0) of_warp[0][warp][pair] = m;
         __syncthreads();
+        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // every CTA of the cluster has begun
         if (warp == 0 && run == 0) {
             Map2 all{1.f, 0.f, 1.f, 0.f};
             for (int k = 0; k < kWarps; ++k) all = then(all, of_warp[0][k][pair]);
             for (int k = 0; k < ncta; ++k) *cluster.map_shared_rank(&of_cta[rank][pair], k) = all;
         }
-        cluster.sync();
+        cluster.sync();  // the maps are there, and no CTA writes to another from here on
         for (int k = 0; k < rank; ++k) {
             const Map2 g = of_cta[k][pair];
             carry.x = apply(g.a0, g.v0, carry.x);
@@ -417,7 +420,6 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
         if (in0) P.last[b * P.C + c] = carry.x;
         if (in1) P.last[b * P.C + c + 1] = carry.y;
     }
-    if (ncta > 1) cluster.sync();  // no CTA leaves while another may still write to it
 }
 
 template <typename T, int GATE, bool BACK, int CH> cudaError_t launch(Params P, int B, cudaStream_t s) {
