@@ -11,7 +11,7 @@
 // is read once and every output written once, which bounds it (HBM); the next round's rows are on their way (cp.async,
 // each warp its own) meanwhile.  Two CTAs of 8 warps on an SM, because a round's phases wait for one another: one CTA of
 // 16 warps gave 4.0 TB/s where these give 5.4 (64 x 1024 x 2048, bf16).
-// Where batch and channels give too few CTAs even in narrow blocks, time is cut into up to 16 parts, the CTAs of a
+// Where batch and channels give too few CTAs even in blocks of 16 channels, time is cut into up to 16 parts, the CTAs of a
 // cluster: each first forms its part's map (its warps side by side, without rounds), they exchange these once through
 // distributed shared memory, and each walks its part as above, reading it again.  (Exchanging in every round instead, so
 // that nothing is read twice, took three times as long: a cluster's barrier costs microseconds.)
@@ -123,6 +123,7 @@ __device__ __forceinline__ Map2 then(const Map2 &f, const Map2 &g) {  // first f
 
 // CH: channels of a CTA.
 template <typename T, int GATE, bool BACK, int CH> struct Shape {
+    static constexpr bool PARTS = CH == 16;                             // time may be cut into parts
     static constexpr int NT = !BACK ? 2 : GATE == LA_GATE_LOG ? 3 : 4;  // operands read
     static constexpr int LANES = CH / 2, RUNS = 32 / LANES;             // lanes of a run, runs of a warp
     static constexpr int SEG = (NT == 4 ? 16 : 32) / (int)sizeof(T);    // rows of a run: 16 or 8 (bf16), 8 or 4 (fp32)
@@ -141,11 +142,13 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
     constexpr int E = 16 / (int)sizeof(T);
     extern __shared__ __align__(128) unsigned char stages[];
     __shared__ __align__(16) Map2 of_warp[2][kWarps][LANES];
-    __shared__ __align__(16) Map2 of_cta[kMaxCluster][LANES];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int ncta = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    // A CTA's shared memory may be written by others once it has begun: said here, waited for before the first such write.
-    if (ncta > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    __shared__ __align__(16) Map2 of_cta[S::PARTS ? kMaxCluster : 1][LANES];
+    int ncta = 1, rank = 0;
+    if constexpr (S::PARTS) {
+        ncta = (int)cg::this_cluster().num_blocks(), rank = (int)cg::this_cluster().block_rank();
+        // A CTA's shared memory may be written by others once it has begun: said here, waited for before the first such write.
+        if (ncta > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int block = (int)(blockIdx.x / (unsigned)ncta);
     const long long b = block / P.cblocks;
@@ -261,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
         if (in0) carry.x = P.first[b * P.C + c];
         if (in1) carry.y = P.first[b * P.C + c + 1];
     }
-    if (ncta > 1) {
+    if (S::PARTS && ncta > 1) {
+        const cg::cluster_group cluster = cg::this_cluster();
         // the part's map: each warp R runs, one behind another, then the warps' in order
         Map2 m{1.f, 0.f, 1.f, 0.f};
 #pragma unroll
@@ -435,12 +439,13 @@ template <typename T, int GATE, bool BACK, int CH> cudaError_t launch(Params P, 
     // Parts of time, which are read twice: none where the channel blocks make a CTA for every other SM, else doubled until
     // there are three for two SMs, as long as each has two rounds.  (For 1, 2, 4, 8, 16 parts: 1 x 65536 x 512, fp32, 32
     // blocks: 339, 270, 151, 129, 157 us; 1 x 8192 x 1024, bf16, backward, 64 blocks: 76, 60, 52, 57, 81; 2 x 30000 x 640,
-    // fp32, 80 blocks: 188, 223, 195, 169, 199; 1 x 8192 x 2048, bf16, 128 blocks: 50, 66, 71, 72, 109.)
+    // fp32, 80 blocks: 188, 223, 195, 169, 199; 1 x 8192 x 2048, bf16, 128 blocks: 50, 66, 71, 72, 109.)  Wider blocks, which
+    // are taken only where they make CTAs enough, are never cut.
     P.cblocks = (P.C + CH - 1) / CH;
     const long long blocks = (long long)B * P.cblocks;
     const int round = kWarps * Sh::RUNS * Sh::SEG, all = (P.N + round - 1) / round;
     int ncta = 1;
-    if (blocks < kFew)
+    if (Sh::PARTS && blocks < kFew)
         while (ncta < kMaxCluster && blocks * ncta < kEnough && 4 * ncta <= all) ncta *= 2;
     P.rounds = (all + ncta - 1) / ncta;
     if (blocks * ncta >= (1LL << 31)) return cudaErrorInvalidConfiguration;
@@ -455,7 +460,7 @@ template <typename T, int GATE, bool BACK, int CH> cudaError_t launch(Params P, 
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = Sh::PARTS ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, scan_kernel<T, GATE, BACK, CH>, P);
 }
 
