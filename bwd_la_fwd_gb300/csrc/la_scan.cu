@@ -16,9 +16,10 @@
 // distributed shared memory, and each walks its part as above, reading it again.  (Exchanging in every round instead, so
 // that nothing is read twice, took three times as long: a cluster's barrier costs microseconds.)
 //
-// Everything is held in fp32.  A gate is rounded once, to 2^-24: the same gate at every step leaves an error of up to
-// 2^-24 / (1 - a) of the value.  A gate of exactly 0 cuts: what came before, infinities and NaN included, has no
-// part in what follows.  A product of nonzero gates that underflows is held at the smallest denormal for that.
+// Everything is held in fp32.  A gate is within 5 (log) or 9 (sigmoid) half steps of 2^-24: the same gate at every step
+// leaves an error of up to that many 2^-24 / (1 - a) of the value.  A gate of exactly 0 cuts: what came before, infinities
+// and NaN included, has no part in what follows.  A product of nonzero gates that underflows is held at the smallest
+// denormal for that.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -73,16 +74,18 @@ __device__ __forceinline__ void store1(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) { *(__nv_bfloat162 *)p = __floats2bfloat162_rn(x, y); }
 __device__ __forceinline__ void store2(float *p, float x, float y) { *(float2 *)p = make_float2(x, y); }
 
-// e^w: 2^(w log2 e) by the hardware's 2^x, within 2 ulp, and the product's rounding error put back.  Below 2^-126: 0.
+// e^w: 2^(w log2 e) by the hardware's 2^x, within 2 ulp, and the product's rounding error put back: 5 half steps in all.
+// Below 2^-126: 0.  Where the power is 0 or infinite there is nothing to put back, and the error of a product past fp32's
+// range (w near the type's lowest value) is no number that could be.
 __device__ __forceinline__ float2 exp_of(float2 w) {
     const float2 y = mul2(w, both(1.44269502f));
     float2 t = fma2(w, both(1.92596299e-8f), fma2(w, both(1.44269502f), make_float2(-y.x, -y.y)));
     t = mul2(t, both(0.693147182f));
-    t = make_float2(fmaxf(t.x, -1.f), fmaxf(t.y, -1.f));  // (no number where w = -inf, whose power is 0)
     float2 e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
-    return fma2(e, t, e);
+    const float2 r = fma2(e, t, e);
+    return make_float2(fabsf(y.x) < 128.f ? r.x : e.x, fabsf(y.y) < 128.f ? r.y : e.y);
 }
 
 // a and b of two gates.  The sigmoid's smaller half comes from e^-|w|, so that neither loses its leading digits.
