@@ -108,18 +108,27 @@ template <int GATE> __device__ __forceinline__ float gated(float b, float x) {
     return GATE == LA_GATE_LOG ? x : (b == 0.f ? 0.f : b * x);
 }
 
-// h -> a h + v, with a = 0 a cut.
-__device__ __forceinline__ float apply(float a, float v, float h) { return a == 0.f ? v : fmaf(a, h, v); }
-__device__ __forceinline__ float cut(float a, float h) { return a == 0.f ? 0.f : __fmul_rn(a, h); }
+// h -> a h + v, with a = 0 a cut, and with 0 kept 0 by a product of gates that is beyond fp32.
+__device__ __forceinline__ float cut(float a, float h) {
+    return a == 0.f || (h == 0.f && a > 0.f) ? 0.f : __fmul_rn(a, h);
+}
+__device__ __forceinline__ float apply(float a, float v, float h) {
+    return a == 0.f || (h == 0.f && a > 0.f) ? v : fmaf(a, h, v);
+}
+// A cut among the gates makes the product one, whatever the others are.
 __device__ __forceinline__ float product(float a, float b) {
     const float p = a * b;
-    return p == 0.f && a != 0.f && b != 0.f ? 1.4e-45f : p;
+    return a == 0.f || b == 0.f ? 0.f : p == 0.f ? 1.4e-45f : p;
 }
 
 // The map of a run of steps on a lane's two channels.
 struct Map2 {
     float a0, v0, a1, v1;
 };
+// Whether a map that was formed by plain products and sums is what it has to be: nothing was cut, nothing overflowed.
+__device__ __forceinline__ bool plain(const Map2 &m) {
+    return m.a0 > 0.f && m.a0 < INFINITY && m.a1 > 0.f && m.a1 < INFINITY && fabsf(m.v0) < INFINITY && fabsf(m.v1) < INFINITY;
+}
 __device__ __forceinline__ Map2 then(const Map2 &f, const Map2 &g) {  // first f, then g
     return Map2{product(f.a0, g.a0), apply(g.a0, g.v0, f.v0), product(f.a1, g.a1), apply(g.a1, g.v1, f.v1)};
 }
@@ -218,9 +227,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
             V = BACK ? mul2(a[j], add2(u[j], V)) : fma2(a[j], V, u[j]);  // backwards a_j G_j leaves row j
         }
         Map2 m{A.x, V.x, A.y, V.y};
-        const bool odd = !(m.a0 > 0.f && m.a0 < INFINITY && m.a1 > 0.f && m.a1 < INFINITY && fabsf(m.v0) < INFINITY &&
-                           fabsf(m.v1) < INFINITY);
-        if (__any_sync(0xffffffffu, odd)) {
+        if (__any_sync(0xffffffffu, !plain(m))) {
             if (!BACK && GATE == LA_GATE_SIGMOID) {  // an input that the gate shuts out has no part
 #pragma unroll
                 for (int j = 0; j < SEG; ++j) {
@@ -251,12 +258,22 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
         return Map2{__shfl_sync(0xffffffffu, m.a0, from), __shfl_sync(0xffffffffu, m.v0, from),
                     __shfl_sync(0xffffffffu, m.a1, from), __shfl_sync(0xffffffffu, m.v1, from)};
     };
-    // the maps of the warp's runs up to and with this lane's
-    auto upto = [&](Map2 m) {
+    // the maps of the warp's runs up to and with this lane's: plainly, and again with cuts as in map_of
+    auto upto = [&](const Map2 &mine) {
+        if (RUNS == 1) return mine;
+        Map2 m = mine;
 #pragma unroll
         for (int d = 1; d < RUNS; d *= 2) {
             const Map2 before = shuffled(m, (run - d) * LANES + pair);
-            if (run >= d) m = then(before, m);
+            if (run >= d) m = Map2{before.a0 * m.a0, fmaf(m.a0, before.v0, m.v0), before.a1 * m.a1, fmaf(m.a1, before.v1, m.v1)};
+        }
+        if (__any_sync(0xffffffffu, !plain(m))) {
+            m = mine;
+#pragma unroll
+            for (int d = 1; d < RUNS; d *= 2) {
+                const Map2 before = shuffled(m, (run - d) * LANES + pair);
+                if (run >= d) m = then(before, m);
+            }
         }
         return m;
     };

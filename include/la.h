@@ -301,8 +301,10 @@ int la_rotary_backward(const void *dQr, const void *dKr, void *dQ, void *dK, con
 /*
  * Gated linear recurrence over N rows of C channels, each channel by itself:
  *   h_t = a_t h_{t-1} + b_t x_t,   LA_GATE_LOG: a = e^w, b = 1;   LA_GATE_SIGMOID: a = 1 / (1 + e^-w), b = 1 - a
- * A gate whose a is 0 in fp32 (w = -inf, and below some -87) cuts: what came before, infinities and NaN included, has no part in what
- * follows, so packed sequences restart with it; an input whose b is 0 has none either.
+ * A gate whose a is 0 in fp32 (w below some -87: -inf, a type's lowest value) cuts: what came before, infinities and NaN
+ * included (gates that are NaN too), has no part in what follows, so packed sequences restart with it; an input whose b is
+ * 0 has none either.  Gates above 1 (log, w > 0) have to keep the product of any run of rows within fp32, as h itself: where
+ * it is not, 0 stays 0 and anything else becomes infinite, however small it was.
  *   X, W, H   in, in, out: [B,N,C] of `dtype`
  *   h0        in : float [B,C], the value before the first row, or NULL for 0
  *   h_last    out: float [B,C], the value after the last row (h0 when N = 0), or NULL
