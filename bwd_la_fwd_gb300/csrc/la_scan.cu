@@ -74,18 +74,28 @@ __device__ __forceinline__ void store1(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) { *(__nv_bfloat162 *)p = __floats2bfloat162_rn(x, y); }
 __device__ __forceinline__ void store2(float *p, float x, float y) { *(float2 *)p = make_float2(x, y); }
 
+// The larger of the two; NaN stays NaN.
+__device__ __forceinline__ float at_least(float x, float least) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(least));
+    return y;
+}
 // e^w: 2^(w log2 e) by the hardware's 2^x, within 2 ulp, and the product's rounding error put back: 5 half steps in all.
-// Below 2^-126: 0.  Where the power is 0 or infinite there is nothing to put back, and the error of a product past fp32's
-// range (w near the type's lowest value) is no number that could be.
+// Below 2^-126: 0; w is held where that error is a number (near the type's lowest value the product is infinite).  Where the
+// power is infinite, infinite or NaN: grown() tells.
 __device__ __forceinline__ float2 exp_of(float2 w) {
+    w = make_float2(at_least(w.x, -200.f), at_least(w.y, -200.f));
     const float2 y = mul2(w, both(1.44269502f));
     float2 t = fma2(w, both(1.92596299e-8f), fma2(w, both(1.44269502f), make_float2(-y.x, -y.y)));
     t = mul2(t, both(0.693147182f));
     float2 e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
-    const float2 r = fma2(e, t, e);
-    return make_float2(fabsf(y.x) < 128.f ? r.x : e.x, fabsf(y.y) < 128.f ? r.y : e.y);
+    return fma2(e, t, e);
+}
+// e^w where it may be infinite: at 88.7228394, whose product with log2 e rounds to 128, and above.
+__device__ __forceinline__ float2 grown(float2 a, float2 w) {
+    return make_float2(w.x >= 88.7228394f ? INFINITY : a.x, w.y >= 88.7228394f ? INFINITY : a.y);
 }
 
 // a and b of two gates.  The sigmoid's smaller half comes from e^-|w|, so that neither loses its leading digits.
@@ -108,13 +118,11 @@ template <int GATE> __device__ __forceinline__ float gated(float b, float x) {
     return GATE == LA_GATE_LOG ? x : (b == 0.f ? 0.f : b * x);
 }
 
-// h -> a h + v, with a = 0 a cut, and with 0 kept 0 by a product of gates that is beyond fp32.
-__device__ __forceinline__ float cut(float a, float h) {
-    return a == 0.f || (h == 0.f && a > 0.f) ? 0.f : __fmul_rn(a, h);
-}
-__device__ __forceinline__ float apply(float a, float v, float h) {
-    return a == 0.f || (h == 0.f && a > 0.f) ? v : fmaf(a, h, v);
-}
+// h -> a h + v, with a = 0 a cut.
+__device__ __forceinline__ float apply(float a, float v, float h) { return a == 0.f ? v : fmaf(a, h, v); }
+__device__ __forceinline__ float cut(float a, float h) { return a == 0.f ? 0.f : __fmul_rn(a, h); }
+// The same with a product of gates, which may be beyond fp32: 0 stays 0.
+__device__ __forceinline__ float enter(float a, float v, float h) { return a == 0.f || (h == 0.f && a > 0.f) ? v : fmaf(a, h, v); }
 // A cut among the gates makes the product one, whatever the others are.
 __device__ __forceinline__ float product(float a, float b) {
     const float p = a * b;
@@ -130,7 +138,7 @@ __device__ __forceinline__ bool plain(const Map2 &m) {
     return m.a0 > 0.f && m.a0 < INFINITY && m.a1 > 0.f && m.a1 < INFINITY && fabsf(m.v0) < INFINITY && fabsf(m.v1) < INFINITY;
 }
 __device__ __forceinline__ Map2 then(const Map2 &f, const Map2 &g) {  // first f, then g
-    return Map2{product(f.a0, g.a0), apply(g.a0, g.v0, f.v0), product(f.a1, g.a1), apply(g.a1, g.v1, f.v1)};
+    return Map2{product(f.a0, g.a0), enter(g.a0, g.v0, f.v0), product(f.a1, g.a1), enter(g.a1, g.v1, f.v1)};
 }
 
 // CH: channels of a CTA.
@@ -161,6 +169,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
         // A CTA's shared memory may be written by others once it has begun: said here, waited for before the first such write.
         if (ncta > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     }
+    // Forward, rank is not to be known to be 0: row addresses are then formed where they are used (8 x 2048 x 2048, sigmoid,
+    // bf16: 47.6 us where 49.5; the gradient is slower so, 79.5 where 77).
+    if (!BACK) asm volatile("" : "+r"(rank));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int block = (int)(blockIdx.x / (unsigned)ncta);
     const long long b = block / P.cblocks;
@@ -228,7 +239,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
         }
         Map2 m{A.x, V.x, A.y, V.y};
         if (__any_sync(0xffffffffu, !plain(m))) {
-            if (!BACK && GATE == LA_GATE_SIGMOID) {  // an input that the gate shuts out has no part
+            if (GATE == LA_GATE_LOG) {
+#pragma unroll
+                for (int j = 0; j < SEG; ++j) a[j] = grown(a[j], load2(wt + j * CH));
+            } else if (!BACK) {  // an input that the gate shuts out has no part
 #pragma unroll
                 for (int j = 0; j < SEG; ++j) {
                     float2 t, g;
@@ -260,20 +274,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
     };
     // the maps of the warp's runs up to and with this lane's: plainly, and again with cuts as in map_of
     auto upto = [&](const Map2 &mine) {
-        if (RUNS == 1) return mine;
         Map2 m = mine;
 #pragma unroll
         for (int d = 1; d < RUNS; d *= 2) {
             const Map2 before = shuffled(m, (run - d) * LANES + pair);
-            if (run >= d) m = Map2{before.a0 * m.a0, fmaf(m.a0, before.v0, m.v0), before.a1 * m.a1, fmaf(m.a1, before.v1, m.v1)};
-        }
-        if (__any_sync(0xffffffffu, !plain(m))) {
-            m = mine;
-#pragma unroll
-            for (int d = 1; d < RUNS; d *= 2) {
-                const Map2 before = shuffled(m, (run - d) * LANES + pair);
-                if (run >= d) m = then(before, m);
-            }
+            if (run >= d) m = then(before, m);
         }
         return m;
     };
@@ -314,8 +319,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
         cluster.sync();  // the maps are there, and no CTA writes to another from here on
         for (int k = 0; k < rank; ++k) {
             const Map2 g = of_cta[k][pair];
-            carry.x = apply(g.a0, g.v0, carry.x);
-            carry.y = apply(g.a1, g.v1, carry.y);
+            carry.x = enter(g.a0, g.v0, carry.x);
+            carry.y = enter(g.a1, g.v1, carry.y);
         }
     }
 #pragma unroll
@@ -347,13 +352,13 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
             for (int k = 0; k < kWarps; ++k) {
                 if (k == warp) h = end;
                 const Map2 g = of_warp[r & 1][k][pair];
-                end = make_float2(apply(g.a0, g.v0, end.x), apply(g.a1, g.v1, end.y));
+                end = make_float2(enter(g.a0, g.v0, end.x), enter(g.a1, g.v1, end.y));
             }
         }
         carry = end;
         if (RUNS > 1) {  // through the warp's runs before this lane's
             const Map2 before = shuffled(sofar, (run - 1) * LANES + pair);
-            if (run > 0) h = make_float2(apply(before.a0, before.v0, h.x), apply(before.a1, before.v1, h.y));
+            if (run > 0) h = make_float2(enter(before.a0, before.v0, h.x), enter(before.a1, before.v1, h.y));
         }
         const bool whole = b0 + RUNS * SEG <= P.N && c0 + CH <= P.C;  // the same for the warp: no row or channel is missing
         // The rows from the value that they are entered with: plainly, and again with cuts where that ends in something
@@ -525,6 +530,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const T *x, const T 
     }
     float2 a, g;
     gate<GATE>(wv, a, g);
+    if (GATE == LA_GATE_LOG) a = grown(a, wv);
     const float h0 = apply(a.x, gated<GATE>(g.x, xv.x), st[0]);
     st[0] = h0;
     if (!two) {
