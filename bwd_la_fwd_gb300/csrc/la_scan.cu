@@ -38,6 +38,7 @@ namespace scan {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxRows = 0x7fffffff - 1024;  // the end of a round, of at most 512 rows, is an int
 constexpr int kMaxCluster = 16;  // parts that time is cut into
 constexpr int kEnough = 228, kFew = 76;  // CTAs: three for two SMs, one for two SMs
 
@@ -554,7 +555,7 @@ template <typename T> cudaError_t step(const void *x, const void *w, void *h, fl
 int check_kind(int B, int N, int C, int gate_kind, int dtype, bool *empty) {
     if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
     if (gate_kind != LA_GATE_LOG && gate_kind != LA_GATE_SIGMOID) return LA_ERR_INVALID_ARG;
-    if (B < 0 || N < 0 || C < 0) return LA_ERR_INVALID_ARG;
+    if (B < 0 || N < 0 || N > kMaxRows || C < 0) return LA_ERR_INVALID_ARG;
     if ((long long)B * C >= (1LL << 40) / (N > 0 ? N : 1)) return LA_ERR_INVALID_ARG;
     *empty = B == 0 || C == 0;
     return LA_OK;

@@ -306,7 +306,7 @@ int la_rotary_backward(const void *dQr, const void *dKr, void *dQ, void *dK, con
  * 0 has none either.  Gates above 1 (log, w > 0) have to keep the product of any run of rows within fp32, as h itself: where
  * it is not, 0 stays 0 and anything else becomes infinite, however small it was (0 and one infinite gate, w above 88.7, give
  * NaN).
- *   X, W, H   in, in, out: [B,N,C] of `dtype`
+ *   X, W, H   in, in, out: [B,N,C] of `dtype`;  N < 2^31 - 1024
  *   h0        in : float [B,C], the value before the first row, or NULL for 0
  *   h_last    out: float [B,C], the value after the last row (h0 when N = 0), or NULL
  *   strides   in : host array, (batch, row) element strides of X, W, H (6 values; the rules of the strided passes), or

@@ -1,0 +1,19 @@
+"""Sizes at the ends of the kernels' index arithmetic are refused on the host (no GPU: nothing is launched)."""
+INT_MAX = 2 ** 31 - 1
+
+
+def test_the_recurrence_refuses_more_rows_than_its_rounds_number():
+    """The last round's end has to be an int; B = 0 does nothing, after the sizes' checks."""
+    from bwd_la_fwd_gb300 import la
+    lib = la.load_library()
+
+    def forward(N, B=1):
+        return lib.la_gated_scan(0x10000, 0x1000000000000, None, 0x2000000000000, None, B, N, 8, 0, 1, None, None)
+
+    def backward(N, B=1):
+        return lib.la_gated_scan_backward(*((k + 1) << 48 for k in range(4)), None, None, 5 << 48, 6 << 48, None, B, N, 8, 0,
+                                          1, None, None)
+
+    for f in (forward, backward):
+        assert f(INT_MAX) == 1 and f(INT_MAX - 1023) == 1
+        assert f(INT_MAX, B=0) == 1 and f(INT_MAX - 1024, B=0) == 0
