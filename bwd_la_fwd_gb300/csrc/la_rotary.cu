@@ -28,6 +28,8 @@ constexpr int kThreads = 256;
 constexpr int kMaxPairs = 128;  // D <= 256
 constexpr int kTable = 1024;    // sines of a block
 constexpr int kAhead = 4;       // heads of a thread on their way
+// A block's last row and a thread's last head on its way are ints.
+constexpr int kMaxRows = 0x7fffffff - 1024, kMaxHeads = (1 << 30) - 1;
 
 struct Side {  // Q or K: from, to, their (batch, head, row) strides in elements
     const void *x;
@@ -225,7 +227,8 @@ int rotary(const void *Q, const void *K, void *Qr, void *Kr, const unsigned long
            long long position_stride, long long first, int interleaved, float magnitude, int inverse, int B, int Hq,
            int Hk, int N, int D, int R, int dtype, const long long *strides, void *stream) {
     if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
-    if (B < 0 || N < 0 || Hq < 1 || Hk < 0 || D < 1) return LA_ERR_INVALID_ARG;
+    if (B < 0 || N < 0 || N > kMaxRows || Hq < 1 || Hk < 0 || D < 1) return LA_ERR_INVALID_ARG;
+    if ((long long)Hq + Hk > kMaxHeads) return LA_ERR_INVALID_ARG;
     const int elem = dtype == LA_BF16 ? 2 : 4;
     if (D > 2 * kMaxPairs || (D * elem) % 16 != 0) return LA_ERR_UNSUPPORTED;
     if (R < 2 || R > D || R % 2 != 0 || !freq) return LA_ERR_INVALID_ARG;

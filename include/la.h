@@ -268,7 +268,8 @@ int la_prompt(const void *Q, const void *K, const void *V, const int *seq_offset
  * Rotary positions.  Pair i of a row at position p is turned by p f_i and scaled by `magnitude` m:
  *   y1 = m (x1 cos - x2 sin),  y2 = m (x1 sin + x2 cos)
  * A pair is channels (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with `interleaved`; channels from rotary_dim on are
- * copied.  Q [B,Hq,N,D] and K [B,Hk,N,D] (Hk = 0: none, K and Kr unused) go in one launch.
+ * copied.  Q [B,Hq,N,D] and K [B,Hk,N,D] (Hk = 0: none, K and Kr unused) go in one launch; N < 2^31 - 1024,
+ * Hq + Hk < 2^30.
  *   frequencies      in : HOST array [rotary_dim / 2], f_i / 2 pi in units of 2^-64 turns per position, read during the
  *                    call; la_rotary_frequencies fills one.  The phase p f_i is then exact for every position.
  *   positions        in : device int, the position of (b, i) at positions[b position_stride + i] (position_stride 0:
