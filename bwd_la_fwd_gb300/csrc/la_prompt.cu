@@ -7,6 +7,7 @@
 // la_decode_step_grouped continues from.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "la_f32x2.cuh"
@@ -26,9 +27,9 @@ namespace prompt {
 // w + 8, ..., one lane per column (and per row j of W), so a query head's rows stay within a warp.
 //
 // fp32 tokens keep an fp64 state, as la_decode_step does, but this GPU has two fp64 multiply-adds per SM and clock;
-// a sum is therefore two floats here (the product's and the sum's rounding errors are exact in fp32 and gathered in
-// the low one), good to 2^-46, and becomes a double once, at the end.  O is formed in fp32 from the high floats, so the
-// second walk sums in plain fp32.  1,500 tokens in 7 sequences, 8 query and 4 key/value heads of 64, fp32: 68 us (one
+// a sum of rows is therefore two floats here (the product's and the sum's rounding errors, exact in fp32 by Dekker's and
+// Knuth's steps, are gathered in the low one), good to 2^-46, and becomes a double once, when it is added to the state that
+// the sequence started from.  O is formed in fp32 from the high floats, so the second walk sums in plain fp32.  1,500 tokens in 7 sequences, 8 query and 4 key/value heads of 64, fp32: 66 us (one
 // walk for both, one CTA to a sequence: 405 us; the whole exchange in every CTA and scalar multiply-adds: 92 us).
 // Bound by fp32 arithmetic, ten operations for a product of the sums, in the SMs that have the longest sequence's
 // cluster: a block of 32 rows takes a CTA 4 us for the sums and 5 us for O, and up to three share an SM.
@@ -73,7 +74,8 @@ template <> struct Sum<float> {
         add(s.hi);
         lo = __fadd_rn(lo, s.lo);
     }
-    __device__ double get() const { return (double)hi + (double)lo; }
+    // (an infinite sum's error is no number)
+    __device__ double get() const { return fabsf(hi) < INFINITY ? (double)hi + (double)lo : (double)hi; }
 };
 
 // a += x.x y, b += x.y y; the two floats of each in ten packed operations.  -p is formed as x (-y), and differences as
@@ -97,6 +99,7 @@ template <typename T, int D> struct Tile {
     static constexpr int RE = 32 / E;               // halves of a warp that share the sums of O (2 where E = 16)
     static constexpr int NS = D * E / kThreads;     // elements of S of a thread: column t % E, rows from t / E * NS
     static constexpr int PER = kRows / kWarps;      // rows of a block of a warp
+    static constexpr int PER_SM = D <= 64 ? 3 : D == 128 ? 2 : 1;  // CTAs that registers leave room for (of the case above: two 70 us)
     static constexpr size_t FLOATS = 2 * kRows * LD + kRows * E + kRows * kRows + D * E + D + E;
     static constexpr int SUMS = D * E + D + E;      // S, z and a of a CTA
     static constexpr size_t SMEM = sizeof(float) * FLOATS + sizeof(Sum<T>) * SUMS + sizeof(typename Sum<T>::Acc) * D;
@@ -118,7 +121,7 @@ __device__ __forceinline__ void load_rows(float *dst, int pitch, const T *src, l
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_constant__ Args A) {
+__global__ void __launch_bounds__(kThreads, Tile<T, D>::PER_SM) prompt_simt_kernel(const __grid_constant__ Args A) {
     using C = Tile<T, D>;
     using Acc = typename Sum<T>::Acc;
     constexpr int E = C::E, LD = C::LD, NS = C::NS, PER = C::PER;
@@ -196,8 +199,10 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
         for (int x = part * per + t; x < min((part + 1) * per, C::SUMS); x += kThreads) {
             const bool of_z = x >= D * E && x < D * E + D;
             Acc *state = x < D * E ? S + (long long)(x / E) * D + e0 + x % E : of_z ? z + (x - D * E) : a + e0 + (x - D * E - D);
-            Sum<T> run;
-            run.set(resume ? of_z ? z0[x - D * E] : *state : (Acc)0);
+            auto start = [&] { return resume ? of_z ? z0[x - D * E] : *state : (Acc)0; };
+            float run = (float)start();  // the state before each part, as O takes it
+            Sum<T> rows;              // the sum of all parts: added to the whole of an fp64 state, once
+            rows.set(0);
             constexpr int kAhead = 8;
             for (int p0 = 0; p0 < parts; p0 += kAhead) {
                 Sum<T> v[kAhead];
@@ -207,11 +212,13 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
 #pragma unroll
                 for (int p = 0; p < kAhead; ++p)
                     if (p0 + p < parts) {
-                        *cluster.map_shared_rank(Sf + x, (p0 + p) * gridDim.y + blockIdx.y) = run.hi;  // Sf, zs, as in a row
-                        run.join(v[p]);
+                        *cluster.map_shared_rank(Sf + x, (p0 + p) * gridDim.y + blockIdx.y) = run;  // Sf, zs, as in a row
+                        run += v[p].hi;
+                        rows.join(v[p]);
                     }
             }
-            if (S && (!of_z || blockIdx.y == 0)) *state = run.get();
+            if (S && (!of_z || blockIdx.y == 0) && !(resume && len == 0))
+                *state = sizeof(Acc) == 8 ? (Acc)(start() + rows.get()) : (Acc)run;
         }
         if (S && part == 0 && blockIdx.y == 0 && t == 0) A.n[at] = n0 + len;
     }

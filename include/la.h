@@ -256,6 +256,8 @@ int la_decode_step_grouped(const void *q, const void *k, const void *v, void *o,
  *   strides      in : host array, (head, row) element strides of Q, K, V, O (8 values; the rules of the strided
  *                passes), or NULL for contiguous [T,H,D]
  *   workspace    in/out: workspace_bytes >= la_prompt_workspace_bytes(), under the workspace rules above
+ * For fp32 tokens the fp64 state takes the sums of this call's rows, formed in pairs of floats (products and sums within
+ * fp32's range), with all of its own bits, and is left as it is by a resumed sequence without rows; O is formed in fp32.
  * A sequence's rows do not depend on other sequences, nor on the rows around them, whatever those hold (infinities
  * and NaN included).  A NaN or an infinity of its own K or V may reach every row of the sequence.
  */
