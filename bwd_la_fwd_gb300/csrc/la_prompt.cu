@@ -29,8 +29,9 @@ namespace prompt {
 // fp32 tokens keep an fp64 state, as la_decode_step does, but this GPU has two fp64 multiply-adds per SM and clock;
 // a sum of rows is therefore two floats here (the product's and the sum's rounding errors, exact in fp32 by Dekker's and
 // Knuth's steps, are gathered in the low one), good to 2^-46, and becomes a double once, when it is added to the state that
-// the sequence started from.  O is formed in fp32 from the high floats, so the second walk sums in plain fp32.  1,500 tokens in 7 sequences, 8 query and 4 key/value heads of 64, fp32: 66 us (one
-// walk for both, one CTA to a sequence: 405 us; the whole exchange in every CTA and scalar multiply-adds: 92 us).
+// the sequence started from.  O is formed in fp32 from the high floats, so the second walk sums in plain fp32.  1,500 tokens
+// in 7 sequences, 8 query and 4 key/value heads of 64, fp32: 66 us (one walk for both, one CTA to a sequence: 405 us; the
+// whole exchange in every CTA and scalar multiply-adds: 92 us).
 // Bound by fp32 arithmetic, ten operations for a product of the sums, in the SMs that have the longest sequence's
 // cluster: a block of 32 rows takes a CTA 4 us for the sums and 5 us for O, and up to three share an SM.
 // ----------------------------------------------------------------------------------------------------------------
@@ -372,18 +373,36 @@ template <typename T, int D> cudaError_t launch_simt(const Args &A, cudaStream_t
     return cudaLaunchKernelEx(&cfg, prompt_simt_kernel<T, D>, A);
 }
 
-template <typename T> cudaError_t simt_by_d(const Args &A, cudaStream_t s) {
-    switch (A.D) {
-        case 16: return launch_simt<T, 16>(A, s);
-        case 32: return launch_simt<T, 32>(A, s);
-        case 64: return launch_simt<T, 64>(A, s);
-        case 128: return launch_simt<T, 128>(A, s);
-        default: return launch_simt<T, 256>(A, s);
+cudaError_t simt(const Args &A, int dtype, cudaStream_t s) {
+    cudaError_t e;
+    if (dtype == LA_BF16) {
+        e = A.D == 16 ? launch_simt<__nv_bfloat16, 16>(A, s) : launch_simt<__nv_bfloat16, 256>(A, s);
+    } else {
+        switch (A.D) {
+            case 16: e = launch_simt<float, 16>(A, s); break;
+            case 32: e = launch_simt<float, 32>(A, s); break;
+            case 64: e = launch_simt<float, 64>(A, s); break;
+            case 128: e = launch_simt<float, 128>(A, s); break;
+            default: e = launch_simt<float, 256>(A, s);
+        }
     }
+    if (e == cudaSuccess) count_launches(1);
+    return e;
 }
 
-cudaError_t simt(const Args &A, int dtype, cudaStream_t s) {
-    const cudaError_t e = dtype == LA_BF16 ? simt_by_d<__nv_bfloat16>(A, s) : simt_by_d<float>(A, s);
+// T = 0: a sequence that starts empty leaves an empty state, one that is continued its own.
+template <typename Acc> __global__ void __launch_bounds__(kThreads) no_rows_kernel(const __grid_constant__ Args A) {
+    if (!offsets_in_order(A) || !A.S || A.resume) return;
+    const long long at = blockIdx.x;
+    for (int x = threadIdx.x; x < A.D * A.D; x += kThreads) ((Acc *)A.S)[at * A.D * A.D + x] = 0;
+    for (int x = threadIdx.x; x < A.D; x += kThreads) ((Acc *)A.z)[at * A.D + x] = ((Acc *)A.a)[at * A.D + x] = 0;
+    if (threadIdx.x == 0) A.n[at] = 0;
+}
+
+cudaError_t no_rows(const Args &A, int dtype, cudaStream_t s) {
+    auto *k = dtype == LA_BF16 ? no_rows_kernel<float> : no_rows_kernel<double>;
+    k<<<(unsigned)(A.nseq * A.Hkv), kThreads, 0, s>>>(A);
+    const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
@@ -470,10 +489,10 @@ int la_prompt(const void *Q, const void *K, const void *V, const int *seq_offset
     A.qh = v[0].st[1], A.qn = v[0].st[2], A.kh = v[1].st[1], A.kn = v[1].st[2];
     A.vh = v[2].st[1], A.vn = v[2].st[2], A.oh = v[3].st[1], A.on = v[3].st[2];
     A.status = (uint32_t *)workspace;
-    // without rows there is nothing to map for the tensor-core form; the other one leaves the states as they should be
-    const cudaError_t e = tc_supported(D, dtype) && T > 0
-                              ? tensor_cores(A, (unsigned char *)workspace, (cudaStream_t)stream)
-                              : simt(A, dtype, (cudaStream_t)stream);
+    cudaStream_t cs = (cudaStream_t)stream;
+    const cudaError_t e = T == 0 ? no_rows(A, dtype, cs)
+                          : tc_supported(D, dtype) ? tensor_cores(A, (unsigned char *)workspace, cs)
+                                                   : simt(A, dtype, cs);
     return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 

@@ -39,7 +39,7 @@ __device__ __forceinline__ bool offsets_in_order(const Args &A) {
 bool tc_supported(int D, int dtype);  // the tensor-core form: bf16, D = 32, 64, 128
 size_t tc_workspace_bytes(int T, int nseq, int Hkv, int r, int D);
 cudaError_t tensor_cores(const Args &A, unsigned char *ws, cudaStream_t s);  // T > 0
-cudaError_t simt(const Args &A, int dtype, cudaStream_t s);
+cudaError_t simt(const Args &A, int dtype, cudaStream_t s);  // T > 0, what tensor_cores() does not do
 
 }  // namespace prompt
 }  // namespace la

@@ -1,4 +1,4 @@
-"""What la_prompt does to a state of fp32 tokens (64 bits): it continues from all of its bits."""
+"""What la_prompt does to the state that it continues from: it keeps all of its bits (64 of them for fp32 tokens)."""
 import math
 
 import pytest
@@ -33,6 +33,28 @@ def test_a_sequence_without_rows_keeps_its_state(D, rows):
         for t, was in zip((state.S, state.z, state.a, state.n), before):
             assert torch.equal(torch.nan_to_num(t[i].double(), 7.0, 8.0, 9.0), torch.nan_to_num(was[i].double(), 7.0, 8.0, 9.0))
             assert torch.equal(torch.isfinite(t[i]), torch.isfinite(was[i]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [16, 64, 128, 256])
+@pytest.mark.parametrize("rows", [0, 200])
+def test_a_bf16_sequence_without_rows_keeps_its_state(D, rows):
+    """Between sequences with rows and without any; unresumed, it is emptied."""
+    from bwd_la_fwd_gb300 import la
+    off = _offsets([0, rows, 0])
+    q, k, v = _tokens(off[-1], 4, 2, D, "bf16", seed=D)
+    state = _state(3, 2, D, "bf16")
+    _fill(state, D)
+    state.S[0, 0, 3, 5], state.z[0, 1, 2], state.a[2, 0, 1] = math.inf, -math.inf, math.nan
+    before = [t.clone() for t in (state.S, state.z, state.a, state.n)]
+    o = torch.tensor(off, dtype=torch.int32, device="cuda")
+    la.la_prompt(q, k, v, o, state, resume=True)
+    for i in (0, 2) if rows else (0, 1, 2):
+        for t, was in zip((state.S, state.z, state.a, state.n), before):
+            assert torch.equal(torch.nan_to_num(t[i].double(), 7.0, 8.0, 9.0), torch.nan_to_num(was[i].double(), 7.0, 8.0, 9.0))
+    la.la_prompt(q, k, v, o, state)
+    for i in (0, 2) if rows else (0, 1, 2):
+        assert not any(bool(t[i].any()) for t in (state.S, state.z, state.a, state.n))
 
 
 @pytest.mark.gpu
