@@ -134,7 +134,7 @@ __device__ __forceinline__ float product(float a, float b) {
 struct Map2 {
     float a0, v0, a1, v1;
 };
-// Whether a map that was formed by plain products and sums is what it has to be: nothing was cut, nothing overflowed.
+// Whether a map formed by plain products and sums is right as it is: nothing was cut, nothing overflowed or vanished.
 __device__ __forceinline__ bool plain(const Map2 &m) {
     return m.a0 > 0.f && m.a0 < INFINITY && m.a1 > 0.f && m.a1 < INFINITY && fabsf(m.v0) < INFINITY && fabsf(m.v1) < INFINITY;
 }
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
         return Map2{__shfl_sync(0xffffffffu, m.a0, from), __shfl_sync(0xffffffffu, m.v0, from),
                     __shfl_sync(0xffffffffu, m.a1, from), __shfl_sync(0xffffffffu, m.v1, from)};
     };
-    // the maps of the warp's runs up to and with this lane's: plainly, and again with cuts as in map_of
+    // the maps of the warp's runs up to and with this lane's
     auto upto = [&](const Map2 &mine) {
         Map2 m = mine;
 #pragma unroll
@@ -676,7 +676,7 @@ int la_gated_scan_step(const void *x, const void *w, void *h, float *state, int 
     long long st[3];
     for (int k = 0; k < 3; ++k) {  // (x, w, h): the row stride of [B, C]
         const long long row[2] = {strides ? strides[k] : C, C};
-        // a dense [B, C] needs no row of whole vectors: two channels of a row are loaded at a time where C is even
+        // (several rows have to be whole 16-byte vectors apart, as everywhere; C itself may be odd)
         if ((rc = check_op(v[k], ptr[k], B, 1, C, elem, row))) return rc;
         st[k] = v[k].st[0];
     }

@@ -416,8 +416,9 @@ def la_prompt(Q, K, V, seq_offsets, state=None, resume: bool = False, O=None, wo
     Q [T,Hq,D], K and V [T,Hkv,D] (strided views with contiguous D are taken as they are); sequence i has rows
     seq_offsets[i] ... seq_offsets[i+1] - 1 (int32 on the device).  ``state``, a DecodeState(nseq, Hkv, D), receives
     each sequence's state, or with ``resume`` continues from it.  Rows outside every sequence keep what O holds (a new
-    O is zero there).  Offsets that are not in order within [0, T] compute nothing, which la_get_status tells of a
-    ``workspace`` that the caller passes."""
+    O is zero there).  Offsets that are not in order within [0, T] compute nothing, and la_get_status(workspace) tells so:
+    a caller that does not know them to be in order passes a ``workspace`` (new_prompt_workspace; one for the largest T and
+    nseq serves smaller calls too).  One made for a single call, and zeroed for it, is gone with its status."""
     import torch
     if Q.dim() != 3 or K.dim() != 3 or seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1:
         raise ValueError("expected [T, H, D] tensors and [nseq + 1] offsets")
