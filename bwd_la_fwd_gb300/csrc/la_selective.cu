@@ -1,0 +1,830 @@
+// la_selective.cu -- selective state space scan (la_selective_scan), its gradients (la_selective_scan_backward) and one
+// token of it (la_selective_scan_step).
+//
+//   d = softplus(dt + dt_bias) or dt + dt_bias,   h_t[c,n] = e^(d A[c,n]) h_{t-1}[c,n] + d x B_t[n]
+//   y = sum_n C_t[n] h_t[c,n] + D x,   out = y z sigmoid(z)   (or y)
+//   backward, with g = dout z sigmoid(z) and G_t = g C_t + a_{t+1} G_{t+1} (a = e^(d A)):
+//   dx = d sum_n G B + D g,  dd = sum_n a h_{t-1} G A + x sum_n G B,  dA = sum_t d a h_{t-1} G,  dB = sum_c G d x,
+//   dC = sum_c g h,  dD = sum_t g x,  dz = dout y (z sigmoid(z))'
+//
+// A thread holds four states of a channel in registers; S / 4 lanes are a channel, and a CTA has kWarps warps of them.  It
+// walks rows in tiles: all threads form d and d x of a tile (a vector of channels each, whose x, dt, z are loaded while the
+// tile before is scanned), then each walks its states over the tile's rows, reading d, d x, B, C from shared memory, then
+// all write the tile's outputs.  Everything is held in fp32.  A T x C x S scan has T C S exponentials and 4 T C S
+// multiply-adds (16 lane operations of the fp32 pipe, and as many of the special-function unit at half its rate, for
+// four states and a row), which is more than HBM takes for the tensors: issue slots bound it.
+// Where there are few channels time is cut into parts: a first launch forms each part's last state, started from zero (the
+// first part of a sequence: from its state), and the sum of its d, whose e^(A sum) is the part's decay; the second launch
+// folds them into the state that each part starts from.
+#include <math.h>
+
+#include "la_f32x2.cuh"
+#include "la_rows.cuh"
+
+namespace la {
+namespace sel {
+
+using namespace rows;
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kMark = 16;      // rows between the states that a forward keeps for its backward
+constexpr int kSMs = 152;
+constexpr int kMaxParts = 64;  // of a sequence
+
+struct GOp {                   // B, C: [.., G, S]
+    const void *p;
+    long long sb, sn, sg;
+};
+
+struct Params {
+    Op x, dt, z, y;            // z.p null: no gate
+    GOp B, C;
+    const float *A, *D, *bias;
+    const float *first;        // [nseq, C, S] or null
+    float *last, *marks;       // [nseq, C, S], [slots, C, S], or null
+    Seqs seq;
+    int C_, G, cpg, bpg;       // channels, groups, channels and blocks of a group
+    int part, parts;           // rows of a part (a multiple of the tile's); units in all
+    int softplus;
+    float *ends, *sums;        // [units, C, S], [units, C]: parts' last states and sums of d
+    // backward
+    Op dO, dx, ddt, dz;
+    const float *dlast;        // [nseq, C, S] or null
+    float *dfirst;
+    float *pbc;                // [bpg, T, G, 2 S]
+    float *pa;                 // [walkers, C, S], then [walkers, C] of dD and of d(dt_bias)
+    int walkers;
+    uint32_t *valid;           // whether the offsets were in order, for the sums behind
+};
+
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// log(1 + e^v) = max(v, 0) + log1p(e^-|v|)
+__device__ __forceinline__ float softplus_of(float v) { return fmaxf(v, 0.f) + log1pf(exp_fast(-fabsf(v))); }
+__device__ __forceinline__ float step_of(const Params &P, float v) {
+    // NaN stays NaN (fmaxf would lose it)
+    return P.softplus ? (v != v ? v : softplus_of(v)) : v;
+}
+
+// Four states.
+struct F4 {
+    float2 a, b;
+};
+__device__ __forceinline__ F4 load4(const float *p) {
+    const float4 v = *(const float4 *)p;
+    return F4{make_float2(v.x, v.y), make_float2(v.z, v.w)};
+}
+__device__ __forceinline__ void store4(float *p, const F4 &v) { *(float4 *)p = make_float4(v.a.x, v.a.y, v.b.x, v.b.y); }
+__device__ __forceinline__ F4 zero4() { return F4{both(0.f), both(0.f)}; }
+__device__ __forceinline__ F4 mul4(const F4 &x, const F4 &y) { return F4{mul2(x.a, y.a), mul2(x.b, y.b)}; }
+__device__ __forceinline__ F4 mul4(const F4 &x, float y) { return F4{mul2(x.a, both(y)), mul2(x.b, both(y))}; }
+__device__ __forceinline__ F4 fma4(const F4 &x, const F4 &y, const F4 &z) { return F4{fma2(x.a, y.a, z.a), fma2(x.b, y.b, z.b)}; }
+__device__ __forceinline__ F4 fma4(const F4 &x, float y, const F4 &z) { return F4{fma2(x.a, both(y), z.a), fma2(x.b, both(y), z.b)}; }
+__device__ __forceinline__ float dot4(const F4 &x, const F4 &y) {
+    const float2 s = fma2(x.b, y.b, mul2(x.a, y.a));
+    return s.x + s.y;
+}
+__device__ __forceinline__ F4 decay4(const F4 &a2, float d) {  // 2^(a2 d)
+    const F4 e = mul4(a2, d);
+    return F4{make_float2(ex2(e.a.x), ex2(e.a.y)), make_float2(ex2(e.b.x), ex2(e.b.y))};
+}
+
+// Sums over L lanes (q of them this one's number, lanes STEP apart) of L values each; lane q gets value q's.
+template <int L, int STEP> __device__ __forceinline__ float lanes_sum(float (&v)[L], int q) {
+#pragma unroll
+    for (int d = L / 2; d > 0; d /= 2) {
+#pragma unroll
+        for (int i = 0; i < d; ++i) {
+            const bool up = q & d;
+            const float keep = up ? v[i + d] : v[i], send = up ? v[i] : v[i + d];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, d * STEP);
+        }
+    }
+    return v[0];
+}
+
+template <int S> struct Tile {
+    static constexpr int L = S / 4, CW = 32 / L, CH = kWarps * CW;  // lanes of a channel, channels of a warp, of a CTA
+    static constexpr int R = 2 * S;                                 // rows of a forward tile: 8 elements to a thread
+    static constexpr int NB = S * S / 256 > 0 ? S * S / 256 : 1;    // vectors of four of B and C to a thread
+};
+
+// The unit's sequence and part.  A sequence's parts are units i + off[i] / part onwards: there are as many as it needs.
+__device__ __forceinline__ bool unit_of(const Params &P, int unit, int &seq, int &j, int &len) {
+    if (!P.seq.off) {
+        const int per = max(1, (P.seq.N + P.part - 1) / P.part);
+        seq = unit / per, j = unit - seq * per, len = P.seq.N;
+        return true;
+    }
+    int n;
+    if (!offsets_in_order(P.seq, n, [&](int i, int lo) { return i + lo / P.part <= unit; })) return false;
+    seq = n - 1;
+    if (seq < 0) {  // (the first sequence begins behind the first part)
+        j = len = 0;
+        seq = P.seq.nseq;
+        return true;
+    }
+    const int lo = P.seq.off[seq];
+    j = unit - (seq + lo / P.part), len = P.seq.off[seq + 1] - lo;
+    return true;
+}
+__device__ __forceinline__ long long mark_slot(const Params &P, int seq, int row) {
+    const long long lo = P.seq.off ? P.seq.off[seq] : (long long)seq * P.seq.N;
+    return seq + lo / kMark + row / kMark;
+}
+
+// ENDS: the first launch, which forms the parts' last states only.
+template <typename T, int S, bool ENDS>
+__global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_constant__ Params P) {
+    using K = Tile<S>;
+    constexpr int L = K::L, CW = K::CW, CH = K::CH, R = K::R, NB = K::NB;
+    __shared__ __align__(16) float2 dd[R][CH];
+    __shared__ __align__(16) float ys[ENDS ? 1 : R][ENDS ? 4 : CH];
+    __shared__ __align__(16) float bc[2][R][S];
+    const int cblocks = P.G * P.bpg, unit = blockIdx.x / cblocks, cb = blockIdx.x - unit * cblocks;
+    int seq, j, len;
+    if (!unit_of(P, unit, seq, j, len)) return;
+    if (seq >= P.seq.nseq) return;
+    const long long t0 = (long long)j * P.part;
+    if (j > 0 && t0 >= len) return;
+    const int lo = (int)t0, hi = min(len, (int)min(t0 + P.part, (long long)len));
+    if (ENDS && hi == len) return;  // nothing follows
+    const int g = cb / P.bpg, c0 = g * P.cpg + (cb - g * P.bpg) * CH, nc = min(CH, (g + 1) * P.cpg - c0);
+    // this thread's vector of the tile
+    const int er = threadIdx.x / (CH / 8), ec = threadIdx.x % (CH / 8) * 8, en = nc - ec;
+    const T *x = rows_of<const T>(P.seq, P.x, seq) + c0 + ec, *dt = rows_of<const T>(P.seq, P.dt, seq) + c0 + ec;
+    const T *z = P.z.p ? rows_of<const T>(P.seq, P.z, seq) + c0 + ec : nullptr;
+    T *y = ENDS ? nullptr : rows_of<T>(P.seq, P.y, seq) + c0 + ec;
+    const GOp &OB = P.B, &OC = P.C;
+    const T *Bp = (const T *)OB.p + (P.seq.off ? P.seq.off[seq] * OB.sn : seq * OB.sb) + g * OB.sg;
+    const T *Cp = (const T *)OC.p + (P.seq.off ? P.seq.off[seq] * OC.sn : seq * OC.sb) + g * OC.sg;
+    float bias[8], D[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        bias[k] = P.bias && k < en ? P.bias[c0 + ec + k] : 0.f;
+        D[k] = P.D && k < en ? P.D[c0 + ec + k] : 0.f;
+    }
+    // this thread's states
+    const int lane = threadIdx.x & 31, q = lane % L, ch = (threadIdx.x >> 5) * CW + lane / L, c = c0 + ch;
+    const bool mine = ch < nc;
+    F4 a2 = zero4(), h = zero4();
+    if (mine) {
+        a2 = mul4(load4(P.A + (long long)c * S + 4 * q), kLog2e);
+        if (j == 0 || ENDS) {
+            if (P.first && j == 0) h = load4(P.first + ((long long)seq * P.C_ + c) * S + 4 * q);
+        } else {
+            for (int p = unit - j; p < unit; ++p) {
+                const F4 e = load4(P.ends + ((long long)p * P.C_ + c) * S + 4 * q);
+                h = p == unit - j ? e : fma4(decay4(a2, P.sums[(long long)p * P.C_ + c]), h, e);
+            }
+        }
+    }
+    Vec<T, 8> vx, vd, vz, nx, nd, nz;
+    Vec<T, 4> vb[NB];
+    auto fetch = [&](int t) {  // the tile from row t on
+        const bool in = t + er < hi && en > 0;
+        if (in) {
+            nx = load_vec<T, 8>(x + (t + er) * P.x.sn, en);
+            nd = load_vec<T, 8>(dt + (t + er) * P.dt.sn, en);
+            if (!ENDS && z) nz = load_vec<T, 8>(z + (t + er) * P.z.sn, en);
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int v = i * kThreads + threadIdx.x, which = v / (R * S / 4), row = v % (R * S / 4) / (S / 4), col = v % (S / 4) * 4;
+            if (which < (ENDS ? 1 : 2) && t + row < hi)
+                vb[i] = *(const Vec<T, 4> *)((which ? Cp : Bp) + (t + row) * (which ? OC.sn : OB.sn) + col);
+        }
+    };
+    float sum = 0.f;
+    fetch(lo);
+    for (int t = lo; t < hi; t += R) {
+        vx = nx, vd = nd;
+        if (!ENDS) vz = nz;
+        const bool in = t + er < hi && en > 0;
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+            float2 d = make_float2(0.f, 0.f), u = d;  // no row: nothing happens
+            if (in && k < en) d.x = step_of(P, to_f(vd.e[k]) + bias[k]), u.x = d.x * to_f(vx.e[k]);
+            if (in && k + 1 < en) d.y = step_of(P, to_f(vd.e[k + 1]) + bias[k + 1]), u.y = d.y * to_f(vx.e[k + 1]);
+            *(float4 *)&dd[er][ec + k] = make_float4(d.x, u.x, d.y, u.y);
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int v = i * kThreads + threadIdx.x, which = v / (R * S / 4), row = v % (R * S / 4) / (S / 4), col = v % (S / 4) * 4;
+            if (which >= (ENDS ? 1 : 2)) continue;
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t + row < hi) f = make_float4(to_f(vb[i].e[0]), to_f(vb[i].e[1]), to_f(vb[i].e[2]), to_f(vb[i].e[3]));
+            *(float4 *)&bc[which][row][col] = f;
+        }
+        __syncthreads();
+        if (t + R < hi) fetch(t + R);
+        const int rows = min(R, hi - t);
+        for (int r0 = 0; r0 < rows; r0 += kMark) {
+            if (!ENDS && P.marks && mine) store4(P.marks + (mark_slot(P, seq, t + r0) * P.C_ + c) * S + 4 * q, h);
+#pragma unroll
+            for (int r1 = 0; r1 < kMark; r1 += L) {
+                float part[L];
+#pragma unroll
+                for (int i = 0; i < L; ++i) {
+                    const int r = r0 + r1 + i;
+                    const float2 du = dd[r][ch];
+                    h = fma4(decay4(a2, du.x), h, mul4(load4(&bc[0][r][4 * q]), du.y));
+                    if (ENDS) sum += du.x;
+                    else part[i] = dot4(load4(&bc[1][r][4 * q]), h);
+                }
+                if (!ENDS) {
+                    const float s = lanes_sum<L, 1>(part, q);
+                    ys[r0 + r1 + q][ch] = s;
+                }
+            }
+        }
+        __syncthreads();
+        if (!ENDS && in) {
+            Vec<T, 8> out;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float v = fmaf(D[k], to_f(vx.e[k]), ys[er][ec + k]);
+                if (z) {
+                    const float zk = to_f(vz.e[k]);
+                    v *= zk * sigmoid(zk);
+                }
+                put(&out.e[k], v);
+            }
+            store_vec<T, 8>(y + (t + er) * P.y.sn, out, en);
+        }
+    }
+    if (!mine) return;
+    if (ENDS) {
+        store4(P.ends + ((long long)unit * P.C_ + c) * S + 4 * q, h);
+        if (q == 0) P.sums[(long long)unit * P.C_ + c] = sum;
+    } else if (P.last && hi == len) {
+        store4(P.last + ((long long)seq * P.C_ + c) * S + 4 * q, h);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------------- backward
+// A tile is kMark rows, entered with the state that the forward kept.  Its states are formed again into shared memory, then
+// the rows are walked from the last to the first with G; sums over states and over a warp's channels by transposing
+// butterflies of shuffles, the warps' sums of dB and dC through shared memory.
+template <typename T, int S> struct Back {
+    static constexpr int L = S / 4, CW = 32 / L, CH = kWarps * CW, R = kMark;
+    static constexpr int EV = R * CH / kThreads, PER = CH / EV;  // elements of a thread, vectors of a row
+    static constexpr int NBT = 2 * R * S / 4;                    // vectors of four of B and C
+    static constexpr int NB = (NBT + kThreads - 1) / kThreads;
+    struct Smem {
+        float4 hs[R][kThreads];           // the state before each row
+        float2 dd[R][CH];
+        float gs[R][CH], ws[R][CH], es[R][CH], ys[R][CH];
+        float bc[2][R][S];
+        float red[kWarps][R][2 * S];
+    };
+};
+
+template <typename T, int S>
+__global__ void __launch_bounds__(kThreads, 2) backward_kernel(const __grid_constant__ Params P) {
+    using K = Back<T, S>;
+    constexpr int L = K::L, CW = K::CW, CH = K::CH, R = K::R, EV = K::EV, NB = K::NB;
+    extern __shared__ __align__(16) unsigned char raw[];
+    typename K::Smem &M = *(typename K::Smem *)raw;
+    const int cblocks = P.G * P.bpg, walker = blockIdx.x / cblocks, cb = blockIdx.x - walker * cblocks;
+    const int g = cb / P.bpg, c0 = g * P.cpg + (cb - g * P.bpg) * CH, nc = min(CH, (g + 1) * P.cpg - c0);
+    const int er = threadIdx.x / K::PER, ec = threadIdx.x % K::PER * EV, en = nc - ec;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = lane % L, ch = warp * CW + lane / L, c = c0 + ch;
+    const bool mine = ch < nc;
+    float bias[EV], D[EV], dD[EV], dbias[EV];
+#pragma unroll
+    for (int k = 0; k < EV; ++k) {
+        bias[k] = P.bias && k < en ? P.bias[c0 + ec + k] : 0.f;
+        D[k] = P.D && k < en ? P.D[c0 + ec + k] : 0.f;
+        dD[k] = dbias[k] = 0.f;
+    }
+    F4 a2 = zero4(), dA = zero4();
+    if (mine) a2 = mul4(load4(P.A + (long long)c * S + 4 * q), kLog2e);
+    bool fine = true;
+    if (P.seq.off) {
+        int n;
+        fine = offsets_in_order(P.seq, n, [](int, int) { return false; });
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *P.valid = fine;
+    for (int seq = walker; seq < P.seq.nseq && fine; seq += P.walkers) {
+        const int first = P.seq.off ? P.seq.off[seq] : seq * P.seq.N, len = P.seq.off ? P.seq.off[seq + 1] - first : P.seq.N;
+        const T *x = rows_of<const T>(P.seq, P.x, seq) + c0 + ec, *dt = rows_of<const T>(P.seq, P.dt, seq) + c0 + ec;
+        const T *z = P.z.p ? rows_of<const T>(P.seq, P.z, seq) + c0 + ec : nullptr;
+        const T *dO = rows_of<const T>(P.seq, P.dO, seq) + c0 + ec;
+        T *dx = rows_of<T>(P.seq, P.dx, seq) + c0 + ec, *ddt = rows_of<T>(P.seq, P.ddt, seq) + c0 + ec;
+        T *dz = z ? rows_of<T>(P.seq, P.dz, seq) + c0 + ec : nullptr;
+        const GOp &OB = P.B, &OC = P.C;
+        const T *Bp = (const T *)OB.p + (P.seq.off ? first * OB.sn : seq * OB.sb) + g * OB.sg;
+        const T *Cp = (const T *)OC.p + (P.seq.off ? first * OC.sn : seq * OC.sb) + g * OC.sg;
+        F4 carry = zero4();  // a_{t+1} G_{t+1}
+        if (P.dlast && mine) carry = load4(P.dlast + ((long long)seq * P.C_ + c) * S + 4 * q);
+        Vec<T, EV> nx, nd, nz, no;
+        Vec<T, 4> vb[NB];
+        F4 nh = zero4();
+        auto fetch = [&](int t) {
+            if (t + er < len && en > 0) {
+                nx = load_vec<T, EV>(x + (t + er) * P.x.sn, en);
+                nd = load_vec<T, EV>(dt + (t + er) * P.dt.sn, en);
+                no = load_vec<T, EV>(dO + (t + er) * P.dO.sn, en);
+                if (z) nz = load_vec<T, EV>(z + (t + er) * P.z.sn, en);
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int v = i * kThreads + threadIdx.x, which = v / (R * S / 4), row = v % (R * S / 4) / (S / 4), col = v % (S / 4) * 4;
+                if (which < 2 && t + row < len)
+                    vb[i] = *(const Vec<T, 4> *)((which ? Cp : Bp) + (t + row) * (which ? OC.sn : OB.sn) + col);
+            }
+            if (mine) nh = load4(P.marks + (mark_slot(P, seq, t) * P.C_ + c) * S + 4 * q);
+        };
+        const int tiles = (len + R - 1) / R;
+        if (tiles > 0) fetch((tiles - 1) * R);
+        for (int k = tiles - 1; k >= 0; --k) {
+            const int t = k * R;
+            const Vec<T, EV> vx = nx, vd = nd, vz = nz, vo = no;
+            const bool in = t + er < len && en > 0;
+            float d[EV], gg[EV], slope[EV];  // d, g, d's derivative
+#pragma unroll
+            for (int e = 0; e < EV; ++e) {
+                d[e] = gg[e] = slope[e] = 0.f;
+                if (in && e < en) {
+                    const float v = to_f(vd.e[e]) + bias[e];
+                    d[e] = step_of(P, v);
+                    slope[e] = P.softplus ? sigmoid(v) : 1.f;
+                    gg[e] = to_f(vo.e[e]);
+                    if (z) {
+                        const float zk = to_f(vz.e[e]);
+                        gg[e] *= zk * sigmoid(zk);
+                    }
+                }
+                M.dd[er][ec + e] = make_float2(d[e], in && e < en ? d[e] * to_f(vx.e[e]) : 0.f);
+                M.gs[er][ec + e] = gg[e];
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int v = i * kThreads + threadIdx.x, which = v / (R * S / 4), row = v % (R * S / 4) / (S / 4), col = v % (S / 4) * 4;
+                if (which >= 2) continue;
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (t + row < len) f = make_float4(to_f(vb[i].e[0]), to_f(vb[i].e[1]), to_f(vb[i].e[2]), to_f(vb[i].e[3]));
+                *(float4 *)&M.bc[which][row][col] = f;
+            }
+            F4 h = nh;
+            __syncthreads();
+            if (k > 0) fetch(t - R);
+            // the tile's states, and y
+#pragma unroll
+            for (int r1 = 0; r1 < R; r1 += L) {
+                float part[L];
+#pragma unroll
+                for (int i = 0; i < L; ++i) {
+                    const int r = r1 + i;
+                    const float2 du = M.dd[r][ch];
+                    store4((float *)&M.hs[r][threadIdx.x], h);
+                    h = fma4(decay4(a2, du.x), h, mul4(load4(&M.bc[0][r][4 * q]), du.y));
+                    if (P.z.p) part[i] = dot4(load4(&M.bc[1][r][4 * q]), h);
+                }
+                if (P.z.p) {
+                    const float s = lanes_sum<L, 1>(part, q);
+                    M.ys[r1 + q][ch] = s;
+                }
+            }
+            // backwards
+#pragma unroll
+            for (int r1 = R - L; r1 >= 0; r1 -= L) {
+                float pw[L], pe[L];
+#pragma unroll
+                for (int i = L - 1; i >= 0; --i) {
+                    const int r = r1 + i;
+                    const float2 du = M.dd[r][ch];
+                    const float gr = M.gs[r][ch];
+                    const F4 B = load4(&M.bc[0][r][4 * q]), C = load4(&M.bc[1][r][4 * q]);
+                    const F4 before = load4((const float *)&M.hs[r][threadIdx.x]);
+                    const F4 G = fma4(C, gr, carry);
+                    F4 dB = mul4(G, du.y), dC = mul4(h, gr);
+                    pw[i] = dot4(G, B);
+                    carry = mul4(decay4(a2, du.x), G);
+                    const F4 e = mul4(carry, before);
+                    pe[i] = dot4(e, a2);
+                    dA = fma4(e, du.x, dA);
+                    h = before;
+                    // over the warp's channels
+                    float v[8] = {dB.a.x, dB.a.y, dB.b.x, dB.b.y, dC.a.x, dC.a.y, dC.b.x, dC.b.y};
+                    if constexpr (CW >= 8) {
+                        const int p = lane / L;
+                        float s = lanes_sum<8, L>(v, p % 8);
+                        if (CW == 16) s += __shfl_xor_sync(0xffffffffu, s, 8 * L);
+                        if (p < 8) M.red[warp][r][(p & 4) / 4 * S + 4 * q + (p & 3)] = s;
+                    } else {
+                        const int p = lane / L;  // four channels: two values to a lane
+                        float lo[4] = {v[0], v[1], v[2], v[3]}, up[4] = {v[4], v[5], v[6], v[7]};
+                        M.red[warp][r][4 * q + p] = lanes_sum<4, L>(lo, p);
+                        M.red[warp][r][S + 4 * q + p] = lanes_sum<4, L>(up, p);
+                    }
+                }
+                const float w = lanes_sum<L, 1>(pw, q), e = lanes_sum<L, 1>(pe, q);
+                M.ws[r1 + q][ch] = w;
+                M.es[r1 + q][ch] = e;
+            }
+            __syncthreads();
+            if (in) {
+                Vec<T, EV> ox, od, oz;
+#pragma unroll
+                for (int e = 0; e < EV; ++e) {
+                    if (e >= en) break;
+                    const float xe = to_f(vx.e[e]), w = M.ws[er][ec + e];
+                    put(&ox.e[e], fmaf(d[e], w, D[e] * gg[e]));
+                    const float s = fmaf(M.es[er][ec + e], kLn2, xe * w) * slope[e];
+                    put(&od.e[e], s);
+                    dbias[e] += s;
+                    dD[e] = fmaf(gg[e], xe, dD[e]);
+                    if (z) {
+                        const float zk = to_f(vz.e[e]);
+                        put(&oz.e[e], to_f(vo.e[e]) * fmaf(D[e], xe, M.ys[er][ec + e]) * silu_grad(zk, sigmoid(zk)));
+                    }
+                }
+                store_vec<T, EV>(dx + (t + er) * P.dx.sn, ox, en);
+                store_vec<T, EV>(ddt + (t + er) * P.ddt.sn, od, en);
+                if (z) store_vec<T, EV>(dz + (t + er) * P.dz.sn, oz, en);
+            }
+            float *pbc = P.pbc + ((long long)(cb - g * P.bpg) * P.seq.T + first + t) * P.G * 2 * S + g * 2 * S;
+            for (int v = threadIdx.x; v < R * 2 * S; v += kThreads) {
+                const int r = v / (2 * S), n = v % (2 * S);
+                if (t + r >= len) break;
+                float s = M.red[0][r][n];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) s += M.red[w][r][n];
+                pbc[(long long)r * P.G * 2 * S + n] = s;
+            }
+        }
+        if (P.dfirst && mine) store4(P.dfirst + ((long long)seq * P.C_ + c) * S + 4 * q, carry);
+        __syncthreads();  // the last tile's shared memory has been read
+    }
+    if (mine) store4(P.pa + ((long long)walker * P.C_ + c) * S + 4 * q, dA);
+    // dD and the bias: over the tile's rows
+    float *sd = &M.ws[0][0], *sb = &M.es[0][0];
+#pragma unroll
+    for (int e = 0; e < EV; ++e) sd[er * CH + ec + e] = dD[e], sb[er * CH + ec + e] = dbias[e];
+    __syncthreads();
+    float *pd = P.pa + (long long)P.walkers * P.C_ * S + (long long)walker * 2 * P.C_;
+    for (int v = threadIdx.x; v < nc; v += kThreads) {
+        float s = 0.f, b = 0.f;
+        for (int r = 0; r < R; ++r) s += sd[r * CH + v], b += sb[r * CH + v];
+        pd[c0 + v] = s;
+        pd[P.C_ + c0 + v] = b;
+    }
+}
+
+// dB and dC: the channel blocks' sums, rounded once.
+template <typename T, int S> __global__ void __launch_bounds__(256) sum_bc_kernel(const __grid_constant__ Params P, T *dB, T *dC) {
+    if (P.seq.off && *P.valid == 0) return;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, row_w = (long long)P.G * 2 * S, row = i / row_w;
+    const int at = (int)(i - row * row_w);
+    if (row >= P.seq.T) return;
+    if (P.seq.off && (row < P.seq.off[0] || row >= P.seq.off[P.seq.nseq])) return;
+    float s = 0.f;
+#pragma unroll 4
+    for (int b = 0; b < P.bpg; ++b) s += P.pbc[(long long)b * P.seq.T * row_w + i];
+    const int g = at / (2 * S), n = at % (2 * S);
+    put((n < S ? dB : dC) + (row * P.G + g) * S + n % S, s);
+}
+
+// ----------------------------------------------------------------------------------------------------------- step
+// S / 4 lanes to a channel, as above; a block keeps its channels' A and walks `rows` sequences.  Bound by the state's bytes.
+template <typename T, int S> __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Params P, int per) {
+    constexpr int L = S / 4;
+    const int q = threadIdx.x % L, c = (int)((blockIdx.x * (long long)kThreads + threadIdx.x) / L);
+    const bool mine = c < P.C_;
+    const int cc = mine ? c : 0, g = cc / P.cpg;
+    const F4 a2 = mul4(load4(P.A + (long long)cc * S + 4 * q), kLog2e);
+    const float bias = P.bias ? P.bias[cc] : 0.f, D = P.D ? P.D[cc] : 0.f;
+    const int b1 = min((int)(blockIdx.y + 1) * per, P.seq.nseq);
+#pragma unroll 4
+    for (int b = blockIdx.y * per; b < b1; ++b) {
+        float *st = P.last + ((long long)b * P.C_ + cc) * S + 4 * q;
+        const F4 h0 = load4(st);
+        const float x = to_f(((const T *)P.x.p)[b * P.x.sb + cc]);
+        const float d = step_of(P, to_f(((const T *)P.dt.p)[b * P.dt.sb + cc]) + bias);
+        const Vec<T, 4> vb = *(const Vec<T, 4> *)((const T *)P.B.p + b * P.B.sb + g * P.B.sg + 4 * q);
+        const Vec<T, 4> vc = *(const Vec<T, 4> *)((const T *)P.C.p + b * P.C.sb + g * P.C.sg + 4 * q);
+        const F4 B{make_float2(to_f(vb.e[0]), to_f(vb.e[1])), make_float2(to_f(vb.e[2]), to_f(vb.e[3]))};
+        const F4 C{make_float2(to_f(vc.e[0]), to_f(vc.e[1])), make_float2(to_f(vc.e[2]), to_f(vc.e[3]))};
+        const F4 h = fma4(decay4(a2, d), h0, mul4(B, d * x));
+        if (mine) store4(st, h);
+        float y = dot4(C, h);
+#pragma unroll
+        for (int k = L / 2; k > 0; k /= 2) y += __shfl_xor_sync(0xffffffffu, y, k);
+        if (q == 0 && mine) {
+            y = fmaf(D, x, y);
+            if (P.z.p) {
+                const float z = to_f(((const T *)P.z.p)[b * P.z.sb + cc]);
+                y *= z * sigmoid(z);
+            }
+            put((T *)P.y.p + b * P.y.sb + cc, y);
+        }
+    }
+}
+
+// ----------------------------------------------------------------------------------------------------------- host
+int channels_of(int S) { return kWarps * 32 / (S / 4); }
+int blocks_per_group(int C, int G, int S) { return (C / G + channels_of(S) - 1) / channels_of(S); }
+
+// Rows of a part: all, where the sequences' channel blocks make kEnough CTAs, else as many parts of a sequence of the mean
+// length as do, of kLeastPart rows at least.
+constexpr int kEnough = 152, kLeastPart = 512;
+int part_rows(int T, int nseq, int C, int G, int S) {
+    const long long ctas = (long long)nseq * G * blocks_per_group(C, G, S);
+    const int whole = ((T > 0 ? T : 1) + kLeastPart - 1) / kLeastPart * kLeastPart;  // a multiple of every tile
+    if (ctas >= kEnough || T / (nseq > 0 ? nseq : 1) < 2 * kLeastPart) return whole;
+    long long want = (2 * kEnough + ctas - 1) / ctas;
+    if (want > kMaxParts) want = kMaxParts;
+    const long long rows = ((long long)T + nseq * want - 1) / (nseq * want);
+    const long long part = (rows + kLeastPart - 1) / kLeastPart * kLeastPart;
+    return part < whole ? (int)part : whole;
+}
+long long units_of(int T, int nseq, int N, int part, bool packed) {
+    if (packed) return nseq + T / part;
+    return (long long)nseq * (N > 0 ? (N + part - 1) / part : 1);
+}
+int walkers_of(int nseq, int C, int G, int S) {
+    const long long cblocks = (long long)G * blocks_per_group(C, G, S), want = (4 * kSMs + cblocks - 1) / cblocks;
+    return (int)(nseq < want ? nseq : want);
+}
+struct Space {  // byte offsets of the workspace's arrays
+    size_t ends, sums, pbc, pa, bytes;
+};
+Space space_of(int T, int nseq, int C, int G, int S, bool back) {
+    Space w = {};
+    size_t at = 256;
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += (n + 255) & ~(size_t)255;
+        return here;
+    };
+    if (back) {
+        const size_t walkers = walkers_of(nseq, C, G, S);
+        w.pbc = take((size_t)blocks_per_group(C, G, S) * T * G * 2 * S * 4);
+        w.pa = take(walkers * C * (S + 2) * 4);
+    } else {
+        const int part = part_rows(T, nseq, C, G, S);
+        if (part < T) {
+            const size_t units = (size_t)nseq + T / part + 1;  // a batch has no more
+            w.ends = take(units * C * S * 4);
+            w.sums = take(units * C * 4);
+        }
+    }
+    w.bytes = at;
+    return w;
+}
+
+int check_sizes(int nseq, int N, int C, int G, int S, int dtype, bool packed) {
+    if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
+    if (nseq < 0 || N < 0 || C < 1 || G < 1 || S < 1 || C % G != 0) return LA_ERR_INVALID_ARG;
+    const long long T = packed ? N : (long long)nseq * N;
+    if (T > kMaxRows || nseq > kMaxRows || T >= (1LL << 40) / C || (long long)nseq * S >= (1LL << 40) / C ||
+        (long long)G * S >= (1LL << 31) / 2 || T >= (1LL << 40) / ((long long)G * S))
+        return LA_ERR_INVALID_ARG;
+    if ((S != 8 && S != 16 && S != 32) || (G > 1 && (C / G) % 8 != 0)) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+// A [B, N, G, S] operand.
+int group_view(View &v, const void *p, int B, int N, int G, int S, int elem, const long long *strides) {
+    if (!p || ((uintptr_t)p & 15)) return LA_ERR_INVALID_ARG;
+    v = View{p, {B, N, G}, {}, S, elem};
+    const long long dense[3] = {(long long)N * G * S, (long long)G * S, S};
+    return set_view(v, strides ? strides : dense, dense);
+}
+
+// What the three calls share: parameters and views of (X, dt, z, Y or dO) x (batch, row), and B, C x (batch, row, group).
+struct Call {
+    Params P = {};
+    View v[6] = {};
+    Range rin[8] = {};
+};
+int take_inputs(Call &K, const void *X, const void *dt, const float *A, const void *B, const void *C, const float *D,
+                const void *z, const float *bias, const void *other, const float *state, const int *off, int nseq, int N,
+                int Cn, int G, int S, int softplus, int dtype, const long long *strides) {
+    const bool packed = off != nullptr;
+    const int elem = dtype == LA_BF16 ? 2 : 4, batch = packed ? 1 : nseq, T = packed ? N : nseq * N;
+    if (!A || ((uintptr_t)A & 15) || ((uintptr_t)D & 15) || ((uintptr_t)bias & 15) || ((uintptr_t)state & 15) || ((uintptr_t)off & 3))
+        return LA_ERR_INVALID_ARG;
+    const void *ptr[4] = {X, dt, z, other};
+    int rc;
+    for (int k = 0; k < 4 && T > 0; ++k) {
+        if (k == 2 && !z) continue;
+        if ((rc = rows_view(K.v[k], ptr[k], batch, N, Cn, elem, strides ? strides + 2 * k : nullptr))) return rc;
+    }
+    if (T > 0) {
+        if ((rc = group_view(K.v[4], B, batch, N, G, S, elem, strides ? strides + 8 : nullptr))) return rc;
+        if ((rc = group_view(K.v[5], C, batch, N, G, S, elem, strides ? strides + 11 : nullptr))) return rc;
+    }
+    Params &P = K.P;
+    auto op = [&](int k) { return Op{ptr[k], K.v[k].st[0], K.v[k].st[1]}; };
+    P.x = op(0), P.dt = op(1), P.z = op(2), P.y = P.dO = op(3);
+    P.B = GOp{B, K.v[4].st[0], K.v[4].st[1], K.v[4].st[2]};
+    P.C = GOp{C, K.v[5].st[0], K.v[5].st[1], K.v[5].st[2]};
+    P.A = A, P.D = D, P.bias = bias, P.first = state;
+    P.seq = Seqs{off, nseq, N, T, nullptr};
+    P.C_ = Cn, P.G = G, P.cpg = Cn / G, P.bpg = blocks_per_group(Cn, G, S);
+    P.softplus = softplus ? 1 : 0;
+    K.rin[0] = {A, (size_t)Cn * S * 4};
+    K.rin[1] = {D, (size_t)Cn * 4};
+    K.rin[2] = {bias, (size_t)Cn * 4};
+    K.rin[3] = {state, (size_t)nseq * Cn * S * 4};
+    K.rin[4] = {off, ((size_t)nseq + 1) * 4};
+    return LA_OK;
+}
+
+template <typename T, int S> cudaError_t forward(const Params &P, long long units, bool split, cudaStream_t s) {
+    const long long blocks = units * P.G * P.bpg;
+    if (blocks >= (1LL << 31)) return cudaErrorInvalidConfiguration;
+    if (split) {
+        forward_kernel<T, S, true><<<(unsigned)blocks, kThreads, 0, s>>>(P);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        count_launches(1);
+    }
+    forward_kernel<T, S, false><<<(unsigned)blocks, kThreads, 0, s>>>(P);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+template <typename T> cudaError_t forward(const Params &P, int S, long long units, bool split, cudaStream_t s) {
+    return S == 8 ? forward<T, 8>(P, units, split, s) : S == 16 ? forward<T, 16>(P, units, split, s) : forward<T, 32>(P, units, split, s);
+}
+
+template <typename T, int S> cudaError_t backward(const Params &P, void *dB, void *dC, float *dA, float *dD, float *dbias, cudaStream_t s) {
+    using M = typename Back<T, S>::Smem;
+    static std::atomic<int> attr_state[kMaxDevices];
+    if (!once_per_device(attr_state, [] {
+            return cudaFuncSetAttribute(backward_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(M)) == cudaSuccess;
+        }))
+        return cudaErrorInvalidValue;
+    const long long blocks = (long long)P.walkers * P.G * P.bpg;
+    if (blocks > 0) {
+        backward_kernel<T, S><<<(unsigned)blocks, kThreads, sizeof(M), s>>>(P);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        count_launches(1);
+        const long long sums = ((long long)P.seq.T * P.G * 2 * S + 255) / 256;
+        if (sums >= (1LL << 31)) return cudaErrorInvalidConfiguration;
+        if (sums > 0) {
+            sum_bc_kernel<T, S><<<(unsigned)sums, 256, 0, s>>>(P, (T *)dB, (T *)dC);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            count_launches(1);
+        }
+    }
+    const cudaError_t e = sum_parts(P.pa, P.walkers, (long long)P.C_ * S, (long long)P.C_ * S, dA, nullptr, s);
+    return e != cudaSuccess ? e : sum_parts(P.pa + (size_t)P.walkers * P.C_ * S, P.walkers, 2LL * P.C_, P.C_, dD, dbias, s);
+}
+template <typename T> cudaError_t backward(const Params &P, int S, void *dB, void *dC, float *dA, float *dD, float *dbias, cudaStream_t s) {
+    return S == 8 ? backward<T, 8>(P, dB, dC, dA, dD, dbias, s) : S == 16 ? backward<T, 16>(P, dB, dC, dA, dD, dbias, s)
+                                                                       : backward<T, 32>(P, dB, dC, dA, dD, dbias, s);
+}
+
+template <typename T, int S> cudaError_t step(const Params &P, cudaStream_t s) {
+    const long long across = ((long long)P.C_ * (S / 4) + kThreads - 1) / kThreads;
+    // Sequences to a block, which read A once: as many as leave 8 blocks to an SM.
+    int per = 1;
+    while (per < 16 && across * ((P.seq.nseq + 2 * per - 1) / (2 * per)) >= 8 * kSMs) per *= 2;
+    while ((P.seq.nseq + per - 1) / per > 65535) per *= 2;
+    step_kernel<T, S><<<dim3((unsigned)across, (unsigned)((P.seq.nseq + per - 1) / per)), kThreads, 0, s>>>(P, per);
+    return cudaGetLastError();
+}
+template <typename T> cudaError_t step(const Params &P, int S, cudaStream_t s) {
+    return S == 8 ? step<T, 8>(P, s) : S == 16 ? step<T, 16>(P, s) : step<T, 32>(P, s);
+}
+
+int status_of(cudaError_t e) { return e == cudaSuccess ? LA_OK : e == cudaErrorInvalidConfiguration ? LA_ERR_INVALID_ARG : LA_ERR_CUDA; }
+
+}  // namespace sel
+}  // namespace la
+
+extern "C" {
+
+size_t la_selective_scan_marks_bytes(int T, int nseq, int C, int S) {
+    if (T < 0 || T > la::rows::kMaxRows || nseq < 0 || C < 1 || (S != 8 && S != 16 && S != 32)) return 0;
+    return ((size_t)nseq + T / la::sel::kMark) * C * S * 4;
+}
+
+size_t la_selective_scan_workspace_bytes(int T, int nseq, int C, int G, int S, int dtype, int backward) {
+    if (la::sel::check_sizes(nseq, T, C, G, S, dtype, true)) return 0;
+    return la::sel::space_of(T, nseq, C, G, S, backward != 0).bytes;
+}
+
+int la_selective_scan(const void *X, const void *dt, const float *A, const void *B, const void *C, const float *D,
+                      const void *z, const float *dt_bias, int softplus, const float *state_in, void *Y,
+                      float *state_out, float *marks, const int *seq_offsets, int nseq, int N, int channels, int G,
+                      int S, int dtype, const long long *strides, void *workspace, size_t workspace_bytes,
+                      void *stream) {
+    using namespace la;
+    using namespace la::sel;
+    const bool packed = seq_offsets != nullptr;
+    int rc = check_sizes(nseq, N, channels, G, S, dtype, packed);
+    if (rc) return rc;
+    const int T = packed ? N : nseq * N;
+    const Space w = space_of(T, nseq, channels, G, S, false);
+    if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < w.bytes) return LA_ERR_WORKSPACE;
+    Call K;
+    if ((rc = take_inputs(K, X, dt, A, B, C, D, z, dt_bias, Y, state_in, seq_offsets, nseq, N, channels, G, S, softplus, dtype, strides)))
+        return rc;
+    if (((uintptr_t)state_out & 15) || ((uintptr_t)marks & 15)) return LA_ERR_INVALID_ARG;
+    const View in[5] = {K.v[0], K.v[1], K.v[2], K.v[4], K.v[5]};
+    const Range rout[3] = {{state_out, (size_t)nseq * channels * S * 4},
+                           {marks, la_selective_scan_marks_bytes(T, nseq, channels, S)},
+                           {workspace, w.bytes}};
+    if (outputs_meet(in, 5, &K.v[3], 1, K.rin, 5, rout, 3)) return LA_ERR_INVALID_ARG;
+    if (nseq == 0) return LA_OK;
+    Params &P = K.P;
+    P.last = state_out, P.marks = marks;
+    P.seq.status = (uint32_t *)workspace;
+    P.part = part_rows(T, nseq, channels, G, S);
+    const long long units = units_of(T, nseq, N, P.part, packed);
+    const bool split = P.part < T && (packed || N > P.part);
+    P.ends = (float *)((char *)workspace + w.ends), P.sums = (float *)((char *)workspace + w.sums);
+    cudaStream_t s = (cudaStream_t)stream;
+    return status_of(dtype == LA_BF16 ? forward<__nv_bfloat16>(P, S, units, split, s) : forward<float>(P, S, units, split, s));
+}
+
+int la_selective_scan_backward(const void *X, const void *dt, const float *A, const void *B, const void *C,
+                               const float *D, const void *z, const float *dt_bias, int softplus, const void *dY,
+                               const float *marks, const float *dstate_out, void *dX, void *ddt, float *dA, void *dB,
+                               void *dC, float *dD, void *dz, float *ddt_bias, float *dstate_in,
+                               const int *seq_offsets, int nseq, int N, int channels, int G, int S, int dtype,
+                               const long long *strides, void *workspace, size_t workspace_bytes, void *stream) {
+    using namespace la;
+    using namespace la::sel;
+    const bool packed = seq_offsets != nullptr;
+    int rc = check_sizes(nseq, N, channels, G, S, dtype, packed);
+    if (rc) return rc;
+    const int T = packed ? N : nseq * N, elem = dtype == LA_BF16 ? 2 : 4;
+    const Space w = space_of(T, nseq, channels, G, S, true);
+    if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < w.bytes) return LA_ERR_WORKSPACE;
+    Call K;
+    if ((rc = take_inputs(K, X, dt, A, B, C, D, z, dt_bias, dY, dstate_out, seq_offsets, nseq, N, channels, G, S, softplus, dtype, strides)))
+        return rc;
+    if (((uintptr_t)marks & 15) || (T > 0 && !marks) || !dA || ((uintptr_t)dA & 15) || ((uintptr_t)dD & 15) ||
+        ((uintptr_t)ddt_bias & 15) || ((uintptr_t)dstate_in & 15) || ((z != nullptr) != (dz != nullptr) && T > 0))
+        return LA_ERR_INVALID_ARG;
+    View out[3] = {};
+    void *const po[3] = {dX, ddt, dz};
+    const long long dense[2] = {(long long)N * channels, channels};
+    if (T > 0) {
+        if (!dB || !dC || ((uintptr_t)dB & 15) || ((uintptr_t)dC & 15)) return LA_ERR_INVALID_ARG;
+        for (int k = 0; k < 3; ++k)
+            if (po[k] && (rc = rows_view(out[k], po[k], packed ? 1 : nseq, N, channels, elem, dense))) return rc;
+        if (!dX || !ddt) return LA_ERR_INVALID_ARG;
+    }
+    const size_t bc = (size_t)T * G * S * elem;
+    K.rin[5] = {marks, la_selective_scan_marks_bytes(T, nseq, channels, S)};
+    const Range rout[7] = {{dA, (size_t)channels * S * 4}, {dB, bc}, {dC, bc}, {dD, (size_t)channels * 4},
+                           {ddt_bias, (size_t)channels * 4}, {dstate_in, (size_t)nseq * channels * S * 4}, {workspace, w.bytes}};
+    if (outputs_meet(K.v, 6, out, 3, K.rin, 6, rout, 7)) return LA_ERR_INVALID_ARG;
+    Params &P = K.P;
+    P.first = nullptr;
+    P.dlast = dstate_out, P.dfirst = dstate_in, P.marks = (float *)marks;
+    P.seq.status = (uint32_t *)workspace;
+    P.valid = (uint32_t *)workspace + offsetof(WsHeader, reserved) / 4;
+    P.dx = Op{dX, out[0].st[0], out[0].st[1]};
+    P.ddt = Op{ddt, out[1].st[0], out[1].st[1]};
+    P.dz = Op{dz, out[2].st[0], out[2].st[1]};
+    P.walkers = walkers_of(nseq, channels, G, S);
+    P.pbc = (float *)((char *)workspace + w.pbc), P.pa = (float *)((char *)workspace + w.pa);
+    cudaStream_t s = (cudaStream_t)stream;
+    return status_of(dtype == LA_BF16 ? backward<__nv_bfloat16>(P, S, dB, dC, dA, dD, ddt_bias, s)
+                                      : backward<float>(P, S, dB, dC, dA, dD, ddt_bias, s));
+}
+
+int la_selective_scan_step(const void *x, const void *dt, const float *A, const void *B, const void *C, const float *D,
+                           const void *z, const float *dt_bias, int softplus, float *state, void *y, int nseq,
+                           int channels, int G, int S, int dtype, const long long *strides, void *stream) {
+    using namespace la;
+    using namespace la::sel;
+    int rc = check_sizes(nseq, 1, channels, G, S, dtype, false);
+    if (rc) return rc;
+    if (nseq == 0) return LA_OK;
+    if (!state) return LA_ERR_INVALID_ARG;
+    long long st[14];  // as take_inputs reads them: a row's strides are those of the sequence
+    if (strides) {
+        for (int k = 0; k < 4; ++k) st[2 * k] = strides[k], st[2 * k + 1] = channels;
+        for (int k = 0; k < 2; ++k) st[8 + 3 * k] = strides[4 + 2 * k], st[9 + 3 * k] = G * S, st[10 + 3 * k] = strides[5 + 2 * k];
+    }
+    Call K;
+    if ((rc = take_inputs(K, x, dt, A, B, C, D, z, dt_bias, y, nullptr, nullptr, nseq, 1, channels, G, S, softplus, dtype, strides ? st : nullptr)))
+        return rc;
+    if ((uintptr_t)state & 15) return LA_ERR_INVALID_ARG;
+    const View in[5] = {K.v[0], K.v[1], K.v[2], K.v[4], K.v[5]};
+    const Range rout[1] = {{state, (size_t)nseq * channels * S * 4}};
+    if (outputs_meet(in, 5, &K.v[3], 1, K.rin, 5, rout, 1)) return LA_ERR_INVALID_ARG;
+    K.P.last = state;
+    cudaStream_t s = (cudaStream_t)stream;
+    const cudaError_t e = dtype == LA_BF16 ? step<__nv_bfloat16>(K.P, S, s) : step<float>(K.P, S, s);
+    if (e == cudaSuccess) count_launches(1);
+    return status_of(e);
+}
+
+}  // extern "C"

@@ -57,7 +57,7 @@ inline bool ranges_meet(const void *a, size_t an, const void *b, size_t bn) {
 
 // Whether delta = sum_k i_k st_k + d for some i_k in [lo_k, hi_k] and |d| < width; st in decreasing order and
 // nested, so at each level only the quotients next to delta / st can work.
-inline bool steps_meet(long long delta, const long long *st, const long long *lo, const long long *hi, int n,
+__attribute__((noinline)) static bool steps_meet(long long delta, const long long *st, const long long *lo, const long long *hi, int n,
                        long long width) {
     if (n == 0) return delta > -width && delta < width;
     const long long q = delta / st[0];

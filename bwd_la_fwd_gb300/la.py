@@ -94,6 +94,33 @@ def open_library(path: str):
     lib.la_gated_scan_backward.restype = i
     lib.la_gated_scan_step.argtypes = [vp, vp, vp, vp, i, i, i, i, lp, vp]
     lib.la_gated_scan_step.restype = i
+    fl = ctypes.c_float
+    lib.la_rms_norm.argtypes = [vp, vp, vp, vp, vp, i, i, i, fl, i, lp, vp]
+    lib.la_rms_norm.restype = i
+    lib.la_rms_norm_8bit.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, fl, i, lp, vp]
+    lib.la_rms_norm_8bit.restype = i
+    lib.la_rms_norm_workspace_bytes.argtypes = [i]
+    lib.la_rms_norm_workspace_bytes.restype = sz
+    lib.la_rms_norm_backward.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, fl, i, lp, vp, sz, vp]
+    lib.la_rms_norm_backward.restype = i
+    lib.la_short_conv.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, lp, vp, sz, vp]
+    lib.la_short_conv.restype = i
+    lib.la_short_conv_workspace_bytes.argtypes = [i, i]
+    lib.la_short_conv_workspace_bytes.restype = sz
+    lib.la_short_conv_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, lp, vp, sz, vp]
+    lib.la_short_conv_backward.restype = i
+    lib.la_short_conv_step.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, lp, vp]
+    lib.la_short_conv_step.restype = i
+    lib.la_selective_scan_marks_bytes.argtypes = [i, i, i, i]
+    lib.la_selective_scan_marks_bytes.restype = sz
+    lib.la_selective_scan_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+    lib.la_selective_scan_workspace_bytes.restype = sz
+    lib.la_selective_scan.argtypes = [vp] * 8 + [i] + [vp] * 5 + [i] * 6 + [lp, vp, sz, vp]
+    lib.la_selective_scan.restype = i
+    lib.la_selective_scan_backward.argtypes = [vp] * 8 + [i] + [vp] * 13 + [i] * 6 + [lp, vp, sz, vp]
+    lib.la_selective_scan_backward.restype = i
+    lib.la_selective_scan_step.argtypes = [vp] * 8 + [i] + [vp] * 2 + [i] * 5 + [lp, vp]
+    lib.la_selective_scan_step.restype = i
     lib.la_get_status.argtypes = [vp, vp]
     lib.la_get_status.restype = i
     lib.la_forward_noalloc.argtypes = [vp, vp, vp, i, vp, vp, i, i, i, i, i, vp]
@@ -349,7 +376,7 @@ def _place(stream, first, *ts):
     return _on(torch.cuda.stream(stream)), stream.cuda_stream
 
 
-_ARRAYS = {n: ctypes.c_longlong * n for n in (3, 6, 8, 12)}
+_ARRAYS = {n: ctypes.c_longlong * n for n in (2, 3, 4, 6, 8, 12, 14)}
 
 
 def _rows(t):
@@ -635,3 +662,414 @@ def la_gated_scan_step(state, x, w, gate: str, h=None, stream=None):
     if st != 0:
         raise LAError(st, "la_gated_scan_step")
     return h
+
+
+def _raw(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _zeroed(n: int, what: str, device):
+    import torch
+    if n == 0:
+        raise LAError(1, what)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _norm_rows(first, *others):
+    """(B, N, C) of [N, C] or [B, N, C] rows, and (batch, row) strides of each; None, an output that the call makes, is
+    contiguous."""
+    shape, dtype = first.shape, first.dtype
+    if len(shape) not in (2, 3):
+        raise ValueError(f"expected a [N, C] or [B, N, C] tensor, got shape {tuple(shape)}")
+    B, N, C = shape if len(shape) == 3 else (1, *shape)
+    strides = []
+    for t in (first, *others):
+        if t is None:
+            strides += (N * C, C)
+            continue
+        if t.shape != shape or t.dtype != dtype:
+            raise ValueError("the tensors must share shape and dtype")
+        s = _rows(t)
+        strides += s[:2] if len(shape) == 3 else (N * C, s[0])
+    return (B, N, C), strides
+
+
+def la_rms_norm(X, weight, residual=None, eps: float = 1e-6, Y=None, sum=None, stream=None):
+    """Y, R = la_rms_norm(X, weight, residual): the root-mean-square norm of r = X + residual over the last dimension of
+    [N,C] or [B,N,C] tensors, times the float32 [C] ``weight``, and r itself, rounded (``sum``, if given; X without a
+    residual).  Strided views with contiguous C are taken as they are; sum = residual and Y = X work in place."""
+    import torch
+    if sum is not None and residual is None:
+        raise ValueError("sum without residual")
+    (B, N, C), strides = _norm_rows(X, residual, sum, Y)
+    _expect(weight, (C,), torch.float32, "weight")
+    dt = _dtype_code(X)
+    on, sp = _place(stream, X, weight, residual, sum, Y)
+    with on:
+        if Y is None:
+            Y = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+        if residual is not None and sum is None:
+            sum = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+        st = load_library().la_rms_norm(X.data_ptr(), _raw(residual), weight.data_ptr(), _raw(sum), Y.data_ptr(), B, N, C, eps,
+                                        dt, _ARRAYS[8](*strides), sp)
+    if st != 0:
+        raise LAError(st, "la_rms_norm")
+    return Y, X if sum is None else sum
+
+
+def la_rms_norm_8bit(X, weight, residual=None, group: int = 128, eps: float = 1e-6, Y8=None, scales=None, sum=None,
+                     stream=None):
+    """Y8, scales, R = la_rms_norm_8bit(X, weight, residual): la_rms_norm with its output in float8_e4m3fn and a float32 scale
+    for each ``group`` of 128 channels ([..., ceil(C / 128)]) or, with group = 0, for each row ([..., 1])."""
+    import torch
+    if sum is not None and residual is None:
+        raise ValueError("sum without residual")
+    if group not in (0, 128):
+        raise ValueError("group must be 128, or 0 for the whole row")
+    (B, N, C), strides = _norm_rows(X, residual, sum)
+    _expect(weight, (C,), torch.float32, "weight")
+    of_scales = (*X.shape[:-1], -(-C // group) if group else 1)
+    if Y8 is not None:
+        _expect(Y8, X.shape, torch.float8_e4m3fn, "Y8")
+    if scales is not None:
+        _expect(scales, of_scales, torch.float32, "scales")
+    dt = _dtype_code(X)
+    on, sp = _place(stream, X, weight, residual, sum, Y8, scales)
+    with on:
+        if Y8 is None:
+            Y8 = torch.empty(X.shape, dtype=torch.float8_e4m3fn, device=X.device)
+        if scales is None:
+            scales = torch.empty(of_scales, dtype=torch.float32, device=X.device)
+        if residual is not None and sum is None:
+            sum = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+        st = load_library().la_rms_norm_8bit(X.data_ptr(), _raw(residual), weight.data_ptr(), _raw(sum), Y8.data_ptr(),
+                                             scales.data_ptr(), group, B, N, C, eps, dt, _ARRAYS[6](*strides), sp)
+    if st != 0:
+        raise LAError(st, "la_rms_norm_8bit")
+    return Y8, scales, X if sum is None else sum
+
+
+def new_rms_norm_workspace(C: int, device="cuda"):
+    """Zero-filled device workspace of la_rms_norm_backward for rows of C channels."""
+    return _zeroed(int(load_library().la_rms_norm_workspace_bytes(C)), "la_rms_norm_workspace_bytes", device)
+
+
+def la_rms_norm_backward(R, weight, dY, dR=None, eps: float = 1e-6, dX=None, dweight=None, workspace=None, stream=None):
+    """dX, dweight = la_rms_norm_backward(R, weight, dY): the gradient of la_rms_norm's X (and residual, alike) at the normed
+    rows R that it returned, and of its weight; ``dR`` is the gradient that reaches R by other ways."""
+    import torch
+    (B, N, C), strides = _norm_rows(R, dY, dR, dX)
+    _expect(weight, (C,), torch.float32, "weight")
+    if dweight is not None:
+        _expect(dweight, (C,), torch.float32, "dweight")
+    dt = _dtype_code(R)
+    on, sp = _place(stream, R, weight, dY, dR, dX, dweight, workspace)
+    with on:
+        if dX is None:
+            dX = torch.empty(R.shape, dtype=R.dtype, device=R.device)
+        if dweight is None:
+            dweight = torch.empty((C,), dtype=torch.float32, device=R.device)
+        if workspace is None:
+            workspace = new_rms_norm_workspace(C, R.device)
+        st = load_library().la_rms_norm_backward(R.data_ptr(), weight.data_ptr(), dY.data_ptr(), _raw(dR), dX.data_ptr(),
+                                                 dweight.data_ptr(), B, N, C, eps, dt, _ARRAYS[8](*strides),
+                                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), sp)
+    if st != 0:
+        raise LAError(st, "la_rms_norm_backward")
+    return dX, dweight
+
+
+_ACTIVATIONS = {"none": 0, "silu": 1}
+
+
+def _sequences(first, seq_offsets, inner: int):
+    """(nseq, N) of [N, ...] rows with offsets, or of a batch [nseq, N, ...]; `inner` dimensions of a row."""
+    import torch
+    if seq_offsets is None:
+        if first.dim() != 2 + inner:
+            raise ValueError(f"expected [nseq, N, ...] tensors without seq_offsets, got shape {tuple(first.shape)}")
+        return first.shape[0], first.shape[1]
+    if first.dim() != 1 + inner:
+        raise ValueError(f"expected packed [T, ...] tensors with seq_offsets, got shape {tuple(first.shape)}")
+    if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1:
+        raise ValueError("expected [nseq + 1] offsets")
+    _expect(seq_offsets, seq_offsets.shape, torch.int32, "seq_offsets")
+    return seq_offsets.shape[0] - 1, first.shape[0]
+
+
+def _sequence_strides(packed: bool, shape, *ts):
+    """(batch, row[, ...]) strides of each tensor; None, an output that the call makes or one that is not there, is
+    contiguous."""
+    out, dense, n = [], [], shape[-1]
+    for k in reversed(shape[:-1]):
+        dense.insert(0, n)
+        n *= k
+    for t in ts:
+        s = dense if t is None else _rows(t)[:-1]
+        out += (0, *s) if packed else s
+    return out
+
+
+def _alike(first, *others):
+    for t in others:
+        if t is not None and (t.shape != first.shape or t.dtype != first.dtype):
+            raise ValueError("the tensors of rows must share shape and dtype")
+
+
+def _taps(W, bias, C: int, activation: str):
+    import torch
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
+    if W.dim() != 2:
+        raise ValueError(f"expected [C, K] taps, got shape {tuple(W.shape)}")
+    K = W.shape[1]
+    _expect(W, (C, K), torch.float32, "W")
+    if bias is not None:
+        _expect(bias, (C,), torch.float32, "bias")
+    return K
+
+
+def new_short_conv_workspace(C: int, K: int, device="cuda"):
+    """Zero-filled device workspace of la_short_conv_backward (and of a packed la_short_conv) for C channels and K taps."""
+    return _zeroed(int(load_library().la_short_conv_workspace_bytes(C, K)), "la_short_conv_workspace_bytes", device)
+
+
+def la_short_conv(X, W, bias=None, activation: str = "none", seq_offsets=None, state_in=None, state_out=None, O=None,
+                  workspace=None, stream=None):
+    """O = la_short_conv(X, W): the causal convolution of each channel of [nseq,N,C] rows with its K = 2 ... 4 taps, float32
+    W [C,K] (the newest row's last) and bias [C], and its activation ("none" or "silu").
+
+    With ``seq_offsets`` (int32 on the device) X is [T,C], sequence i in rows seq_offsets[i] ... seq_offsets[i+1] - 1, and rows
+    outside every sequence keep what O holds (a new O is zero there); offsets out of order compute nothing, which
+    la_get_status(workspace) tells.  ``state_in`` and ``state_out``, [nseq,K-1,C] of X's dtype, are the rows before each
+    sequence (None: zeros) and its last ones."""
+    import torch
+    nseq, N = _sequences(X, seq_offsets, 1)
+    C, packed = X.shape[-1], seq_offsets is not None
+    K = _taps(W, bias, C, activation)
+    _alike(X, O)
+    for t, what in ((state_in, "state_in"), (state_out, "state_out")):
+        if t is not None:
+            _expect(t, (nseq, K - 1, C), X.dtype, what)
+    dt = _dtype_code(X)
+    strides = _sequence_strides(packed, X.shape, X, O)
+    on, sp = _place(stream, X, W, bias, seq_offsets, state_in, state_out, O, workspace)
+    with on:
+        if O is None:
+            O = (torch.zeros if packed else torch.empty)(X.shape, dtype=X.dtype, device=X.device)
+        if workspace is None and packed:
+            workspace = torch.zeros(256, dtype=torch.uint8, device=X.device)
+        st = load_library().la_short_conv(
+            X.data_ptr(), W.data_ptr(), _raw(bias), _raw(state_in), O.data_ptr(), _raw(state_out), _raw(seq_offsets), nseq, N, C,
+            K, _ACTIVATIONS[activation], dt, _ARRAYS[4](*strides), _raw(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), sp)
+    if st != 0:
+        raise LAError(st, "la_short_conv")
+    return O
+
+
+def la_short_conv_backward(X, W, dO, bias=None, activation: str = "none", seq_offsets=None, state_in=None, dX=None, dW=None,
+                           dbias=None, workspace=None, stream=None):
+    """dX, dW, dbias = la_short_conv_backward(X, W, dO): gradients of sum(dO * O), the other arguments as the forward had
+    them; ``state_in`` is a constant."""
+    import torch
+    nseq, N = _sequences(X, seq_offsets, 1)
+    C, packed = X.shape[-1], seq_offsets is not None
+    K = _taps(W, bias, C, activation)
+    _alike(X, dO, dX)
+    if state_in is not None:
+        _expect(state_in, (nseq, K - 1, C), X.dtype, "state_in")
+    for t, shape, what in ((dW, (C, K), "dW"), (dbias, (C,), "dbias")):
+        if t is not None:
+            _expect(t, shape, torch.float32, what)
+    dt = _dtype_code(X)
+    strides = _sequence_strides(packed, X.shape, X, dO, dX)
+    on, sp = _place(stream, X, W, bias, dO, seq_offsets, state_in, dX, dW, dbias, workspace)
+    with on:
+        if dX is None:
+            dX = (torch.zeros if packed else torch.empty)(X.shape, dtype=X.dtype, device=X.device)
+        dW = torch.empty((C, K), dtype=torch.float32, device=X.device) if dW is None else dW
+        dbias = torch.empty((C,), dtype=torch.float32, device=X.device) if dbias is None else dbias
+        if workspace is None:
+            workspace = new_short_conv_workspace(C, K, X.device)
+        st = load_library().la_short_conv_backward(
+            X.data_ptr(), W.data_ptr(), _raw(bias), _raw(state_in), dO.data_ptr(), dX.data_ptr(), dW.data_ptr(),
+            dbias.data_ptr(), _raw(seq_offsets), nseq, N, C, K, _ACTIVATIONS[activation], dt, _ARRAYS[6](*strides),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), sp)
+    if st != 0:
+        raise LAError(st, "la_short_conv_backward")
+    return dX, dW, dbias
+
+
+def la_short_conv_step(state, x, W, bias=None, activation: str = "none", o=None, stream=None):
+    """o = la_short_conv_step(state, x, W): one token of each sequence, x [nseq,C]; ``state`` [nseq,K-1,C] then holds the
+    newest K - 1 rows, in place."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError(f"expected a [nseq, C] tensor, got shape {tuple(x.shape)}")
+    nseq, C = x.shape
+    K = _taps(W, bias, C, activation)
+    _alike(x, o)
+    _expect(state, (nseq, K - 1, C), x.dtype, "state")
+    dt = _dtype_code(x)
+    strides = (_rows(x)[0], C if o is None else _rows(o)[0])
+    on, sp = _place(stream, x, W, bias, state, o)
+    with on:
+        if o is None:
+            o = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        st = load_library().la_short_conv_step(x.data_ptr(), W.data_ptr(), _raw(bias), state.data_ptr(), o.data_ptr(), nseq, C,
+                                               K, _ACTIVATIONS[activation], dt, _ARRAYS[2](*strides), sp)
+    if st != 0:
+        raise LAError(st, "la_short_conv_step")
+    return o
+
+
+def new_selective_scan_workspace(T: int, nseq: int, C: int, G: int, S: int, dtype: int, backward: bool = False,
+                                 device="cuda"):
+    """Zero-filled device workspace of la_selective_scan (or of its backward) for T rows of nseq sequences together."""
+    n = int(load_library().la_selective_scan_workspace_bytes(T, nseq, C, G, S, int(dtype), int(bool(backward))))
+    return _zeroed(n, "la_selective_scan_workspace_bytes", device)
+
+
+def new_selective_scan_marks(T: int, nseq: int, C: int, S: int, device="cuda"):
+    """The float32 tensor in which la_selective_scan leaves states for la_selective_scan_backward."""
+    import torch
+    n = int(load_library().la_selective_scan_marks_bytes(T, nseq, C, S))
+    if n == 0 and (T > 0 or nseq > 0):
+        raise LAError(1, "la_selective_scan_marks_bytes")
+    return torch.empty(n // 4, dtype=torch.float32, device=device)
+
+
+def _scan_args(X, dt, A, B, C, D, z, dt_bias, rows):
+    """(channels, G, S) of the operands; `rows` leading dimensions."""
+    import torch
+    channels = X.shape[-1]
+    _alike(X, dt, z)
+    if B.dim() != rows + 2 or B.shape[:rows] != X.shape[:rows] or B.dtype != X.dtype:
+        raise ValueError(f"expected B, C of shape {(*X.shape[:rows], 'G', 'S')} and {X.dtype}, got {tuple(B.shape)} {B.dtype}")
+    _alike(B, C)
+    G, S = B.shape[rows:]
+    _expect(A, (channels, S), torch.float32, "A")
+    for t, what in ((D, "D"), (dt_bias, "dt_bias")):
+        if t is not None:
+            _expect(t, (channels,), torch.float32, what)
+    return channels, G, S
+
+
+def _marks_fit(marks, T, nseq, channels, S):
+    import torch
+    n = int(load_library().la_selective_scan_marks_bytes(T, nseq, channels, S)) // 4
+    if marks.dtype != torch.float32 or not marks.is_contiguous() or marks.numel() < n:
+        raise ValueError(f"marks: expected a contiguous float32 tensor of {n} elements (new_selective_scan_marks)")
+
+
+def la_selective_scan(X, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True, seq_offsets=None, state_in=None,
+                      state_out=None, marks=None, Y=None, workspace=None, stream=None):
+    """Y = la_selective_scan(X, dt, A, B, C): per channel c of [nseq,N,channels] rows, with d = softplus(dt + dt_bias),
+
+        h_t[n] = exp(d A[c,n]) h_{t-1}[n] + d x B_t[n],   y = sum_n C_t[n] h_t[n] + D x,   Y = y silu(z)
+
+    A is float32 [channels,S] (S = 8, 16, 32), D and dt_bias float32 [channels] (None: 0), z like X (None: no gate), B and C
+    [nseq,N,G,S], shared by channels / G channels each.  Strided views with contiguous rows are taken as they are.
+
+    With ``seq_offsets`` the tensors are packed, [T,...], as in la_short_conv.  ``state_in`` (None: zeros) and ``state_out``
+    are float32 [nseq,channels,S], ``marks`` (new_selective_scan_marks) keeps what la_selective_scan_backward starts from."""
+    import torch
+    nseq, N = _sequences(X, seq_offsets, 1)
+    packed = seq_offsets is not None
+    rows = 1 if packed else 2
+    channels, G, S = _scan_args(X, dt, A, B, C, D, z, dt_bias, rows)
+    _alike(X, Y)
+    T = N if packed else nseq * N
+    for t, what in ((state_in, "state_in"), (state_out, "state_out")):
+        if t is not None:
+            _expect(t, (nseq, channels, S), torch.float32, what)
+    if marks is not None:
+        _marks_fit(marks, T, nseq, channels, S)
+    code = _dtype_code(X)
+    strides = _sequence_strides(packed, X.shape, X, dt, z, Y) + _sequence_strides(packed, B.shape, B, C)
+    on, sp = _place(stream, X, dt, A, B, C, D, z, dt_bias, seq_offsets, state_in, state_out, marks, Y, workspace)
+    with on:
+        if Y is None:
+            Y = (torch.zeros if packed else torch.empty)(X.shape, dtype=X.dtype, device=X.device)
+        if workspace is None:
+            workspace = new_selective_scan_workspace(T, nseq, channels, G, S, code, device=X.device)
+        st = load_library().la_selective_scan(
+            X.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _raw(D), _raw(z), _raw(dt_bias),
+            int(bool(softplus)), _raw(state_in), Y.data_ptr(), _raw(state_out), _raw(marks), _raw(seq_offsets), nseq, N,
+            channels, G, S, code, _ARRAYS[14](*strides), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), sp)
+    if st != 0:
+        raise LAError(st, "la_selective_scan")
+    return Y
+
+
+class SelectiveScanGradients:
+    """What la_selective_scan_backward returns: dX, ddt, dA, dB, dC, dD, dz (None without z), ddt_bias, dstate_in."""
+
+    __slots__ = ("dX", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dstate_in")
+
+
+def la_selective_scan_backward(X, dt, A, B, C, dY, marks, D=None, z=None, dt_bias=None, softplus: bool = True,
+                               seq_offsets=None, dstate_out=None, workspace=None, stream=None):
+    """SelectiveScanGradients of sum(dY * Y) + sum(dstate_out * state_out): ``marks`` as la_selective_scan left them for the
+    same inputs, the other arguments as it had them.  The gradients are new tensors (zero in rows outside every packed
+    sequence), with the same bits for the same inputs."""
+    import torch
+    nseq, N = _sequences(X, seq_offsets, 1)
+    packed = seq_offsets is not None
+    rows = 1 if packed else 2
+    channels, G, S = _scan_args(X, dt, A, B, C, D, z, dt_bias, rows)
+    _alike(X, dY)
+    T = N if packed else nseq * N
+    if dstate_out is not None:
+        _expect(dstate_out, (nseq, channels, S), torch.float32, "dstate_out")
+    _marks_fit(marks, T, nseq, channels, S)
+    code = _dtype_code(X)
+    strides = _sequence_strides(packed, X.shape, X, dt, z, dY) + _sequence_strides(packed, B.shape, B, C)
+    on, sp = _place(stream, X, dt, A, B, C, dY, marks, D, z, dt_bias, seq_offsets, dstate_out, workspace)
+    with on:
+        new = torch.zeros if packed else torch.empty
+        got = SelectiveScanGradients()
+        got.dX, got.ddt = (new(X.shape, dtype=X.dtype, device=X.device) for _ in range(2))
+        got.dz = new(X.shape, dtype=X.dtype, device=X.device) if z is not None else None
+        got.dB, got.dC = (new(B.shape, dtype=B.dtype, device=X.device) for _ in range(2))
+        got.dA = torch.empty((channels, S), dtype=torch.float32, device=X.device)
+        got.dD, got.ddt_bias = (torch.empty((channels,), dtype=torch.float32, device=X.device) for _ in range(2))
+        got.dstate_in = torch.zeros((nseq, channels, S), dtype=torch.float32, device=X.device) if dstate_out is not None else None
+        if workspace is None:
+            workspace = new_selective_scan_workspace(T, nseq, channels, G, S, code, backward=True, device=X.device)
+        st = load_library().la_selective_scan_backward(
+            X.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _raw(D), _raw(z), _raw(dt_bias),
+            int(bool(softplus)), dY.data_ptr(), marks.data_ptr(), _raw(dstate_out), got.dX.data_ptr(), got.ddt.data_ptr(),
+            got.dA.data_ptr(), got.dB.data_ptr(), got.dC.data_ptr(), got.dD.data_ptr(), _raw(got.dz), got.ddt_bias.data_ptr(),
+            _raw(got.dstate_in), _raw(seq_offsets), nseq, N, channels, G, S, code, _ARRAYS[14](*strides),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), sp)
+    if st != 0:
+        raise LAError(st, "la_selective_scan_backward")
+    return got
+
+
+def la_selective_scan_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True, y=None, stream=None):
+    """y = la_selective_scan_step(state, x, dt, A, B, C): one token of each sequence, x [nseq,channels], B and C [nseq,G,S];
+    ``state``, float32 [nseq,channels,S], is advanced in place."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError(f"expected a [nseq, channels] tensor, got shape {tuple(x.shape)}")
+    channels, G, S = _scan_args(x, dt, A, B, C, D, z, dt_bias, 1)
+    _alike(x, y)
+    nseq = x.shape[0]
+    _expect(state, (nseq, channels, S), torch.float32, "state")
+    code = _dtype_code(x)
+    strides = [_rows(x)[0], _rows(dt)[0], channels if z is None else _rows(z)[0], channels if y is None else _rows(y)[0],
+               *_rows(B)[:2], *_rows(C)[:2]]
+    on, sp = _place(stream, x, dt, A, B, C, D, z, dt_bias, state, y)
+    with on:
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        st = load_library().la_selective_scan_step(
+            x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _raw(D), _raw(z), _raw(dt_bias),
+            int(bool(softplus)), state.data_ptr(), y.data_ptr(), nseq, channels, G, S, code, _ARRAYS[8](*strides), sp)
+    if st != 0:
+        raise LAError(st, "la_selective_scan_step")
+    return y

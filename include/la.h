@@ -58,8 +58,8 @@ typedef enum {
     LA_ERR_TIMEOUT = 5,     /* device: a bounded barrier wait inside a kernel gave up (reported by la_get_status) */
     LA_ERR_BOUNDS = 6,      /* device: an internal layout check failed -- a kernel's shared-memory window was not
                                1024-byte aligned, so it computed nothing; or, in the index-checked test build
-                               (libla_gb300_checked.so), an index out of its array was skipped; or la_prompt's
-                               offsets are not in order within its rows (reported by la_get_status) */
+                               (libla_gb300_checked.so), an index out of its array was skipped; or a packed
+                               call's offsets are not in order within its rows (reported by la_get_status) */
     LA_ERR_STATE = 7        /* device: la_backward_with_forward_state found no matching forward state */
 } la_status;
 
@@ -338,6 +338,142 @@ int la_gated_scan_backward(const void *X, const void *W, const void *H, const vo
  */
 int la_gated_scan_step(const void *x, const void *w, void *h, float *state, int B, int C, int gate, int dtype,
                        const long long *strides, void *stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition:
+ *   r = x + residual (fp32),  y_c = w_c r_c rstd,  rstd = (sum_c r_c^2 / C + eps)^-1/2
+ *   X, Y       in, out: [B,N,C] of `dtype`;  C <= 16384, N < 2^31 - 1024
+ *   residual, sum  in, out: [B,N,C], r rounded to `dtype`; both or neither.  y is that of r before this rounding.
+ *   weight     in : float [C]
+ *   strides    in : host array, (batch, row) element strides of X, residual, sum, Y (8 values; the rules of the strided
+ *              passes), or NULL for contiguous tensors
+ * A row is read before it is written: an output may be an input itself (same pointer and strides; sum = residual, Y = X).
+ * Squares are summed in fp32: rows beyond some 1e18 overflow (rstd = 0).  B = 0 or N = 0 does nothing.
+ */
+int la_rms_norm(const void *X, const void *residual, const float *weight, void *sum, void *Y, int B, int N, int C,
+                float eps, int dtype, const long long *strides, void *stream);
+
+/*
+ * The same with y in 8 bits (e4m3: 3 bits of mantissa, largest value 448, NaN but no infinities) and scales:
+ *   s = max(max |y|, 2^-100) / 448 over each group of 128 channels (`group` = 128) or the row (`group` = 0), y8 = y / s
+ *   Y8, scales   out: contiguous [B,N,C] bytes and float [B,N,ceil(C / group)] ([B,N] for the row); Y8 16-byte aligned
+ *   strides      in : (batch, row) of X, residual, sum (6 values), or NULL
+ * A group that holds a NaN or an infinity becomes NaN.
+ */
+int la_rms_norm_8bit(const void *X, const void *residual, const float *weight, void *sum, unsigned char *Y8,
+                     float *scales, int group, int B, int N, int C, float eps, int dtype, const long long *strides,
+                     void *stream);
+
+/*
+ * Gradients at R, the normed rows as stored (la_rms_norm's sum, or its X): with g = w dY,
+ *   dX = dR + rstd (g - R rstd^2 sum_c(g R) / C)   (of X and of the residual alike),   dweight_c = sum over rows of dY R rstd
+ *   dR         in : [B,N,C], the gradient that reaches R by other ways, or NULL for 0
+ *   dX         out: [B,N,C]; may be R, dY or dR itself
+ *   dweight    out: float [C] (0 without rows), the same bits for the same inputs
+ *   strides    in : (batch, row) of R, dY, dR, dX (8 values), or NULL
+ *   workspace  workspace_bytes >= la_rms_norm_workspace_bytes(C), under the workspace rules above
+ */
+size_t la_rms_norm_workspace_bytes(int C);
+int la_rms_norm_backward(const void *R, const float *weight, const void *dY, const void *dR, void *dX, float *dweight,
+                         int B, int N, int C, float eps, int dtype, const long long *strides, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * Short causal convolution over time, each channel by itself:
+ *   p_t = bias + sum_{j<K} W[c][j] x_{t-K+1+j},   o = p (LA_CONV_NONE) or p / (1 + e^-p) (LA_CONV_SILU);   K = 2, 3, 4
+ * Before a sequence's first row stand the K - 1 rows of its state_in, the newest last, or zeros.
+ *   X, O         in, out: [nseq,N,C] of `dtype`; with seq_offsets N rows of nseq sequences end to end, [N,C], as in la_prompt
+ *                (rows outside every sequence are neither read into a result nor written; offsets out of order compute
+ *                nothing and LA_ERR_BOUNDS is reported).  All rows together < 2^31 - 1024.
+ *   W, bias      in : float [C,K] and [C] (or NULL for 0)
+ *   state_in     in : [nseq,K-1,C] of `dtype`, or NULL;  state_out out: the same of each sequence's end, or NULL.  Not the
+ *                same array.
+ *   seq_offsets  in : device int [nseq + 1], or NULL for a batch
+ *   strides      in : host array, (batch, row) element strides of X, O (4 values; the rules of the strided passes; packed,
+ *                the batch's is not used), or NULL for contiguous tensors
+ *   workspace    of a packed call, for its status: 256 bytes at least (la_short_conv_workspace_bytes() is more); else unused
+ */
+typedef enum { LA_CONV_NONE = 0, LA_CONV_SILU = 1 } la_conv_activation;
+int la_short_conv(const void *X, const float *W, const float *bias, const void *state_in, void *O, void *state_out,
+                  const int *seq_offsets, int nseq, int N, int C, int K, int activation, int dtype,
+                  const long long *strides, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of sum dO . O; the state that a sequence starts from is a constant.
+ *   dX         out: [nseq,N,C] (packed [N,C]);  dW, dbias out: float [C,K], [C] (dbias may be NULL; 0 without rows), the
+ *              same bits for the same inputs
+ *   strides    in : (batch, row) of X, dO, dX (6 values), or NULL
+ *   workspace  workspace_bytes >= la_short_conv_workspace_bytes(C, K)
+ * Offsets out of order leave dX as it is and the parameters' gradients 0.
+ */
+size_t la_short_conv_workspace_bytes(int C, int K);
+int la_short_conv_backward(const void *X, const float *W, const float *bias, const void *state_in, const void *dO,
+                           void *dX, float *dW, float *dbias, const int *seq_offsets, int nseq, int N, int C, int K,
+                           int activation, int dtype, const long long *strides, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/*
+ * One token of each sequence: o of the state's K - 1 rows and x; the state then holds the newest K - 1, in place.
+ *   x, o     in, out: [nseq,C] of `dtype`;  state in/out: [nseq,K-1,C]
+ *   strides  in : the row strides of x, o (2 values), or NULL
+ */
+int la_short_conv_step(const void *x, const float *W, const float *bias, void *state, void *o, int nseq, int C, int K,
+                       int activation, int dtype, const long long *strides, void *stream);
+
+/*
+ * Selective state space scan: per channel c a state of S numbers, driven by the tokens.  With C = `channels`, channel c's
+ * group g = c / (C / G):
+ *   d = softplus(dt + dt_bias) (or dt + dt_bias),   h_t[c,n] = e^(d A[c,n]) h_{t-1}[c,n] + d x B_t[g,n]
+ *   y = sum_n C_t[g,n] h_t[c,n] + D x,   Y = y z / (1 + e^-z)   (y without z)
+ *   X, dt, z, Y  in, in, in, out: [nseq,N,C] of `dtype`; with seq_offsets N rows of nseq sequences end to end, [N,C], as in
+ *                la_prompt (rows outside every sequence are neither read into a result nor written; offsets out of order
+ *                compute nothing and LA_ERR_BOUNDS is reported).  z may be NULL.  All rows together < 2^31 - 1024.
+ *   B, C         in : [nseq,N,G,S] (packed [N,G,S]) of `dtype`;  S = 8, 16 or 32;  with G > 1 C / G a multiple of 8
+ *   A, D, dt_bias  in : float [C,S], [C], [C]; D and dt_bias may be NULL for 0.  A is finite (negative for states that fade).
+ *   state_in     in : float [nseq,C,S], or NULL for 0;  state_out out: the same of each sequence's end, or NULL.  Not the
+ *                same array.
+ *   marks        out: la_selective_scan_marks_bytes() of states for la_selective_scan_backward, or NULL
+ *   seq_offsets  in : device int [nseq + 1], or NULL for a batch
+ *   strides      in : host array, (batch, row) element strides of X, dt, z, Y and (batch, row, group) of B, C (14 values;
+ *                the rules of the strided passes; packed, the batch's are not used), or NULL for contiguous tensors
+ *   workspace    workspace_bytes >= la_selective_scan_workspace_bytes(T, ...), T = all rows together, under the workspace
+ *                rules above; one for the largest T and nseq may be too small for other shapes: ask for each
+ * The states and sums are held in fp32.  A sequence's rows do not depend on other sequences, whatever those hold; an
+ * infinity or a NaN of its own may reach every later row of it.
+ */
+size_t la_selective_scan_marks_bytes(int T, int nseq, int C, int S);
+size_t la_selective_scan_workspace_bytes(int T, int nseq, int C, int G, int S, int dtype, int backward);
+int la_selective_scan(const void *X, const void *dt, const float *A, const void *B, const void *C, const float *D,
+                      const void *z, const float *dt_bias, int softplus, const float *state_in, void *Y,
+                      float *state_out, float *marks, const int *seq_offsets, int nseq, int N, int channels, int G,
+                      int S, int dtype, const long long *strides, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+/*
+ * Gradients of sum dY . Y + sum dstate_out . state_out, from the marks that the forward left for the same inputs:
+ *   dX, ddt, dz  out: contiguous [nseq,N,C] (packed [N,C]) of `dtype`; dz with z only
+ *   dB, dC       out: contiguous [nseq,N,G,S] (packed [N,G,S]) of `dtype`, summed in fp32 and rounded once
+ *   dA, dD, ddt_bias  out: float [C,S], [C], [C] (the last two may be NULL; 0 without rows)
+ *   dstate_out   in : float [nseq,C,S], or NULL for 0;  dstate_in out: the same for state_in, or NULL
+ *   strides      in : (batch, row) of X, dt, z, dY and (batch, row, group) of B, C (14 values), or NULL
+ * All gradients are the same bits for the same inputs.  Offsets out of order leave the rows' gradients as they are and the
+ * parameters' 0.
+ */
+int la_selective_scan_backward(const void *X, const void *dt, const float *A, const void *B, const void *C,
+                               const float *D, const void *z, const float *dt_bias, int softplus, const void *dY,
+                               const float *marks, const float *dstate_out, void *dX, void *ddt, float *dA, void *dB,
+                               void *dC, float *dD, void *dz, float *ddt_bias, float *dstate_in,
+                               const int *seq_offsets, int nseq, int N, int channels, int G, int S, int dtype,
+                               const long long *strides, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of each sequence: the state is advanced in place, y as above.
+ *   x, dt, z, y  in, in, in, out: [nseq,C] of `dtype` (z may be NULL);  B, C in: [nseq,G,S];  state in/out: float [nseq,C,S]
+ *   strides      in : the row strides of x, dt, z, y and (row, group) of B, C (8 values), or NULL
+ */
+int la_selective_scan_step(const void *x, const void *dt, const float *A, const void *B, const void *C, const float *D,
+                           const void *z, const float *dt_bias, int softplus, float *state, void *y, int nseq,
+                           int channels, int G, int S, int dtype, const long long *strides, void *stream);
 
 /*
  * Synchronises `stream`, then returns and clears the sticky device status recorded in `workspace`
