@@ -38,6 +38,25 @@ template <typename T, int V> __device__ __forceinline__ Vec<T, V> load_vec(const
     for (int k = 0; k < V; ++k) r.e[k] = k < n ? p[k] : T(0.f);
     return r;
 }
+// A whole vector loaded into `r` where `on` holds, for use after other work: the load stays where it is written (a plain one
+// may be moved down to its first use) and has no branch, whose end would wait for it.
+template <typename T, int V> __device__ __forceinline__ void load_ahead(Vec<T, V> &r, const T *p, bool on) {
+    constexpr int WORDS = (int)sizeof(T) * V / 4;
+    uint32_t *w = (uint32_t *)&r;
+    if constexpr (WORDS == 1) {
+        asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\n@p ld.global.b32 %0, [%1];\n}" : "+r"(w[0]) : "l"(p), "r"((int)on));
+    } else if constexpr (WORDS == 2) {
+        asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %3, 0;\n@p ld.global.v2.b32 {%0, %1}, [%2];\n}"
+                     : "+r"(w[0]), "+r"(w[1])
+                     : "l"(p), "r"((int)on));
+    } else {
+#pragma unroll
+        for (int k = 0; k < WORDS; k += 4)
+            asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %5, 0;\n@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n}"
+                         : "+r"(w[k]), "+r"(w[k + 1]), "+r"(w[k + 2]), "+r"(w[k + 3])
+                         : "l"((const char *)p + 4 * k), "r"((int)on));
+    }
+}
 template <typename T, int V> __device__ __forceinline__ void store_vec(T *p, const Vec<T, V> &x, int n, bool aligned = true) {
     if (n >= V && aligned) {
         *(Vec<T, V> *)p = x;

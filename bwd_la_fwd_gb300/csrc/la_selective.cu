@@ -7,16 +7,19 @@
 //   dx = d sum_n G B + D g,  dd = sum_n a h_{t-1} G A + x sum_n G B,  dA = sum_t d a h_{t-1} G,  dB = sum_c G d x,
 //   dC = sum_c g h,  dD = sum_t g x,  dz = dout y (z sigmoid(z))'
 //
-// A thread holds four states of a channel in registers; S / 4 lanes are a channel, and a CTA has kWarps warps of them.  It
-// walks rows in tiles: all threads form d and d x of a tile (a vector of channels each, whose x, dt, z are loaded while the
-// tile before is scanned), then each walks its states over the tile's rows, reading d, d x, B, C from shared memory, then
-// all write the tile's outputs.  Everything is held in fp32.  A T x C x S scan has T C S exponentials and 4 T C S
-// multiply-adds (16 lane operations of the fp32 pipe, and as many of the special-function unit at half its rate, for
-// four states and a row), which is more than HBM takes for the tensors: issue slots bound it.
+// A scanning thread holds four states of two channels in registers, a warp four states of 64 channels, and the warps of the
+// other states stand beside it.  They walk rows in tiles of 16, reading d, d x, B and C from shared memory and leaving each
+// row's part of y there, while four helping warps form d and d x of the next tile from dt and x and write the outputs of the
+// tile before; one barrier a tile.  Everything is held in fp32.
+// T C S exponentials and 4 T C S multiply-adds bind it, and more than these what a row brings through shared memory: a warp's
+// 16-byte load of B (the same for all lanes) takes two clocks of the SM, one of d two for 32 channels.  Two channels to a
+// thread share the loads of B and C.
 // Where there are few channels time is cut into parts: a first launch forms each part's last state, started from zero (the
 // first part of a sequence: from its state), and the sum of its d, whose e^(A sum) is the part's decay; the second launch
 // folds them into the state that each part starts from.
 #include <math.h>
+
+#include <type_traits>
 
 #include "la_f32x2.cuh"
 #include "la_rows.cuh"
@@ -26,7 +29,7 @@ namespace sel {
 
 using namespace rows;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;  // backward, step
 constexpr int kMark = 16;      // rows between the states that a forward keeps for its backward
 constexpr int kSMs = 152;
 constexpr int kMaxParts = 64;  // of a sequence
@@ -64,12 +67,20 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// log(1 + e^v) = max(v, 0) + log1p(e^-|v|)
-__device__ __forceinline__ float softplus_of(float v) { return fmaxf(v, 0.f) + log1pf(exp_fast(-fabsf(v))); }
-__device__ __forceinline__ float step_of(const Params &P, float v) {
-    // NaN stays NaN (fmaxf would lose it)
-    return P.softplus ? (v != v ? v : softplus_of(v)) : v;
+// log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v|; log(1 + e) = 2 artanh(s), s = e / (2 + e) <= 1/3, by its series to
+// s^13 (the next term is 2^-26 of the sum): as exact for small e as for large.  NaN stays NaN.
+__device__ __forceinline__ float2 softplus2(float2 v) {
+    const float2 e = make_float2(exp_fast(-fabsf(v.x)), exp_fast(-fabsf(v.y)));
+    const float2 s = mul2(e, make_float2(rcp_fast(2.f + e.x), rcp_fast(2.f + e.y))), q = mul2(s, s);
+    float2 p = fma2(q, both(2.f / 13.f), both(2.f / 11.f));
+    p = fma2(q, p, both(2.f / 9.f));
+    p = fma2(q, p, both(2.f / 7.f));
+    p = fma2(q, p, both(2.f / 5.f));
+    p = fma2(q, p, both(2.f / 3.f));
+    p = fma2(q, p, both(2.f));
+    return fma2(s, p, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
+__device__ __forceinline__ float2 step_of(const Params &P, float2 v) { return P.softplus ? softplus2(v) : v; }
 
 // Four states.
 struct F4 {
@@ -109,9 +120,17 @@ template <int L, int STEP> __device__ __forceinline__ float lanes_sum(float (&v)
 }
 
 template <int S> struct Tile {
-    static constexpr int L = S / 4, CW = 32 / L, CH = kWarps * CW;  // lanes of a channel, channels of a warp, of a CTA
-    static constexpr int R = 2 * S;                                 // rows of a forward tile: 8 elements to a thread
-    static constexpr int NB = S * S / 256 > 0 ? S * S / 256 : 1;    // vectors of four of B and C to a thread
+    static constexpr int R = kMark;                                       // rows
+    static constexpr int QW = S / 4, GW = QW > 4 ? 1 : 4 / QW;            // warps of a channel group, groups
+    static constexpr int CH = 64 * GW, HELP = CH == 64 ? 256 : 2 * CH;  // channels of a CTA, helping threads
+    static constexpr int THREADS = HELP + 32 * QW * GW;
+    static constexpr int NV = R * CH / 4 / HELP;                          // vectors of four channels to a helper
+    static constexpr int NB = (2 * R * S / 4 + HELP - 1) / HELP;          // of four of B and C
+    struct Smem {
+        float ds[2][R][CH], us[2][R][CH];  // d and d x
+        float bc[2][2][R][S];
+        float ys[2][QW][R][CH];            // parts of y (the last member: a launch for ends has none)
+    };
 };
 
 // The unit's sequence and part.  A sequence's parts are units i + off[i] / part onwards: there are as many as it needs.
@@ -140,130 +159,210 @@ __device__ __forceinline__ long long mark_slot(const Params &P, int seq, int row
 
 // ENDS: the first launch, which forms the parts' last states only.
 template <typename T, int S, bool ENDS>
-__global__ void __launch_bounds__(kThreads, 2) forward_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(Tile<S>::THREADS, S == 16 ? 2 : 1) forward_kernel(const __grid_constant__ Params P) {
     using K = Tile<S>;
-    constexpr int L = K::L, CW = K::CW, CH = K::CH, R = K::R, NB = K::NB;
-    __shared__ __align__(16) float2 dd[R][CH];
-    __shared__ __align__(16) float ys[ENDS ? 1 : R][ENDS ? 4 : CH];
-    __shared__ __align__(16) float bc[2][R][S];
+    constexpr int CH = K::CH, R = K::R, NV = K::NV, NB = K::NB, QW = K::QW, HELP = K::HELP;
+    extern __shared__ __align__(16) unsigned char raw[];
+    typename K::Smem &M = *(typename K::Smem *)raw;
     const int cblocks = P.G * P.bpg, unit = blockIdx.x / cblocks, cb = blockIdx.x - unit * cblocks;
     int seq, j, len;
     if (!unit_of(P, unit, seq, j, len)) return;
     if (seq >= P.seq.nseq) return;
     const long long t0 = (long long)j * P.part;
     if (j > 0 && t0 >= len) return;
-    const int lo = (int)t0, hi = min(len, (int)min(t0 + P.part, (long long)len));
+    const int lo = (int)t0, hi = (int)min(t0 + P.part, (long long)len);
     if (ENDS && hi == len) return;  // nothing follows
     const int g = cb / P.bpg, c0 = g * P.cpg + (cb - g * P.bpg) * CH, nc = min(CH, (g + 1) * P.cpg - c0);
-    // this thread's vector of the tile
-    const int er = threadIdx.x / (CH / 8), ec = threadIdx.x % (CH / 8) * 8, en = nc - ec;
-    const T *x = rows_of<const T>(P.seq, P.x, seq) + c0 + ec, *dt = rows_of<const T>(P.seq, P.dt, seq) + c0 + ec;
-    const T *z = P.z.p ? rows_of<const T>(P.seq, P.z, seq) + c0 + ec : nullptr;
-    T *y = ENDS ? nullptr : rows_of<T>(P.seq, P.y, seq) + c0 + ec;
-    const GOp &OB = P.B, &OC = P.C;
-    const T *Bp = (const T *)OB.p + (P.seq.off ? P.seq.off[seq] * OB.sn : seq * OB.sb) + g * OB.sg;
-    const T *Cp = (const T *)OC.p + (P.seq.off ? P.seq.off[seq] * OC.sn : seq * OC.sb) + g * OC.sg;
-    float bias[8], D[8];
+    const int tiles = (hi - lo + R - 1) / R, helper = (int)threadIdx.x - 32 * QW * K::GW;
+    if (helper >= 0) {
+        const T *x = rows_of<const T>(P.seq, P.x, seq) + c0, *dt = rows_of<const T>(P.seq, P.dt, seq) + c0;
+        const T *z = P.z.p ? rows_of<const T>(P.seq, P.z, seq) + c0 : nullptr;
+        T *y = ENDS ? nullptr : rows_of<T>(P.seq, P.y, seq) + c0;
+        const T *Bp = (const T *)P.B.p + (P.seq.off ? P.seq.off[seq] * P.B.sn : seq * P.B.sb) + g * P.B.sg;
+        const T *Cp = (const T *)P.C.p + (P.seq.off ? P.seq.off[seq] * P.C.sn : seq * P.C.sb) + g * P.C.sg;
+        // vectors helper, helper + HELP, ... of a tile: the same channels in rows STEP apart
+        constexpr int STEP = HELP / (CH / 4);
+        const int row = helper / (CH / 4), col = helper % (CH / 4) * 4, n = nc - col;
+        float bias[4], D[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        bias[k] = P.bias && k < en ? P.bias[c0 + ec + k] : 0.f;
-        D[k] = P.D && k < en ? P.D[c0 + ec + k] : 0.f;
+        for (int k = 0; k < 4; ++k) {
+            bias[k] = P.bias && k < n ? P.bias[c0 + col + k] : 0.f;
+            D[k] = P.D && k < n ? P.D[c0 + col + k] : 0.f;
+        }
+        // x, dt, B, C on their way to d, and x, z to the outputs: two tiles of each, so that a load has two steps' time
+        Vec<T, 4> px[2][NV], pd[2][NV], ex[2][NV], ez[2][NV], vb[2][NB];
+        auto fetch = [&](int k, Vec<T, 4>(&px)[NV], Vec<T, 4>(&pd)[NV], Vec<T, 4>(&vb)[NB]) {
+            const int t = lo + k * R;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int r = t + row + i * STEP;
+                load_ahead(px[i], x + r * P.x.sn + col, r < hi && n >= 4);
+                load_ahead(pd[i], dt + r * P.dt.sn + col, r < hi && n >= 4);
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int v = i * HELP + helper, which = v / (R * S / 4), r = t + v % (R * S / 4) / (S / 4), s = v % (S / 4) * 4;
+                load_ahead(vb[i], (which ? Cp + r * P.C.sn : Bp + r * P.B.sn) + s, which < (ENDS ? 1 : 2) && r < hi);
+            }
+        };
+        const bool whole = nc == CH;
+        auto produce = [&](int k, Vec<T, 4>(&px)[NV], Vec<T, 4>(&pd)[NV], Vec<T, 4>(&vb)[NB]) {
+            const int t = lo + k * R, buf = k & 1;
+            const bool full = whole && t + R <= hi;  // no row or channel is missing
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int r = row + i * STEP;
+                if (full) {
+                    const float2 v = step_of(P, make_float2(to_f(pd[i].e[0]) + bias[0], to_f(pd[i].e[1]) + bias[1]));
+                    const float2 w = step_of(P, make_float2(to_f(pd[i].e[2]) + bias[2], to_f(pd[i].e[3]) + bias[3]));
+                    *(float4 *)&M.ds[buf][r][col] = make_float4(v.x, v.y, w.x, w.y);
+                    *(float4 *)&M.us[buf][r][col] = make_float4(v.x * to_f(px[i].e[0]), v.y * to_f(px[i].e[1]),
+                                                                w.x * to_f(px[i].e[2]), w.y * to_f(px[i].e[3]));
+                    continue;
+                }
+                const bool in = t + r < hi;
+                if (in && n > 0 && n < 4) {  // the last channels, where they are no whole vector
+                    px[i] = load_vec<T, 4>(x + (t + r) * P.x.sn + col, n);
+                    pd[i] = load_vec<T, 4>(dt + (t + r) * P.dt.sn + col, n);
+                }
+                float d[4], u[4];
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const float2 v = step_of(P, make_float2(to_f(pd[i].e[e]) + bias[e], to_f(pd[i].e[e + 1]) + bias[e + 1]));
+                    d[e] = in && e < n ? v.x : 0.f;  // no row: nothing happens
+                    d[e + 1] = in && e + 1 < n ? v.y : 0.f;
+                    u[e] = in && e < n ? v.x * to_f(px[i].e[e]) : 0.f;
+                    u[e + 1] = in && e + 1 < n ? v.y * to_f(px[i].e[e + 1]) : 0.f;
+                }
+                *(float4 *)&M.ds[buf][r][col] = make_float4(d[0], d[1], d[2], d[3]);
+                *(float4 *)&M.us[buf][r][col] = make_float4(u[0], u[1], u[2], u[3]);
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int v = i * HELP + helper, which = v / (R * S / 4), r = v % (R * S / 4) / (S / 4), s = v % (S / 4) * 4;
+                if (which >= (ENDS ? 1 : 2)) continue;
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (t + r < hi) f = make_float4(to_f(vb[i].e[0]), to_f(vb[i].e[1]), to_f(vb[i].e[2]), to_f(vb[i].e[3]));
+                *(float4 *)&M.bc[buf][which][r][s] = f;
+            }
+        };
+        auto fetch_out = [&](int k, Vec<T, 4>(&ex)[NV], Vec<T, 4>(&ez)[NV]) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int r = lo + k * R + row + i * STEP;
+                load_ahead(ex[i], x + r * P.x.sn + col, r < hi && n >= 4);
+                load_ahead(ez[i], z + r * P.z.sn + col, z && r < hi && n >= 4);
+            }
+        };
+        auto finish = [&](int k, Vec<T, 4>(&ex)[NV], Vec<T, 4>(&ez)[NV]) {
+            const int t = lo + k * R, buf = k & 1;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int r = row + i * STEP;
+                if (t + r >= hi || n <= 0) continue;
+                if (n < 4) {
+                    ex[i] = load_vec<T, 4>(x + (t + r) * P.x.sn + col, n);
+                    if (z) ez[i] = load_vec<T, 4>(z + (t + r) * P.z.sn + col, n);
+                }
+                float4 s = *(const float4 *)&M.ys[buf][0][r][col];
+#pragma unroll
+                for (int w = 1; w < QW; ++w) {
+                    const float4 o = *(const float4 *)&M.ys[buf][w][r][col];
+                    s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
+                }
+                const float v[4] = {s.x, s.y, s.z, s.w};
+                Vec<T, 4> out;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float f = fmaf(D[e], to_f(ex[i].e[e]), v[e]);
+                    if (z) {
+                        const float ze = to_f(ez[i].e[e]);
+                        f *= ze * sigmoid(ze);
+                    }
+                    put(&out.e[e], f);
+                }
+                store_vec<T, 4>(y + (t + r) * P.y.sn + col, out, n);
+            }
+        };
+        // Step k, while tile k is scanned: d of tile k + 1, the outputs of tile k - 1.
+        auto step = [&](int k, auto parity) {
+            constexpr int a = decltype(parity)::value, b = 1 - a;  // of k, of its neighbours
+            __syncthreads();
+            if (k + 1 < tiles) produce(k + 1, px[b], pd[b], vb[b]);
+            fetch(k + 3, px[b], pd[b], vb[b]);
+            if (ENDS) return;
+            if (k > 0) finish(k - 1, ex[b], ez[b]);
+            fetch_out(k + 1, ex[b], ez[b]);
+        };
+        fetch(0, px[0], pd[0], vb[0]);
+        fetch(1, px[1], pd[1], vb[1]);
+        if (!ENDS) fetch_out(0, ex[0], ez[0]);
+        if (tiles > 0) produce(0, px[0], pd[0], vb[0]);
+        fetch(2, px[0], pd[0], vb[0]);
+        for (int k = 0; k <= tiles; k += 2) {
+            step(k, std::integral_constant<int, 0>());
+            if (k < tiles) step(k + 1, std::integral_constant<int, 1>());
+        }
+        return;
     }
-    // this thread's states
-    const int lane = threadIdx.x & 31, q = lane % L, ch = (threadIdx.x >> 5) * CW + lane / L, c = c0 + ch;
-    const bool mine = ch < nc;
-    F4 a2 = zero4(), h = zero4();
-    if (mine) {
-        a2 = mul4(load4(P.A + (long long)c * S + 4 * q), kLog2e);
-        if (j == 0 || ENDS) {
-            if (P.first && j == 0) h = load4(P.first + ((long long)seq * P.C_ + c) * S + 4 * q);
-        } else {
+    // four states of two neighbouring channels
+    const int warp = threadIdx.x >> 5, q = warp % QW, ch = warp / QW * 64 + (threadIdx.x & 31) * 2, c = c0 + ch;
+    F4 a2[2] = {zero4(), zero4()}, h[2] = {zero4(), zero4()};
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (ch + i >= nc) continue;
+        const long long at = (long long)(c + i) * S + 4 * q;
+        a2[i] = mul4(load4(P.A + at), kLog2e);
+        if (j == 0) {
+            if (P.first) h[i] = load4(P.first + (long long)seq * P.C_ * S + at);
+        } else if (!ENDS) {
             for (int p = unit - j; p < unit; ++p) {
-                const F4 e = load4(P.ends + ((long long)p * P.C_ + c) * S + 4 * q);
-                h = p == unit - j ? e : fma4(decay4(a2, P.sums[(long long)p * P.C_ + c]), h, e);
+                const F4 e = load4(P.ends + (long long)p * P.C_ * S + at);
+                h[i] = p == unit - j ? e : fma4(decay4(a2[i], P.sums[(long long)p * P.C_ + c + i]), h[i], e);
             }
         }
     }
-    Vec<T, 8> vx, vd, vz, nx, nd, nz;
-    Vec<T, 4> vb[NB];
-    auto fetch = [&](int t) {  // the tile from row t on
-        const bool in = t + er < hi && en > 0;
-        if (in) {
-            nx = load_vec<T, 8>(x + (t + er) * P.x.sn, en);
-            nd = load_vec<T, 8>(dt + (t + er) * P.dt.sn, en);
-            if (!ENDS && z) nz = load_vec<T, 8>(z + (t + er) * P.z.sn, en);
-        }
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const int v = i * kThreads + threadIdx.x, which = v / (R * S / 4), row = v % (R * S / 4) / (S / 4), col = v % (S / 4) * 4;
-            if (which < (ENDS ? 1 : 2) && t + row < hi)
-                vb[i] = *(const Vec<T, 4> *)((which ? Cp : Bp) + (t + row) * (which ? OC.sn : OB.sn) + col);
-        }
-    };
-    float sum = 0.f;
-    fetch(lo);
-    for (int t = lo; t < hi; t += R) {
-        vx = nx, vd = nd;
-        if (!ENDS) vz = nz;
-        const bool in = t + er < hi && en > 0;
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-            float2 d = make_float2(0.f, 0.f), u = d;  // no row: nothing happens
-            if (in && k < en) d.x = step_of(P, to_f(vd.e[k]) + bias[k]), u.x = d.x * to_f(vx.e[k]);
-            if (in && k + 1 < en) d.y = step_of(P, to_f(vd.e[k + 1]) + bias[k + 1]), u.y = d.y * to_f(vx.e[k + 1]);
-            *(float4 *)&dd[er][ec + k] = make_float4(d.x, u.x, d.y, u.y);
-        }
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const int v = i * kThreads + threadIdx.x, which = v / (R * S / 4), row = v % (R * S / 4) / (S / 4), col = v % (S / 4) * 4;
-            if (which >= (ENDS ? 1 : 2)) continue;
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (t + row < hi) f = make_float4(to_f(vb[i].e[0]), to_f(vb[i].e[1]), to_f(vb[i].e[2]), to_f(vb[i].e[3]));
-            *(float4 *)&bc[which][row][col] = f;
-        }
+    for (int k = 0; k <= tiles; ++k) {
         __syncthreads();
-        if (t + R < hi) fetch(t + R);
-        const int rows = min(R, hi - t);
-        for (int r0 = 0; r0 < rows; r0 += kMark) {
-            if (!ENDS && P.marks && mine) store4(P.marks + (mark_slot(P, seq, t + r0) * P.C_ + c) * S + 4 * q, h);
+        if (k == tiles) break;
+        const int buf = k & 1;
+        if (!ENDS && P.marks)
 #pragma unroll
-            for (int r1 = 0; r1 < kMark; r1 += L) {
-                float part[L];
+            for (int i = 0; i < 2; ++i)
+                if (ch + i < nc) store4(P.marks + (mark_slot(P, seq, lo + k * R) * P.C_ + c + i) * S + 4 * q, h[i]);
+        // A row's operands are loaded a row ahead of it, before the parts of y of the row between are stored (which the
+        // compiler has to take for stores to them).
+        struct Row {
+            float2 d, u;
+            F4 B, C;
+        } ahead[2];
+        auto load = [&](int r, Row &o) {
+            o.d = *(const float2 *)&M.ds[buf][r][ch], o.u = *(const float2 *)&M.us[buf][r][ch];
+            o.B = load4(&M.bc[buf][0][r][4 * q]);
+            if (!ENDS) o.C = load4(&M.bc[buf][1][r][4 * q]);
+        };
+        load(0, ahead[0]);
 #pragma unroll
-                for (int i = 0; i < L; ++i) {
-                    const int r = r0 + r1 + i;
-                    const float2 du = dd[r][ch];
-                    h = fma4(decay4(a2, du.x), h, mul4(load4(&bc[0][r][4 * q]), du.y));
-                    if (ENDS) sum += du.x;
-                    else part[i] = dot4(load4(&bc[1][r][4 * q]), h);
-                }
-                if (!ENDS) {
-                    const float s = lanes_sum<L, 1>(part, q);
-                    ys[r0 + r1 + q][ch] = s;
-                }
-            }
-        }
-        __syncthreads();
-        if (!ENDS && in) {
-            Vec<T, 8> out;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float v = fmaf(D[k], to_f(vx.e[k]), ys[er][ec + k]);
-                if (z) {
-                    const float zk = to_f(vz.e[k]);
-                    v *= zk * sigmoid(zk);
-                }
-                put(&out.e[k], v);
-            }
-            store_vec<T, 8>(y + (t + er) * P.y.sn, out, en);
+        for (int r = 0; r < R; ++r) {
+            if (r + 1 < R) load(r + 1, ahead[(r + 1) % 2]);
+            const Row &o = ahead[r % 2];
+            h[0] = fma4(decay4(a2[0], o.d.x), h[0], mul4(o.B, o.u.x));
+            h[1] = fma4(decay4(a2[1], o.d.y), h[1], mul4(o.B, o.u.y));
+            if (ENDS) sum[0] += o.d.x, sum[1] += o.d.y;
+            else *(float2 *)&M.ys[buf][q][r][ch] = make_float2(dot4(o.C, h[0]), dot4(o.C, h[1]));
         }
     }
-    if (!mine) return;
-    if (ENDS) {
-        store4(P.ends + ((long long)unit * P.C_ + c) * S + 4 * q, h);
-        if (q == 0) P.sums[(long long)unit * P.C_ + c] = sum;
-    } else if (P.last && hi == len) {
-        store4(P.last + ((long long)seq * P.C_ + c) * S + 4 * q, h);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (ch + i >= nc) continue;
+        const long long at = (long long)(c + i) * S + 4 * q;
+        if (ENDS) {
+            store4(P.ends + (long long)unit * P.C_ * S + at, h[i]);
+            if (q == 0) P.sums[(long long)unit * P.C_ + c + i] = sum[i];
+        } else if (P.last && hi == len) {
+            store4(P.last + (long long)seq * P.C_ * S + at, h[i]);
+        }
     }
 }
 
@@ -325,35 +424,39 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const __grid_cons
         if (P.dlast && mine) carry = load4(P.dlast + ((long long)seq * P.C_ + c) * S + 4 * q);
         Vec<T, EV> nx, nd, nz, no;
         Vec<T, 4> vb[NB];
-        F4 nh = zero4();
+        Vec<float, 4> nh = {};
         auto fetch = [&](int t) {
-            if (t + er < len && en > 0) {
-                nx = load_vec<T, EV>(x + (t + er) * P.x.sn, en);
-                nd = load_vec<T, EV>(dt + (t + er) * P.dt.sn, en);
-                no = load_vec<T, EV>(dO + (t + er) * P.dO.sn, en);
-                if (z) nz = load_vec<T, EV>(z + (t + er) * P.z.sn, en);
-            }
+            const bool on = t + er < len && en >= EV;
+            load_ahead(nx, x + (t + er) * P.x.sn, on);
+            load_ahead(nd, dt + (t + er) * P.dt.sn, on);
+            load_ahead(no, dO + (t + er) * P.dO.sn, on);
+            load_ahead(nz, z + (t + er) * P.z.sn, on && z);
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 const int v = i * kThreads + threadIdx.x, which = v / (R * S / 4), row = v % (R * S / 4) / (S / 4), col = v % (S / 4) * 4;
-                if (which < 2 && t + row < len)
-                    vb[i] = *(const Vec<T, 4> *)((which ? Cp : Bp) + (t + row) * (which ? OC.sn : OB.sn) + col);
+                load_ahead(vb[i], (which ? Cp : Bp) + (t + row) * (which ? OC.sn : OB.sn) + col, which < 2 && t + row < len);
             }
-            if (mine) nh = load4(P.marks + (mark_slot(P, seq, t) * P.C_ + c) * S + 4 * q);
+            load_ahead(nh, P.marks + (mark_slot(P, seq, t) * P.C_ + c) * S + 4 * q, mine);
         };
         const int tiles = (len + R - 1) / R;
         if (tiles > 0) fetch((tiles - 1) * R);
         for (int k = tiles - 1; k >= 0; --k) {
             const int t = k * R;
-            const Vec<T, EV> vx = nx, vd = nd, vz = nz, vo = no;
             const bool in = t + er < len && en > 0;
+            if (in && en < EV) {  // the last channels, where they are no whole vector
+                nx = load_vec<T, EV>(x + (t + er) * P.x.sn, en);
+                nd = load_vec<T, EV>(dt + (t + er) * P.dt.sn, en);
+                no = load_vec<T, EV>(dO + (t + er) * P.dO.sn, en);
+                if (z) nz = load_vec<T, EV>(z + (t + er) * P.z.sn, en);
+            }
+            const Vec<T, EV> vx = nx, vd = nd, vz = nz, vo = no;
             float d[EV], gg[EV], slope[EV];  // d, g, d's derivative
 #pragma unroll
             for (int e = 0; e < EV; ++e) {
                 d[e] = gg[e] = slope[e] = 0.f;
                 if (in && e < en) {
                     const float v = to_f(vd.e[e]) + bias[e];
-                    d[e] = step_of(P, v);
+                    d[e] = step_of(P, both(v)).x;
                     slope[e] = P.softplus ? sigmoid(v) : 1.f;
                     gg[e] = to_f(vo.e[e]);
                     if (z) {
@@ -372,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const __grid_cons
                 if (t + row < len) f = make_float4(to_f(vb[i].e[0]), to_f(vb[i].e[1]), to_f(vb[i].e[2]), to_f(vb[i].e[3]));
                 *(float4 *)&M.bc[which][row][col] = f;
             }
-            F4 h = nh;
+            F4 h{make_float2(nh.e[0], nh.e[1]), make_float2(nh.e[2], nh.e[3])};
             __syncthreads();
             if (k > 0) fetch(t - R);
             // the tile's states, and y
@@ -507,7 +610,7 @@ template <typename T, int S> __global__ void __launch_bounds__(kThreads) step_ke
         float *st = P.last + ((long long)b * P.C_ + cc) * S + 4 * q;
         const F4 h0 = load4(st);
         const float x = to_f(((const T *)P.x.p)[b * P.x.sb + cc]);
-        const float d = step_of(P, to_f(((const T *)P.dt.p)[b * P.dt.sb + cc]) + bias);
+        const float d = step_of(P, both(to_f(((const T *)P.dt.p)[b * P.dt.sb + cc]) + bias)).x;
         const Vec<T, 4> vb = *(const Vec<T, 4> *)((const T *)P.B.p + b * P.B.sb + g * P.B.sg + 4 * q);
         const Vec<T, 4> vc = *(const Vec<T, 4> *)((const T *)P.C.p + b * P.C.sb + g * P.C.sg + 4 * q);
         const F4 B{make_float2(to_f(vb.e[0]), to_f(vb.e[1])), make_float2(to_f(vb.e[2]), to_f(vb.e[3]))};
@@ -529,28 +632,29 @@ template <typename T, int S> __global__ void __launch_bounds__(kThreads) step_ke
 }
 
 // ----------------------------------------------------------------------------------------------------------- host
-int channels_of(int S) { return kWarps * 32 / (S / 4); }
-int blocks_per_group(int C, int G, int S) { return (C / G + channels_of(S) - 1) / channels_of(S); }
+int forward_channels(int S) { return S == 8 ? Tile<8>::CH : S == 16 ? Tile<16>::CH : Tile<32>::CH; }
+int back_channels(int S) { return kWarps * 32 / (S / 4); }
+int blocks_per_group(int C, int G, int channels) { return (C / G + channels - 1) / channels; }
 
 // Rows of a part: all, where the sequences' channel blocks make kEnough CTAs, else as many parts of a sequence of the mean
-// length as do, of kLeastPart rows at least.
-constexpr int kEnough = 152, kLeastPart = 512;
+// length as make two CTAs to an SM and no more, of kLeastPart rows at least.
+constexpr int kEnough = 76, kLeastPart = 512;
 int part_rows(int T, int nseq, int C, int G, int S) {
-    const long long ctas = (long long)nseq * G * blocks_per_group(C, G, S);
-    const int whole = ((T > 0 ? T : 1) + kLeastPart - 1) / kLeastPart * kLeastPart;  // a multiple of every tile
-    if (ctas >= kEnough || T / (nseq > 0 ? nseq : 1) < 2 * kLeastPart) return whole;
-    long long want = (2 * kEnough + ctas - 1) / ctas;
+    const long long n = nseq > 0 ? nseq : 1, ctas = n * G * blocks_per_group(C, G, forward_channels(S));
+    const long long whole = ((long long)T + kMark) / kMark * kMark;
+    if (ctas >= kEnough || T / n < 2 * kLeastPart) return (int)whole;
+    long long want = 2 * kSMs / ctas;
     if (want > kMaxParts) want = kMaxParts;
-    const long long rows = ((long long)T + nseq * want - 1) / (nseq * want);
-    const long long part = (rows + kLeastPart - 1) / kLeastPart * kLeastPart;
-    return part < whole ? (int)part : whole;
+    long long part = ((T + n * want - 1) / (n * want) + kMark - 1) / kMark * kMark;
+    if (part < kLeastPart) part = kLeastPart;
+    return (int)(part < whole ? part : whole);
 }
 long long units_of(int T, int nseq, int N, int part, bool packed) {
     if (packed) return nseq + T / part;
     return (long long)nseq * (N > 0 ? (N + part - 1) / part : 1);
 }
 int walkers_of(int nseq, int C, int G, int S) {
-    const long long cblocks = (long long)G * blocks_per_group(C, G, S), want = (4 * kSMs + cblocks - 1) / cblocks;
+    const long long cblocks = (long long)G * blocks_per_group(C, G, back_channels(S)), want = (4 * kSMs + cblocks - 1) / cblocks;
     return (int)(nseq < want ? nseq : want);
 }
 struct Space {  // byte offsets of the workspace's arrays
@@ -566,7 +670,7 @@ Space space_of(int T, int nseq, int C, int G, int S, bool back) {
     };
     if (back) {
         const size_t walkers = walkers_of(nseq, C, G, S);
-        w.pbc = take((size_t)blocks_per_group(C, G, S) * T * G * 2 * S * 4);
+        w.pbc = take((size_t)blocks_per_group(C, G, back_channels(S)) * T * G * 2 * S * 4);
         w.pa = take(walkers * C * (S + 2) * 4);
     } else {
         const int part = part_rows(T, nseq, C, G, S);
@@ -629,7 +733,7 @@ int take_inputs(Call &K, const void *X, const void *dt, const float *A, const vo
     P.C = GOp{C, K.v[5].st[0], K.v[5].st[1], K.v[5].st[2]};
     P.A = A, P.D = D, P.bias = bias, P.first = state;
     P.seq = Seqs{off, nseq, N, T, nullptr};
-    P.C_ = Cn, P.G = G, P.cpg = Cn / G, P.bpg = blocks_per_group(Cn, G, S);
+    P.C_ = Cn, P.G = G, P.cpg = Cn / G;
     P.softplus = softplus ? 1 : 0;
     K.rin[0] = {A, (size_t)Cn * S * 4};
     K.rin[1] = {D, (size_t)Cn * 4};
@@ -640,15 +744,23 @@ int take_inputs(Call &K, const void *X, const void *dt, const float *A, const vo
 }
 
 template <typename T, int S> cudaError_t forward(const Params &P, long long units, bool split, cudaStream_t s) {
+    using K = Tile<S>;
+    constexpr int all = (int)sizeof(typename K::Smem), some = (int)offsetof(typename K::Smem, ys);
+    static std::atomic<int> attr_state[kMaxDevices];
+    if (!once_per_device(attr_state, [] {
+            return cudaFuncSetAttribute(forward_kernel<T, S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, some) == cudaSuccess &&
+                   cudaFuncSetAttribute(forward_kernel<T, S, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, all) == cudaSuccess;
+        }))
+        return cudaErrorInvalidValue;
     const long long blocks = units * P.G * P.bpg;
     if (blocks >= (1LL << 31)) return cudaErrorInvalidConfiguration;
     if (split) {
-        forward_kernel<T, S, true><<<(unsigned)blocks, kThreads, 0, s>>>(P);
+        forward_kernel<T, S, true><<<(unsigned)blocks, K::THREADS, some, s>>>(P);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         count_launches(1);
     }
-    forward_kernel<T, S, false><<<(unsigned)blocks, kThreads, 0, s>>>(P);
+    forward_kernel<T, S, false><<<(unsigned)blocks, K::THREADS, all, s>>>(P);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) count_launches(1);
     return e;
@@ -741,6 +853,7 @@ int la_selective_scan(const void *X, const void *dt, const float *A, const void 
     if (nseq == 0) return LA_OK;
     Params &P = K.P;
     P.last = state_out, P.marks = marks;
+    P.bpg = blocks_per_group(channels, G, forward_channels(S));
     P.seq.status = (uint32_t *)workspace;
     P.part = part_rows(T, nseq, channels, G, S);
     const long long units = units_of(T, nseq, N, P.part, packed);
@@ -786,6 +899,7 @@ int la_selective_scan_backward(const void *X, const void *dt, const float *A, co
     if (outputs_meet(K.v, 6, out, 3, K.rin, 6, rout, 7)) return LA_ERR_INVALID_ARG;
     Params &P = K.P;
     P.first = nullptr;
+    P.bpg = blocks_per_group(channels, G, back_channels(S));
     P.dlast = dstate_out, P.dfirst = dstate_in, P.marks = (float *)marks;
     P.seq.status = (uint32_t *)workspace;
     P.valid = (uint32_t *)workspace + offsetof(WsHeader, reserved) / 4;
