@@ -29,8 +29,9 @@ namespace sel {
 
 using namespace rows;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;  // backward, step
-constexpr int kMark = 16;      // rows between the states that a forward keeps for its backward
+constexpr int kThreads = 256;  // of a step's block
+constexpr int kMark = 8;       // rows between the states that a forward keeps for its backward, and of its tile
+constexpr int kTile = 16;      // rows of a forward tile
 constexpr int kSMs = 152;
 constexpr int kMaxParts = 64;  // of a sequence
 
@@ -54,7 +55,7 @@ struct Params {
     Op dO, dx, ddt, dz;
     const float *dlast;        // [nseq, C, S] or null
     float *dfirst;
-    float *pbc;                // [bpg, T, G, 2 S]
+    float *pbc;                // [groups of 64 channels, T, G, 2 S]
     float *pa;                 // [walkers, C, S], then [walkers, C] of dD and of d(dt_bias)
     int walkers;
     uint32_t *valid;           // whether the offsets were in order, for the sums behind
@@ -120,7 +121,7 @@ template <int L, int STEP> __device__ __forceinline__ float lanes_sum(float (&v)
 }
 
 template <int S> struct Tile {
-    static constexpr int R = kMark;                                       // rows
+    static constexpr int R = kTile;                                       // rows
     static constexpr int QW = S / 4, GW = QW > 4 ? 1 : 4 / QW;            // warps of a channel group, groups
     static constexpr int CH = 64 * GW, HELP = CH == 64 ? 256 : 2 * CH;  // channels of a CTA, helping threads
     static constexpr int THREADS = HELP + 32 * QW * GW;
@@ -327,10 +328,7 @@ __global__ void __launch_bounds__(Tile<S>::THREADS, S == 16 ? 2 : 1) forward_ker
         __syncthreads();
         if (k == tiles) break;
         const int buf = k & 1;
-        if (!ENDS && P.marks)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (ch + i < nc) store4(P.marks + (mark_slot(P, seq, lo + k * R) * P.C_ + c + i) * S + 4 * q, h[i]);
+        float *mark = !ENDS && P.marks ? P.marks + (mark_slot(P, seq, lo + k * R) * P.C_ + c) * S + 4 * q : nullptr;
         // A row's operands are loaded a row ahead of it, before the parts of y of the row between are stored (which the
         // compiler has to take for stores to them).
         struct Row {
@@ -347,6 +345,11 @@ __global__ void __launch_bounds__(Tile<S>::THREADS, S == 16 ? 2 : 1) forward_ker
         for (int r = 0; r < R; ++r) {
             if (r + 1 < R) load(r + 1, ahead[(r + 1) % 2]);
             const Row &o = ahead[r % 2];
+            if (r % kMark == 0 && mark && lo + k * R + r < hi) {
+                float *m = mark + (long long)(r / kMark) * P.C_ * S;
+                if (ch < nc) store4(m, h[0]);
+                if (ch + 1 < nc) store4(m + S, h[1]);
+            }
             h[0] = fma4(decay4(a2[0], o.d.x), h[0], mul4(o.B, o.u.x));
             h[1] = fma4(decay4(a2[1], o.d.y), h[1], mul4(o.B, o.u.y));
             if (ENDS) sum[0] += o.d.x, sum[1] += o.d.y;
@@ -367,218 +370,282 @@ __global__ void __launch_bounds__(Tile<S>::THREADS, S == 16 ? 2 : 1) forward_ker
 }
 
 // ------------------------------------------------------------------------------------------------------- backward
-// A tile is kMark rows, entered with the state that the forward kept.  Its states are formed again into shared memory, then
-// the rows are walked from the last to the first with G; sums over states and over a warp's channels by transposing
-// butterflies of shuffles, the warps' sums of dB and dC through shared memory.
-template <typename T, int S> struct Back {
-    static constexpr int L = S / 4, CW = 32 / L, CH = kWarps * CW, R = kMark;
-    static constexpr int EV = R * CH / kThreads, PER = CH / EV;  // elements of a thread, vectors of a row
-    static constexpr int NBT = 2 * R * S / 4;                    // vectors of four of B and C
-    static constexpr int NB = (NBT + kThreads - 1) / kThreads;
+// The same roles.  A tile is kMark rows, entered with the state that the forward kept: its states are formed again, in
+// registers, and its rows walked from the last to the first with G.  Four states of two channels leave a row's parts of y,
+// sum G B and sum a h G A in shared memory, where the helping warps add them up and form the gradients of rows; dB and dC are
+// summed over the warp's 64 channels, in the thread and then by butterflies of shuffles that hand each lane a value of its
+// own (8 values over 8 lanes, then four rows of them over the four groups of lanes), and over the channel blocks by a launch
+// of its own.  Bound by shared memory and issue slots alike: some 190 clocks of an SM for a row of 64 channels.
+template <int S> struct Back {
+    static constexpr int R = kMark, QW = S / 4, GW = QW > 4 ? 1 : 4 / QW, CH = 64 * GW;
+    static constexpr int HELP = R * CH / 4, SCAN = 32 * QW * GW, THREADS = HELP + SCAN;  // a vector of four channels to a helper
+    static constexpr int NB = (2 * R * S / 4 + HELP - 1) / HELP;
+    static constexpr int FLUSH = 8;  // tiles between additions to dA's sums, which so pass fewer roundings
     struct Smem {
-        float4 hs[R][kThreads];           // the state before each row
-        float2 dd[R][CH];
-        float gs[R][CH], ws[R][CH], es[R][CH], ys[R][CH];
-        float bc[2][R][S];
-        float red[kWarps][R][2 * S];
+        float ds[3][R][CH], us[2][R][CH], gs[2][R][CH];  // d, d x, g
+        float bc[2][2][R][S];
+        float ys[2][QW][R][CH], ws[2][QW][R][CH], es[2][QW][R][CH];
+        float4 dA[2][SCAN];
     };
 };
 
 template <typename T, int S>
-__global__ void __launch_bounds__(kThreads, 2) backward_kernel(const __grid_constant__ Params P) {
-    using K = Back<T, S>;
-    constexpr int L = K::L, CW = K::CW, CH = K::CH, R = K::R, EV = K::EV, NB = K::NB;
+__global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_kernel(const __grid_constant__ Params P) {
+    using K = Back<S>;
+    constexpr int CH = K::CH, R = K::R, NB = K::NB, QW = K::QW, HELP = K::HELP;
     extern __shared__ __align__(16) unsigned char raw[];
     typename K::Smem &M = *(typename K::Smem *)raw;
     const int cblocks = P.G * P.bpg, walker = blockIdx.x / cblocks, cb = blockIdx.x - walker * cblocks;
     const int g = cb / P.bpg, c0 = g * P.cpg + (cb - g * P.bpg) * CH, nc = min(CH, (g + 1) * P.cpg - c0);
-    const int er = threadIdx.x / K::PER, ec = threadIdx.x % K::PER * EV, en = nc - ec;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = lane % L, ch = warp * CW + lane / L, c = c0 + ch;
-    const bool mine = ch < nc;
-    float bias[EV], D[EV], dD[EV], dbias[EV];
-#pragma unroll
-    for (int k = 0; k < EV; ++k) {
-        bias[k] = P.bias && k < en ? P.bias[c0 + ec + k] : 0.f;
-        D[k] = P.D && k < en ? P.D[c0 + ec + k] : 0.f;
-        dD[k] = dbias[k] = 0.f;
-    }
-    F4 a2 = zero4(), dA = zero4();
-    if (mine) a2 = mul4(load4(P.A + (long long)c * S + 4 * q), kLog2e);
     bool fine = true;
     if (P.seq.off) {
         int n;
         fine = offsets_in_order(P.seq, n, [](int, int) { return false; });
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) *P.valid = fine;
-    for (int seq = walker; seq < P.seq.nseq && fine; seq += P.walkers) {
-        const int first = P.seq.off ? P.seq.off[seq] : seq * P.seq.N, len = P.seq.off ? P.seq.off[seq + 1] - first : P.seq.N;
-        const T *x = rows_of<const T>(P.seq, P.x, seq) + c0 + ec, *dt = rows_of<const T>(P.seq, P.dt, seq) + c0 + ec;
-        const T *z = P.z.p ? rows_of<const T>(P.seq, P.z, seq) + c0 + ec : nullptr;
-        const T *dO = rows_of<const T>(P.seq, P.dO, seq) + c0 + ec;
-        T *dx = rows_of<T>(P.seq, P.dx, seq) + c0 + ec, *ddt = rows_of<T>(P.seq, P.ddt, seq) + c0 + ec;
-        T *dz = z ? rows_of<T>(P.seq, P.dz, seq) + c0 + ec : nullptr;
-        const GOp &OB = P.B, &OC = P.C;
-        const T *Bp = (const T *)OB.p + (P.seq.off ? first * OB.sn : seq * OB.sb) + g * OB.sg;
-        const T *Cp = (const T *)OC.p + (P.seq.off ? first * OC.sn : seq * OC.sb) + g * OC.sg;
-        F4 carry = zero4();  // a_{t+1} G_{t+1}
-        if (P.dlast && mine) carry = load4(P.dlast + ((long long)seq * P.C_ + c) * S + 4 * q);
-        Vec<T, EV> nx, nd, nz, no;
+    const int helper = (int)threadIdx.x - K::SCAN;
+    if (helper >= 0) {
+        const int row = helper / (CH / 4), col = helper % (CH / 4) * 4, n = nc - col;
+        float bias[4], D[4], dD[4], dbias[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            bias[e] = P.bias && e < n ? P.bias[c0 + col + e] : 0.f;
+            D[e] = P.D && e < n ? P.D[c0 + col + e] : 0.f;
+            dD[e] = dbias[e] = 0.f;
+        }
+        struct Four {
+            Vec<T, 4> x, d, o, z;
+        } in, out;  // on their way to d and g; to the gradients of rows
         Vec<T, 4> vb[NB];
-        Vec<float, 4> nh = {};
-        auto fetch = [&](int t) {
-            const bool on = t + er < len && en >= EV;
-            load_ahead(nx, x + (t + er) * P.x.sn, on);
-            load_ahead(nd, dt + (t + er) * P.dt.sn, on);
-            load_ahead(no, dO + (t + er) * P.dO.sn, on);
-            load_ahead(nz, z + (t + er) * P.z.sn, on && z);
+        for (int seq = walker; seq < P.seq.nseq && fine; seq += P.walkers) {
+            const int first = P.seq.off ? P.seq.off[seq] : seq * P.seq.N, len = P.seq.off ? P.seq.off[seq + 1] - first : P.seq.N;
+            const T *x = rows_of<const T>(P.seq, P.x, seq) + c0 + col, *dt = rows_of<const T>(P.seq, P.dt, seq) + c0 + col;
+            const T *z = P.z.p ? rows_of<const T>(P.seq, P.z, seq) + c0 + col : nullptr;
+            const T *dO = rows_of<const T>(P.seq, P.dO, seq) + c0 + col;
+            T *dx = rows_of<T>(P.seq, P.dx, seq) + c0 + col, *ddt = rows_of<T>(P.seq, P.ddt, seq) + c0 + col;
+            T *dz = z ? rows_of<T>(P.seq, P.dz, seq) + c0 + col : nullptr;
+            const T *Bp = (const T *)P.B.p + (P.seq.off ? first * P.B.sn : seq * P.B.sb) + g * P.B.sg;
+            const T *Cp = (const T *)P.C.p + (P.seq.off ? first * P.C.sn : seq * P.C.sb) + g * P.C.sg;
+            const int tiles = (len + R - 1) / R;
+            auto fetch = [&](int k, Four &f) {
+                const int r = k * R + row;
+                const bool on = k >= 0 && r < len && n >= 4;
+                load_ahead(f.x, x + r * P.x.sn, on);
+                load_ahead(f.d, dt + r * P.dt.sn, on);
+                load_ahead(f.o, dO + r * P.dO.sn, on);
+                load_ahead(f.z, z + r * P.z.sn, on && z);
+            };
+            auto rest = [&](int k, Four &f) {  // the last channels, where they are no whole vector
+                const int r = k * R + row;
+                if (r >= len || n <= 0 || n >= 4) return;
+                f.x = load_vec<T, 4>(x + r * P.x.sn, n);
+                f.d = load_vec<T, 4>(dt + r * P.dt.sn, n);
+                f.o = load_vec<T, 4>(dO + r * P.dO.sn, n);
+                if (z) f.z = load_vec<T, 4>(z + r * P.z.sn, n);
+            };
+            auto fetch_bc = [&](int k) {
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int v = i * kThreads + threadIdx.x, which = v / (R * S / 4), row = v % (R * S / 4) / (S / 4), col = v % (S / 4) * 4;
-                load_ahead(vb[i], (which ? Cp : Bp) + (t + row) * (which ? OC.sn : OB.sn) + col, which < 2 && t + row < len);
-            }
-            load_ahead(nh, P.marks + (mark_slot(P, seq, t) * P.C_ + c) * S + 4 * q, mine);
-        };
-        const int tiles = (len + R - 1) / R;
-        if (tiles > 0) fetch((tiles - 1) * R);
-        for (int k = tiles - 1; k >= 0; --k) {
-            const int t = k * R;
-            const bool in = t + er < len && en > 0;
-            if (in && en < EV) {  // the last channels, where they are no whole vector
-                nx = load_vec<T, EV>(x + (t + er) * P.x.sn, en);
-                nd = load_vec<T, EV>(dt + (t + er) * P.dt.sn, en);
-                no = load_vec<T, EV>(dO + (t + er) * P.dO.sn, en);
-                if (z) nz = load_vec<T, EV>(z + (t + er) * P.z.sn, en);
-            }
-            const Vec<T, EV> vx = nx, vd = nd, vz = nz, vo = no;
-            float d[EV], gg[EV], slope[EV];  // d, g, d's derivative
+                for (int i = 0; i < NB; ++i) {
+                    const int v = i * HELP + helper, which = v / (R * S / 4), r = k * R + v % (R * S / 4) / (S / 4), s = v % (S / 4) * 4;
+                    load_ahead(vb[i], (which ? Cp + r * P.C.sn : Bp + r * P.B.sn) + s, which < 2 && k >= 0 && r < len);
+                }
+            };
+            auto produce = [&](int k) {
+                rest(k, in);
+                const bool live = k * R + row < len;
+                float d[4], u[4], gr[4];
 #pragma unroll
-            for (int e = 0; e < EV; ++e) {
-                d[e] = gg[e] = slope[e] = 0.f;
-                if (in && e < en) {
-                    const float v = to_f(vd.e[e]) + bias[e];
-                    d[e] = step_of(P, both(v)).x;
-                    slope[e] = P.softplus ? sigmoid(v) : 1.f;
-                    gg[e] = to_f(vo.e[e]);
+                for (int e = 0; e < 4; e += 2) {
+                    const float2 v = step_of(P, make_float2(to_f(in.d.e[e]) + bias[e], to_f(in.d.e[e + 1]) + bias[e + 1]));
+                    d[e] = v.x, d[e + 1] = v.y;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    u[e] = d[e] * to_f(in.x.e[e]);
+                    gr[e] = to_f(in.o.e[e]);
                     if (z) {
-                        const float zk = to_f(vz.e[e]);
-                        gg[e] *= zk * sigmoid(zk);
+                        const float ze = to_f(in.z.e[e]);
+                        gr[e] *= ze * sigmoid(ze);
                     }
+                    if (!live || e >= n) d[e] = u[e] = gr[e] = 0.f;  // no row: nothing happens
                 }
-                M.dd[er][ec + e] = make_float2(d[e], in && e < en ? d[e] * to_f(vx.e[e]) : 0.f);
-                M.gs[er][ec + e] = gg[e];
-            }
+                *(float4 *)&M.ds[k % 3][row][col] = make_float4(d[0], d[1], d[2], d[3]);
+                *(float4 *)&M.us[k & 1][row][col] = make_float4(u[0], u[1], u[2], u[3]);
+                *(float4 *)&M.gs[k & 1][row][col] = make_float4(gr[0], gr[1], gr[2], gr[3]);
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int v = i * kThreads + threadIdx.x, which = v / (R * S / 4), row = v % (R * S / 4) / (S / 4), col = v % (S / 4) * 4;
-                if (which >= 2) continue;
-                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (t + row < len) f = make_float4(to_f(vb[i].e[0]), to_f(vb[i].e[1]), to_f(vb[i].e[2]), to_f(vb[i].e[3]));
-                *(float4 *)&M.bc[which][row][col] = f;
-            }
-            F4 h{make_float2(nh.e[0], nh.e[1]), make_float2(nh.e[2], nh.e[3])};
-            __syncthreads();
-            if (k > 0) fetch(t - R);
-            // the tile's states, and y
-#pragma unroll
-            for (int r1 = 0; r1 < R; r1 += L) {
-                float part[L];
-#pragma unroll
-                for (int i = 0; i < L; ++i) {
-                    const int r = r1 + i;
-                    const float2 du = M.dd[r][ch];
-                    store4((float *)&M.hs[r][threadIdx.x], h);
-                    h = fma4(decay4(a2, du.x), h, mul4(load4(&M.bc[0][r][4 * q]), du.y));
-                    if (P.z.p) part[i] = dot4(load4(&M.bc[1][r][4 * q]), h);
+                for (int i = 0; i < NB; ++i) {
+                    const int v = i * HELP + helper, which = v / (R * S / 4), r = v % (R * S / 4) / (S / 4), s = v % (S / 4) * 4;
+                    if (which >= 2) continue;
+                    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k * R + r < len) f = make_float4(to_f(vb[i].e[0]), to_f(vb[i].e[1]), to_f(vb[i].e[2]), to_f(vb[i].e[3]));
+                    *(float4 *)&M.bc[k & 1][which][r][s] = f;
                 }
-                if (P.z.p) {
-                    const float s = lanes_sum<L, 1>(part, q);
-                    M.ys[r1 + q][ch] = s;
+            };
+            auto total = [&](const float (&parts)[QW][R][CH], float (&s)[4]) {
+                float4 a = *(const float4 *)&parts[0][row][col];
+#pragma unroll
+                for (int w = 1; w < QW; ++w) {
+                    const float4 o = *(const float4 *)&parts[w][row][col];
+                    a.x += o.x, a.y += o.y, a.z += o.z, a.w += o.w;
                 }
-            }
-            // backwards
+                s[0] = a.x, s[1] = a.y, s[2] = a.z, s[3] = a.w;
+            };
+            auto finish = [&](int k) {
+                rest(k, out);
+                const int r = k * R + row;
+                if (r >= len || n <= 0) return;
+                float w[4], es[4], ys[4];
+                total(M.ws[k & 1], w), total(M.es[k & 1], es);
+                if (z) total(M.ys[k & 1], ys);
+                const float4 d4 = *(const float4 *)&M.ds[k % 3][row][col];
+                const float d[4] = {d4.x, d4.y, d4.z, d4.w};
+                Vec<T, 4> ox, od, oz;
 #pragma unroll
-            for (int r1 = R - L; r1 >= 0; r1 -= L) {
-                float pw[L], pe[L];
-#pragma unroll
-                for (int i = L - 1; i >= 0; --i) {
-                    const int r = r1 + i;
-                    const float2 du = M.dd[r][ch];
-                    const float gr = M.gs[r][ch];
-                    const F4 B = load4(&M.bc[0][r][4 * q]), C = load4(&M.bc[1][r][4 * q]);
-                    const F4 before = load4((const float *)&M.hs[r][threadIdx.x]);
-                    const F4 G = fma4(C, gr, carry);
-                    F4 dB = mul4(G, du.y), dC = mul4(h, gr);
-                    pw[i] = dot4(G, B);
-                    carry = mul4(decay4(a2, du.x), G);
-                    const F4 e = mul4(carry, before);
-                    pe[i] = dot4(e, a2);
-                    dA = fma4(e, du.x, dA);
-                    h = before;
-                    // over the warp's channels
-                    float v[8] = {dB.a.x, dB.a.y, dB.b.x, dB.b.y, dC.a.x, dC.a.y, dC.b.x, dC.b.y};
-                    if constexpr (CW >= 8) {
-                        const int p = lane / L;
-                        float s = lanes_sum<8, L>(v, p % 8);
-                        if (CW == 16) s += __shfl_xor_sync(0xffffffffu, s, 8 * L);
-                        if (p < 8) M.red[warp][r][(p & 4) / 4 * S + 4 * q + (p & 3)] = s;
-                    } else {
-                        const int p = lane / L;  // four channels: two values to a lane
-                        float lo[4] = {v[0], v[1], v[2], v[3]}, up[4] = {v[4], v[5], v[6], v[7]};
-                        M.red[warp][r][4 * q + p] = lanes_sum<4, L>(lo, p);
-                        M.red[warp][r][S + 4 * q + p] = lanes_sum<4, L>(up, p);
+                for (int e = 0; e < 4; ++e) {
+                    const float xe = to_f(out.x.e[e]), oe = to_f(out.o.e[e]);
+                    float gr = oe;
+                    if (z) {
+                        const float ze = to_f(out.z.e[e]), sg = sigmoid(ze);
+                        gr *= ze * sg;
+                        put(&oz.e[e], oe * fmaf(D[e], xe, ys[e]) * silu_grad(ze, sg));
                     }
-                }
-                const float w = lanes_sum<L, 1>(pw, q), e = lanes_sum<L, 1>(pe, q);
-                M.ws[r1 + q][ch] = w;
-                M.es[r1 + q][ch] = e;
-            }
-            __syncthreads();
-            if (in) {
-                Vec<T, EV> ox, od, oz;
-#pragma unroll
-                for (int e = 0; e < EV; ++e) {
-                    if (e >= en) break;
-                    const float xe = to_f(vx.e[e]), w = M.ws[er][ec + e];
-                    put(&ox.e[e], fmaf(d[e], w, D[e] * gg[e]));
-                    const float s = fmaf(M.es[er][ec + e], kLn2, xe * w) * slope[e];
+                    put(&ox.e[e], fmaf(d[e], w[e], D[e] * gr));
+                    float s = fmaf(es[e], kLn2, xe * w[e]);
+                    if (P.softplus) s *= sigmoid(to_f(out.d.e[e]) + bias[e]);
                     put(&od.e[e], s);
                     dbias[e] += s;
-                    dD[e] = fmaf(gg[e], xe, dD[e]);
-                    if (z) {
-                        const float zk = to_f(vz.e[e]);
-                        put(&oz.e[e], to_f(vo.e[e]) * fmaf(D[e], xe, M.ys[er][ec + e]) * silu_grad(zk, sigmoid(zk)));
-                    }
+                    dD[e] = fmaf(gr, xe, dD[e]);
                 }
-                store_vec<T, EV>(dx + (t + er) * P.dx.sn, ox, en);
-                store_vec<T, EV>(ddt + (t + er) * P.ddt.sn, od, en);
-                if (z) store_vec<T, EV>(dz + (t + er) * P.dz.sn, oz, en);
+                store_vec<T, 4>(dx + r * P.dx.sn, ox, n);
+                store_vec<T, 4>(ddt + r * P.ddt.sn, od, n);
+                if (z) store_vec<T, 4>(dz + r * P.dz.sn, oz, n);
+            };
+            fetch(tiles - 1, in), fetch_bc(tiles - 1);
+            if (tiles > 0) produce(tiles - 1);
+            fetch(tiles - 2, in), fetch_bc(tiles - 2);
+            // while tile k is walked: d and g of tile k - 1, the gradients of tile k + 1
+            for (int k = tiles - 1; k >= -1; --k) {
+                __syncthreads();
+                if (k > 0) produce(k - 1);
+                fetch(k - 2, in), fetch_bc(k - 2);
+                if (k + 1 < tiles) finish(k + 1);
+                fetch(k, out);
             }
-            float *pbc = P.pbc + ((long long)(cb - g * P.bpg) * P.seq.T + first + t) * P.G * 2 * S + g * 2 * S;
-            for (int v = threadIdx.x; v < R * 2 * S; v += kThreads) {
-                const int r = v / (2 * S), n = v % (2 * S);
-                if (t + r >= len) break;
-                float s = M.red[0][r][n];
-#pragma unroll
-                for (int w = 1; w < kWarps; ++w) s += M.red[w][r][n];
-                pbc[(long long)r * P.G * 2 * S + n] = s;
-            }
+            __syncthreads();  // the last tile's shared memory has been read
         }
-        if (P.dfirst && mine) store4(P.dfirst + ((long long)seq * P.C_ + c) * S + 4 * q, carry);
-        __syncthreads();  // the last tile's shared memory has been read
-    }
-    if (mine) store4(P.pa + ((long long)walker * P.C_ + c) * S + 4 * q, dA);
-    // dD and the bias: over the tile's rows
-    float *sd = &M.ws[0][0], *sb = &M.es[0][0];
+        // dD and the bias: over the tile's rows
 #pragma unroll
-    for (int e = 0; e < EV; ++e) sd[er * CH + ec + e] = dD[e], sb[er * CH + ec + e] = dbias[e];
-    __syncthreads();
-    float *pd = P.pa + (long long)P.walkers * P.C_ * S + (long long)walker * 2 * P.C_;
-    for (int v = threadIdx.x; v < nc; v += kThreads) {
-        float s = 0.f, b = 0.f;
-        for (int r = 0; r < R; ++r) s += sd[r * CH + v], b += sb[r * CH + v];
-        pd[c0 + v] = s;
-        pd[P.C_ + c0 + v] = b;
+        for (int e = 0; e < 4; ++e) M.us[0][row][col + e] = dD[e], M.gs[0][row][col + e] = dbias[e];
+        __syncthreads();
+        float *pd = P.pa + (long long)P.walkers * P.C_ * S + (long long)walker * 2 * P.C_;
+        for (int v = helper; v < nc; v += HELP) {
+            float s = 0.f, b = 0.f;
+            for (int r = 0; r < R; ++r) s += M.us[0][r][v], b += M.gs[0][r][v];
+            pd[c0 + v] = s;
+            pd[P.C_ + c0 + v] = b;
+        }
+        return;
     }
+    // four states of two neighbouring channels
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp % QW, group = warp / QW, ch = group * 64 + lane * 2, c = c0 + ch;
+    F4 a2[2] = {zero4(), zero4()}, dA[2] = {zero4(), zero4()};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (ch + i < nc) a2[i] = mul4(load4(P.A + (long long)(c + i) * S + 4 * q), kLog2e);
+        M.dA[i][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    auto flush = [&] {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float4 &s = M.dA[i][threadIdx.x];
+            s = make_float4(s.x + dA[i].a.x, s.y + dA[i].a.y, s.z + dA[i].b.x, s.w + dA[i].b.y);
+            dA[i] = zero4();
+        }
+    };
+    for (int seq = walker; seq < P.seq.nseq && fine; seq += P.walkers) {
+        const int first = P.seq.off ? P.seq.off[seq] : seq * P.seq.N, len = P.seq.off ? P.seq.off[seq + 1] - first : P.seq.N;
+        const int tiles = (len + R - 1) / R;
+        F4 carry[2] = {zero4(), zero4()};  // a_{t+1} G_{t+1}
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (P.dlast && ch + i < nc) carry[i] = load4(P.dlast + ((long long)seq * P.C_ + c + i) * S + 4 * q);
+        Vec<float, 4> mark[2] = {};
+        auto fetch = [&](int k) {
+            const float *m = P.marks + (mark_slot(P, seq, k * R) * P.C_ + c) * S + 4 * q;
+            load_ahead(mark[0], m, k >= 0 && ch < nc);
+            load_ahead(mark[1], m + S, k >= 0 && ch + 1 < nc);
+        };
+        fetch(tiles - 1);
+        // sums of dB (values 0 ... 3) and dC (4 ... 7) of the warp's states: a lane's value of a row of four
+        float *pbc = P.pbc + ((long long)((cb - g * P.bpg) * K::GW + group) * P.seq.T + first) * P.G * 2 * S + g * 2 * S +
+                     (lane & 4 ? S : 0) + 4 * q + (lane & 3);
+        for (int k = tiles - 1; k >= -1; --k) {
+            __syncthreads();
+            if (k < 0) break;
+            const int buf = k & 1;
+            const auto &ds = M.ds[k % 3];
+            F4 h0[2];  // the tile's first state
+#pragma unroll
+            for (int i = 0; i < 2; ++i) h0[i] = F4{make_float2(mark[i].e[0], mark[i].e[1]), make_float2(mark[i].e[2], mark[i].e[3])};
+            fetch(k - 1);
+            auto advance = [&](int r, const F4(&h)[2], F4(&to)[2]) {
+                const float2 d = *(const float2 *)&ds[r][ch], u = *(const float2 *)&M.us[buf][r][ch];
+                const F4 B = load4(&M.bc[buf][0][r][4 * q]);
+                to[0] = fma4(decay4(a2[0], d.x), h[0], mul4(B, u.x));
+                to[1] = fma4(decay4(a2[1], d.y), h[1], mul4(B, u.y));
+            };
+#pragma unroll
+            for (int half = R - 4; half >= 0; half -= 4) {
+                F4 hs[5][2];  // the states before each of four rows, and behind the last
+                hs[0][0] = h0[0], hs[0][1] = h0[1];
+#pragma unroll
+                for (int r = 0; r < half; ++r) advance(r, hs[0], hs[0]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) advance(half + r, hs[r], hs[r + 1]);
+                asm volatile("" ::: "memory");  // d, d x, B and the decays are not kept for the way back: registers are short
+                // Four rows' results are stored together: a store ends what may be loaded early.
+                float four[4];
+                float2 w[4], e[4], y[4];
+#pragma unroll
+                for (int i = 3; i >= 0; --i) {
+                    const int r = half + i;
+                    const float2 d = *(const float2 *)&ds[r][ch], u = *(const float2 *)&M.us[buf][r][ch], gr = *(const float2 *)&M.gs[buf][r][ch];
+                    const F4 B = load4(&M.bc[buf][0][r][4 * q]), C = load4(&M.bc[buf][1][r][4 * q]);
+                    if (P.z.p) y[i] = make_float2(dot4(C, hs[i + 1][0]), dot4(C, hs[i + 1][1]));
+                    const F4 G0 = fma4(C, gr.x, carry[0]), G1 = fma4(C, gr.y, carry[1]);
+                    const F4 dB = fma4(G1, u.y, mul4(G0, u.x)), dC = fma4(hs[i + 1][1], gr.y, mul4(hs[i + 1][0], gr.x));
+                    w[i] = make_float2(dot4(G0, B), dot4(G1, B));
+                    carry[0] = mul4(decay4(a2[0], d.x), G0);
+                    carry[1] = mul4(decay4(a2[1], d.y), G1);
+                    const F4 e0 = mul4(carry[0], hs[i][0]), e1 = mul4(carry[1], hs[i][1]);
+                    dA[0] = fma4(e0, d.x, dA[0]);
+                    dA[1] = fma4(e1, d.y, dA[1]);
+                    e[i] = make_float2(dot4(e0, a2[0]), dot4(e1, a2[1]));
+                    float v[8] = {dB.a.x, dB.a.y, dB.b.x, dB.b.y, dC.a.x, dC.a.y, dC.b.x, dC.b.y};
+                    four[i] = lanes_sum<8, 1>(v, lane & 7);
+                }
+                const float s = lanes_sum<4, 8>(four, lane >> 3);
+                const int at = k * R + half + (lane >> 3);
+                if (at < len) pbc[(long long)at * P.G * 2 * S] = s;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    *(float2 *)&M.ws[buf][q][half + i][ch] = w[i];
+                    *(float2 *)&M.es[buf][q][half + i][ch] = e[i];
+                    if (P.z.p) *(float2 *)&M.ys[buf][q][half + i][ch] = y[i];
+                }
+            }
+            if (k % K::FLUSH == 0) flush();
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (P.dfirst && ch + i < nc) store4(P.dfirst + ((long long)seq * P.C_ + c + i) * S + 4 * q, carry[i]);
+        __syncthreads();
+    }
+    flush();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (ch + i < nc) *(float4 *)(P.pa + ((long long)walker * P.C_ + c + i) * S + 4 * q) = M.dA[i][threadIdx.x];
+    __syncthreads();
 }
 
 // dB and dC: the channel blocks' sums, rounded once.
@@ -590,7 +657,7 @@ template <typename T, int S> __global__ void __launch_bounds__(256) sum_bc_kerne
     if (P.seq.off && (row < P.seq.off[0] || row >= P.seq.off[P.seq.nseq])) return;
     float s = 0.f;
 #pragma unroll 4
-    for (int b = 0; b < P.bpg; ++b) s += P.pbc[(long long)b * P.seq.T * row_w + i];
+    for (int b = 0; b < P.bpg * Back<S>::GW; ++b) s += P.pbc[(long long)b * P.seq.T * row_w + i];
     const int g = at / (2 * S), n = at % (2 * S);
     put((n < S ? dB : dC) + (row * P.G + g) * S + n % S, s);
 }
@@ -633,7 +700,7 @@ template <typename T, int S> __global__ void __launch_bounds__(kThreads) step_ke
 
 // ----------------------------------------------------------------------------------------------------------- host
 int forward_channels(int S) { return S == 8 ? Tile<8>::CH : S == 16 ? Tile<16>::CH : Tile<32>::CH; }
-int back_channels(int S) { return kWarps * 32 / (S / 4); }
+int back_channels(int S) { return S == 8 ? Back<8>::CH : S == 16 ? Back<16>::CH : Back<32>::CH; }
 int blocks_per_group(int C, int G, int channels) { return (C / G + channels - 1) / channels; }
 
 // Rows of a part: all, where the sequences' channel blocks make kEnough CTAs, else as many parts of a sequence of the mean
@@ -641,11 +708,11 @@ int blocks_per_group(int C, int G, int channels) { return (C / G + channels - 1)
 constexpr int kEnough = 76, kLeastPart = 512;
 int part_rows(int T, int nseq, int C, int G, int S) {
     const long long n = nseq > 0 ? nseq : 1, ctas = n * G * blocks_per_group(C, G, forward_channels(S));
-    const long long whole = ((long long)T + kMark) / kMark * kMark;
+    const long long whole = ((long long)T + kTile) / kTile * kTile;
     if (ctas >= kEnough || T / n < 2 * kLeastPart) return (int)whole;
     long long want = 2 * kSMs / ctas;
     if (want > kMaxParts) want = kMaxParts;
-    long long part = ((T + n * want - 1) / (n * want) + kMark - 1) / kMark * kMark;
+    long long part = ((T + n * want - 1) / (n * want) + kTile - 1) / kTile * kTile;
     if (part < kLeastPart) part = kLeastPart;
     return (int)(part < whole ? part : whole);
 }
@@ -670,7 +737,7 @@ Space space_of(int T, int nseq, int C, int G, int S, bool back) {
     };
     if (back) {
         const size_t walkers = walkers_of(nseq, C, G, S);
-        w.pbc = take((size_t)blocks_per_group(C, G, back_channels(S)) * T * G * 2 * S * 4);
+        w.pbc = take((size_t)blocks_per_group(C, G, back_channels(S)) * (back_channels(S) / 64) * T * G * 2 * S * 4);
         w.pa = take(walkers * C * (S + 2) * 4);
     } else {
         const int part = part_rows(T, nseq, C, G, S);
@@ -770,7 +837,7 @@ template <typename T> cudaError_t forward(const Params &P, int S, long long unit
 }
 
 template <typename T, int S> cudaError_t backward(const Params &P, void *dB, void *dC, float *dA, float *dD, float *dbias, cudaStream_t s) {
-    using M = typename Back<T, S>::Smem;
+    using M = typename Back<S>::Smem;
     static std::atomic<int> attr_state[kMaxDevices];
     if (!once_per_device(attr_state, [] {
             return cudaFuncSetAttribute(backward_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(M)) == cudaSuccess;
@@ -778,7 +845,7 @@ template <typename T, int S> cudaError_t backward(const Params &P, void *dB, voi
         return cudaErrorInvalidValue;
     const long long blocks = (long long)P.walkers * P.G * P.bpg;
     if (blocks > 0) {
-        backward_kernel<T, S><<<(unsigned)blocks, kThreads, sizeof(M), s>>>(P);
+        backward_kernel<T, S><<<(unsigned)blocks, Back<S>::THREADS, sizeof(M), s>>>(P);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         count_launches(1);
