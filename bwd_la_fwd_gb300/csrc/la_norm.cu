@@ -42,7 +42,7 @@ template <typename T, int TPR_, int NV_> struct Shape {
     static constexpr int V = 16 / (int)sizeof(T), TPR = TPR_, NV = NV_;
     static constexpr int THREADS = TPR > 256 ? TPR : 256;
     static constexpr int GROUPS = THREADS / TPR;  // rows at a time of a block
-    static constexpr int RPI = NV * V >= 16 ? 1 : 16 / (NV * V);  // rows at a time of a group
+    static constexpr int RPI = NV == 1 ? 2 : 1;  // rows at a time of a group
 };
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -93,13 +93,19 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return (uint32_t)lo | (uint32_t)hi << 16;
 }
 
+// N = 0: the batch entries' rows lie evenly spaced, one entry behind another.
 template <typename T> __device__ __forceinline__ T *row_of(const Op &o, long long row, int N) {
+    if (N == 0) return (T *)o.p + row * o.sn;
     const long long b = row / N;
     return (T *)o.p + b * o.sb + (row - b * N) * o.sn;
 }
 
+// Blocks on an SM, which walk all rows.
+template <int TPR> constexpr int back_per_sm() { return TPR > 256 ? 1 : 2; }  // each leaves sums of dw
+template <int TPR> constexpr int per_sm() { return TPR > 256 ? 1 : 3; }
+
 template <typename T, int TPR, int NV, int KIND>
-__global__ void __launch_bounds__(Shape<T, TPR, NV>::THREADS) forward_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(Shape<T, TPR, NV>::THREADS, per_sm<TPR>()) forward_kernel(const __grid_constant__ Params P) {
     using S = Shape<T, TPR, NV>;
     constexpr int V = S::V, R = S::RPI;
     __shared__ float sm[R * S::THREADS / 32];
@@ -114,36 +120,43 @@ __global__ void __launch_bounds__(Shape<T, TPR, NV>::THREADS) forward_kernel(con
             w[i][k] = c < P.C ? P.w[c] : 0.f;
         }
     const long long step = (long long)gridDim.x * S::GROUPS * R;
+    Vec<T, V> x[R][NV], a[R][NV];  // the next rows, on their way while the last are normed
+    auto fetch = [&](long long first) {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * TPR + t) * V;
+                const bool on = first + j < P.rows && P.C - c >= V;
+                load_ahead(x[j][i], row_of<T>(P.x, first + j, P.N) + c, on);
+                if (P.res.p) load_ahead(a[j][i], row_of<T>(P.res, first + j, P.N) + c, on);
+            }
+    };
+    fetch((long long)blockIdx.x * S::GROUPS * R + group * R);
     for (long long base = (long long)blockIdx.x * S::GROUPS * R; base < P.rows; base += step) {
         const long long first = base + group * R;
         float r[R][NV][V], ss[R];
-        {
-            Vec<T, V> x[R][NV], a[R][NV];
 #pragma unroll
-            for (int j = 0; j < R; ++j)
+        for (int j = 0; j < R; ++j) {
+            ss[j] = 0.f;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int c = (i * TPR + t) * V, n = first + j < P.rows ? P.C - c : 0;
-                    if (n <= 0) continue;
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * TPR + t) * V, n = P.C - c;
+                const bool in = first + j < P.rows && n > 0;
+                if (in && n < V) {  // the last channels, where they are no whole vector
                     x[j][i] = load_vec<T, V>(row_of<T>(P.x, first + j, P.N) + c, n);
                     if (P.res.p) a[j][i] = load_vec<T, V>(row_of<T>(P.res, first + j, P.N) + c, n);
                 }
 #pragma unroll
-            for (int j = 0; j < R; ++j) {
-                ss[j] = 0.f;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int c = (i * TPR + t) * V;
-                    const bool in = first + j < P.rows && c < P.C;
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        r[j][i][k] = in ? to_f(x[j][i].e[k]) : 0.f;
-                        if (P.res.p && in) r[j][i][k] += to_f(a[j][i].e[k]);
-                        ss[j] = fmaf(r[j][i][k], r[j][i][k], ss[j]);
-                    }
+                for (int k = 0; k < V; ++k) {
+                    float v = to_f(x[j][i].e[k]);
+                    if (P.res.p) v += to_f(a[j][i].e[k]);
+                    r[j][i][k] = in ? v : 0.f;
+                    ss[j] = fmaf(r[j][i][k], r[j][i][k], ss[j]);
                 }
             }
         }
+        fetch(first + step);
         if (P.r.p)
 #pragma unroll
             for (int j = 0; j < R; ++j)
@@ -215,7 +228,7 @@ __global__ void __launch_bounds__(Shape<T, TPR, NV>::THREADS) forward_kernel(con
 }
 
 template <typename T, int TPR, int NV>
-__global__ void __launch_bounds__(Shape<T, TPR, NV>::THREADS) backward_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(Shape<T, TPR, NV>::THREADS, back_per_sm<TPR>()) backward_kernel(const __grid_constant__ Params P) {
     using S = Shape<T, TPR, NV>;
     constexpr int V = S::V, R = S::RPI;
     __shared__ float sm[2 * R * S::THREADS / 32];
@@ -231,36 +244,48 @@ __global__ void __launch_bounds__(Shape<T, TPR, NV>::THREADS) backward_kernel(co
             dw[i][k] = 0.f;
         }
     const long long step = (long long)gridDim.x * S::GROUPS * R;
+    Vec<T, V> nr[R][NV], ny[R][NV], nd[R][NV];  // the next rows, on their way meanwhile
+    auto fetch = [&](long long first) {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * TPR + t) * V;
+                const bool on = first + j < P.rows && P.C - c >= V;
+                load_ahead(nr[j][i], row_of<T>(P.x, first + j, P.N) + c, on);
+                load_ahead(ny[j][i], row_of<T>(P.y, first + j, P.N) + c, on);
+                if (P.dr.p) load_ahead(nd[j][i], row_of<T>(P.dr, first + j, P.N) + c, on);
+            }
+    };
+    fetch((long long)blockIdx.x * S::GROUPS * R + group * R);
     for (long long base = (long long)blockIdx.x * S::GROUPS * R; base < P.rows; base += step) {
         const long long first = base + group * R;
         Vec<T, V> r[R][NV], dy[R][NV], dr[R][NV];
         float sums[2 * R];  // of r^2, of g r
 #pragma unroll
-        for (int j = 0; j < R; ++j)
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * TPR + t) * V, n = first + j < P.rows ? P.C - c : 0;
-                if (n <= 0) {
-#pragma unroll
-                    for (int k = 0; k < V; ++k) r[j][i].e[k] = dy[j][i].e[k] = dr[j][i].e[k] = T(0.f);
-                    continue;
-                }
-                r[j][i] = load_vec<T, V>(row_of<T>(P.x, first + j, P.N) + c, n);
-                dy[j][i] = load_vec<T, V>(row_of<T>(P.y, first + j, P.N) + c, n);
-                if (P.dr.p) dr[j][i] = load_vec<T, V>(row_of<T>(P.dr, first + j, P.N) + c, n);
-            }
-#pragma unroll
         for (int j = 0; j < R; ++j) {
             sums[j] = sums[R + j] = 0.f;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * TPR + t) * V, n = first + j < P.rows ? P.C - c : 0;
+                r[j][i] = nr[j][i], dy[j][i] = ny[j][i], dr[j][i] = nd[j][i];
+                if (n > 0 && n < V) {  // the last channels, where they are no whole vector
+                    r[j][i] = load_vec<T, V>(row_of<T>(P.x, first + j, P.N) + c, n);
+                    dy[j][i] = load_vec<T, V>(row_of<T>(P.y, first + j, P.N) + c, n);
+                    if (P.dr.p) dr[j][i] = load_vec<T, V>(row_of<T>(P.dr, first + j, P.N) + c, n);
+                }
+                if (n <= 0)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) r[j][i].e[k] = dy[j][i].e[k] = T(0.f);
 #pragma unroll
                 for (int k = 0; k < V; ++k) {
                     const float x = to_f(r[j][i].e[k]);
                     sums[j] = fmaf(x, x, sums[j]);
                     sums[R + j] = fmaf(w[i][k] * to_f(dy[j][i].e[k]), x, sums[R + j]);
                 }
+            }
         }
+        fetch(first + step);
         combine<TPR, S::THREADS, 2 * R, false>(sums, sm);
 #pragma unroll
         for (int j = 0; j < R; ++j) {
@@ -291,13 +316,11 @@ __global__ void __launch_bounds__(Shape<T, TPR, NV>::THREADS) backward_kernel(co
         }
 }
 
-// Blocks of the backward walk: the rows' groups over all SMs, as many as `per_sm` fit on each.
-constexpr int kPerSM = 2;
-
 template <typename T, int TPR, int NV> cudaError_t launch_forward(const Params &P, int kind, cudaStream_t s) {
     using S = Shape<T, TPR, NV>;
     const long long need = (P.rows + S::GROUPS * S::RPI - 1) / (S::GROUPS * S::RPI);
-    const unsigned grid = (unsigned)(need < 8 * kSMs ? need : 8 * kSMs);
+    const int most = per_sm<TPR>() * kSMs;
+    const unsigned grid = (unsigned)(need < most ? need : most);
     auto *k = kind == kPlain ? forward_kernel<T, TPR, NV, kPlain>
               : kind == kRow8 ? forward_kernel<T, TPR, NV, kRow8>
                               : forward_kernel<T, TPR, NV, kBlock8>;
@@ -308,7 +331,8 @@ template <typename T, int TPR, int NV> cudaError_t launch_forward(const Params &
 template <typename T, int TPR, int NV> int parts_of(long long rows) {
     using S = Shape<T, TPR, NV>;
     const long long need = (rows + S::GROUPS * S::RPI - 1) / (S::GROUPS * S::RPI);
-    return (int)(need < kPerSM * kSMs ? need : kPerSM * kSMs) * S::GROUPS;
+    constexpr int most = back_per_sm<TPR>() * kSMs;
+    return (int)(need < most ? need : most) * S::GROUPS;
 }
 
 template <typename T, int TPR, int NV> cudaError_t launch_backward(const Params &P, float *dw, cudaStream_t s) {
@@ -328,7 +352,7 @@ template <int V, typename F> auto by_shape(int n, F f) {
     if (n <= 128) return f(integral_constant<int, 128>(), integral_constant<int, 1>());
     if (n <= 256) return f(integral_constant<int, 256>(), integral_constant<int, 1>());
     if (n <= 512) return f(integral_constant<int, 256>(), integral_constant<int, 2>());
-    if (n <= 1024) return f(integral_constant<int, 256>(), integral_constant<int, 4>());
+    if (n <= 1024) return f(integral_constant<int, 512>(), integral_constant<int, 2>());
     if (V == 8 || n <= 2048) return f(integral_constant<int, 512>(), integral_constant<int, 4>());
     return f(integral_constant<int, 512>(), integral_constant<int, V == 8 ? 4 : 8>());
 }
@@ -344,7 +368,7 @@ template <typename T> cudaError_t backward(const Params &P, float *dw, cudaStrea
 
 // Sums of dw that a call may leave, whatever its type and rows.
 int most_parts(int C) {
-    auto parts = [](auto tpr, auto) { return kPerSM * kSMs * (tpr.value >= 256 ? 1 : 256 / tpr.value); };
+    auto parts = [](auto tpr, auto) { return back_per_sm<tpr.value>() * kSMs * (tpr.value >= 256 ? 1 : 256 / tpr.value); };
     const int a = by_shape<8>((C + 7) / 8, parts), b = by_shape<4>((C + 3) / 4, parts);
     return a > b ? a : b;
 }
@@ -356,6 +380,13 @@ int check_sizes(int B, int N, int C, float eps, int dtype, bool *empty) {
     if (C > kMaxC) return LA_ERR_UNSUPPORTED;
     *empty = B == 0 || N == 0;
     return LA_OK;
+}
+
+// Whether the batch entries' rows follow one another evenly in all operands.
+bool flat(const View *const *v, int n, int B, int N) {
+    for (int k = 0; k < n; ++k)
+        if (v[k]->p && B > 1 && (N == 1 ? false : v[k]->st[0] != N * v[k]->st[1])) return false;
+    return B == 1 || N > 1;
 }
 
 // The forward calls: y is a view of the tokens' type, or y8 and its scales.
@@ -397,7 +428,8 @@ int forward_call(const void *X, const void *residual, const float *weight, void 
     P.y8 = y8;
     P.scales = scales;
     P.rows = n;
-    P.N = N, P.C = C, P.groups = groups, P.eps = eps;
+    const View *const ops[4] = {&x, &res, &r, &y};
+    P.N = flat(ops, 4, B, N) ? 0 : N, P.C = C, P.groups = groups, P.eps = eps;
     const int kind = !y8 ? kPlain : group ? kBlock8 : kRow8;
     const cudaError_t e = dtype == LA_BF16 ? forward<__nv_bfloat16>(P, kind, s) : forward<float>(P, kind, s);
     if (e != cudaSuccess) return LA_ERR_CUDA;
@@ -503,7 +535,8 @@ int la_rms_norm_backward(const void *R, const float *weight, const void *dY, con
     P.w = weight;
     P.part = (float *)((char *)workspace + 256);
     P.rows = (long long)B * N;
-    P.N = N, P.C = C, P.eps = eps;
+    const View *const ops[4] = {&r, &dy, &dr, &dx};
+    P.N = flat(ops, 4, B, N) ? 0 : N, P.C = C, P.eps = eps;
     const cudaError_t e = dtype == LA_BF16 ? backward<__nv_bfloat16>(P, dweight, s) : backward<float>(P, dweight, s);
     if (e != cudaSuccess) return LA_ERR_CUDA;
     count_launches(1);
