@@ -38,8 +38,13 @@ template <int K, int V> __device__ __forceinline__ void load_taps(const Params &
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const bool in = c + k < P.C;
+        if (K == 4) {
+            const float4 f = in ? *(const float4 *)(P.w + (long long)(c + k) * K) : make_float4(0.f, 0.f, 0.f, 0.f);
+            w[0][k] = f.x, w[1][k] = f.y, w[K - 2][k] = f.z, w[K - 1][k] = f.w;
+        } else {
 #pragma unroll
-        for (int j = 0; j < K; ++j) w[j][k] = in ? P.w[(long long)(c + k) * K + j] : 0.f;
+            for (int j = 0; j < K; ++j) w[j][k] = in ? P.w[(long long)(c + k) * K + j] : 0.f;
+        }
         bias[k] = in && P.bias ? P.bias[c + k] : 0.f;
     }
 }
@@ -67,12 +72,21 @@ template <typename T, int K, bool SILU> __global__ void __launch_bounds__(kThrea
         const T *x = rows_of<const T>(P.seq, P.x, seq);
         T *o = rows_of<T>(P.seq, P.o, seq) + c;
         Vec<T, V> win[K - 1 + kAhead];  // rows t - K + 1 ... t + kAhead - 1
+        Vec<T, V> next[kAhead];         // those behind, on their way
+        auto fetch = [&](int t) {
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) load_ahead(next[a], x + (t + a) * P.x.sn + c, t + a < t1 && n >= V);
+        };
+        fetch(t0);
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) win[j] = row_at<T, K, V>(P, x, seq, t0 - (K - 1) + j, c);
         for (int t = t0; t < t1; t += kAhead) {
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a)
-                if (t + a < t1) win[K - 1 + a] = load_vec<T, V>(x + (t + a) * P.x.sn + c, n);
+            for (int a = 0; a < kAhead; ++a) {
+                if (n < V && t + a < t1) next[a] = load_vec<T, V>(x + (t + a) * P.x.sn + c, n);  // no whole vector
+                win[K - 1 + a] = next[a];
+            }
+            fetch(t + kAhead);
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
                 if (t + a >= t1) break;
@@ -113,8 +127,17 @@ template <typename T, int K, bool SILU> __global__ void __launch_bounds__(kThrea
         if (n <= 0) return;
         const T *x = rows_of<const T>(P.seq, P.x, seq), *d = rows_of<const T>(P.seq, P.dO, seq) + c;
         T *dx = rows_of<T>(P.seq, P.o, seq) + c;
-        Vec<T, V> win[K - 1 + kAhead], dO[kAhead];
+        const int end = min(t1 + K - 1, len);  // rows whose dp reaches the run's
+        Vec<T, V> win[K - 1 + kAhead], dO[kAhead], nx[kAhead], nd[kAhead];
         float dp[K - 1 + kAhead][V];  // of rows t - K + 1 ... t + kAhead - 1
+        auto fetch = [&](int t) {
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                load_ahead(nx[a], x + (t + a) * P.x.sn + c, t + a < end && n >= V);
+                load_ahead(nd[a], d + (t + a) * P.dO.sn, t + a < end && n >= V);
+            }
+        };
+        fetch(t0);
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) {
             win[j] = row_at<T, K, V>(P, x, seq, t0 - (K - 1) + j, c);
@@ -123,14 +146,18 @@ template <typename T, int K, bool SILU> __global__ void __launch_bounds__(kThrea
         }
         for (int t = t0; t < t1 + K - 1; t += kAhead) {
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a)
-                if (t + a < t1 + K - 1 && t + a < len) {
-                    win[K - 1 + a] = load_vec<T, V>(x + (t + a) * P.x.sn + c, n);
-                    dO[a] = load_vec<T, V>(d + (t + a) * P.dO.sn, n);
+            for (int a = 0; a < kAhead; ++a) {
+                if (n < V && t + a < end) {  // no whole vector
+                    nx[a] = load_vec<T, V>(x + (t + a) * P.x.sn + c, n);
+                    nd[a] = load_vec<T, V>(d + (t + a) * P.dO.sn, n);
                 }
+                win[K - 1 + a] = nx[a];
+                dO[a] = nd[a];
+            }
+            fetch(t + kAhead);
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
-                const bool in = t + a < t1 + K - 1 && t + a < len, mine = t + a < t1;
+                const bool in = t + a < end, mine = t + a < t1;
                 Vec<T, V> out;
 #pragma unroll
                 for (int k = 0; k < V; ++k) {
