@@ -8,6 +8,7 @@
 // A thread has one vector of channels and walks a run of rows, the last K - 1 of them in registers, so each row is read
 // once (and K - 1 rows again at a run's start), which bounds it (HBM).  The backward walk is the same with a second window,
 // of dp: dx of a row is complete K - 1 rows later, so a run computes dp of the K - 1 rows behind it again.  Sums are fp32.
+#include "la_f32x2.cuh"
 #include "la_rows.cuh"
 
 namespace la {
@@ -16,12 +17,12 @@ namespace conv {
 using namespace rows;
 
 constexpr int kThreads = 128;
-constexpr int kRun = 32;          // rows of a forward run
+constexpr int kRun = 8;           // rows of a run at least
 constexpr int kMaxParts = 256;    // runs of the backward walk
 constexpr int kMaxK = 4;
-constexpr int kAhead = 4;         // rows loaded together
-constexpr int kBackV = 4;         // channels of a thread in the backward walk, whose windows and sums take the registers
-constexpr int kEnough = 608;      // blocks: four to an SM
+constexpr int kAhead = 4, kFwdAhead = 8;  // rows loaded together
+constexpr int kV = 4;            // channels of a thread
+constexpr int kSMs = 152, kPerSM = 4, kBackPerSM = 3;  // blocks on an SM, all at once
 
 struct Params {
     Op x, o, dO;                  // forward: x, o; backward: x, do, and o is dx
@@ -33,21 +34,46 @@ struct Params {
     float *part;                  // backward: [parts][C][K], then [C], of each part
 };
 
-// Taps and bias of a thread's channels.
-template <int K, int V> __device__ __forceinline__ void load_taps(const Params &P, int c, float (&w)[K][V], float (&bias)[V]) {
+// Taps and bias of a thread's channels, in pairs.
+template <int K> struct Taps {
+    float2 w[K][kV / 2], bias[kV / 2];
+    __device__ __forceinline__ Taps(const Params &P, int c) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        const bool in = c + k < P.C;
-        if (K == 4) {
-            const float4 f = in ? *(const float4 *)(P.w + (long long)(c + k) * K) : make_float4(0.f, 0.f, 0.f, 0.f);
-            w[0][k] = f.x, w[1][k] = f.y, w[K - 2][k] = f.z, w[K - 1][k] = f.w;
-        } else {
+        for (int k = 0; k < kV; ++k) {
+            const bool in = c + k < P.C;
+            float t[K];
+            if constexpr (K == 4) {
+                const float4 f = in ? *(const float4 *)(P.w + (long long)(c + k) * K) : make_float4(0.f, 0.f, 0.f, 0.f);
+                t[0] = f.x, t[1] = f.y, t[2] = f.z, t[3] = f.w;
+            } else {
 #pragma unroll
-            for (int j = 0; j < K; ++j) w[j][k] = in ? P.w[(long long)(c + k) * K + j] : 0.f;
+                for (int j = 0; j < K; ++j) t[j] = in ? P.w[(long long)(c + k) * K + j] : 0.f;
+            }
+            const float b = in && P.bias ? P.bias[c + k] : 0.f;
+#pragma unroll
+            for (int j = 0; j < K; ++j) (k & 1 ? w[j][k / 2].y : w[j][k / 2].x) = t[j];
+            (k & 1 ? bias[k / 2].y : bias[k / 2].x) = b;
         }
-        bias[k] = in && P.bias ? P.bias[c + k] : 0.f;
     }
+    // p of a row whose taps are rows x[0] ... x[K - 1]
+    __device__ __forceinline__ float2 sum(const float2 (*x)[kV / 2], int k) const {
+        float2 p = bias[k];
+#pragma unroll
+        for (int j = 0; j < K; ++j) p = fma2(w[j][k], x[j][k], p);
+        return p;
+    }
+};
+template <typename T> __device__ __forceinline__ void widen(float2 (&to)[kV / 2], const Vec<T, kV> &x) {
+#pragma unroll
+    for (int k = 0; k < kV / 2; ++k) to[k] = make_float2(to_f(x.e[2 * k]), to_f(x.e[2 * k + 1]));
 }
+template <typename T> __device__ __forceinline__ Vec<T, kV> narrow(const float2 (&x)[kV / 2]) {
+    Vec<T, kV> r;
+#pragma unroll
+    for (int k = 0; k < kV / 2; ++k) put(&r.e[2 * k], x[k].x), put(&r.e[2 * k + 1], x[k].y);
+    return r;
+}
+__device__ __forceinline__ float2 sigmoid2(float2 p) { return make_float2(sigmoid(p.x), sigmoid(p.y)); }
 
 // The row `place` of a sequence; negative: of the state before it.
 template <typename T, int K, int V>
@@ -61,47 +87,45 @@ __device__ __forceinline__ Vec<T, V> row_at(const Params &P, const T *x, int seq
     return z;
 }
 
-template <typename T, int K, bool SILU> __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant__ Params P) {
-    constexpr int V = 16 / (int)sizeof(T);
+template <typename T, int K, bool SILU> __global__ void __launch_bounds__(kThreads, kPerSM) forward_kernel(const __grid_constant__ Params P) {
+    constexpr int V = kV, A = kFwdAhead;
     const int c = (blockIdx.x * kThreads + threadIdx.x) * V, n = P.C - c;
     const int r0 = blockIdx.y * P.run, r1 = min(r0 + P.run, P.seq.T);
-    float w[K][V], bias[V];
-    load_taps<K, V>(P, c, w, bias);
+    const Taps<K> taps(P, c);
     for_stretches(P.seq, r0, r1, [&](int seq, int t0, int t1, int len, bool begins) {
         if (n <= 0) return;
         const T *x = rows_of<const T>(P.seq, P.x, seq);
         T *o = rows_of<T>(P.seq, P.o, seq) + c;
-        Vec<T, V> win[K - 1 + kAhead];  // rows t - K + 1 ... t + kAhead - 1
-        Vec<T, V> next[kAhead];         // those behind, on their way
+        float2 win[K - 1 + A][V / 2];  // rows t - K + 1 ... t + A - 1
+        Vec<T, V> next[A];             // those behind, on their way
         auto fetch = [&](int t) {
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) load_ahead(next[a], x + (t + a) * P.x.sn + c, t + a < t1 && n >= V);
+            for (int a = 0; a < A; ++a) load_ahead(next[a], x + (t + a) * P.x.sn + c, t + a < t1 && n >= V);
         };
         fetch(t0);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) win[j] = row_at<T, K, V>(P, x, seq, t0 - (K - 1) + j, c);
-        for (int t = t0; t < t1; t += kAhead) {
+        for (int j = 0; j < K - 1; ++j) widen(win[j], row_at<T, K, V>(P, x, seq, t0 - (K - 1) + j, c));
+        for (int t = t0; t < t1; t += A) {
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
+            for (int a = 0; a < A; ++a) {
                 if (n < V && t + a < t1) next[a] = load_vec<T, V>(x + (t + a) * P.x.sn + c, n);  // no whole vector
-                win[K - 1 + a] = next[a];
+                widen(win[K - 1 + a], next[a]);
             }
-            fetch(t + kAhead);
+            fetch(t + A);
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                if (t + a >= t1) break;
-                Vec<T, V> out;
+            for (int a = 0; a < A; ++a) {
+                float2 p[V / 2];
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    float p = bias[k];
-#pragma unroll
-                    for (int j = 0; j < K; ++j) p = fmaf(w[j][k], to_f(win[a + j].e[k]), p);
-                    put(&out.e[k], SILU ? p * sigmoid(p) : p);
+                for (int k = 0; k < V / 2; ++k) {
+                    p[k] = taps.sum(win + a, k);
+                    if (SILU) p[k] = mul2(p[k], sigmoid2(p[k]));
                 }
-                store_vec<T, V>(o + (t + a) * P.o.sn, out, n);
+                if (t + a < t1) store_vec<T, V>(o + (t + a) * P.o.sn, narrow<T>(p), n);
             }
 #pragma unroll
-            for (int j = 0; j < K - 1; ++j) win[j] = win[j + kAhead];
+            for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k) win[j][k] = win[j + A][k];
         }
         if (begins && P.last)  // (the state before is another array)
 #pragma unroll
@@ -111,28 +135,22 @@ template <typename T, int K, bool SILU> __global__ void __launch_bounds__(kThrea
     });
 }
 
-template <typename T, int K, bool SILU> __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ Params P) {
-    constexpr int V = kBackV;
+template <typename T, int K, bool SILU> __global__ void __launch_bounds__(kThreads, kBackPerSM) backward_kernel(const __grid_constant__ Params P) {
+    constexpr int V = kV, A = kAhead;
     const int c = (blockIdx.x * kThreads + threadIdx.x) * V, n = P.C - c;
     const int r0 = blockIdx.y * P.run, r1 = min(r0 + P.run, P.seq.T);
-    float w[K][V], bias[V], dw[K][V], db[V];
-    load_taps<K, V>(P, c, w, bias);
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        db[k] = 0.f;
-#pragma unroll
-        for (int j = 0; j < K; ++j) dw[j][k] = 0.f;
-    }
+    const Taps<K> taps(P, c);
+    float2 dw[K][V / 2] = {}, db[V / 2] = {};
     for_stretches(P.seq, r0, r1, [&](int seq, int t0, int t1, int len, bool) {
         if (n <= 0) return;
         const T *x = rows_of<const T>(P.seq, P.x, seq), *d = rows_of<const T>(P.seq, P.dO, seq) + c;
         T *dx = rows_of<T>(P.seq, P.o, seq) + c;
         const int end = min(t1 + K - 1, len);  // rows whose dp reaches the run's
-        Vec<T, V> win[K - 1 + kAhead], dO[kAhead], nx[kAhead], nd[kAhead];
-        float dp[K - 1 + kAhead][V];  // of rows t - K + 1 ... t + kAhead - 1
+        float2 win[K - 1 + A][V / 2], dp[K - 1 + A][V / 2];  // of rows t - K + 1 ... t + A - 1
+        Vec<T, V> nx[A], nd[A];
         auto fetch = [&](int t) {
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
+            for (int a = 0; a < A; ++a) {
                 load_ahead(nx[a], x + (t + a) * P.x.sn + c, t + a < end && n >= V);
                 load_ahead(nd[a], d + (t + a) * P.dO.sn, t + a < end && n >= V);
             }
@@ -140,57 +158,49 @@ template <typename T, int K, bool SILU> __global__ void __launch_bounds__(kThrea
         fetch(t0);
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) {
-            win[j] = row_at<T, K, V>(P, x, seq, t0 - (K - 1) + j, c);
+            widen(win[j], row_at<T, K, V>(P, x, seq, t0 - (K - 1) + j, c));
 #pragma unroll
-            for (int k = 0; k < V; ++k) dp[j][k] = 0.f;
+            for (int k = 0; k < V / 2; ++k) dp[j][k] = both(0.f);
         }
-        for (int t = t0; t < t1 + K - 1; t += kAhead) {
+        for (int t = t0; t < t1 + K - 1; t += A) {
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
+            for (int a = 0; a < A; ++a) {
                 if (n < V && t + a < end) {  // no whole vector
                     nx[a] = load_vec<T, V>(x + (t + a) * P.x.sn + c, n);
                     nd[a] = load_vec<T, V>(d + (t + a) * P.dO.sn, n);
                 }
-                win[K - 1 + a] = nx[a];
-                dO[a] = nd[a];
+                widen(win[K - 1 + a], nx[a]);
+                widen(dp[K - 1 + a], nd[a]);
             }
-            fetch(t + kAhead);
+            fetch(t + A);
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                const bool in = t + a < end, mine = t + a < t1;
-                Vec<T, V> out;
+            for (int a = 0; a < A; ++a) {
+                float2 e[V / 2];
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    float g = 0.f;
-                    if (in) {
-                        g = to_f(dO[a].e[k]);
-                        if (SILU) {
-                            float p = bias[k];
+                for (int k = 0; k < V / 2; ++k) {
+                    float2 g = dp[K - 1 + a][k];
+                    if (SILU) {
+                        const float2 p = taps.sum(win + a, k), s = sigmoid2(p);
+                        g = mul2(g, make_float2(silu_grad(p.x, s.x), silu_grad(p.y, s.y)));
+                    }
+                    if (t + a >= end) g = both(0.f);
+                    if (t + a < t1) {
+                        db[k] = add2(db[k], g);
 #pragma unroll
-                            for (int j = 0; j < K; ++j) p = fmaf(w[j][k], to_f(win[a + j].e[k]), p);
-                            g *= silu_grad(p, sigmoid(p));
-                        }
-                        if (mine) {
-                            db[k] += g;
-#pragma unroll
-                            for (int j = 0; j < K; ++j) dw[j][k] = fmaf(g, to_f(win[a + j].e[k]), dw[j][k]);
-                        }
+                        for (int j = 0; j < K; ++j) dw[j][k] = fma2(g, win[a + j][k], dw[j][k]);
                     }
                     dp[K - 1 + a][k] = g;
-                    float e = 0.f;
+                    e[k] = mul2(taps.w[0][k], g);
 #pragma unroll
-                    for (int j = 0; j < K; ++j) e = fmaf(w[j][k], dp[K - 1 + a - j][k], e);
-                    put(&out.e[k], e);
+                    for (int j = 1; j < K; ++j) e[k] = fma2(taps.w[j][k], dp[K - 1 + a - j][k], e[k]);
                 }
                 // the row whose last dp this was
-                if (t + a - (K - 1) >= t0 && t + a < t1 + K - 1) store_vec<T, V>(dx + (t + a - (K - 1)) * P.o.sn, out, n);
+                if (t + a - (K - 1) >= t0 && t + a < t1 + K - 1) store_vec<T, V>(dx + (t + a - (K - 1)) * P.o.sn, narrow<T>(e), n);
             }
 #pragma unroll
-            for (int j = 0; j < K - 1; ++j) {
-                win[j] = win[j + kAhead];
+            for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-                for (int k = 0; k < V; ++k) dp[j][k] = dp[j + kAhead][k];
-            }
+                for (int k = 0; k < V / 2; ++k) win[j][k] = win[j + A][k], dp[j][k] = dp[j + A][k];
         }
     });
     float *part = P.part + (long long)blockIdx.y * P.C * (K + 1);
@@ -198,35 +208,34 @@ template <typename T, int K, bool SILU> __global__ void __launch_bounds__(kThrea
     for (int k = 0; k < V; ++k) {
         if (k >= n) break;
 #pragma unroll
-        for (int j = 0; j < K; ++j) part[(long long)(c + k) * K + j] = dw[j][k];
-        part[(long long)P.C * K + c + k] = db[k];
+        for (int j = 0; j < K; ++j) part[(long long)(c + k) * K + j] = k & 1 ? dw[j][k / 2].y : dw[j][k / 2].x;
+        part[(long long)P.C * K + c + k] = k & 1 ? db[k / 2].y : db[k / 2].x;
     }
 }
 
 template <typename T, int K, bool SILU> __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Params P) {
-    constexpr int V = 16 / (int)sizeof(T);
+    constexpr int V = kV;
     const int per = (P.C + V - 1) / V;  // vectors of a row
     const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
     if (i >= (long long)P.seq.nseq * per) return;
     const int b = (int)(i / per), c = (int)(i - (long long)b * per) * V, n = P.C - c;
     T *st = (T *)P.last + (long long)b * (K - 1) * P.C + c;
-    Vec<T, V> win[K];
+    Vec<T, V> row[K];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) win[j] = load_vec<T, V>(st + (long long)j * P.C, n, P.C % V == 0);
-    win[K - 1] = load_vec<T, V>((const T *)P.x.p + b * P.x.sb + c, n);
-    float w[K][V], bias[V];
-    load_taps<K, V>(P, c, w, bias);
-    Vec<T, V> out;
+    for (int j = 0; j < K - 1; ++j) row[j] = load_vec<T, V>(st + (long long)j * P.C, n, P.C % V == 0);
+    row[K - 1] = load_vec<T, V>((const T *)P.x.p + b * P.x.sb + c, n);
+    const Taps<K> taps(P, c);
+    float2 win[K][V / 2], p[V / 2];
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        float p = bias[k];
+    for (int j = 0; j < K; ++j) widen(win[j], row[j]);
 #pragma unroll
-        for (int j = 0; j < K; ++j) p = fmaf(w[j][k], to_f(win[j].e[k]), p);
-        put(&out.e[k], SILU ? p * sigmoid(p) : p);
+    for (int k = 0; k < V / 2; ++k) {
+        p[k] = taps.sum(win, k);
+        if (SILU) p[k] = mul2(p[k], sigmoid2(p[k]));
     }
-    store_vec<T, V>((T *)P.o.p + b * P.o.sb + c, out, n);
+    store_vec<T, V>((T *)P.o.p + b * P.o.sb + c, narrow<T>(p), n);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) store_vec<T, V>(st + (long long)j * P.C, win[j + 1], n, P.C % V == 0);
+    for (int j = 0; j < K - 1; ++j) store_vec<T, V>(st + (long long)j * P.C, row[j + 1], n, P.C % V == 0);
 }
 
 enum : int { kForward = 0, kBackward, kStep };
@@ -248,6 +257,15 @@ template <int WHAT> int run(const Params &P, int K, int act, int dtype, dim3 gri
     if (e != cudaSuccess) return LA_ERR_CUDA;
     count_launches(1);
     return LA_OK;
+}
+
+// Rows of a run: as many as let all blocks stand on the SMs at once, and kRun at least.
+int run_rows(int T, int across, int per_sm) {
+    const int runs = across < per_sm * kSMs ? per_sm * kSMs / across : 1;
+    int rows = (int)(((long long)T + runs - 1) / runs);
+    if (rows < kRun) rows = kRun;
+    while (((long long)T + rows - 1) / rows > 65535) rows *= 2;
+    return rows;
 }
 
 // Kinds and sizes; N rows each, or (packed) N rows in all.
@@ -304,11 +322,8 @@ int la_short_conv(const void *X, const float *W, const float *bias, const void *
     P.w = W, P.bias = bias, P.first = state_in, P.last = state_out;
     P.seq = Seqs{seq_offsets, nseq, N, T, (uint32_t *)workspace};
     P.C = C;
-    // Shorter runs where long ones would leave SMs without a block.
-    const unsigned across = (unsigned)((C + kThreads * (16 / elem) - 1) / (kThreads * (16 / elem)));
-    P.run = kRun;
-    while (P.run > 8 && (long long)across * ((T + P.run - 1) / P.run) < kEnough) P.run /= 2;
-    while ((T + P.run - 1) / P.run > 65535) P.run *= 2;
+    const unsigned across = (unsigned)((C + kThreads * kV - 1) / (kThreads * kV));
+    P.run = run_rows(T, (int)across, kPerSM);
     const int runs = T > 0 ? (T + P.run - 1) / P.run : 1;
     return run<kForward>(P, K, activation, dtype, dim3(across, (unsigned)runs), stream);
 }
@@ -351,14 +366,11 @@ int la_short_conv_backward(const void *X, const float *W, const float *bias, con
     P.seq = Seqs{seq_offsets, nseq, N, T, (uint32_t *)workspace};
     P.C = C;
     P.part = (float *)((char *)workspace + 256);
-    // Runs of at least 16 rows, as few as fill the SMs, and no more than the workspace has places for.
-    const unsigned across = (unsigned)((C + kThreads * kBackV - 1) / (kThreads * kBackV));
-    int parts = (T + 15) / 16;
-    if (parts > (kEnough + (int)across - 1) / (int)across) parts = (kEnough + (int)across - 1) / (int)across;
-    if (parts > kMaxParts) parts = kMaxParts;
-    if (nseq == 0 || T == 0) parts = 0;
-    if (parts > 0) {
-        P.run = (T + parts - 1) / parts;
+    const unsigned across = (unsigned)((C + kThreads * kV - 1) / (kThreads * kV));
+    int parts = 0;
+    if (nseq > 0 && T > 0) {
+        P.run = run_rows(T, (int)across, kBackPerSM);
+        if ((T + P.run - 1) / P.run > kMaxParts) P.run = (T + kMaxParts - 1) / kMaxParts;
         parts = (T + P.run - 1) / P.run;
         if ((rc = run<kBackward>(P, K, activation, dtype, dim3(across, (unsigned)parts), stream))) return rc;
     }
@@ -387,8 +399,7 @@ int la_short_conv_step(const void *x, const float *W, const float *bias, void *s
     P.w = W, P.bias = bias, P.last = state;
     P.seq = Seqs{nullptr, nseq, 1, nseq, nullptr};
     P.C = C;
-    const int V = 16 / elem;
-    const long long blocks = ((long long)nseq * ((C + V - 1) / V) + kThreads - 1) / kThreads;
+    const long long blocks = ((long long)nseq * ((C + kV - 1) / kV) + kThreads - 1) / kThreads;
     if (blocks >= (1LL << 31)) return LA_ERR_INVALID_ARG;
     return run<kStep>(P, K, activation, dtype, dim3((unsigned)blocks), stream);
 }
