@@ -375,7 +375,7 @@ int la_short_conv_backward(const void *X, const float *W, const float *bias, con
         if ((rc = run<kBackward>(P, K, activation, dtype, dim3(across, (unsigned)parts), stream))) return rc;
     }
     const long long M = (long long)C * (K + 1);
-    return sum_parts(P.part, parts, M, (long long)C * K, dW, dbias, (cudaStream_t)stream) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+    return sum_parts(P.part, parts, M, dW, (long long)C * K, dbias, C, nullptr, (cudaStream_t)stream) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 
 int la_short_conv_step(const void *x, const float *W, const float *bias, void *state, void *o, int nseq, int C, int K,

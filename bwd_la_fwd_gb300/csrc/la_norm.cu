@@ -340,7 +340,7 @@ template <typename T, int TPR, int NV> cudaError_t launch_backward(const Params 
     const int parts = parts_of<T, TPR, NV>(P.rows);
     backward_kernel<T, TPR, NV><<<(unsigned)(parts / S::GROUPS), S::THREADS, 0, s>>>(P);
     const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : sum_parts(P.part, parts, P.C, P.C, dw, nullptr, s);
+    return e != cudaSuccess ? e : sum_parts(P.part, parts, P.C, dw, P.C, nullptr, 0, nullptr, s);
 }
 
 // f(TPR, NV) for rows of n vectors of V elements: as few threads as hold a row in one to four vectors each (in eight, the
@@ -443,8 +443,8 @@ namespace rows {
 
 constexpr int kSumCols = 32, kSumRows = 16;
 
-__global__ void __launch_bounds__(kSumCols *kSumRows) sum_parts_kernel(const float *part, int parts, long long M,
-                                                                       long long first, float *out0, float *out1) {
+__global__ void __launch_bounds__(kSumCols *kSumRows) sum_parts_kernel(const float *part, int parts, long long M, float *out0,
+                                                                       long long n0, float *out1, long long n1, float *out2) {
     __shared__ float sm[kSumRows][kSumCols + 1];
     const int col = threadIdx.x % kSumCols, row = threadIdx.x / kSumCols;
     const long long m = (long long)blockIdx.x * kSumCols + col;
@@ -458,16 +458,16 @@ __global__ void __launch_bounds__(kSumCols *kSumRows) sum_parts_kernel(const flo
     if (row == 0 && m < M) {
 #pragma unroll
         for (int k = 1; k < kSumRows; ++k) a += sm[k][col];
-        float *o = m < first ? out0 : out1;
-        if (o) o[m < first ? m : m - first] = a;
+        float *o = m < n0 ? out0 : m < n0 + n1 ? out1 : out2;
+        if (o) o[m < n0 ? m : m < n0 + n1 ? m - n0 : m - n0 - n1] = a;
     }
 }
 
-cudaError_t sum_parts(const float *part, int parts, long long M, long long first, float *out0, float *out1,
-                      cudaStream_t s) {
+cudaError_t sum_parts(const float *part, int parts, long long M, float *out0, long long n0, float *out1, long long n1,
+                      float *out2, cudaStream_t s) {
     const long long blocks = (M + kSumCols - 1) / kSumCols;
     if (blocks >= (1LL << 31)) return cudaErrorInvalidConfiguration;
-    sum_parts_kernel<<<(unsigned)blocks, kSumCols * kSumRows, 0, s>>>(part, parts, M, first, out0, out1);
+    sum_parts_kernel<<<(unsigned)blocks, kSumCols * kSumRows, 0, s>>>(part, parts, M, out0, n0, out1, n1, out2);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) count_launches(1);
     return e;
@@ -514,7 +514,7 @@ int la_rms_norm_backward(const void *R, const float *weight, const void *dY, con
     const Range rin[1] = {{weight, (size_t)C * 4}}, rout[2] = {{dweight, (size_t)C * 4}, {workspace, need}};
     if (outputs_meet(nullptr, 0, nullptr, 0, rin, 1, rout, 2)) return LA_ERR_INVALID_ARG;
     if (empty) {  // no rows: their sum is zero
-        return sum_parts(nullptr, 0, C, C, dweight, nullptr, s) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+        return sum_parts(nullptr, 0, C, dweight, C, nullptr, 0, nullptr, s) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
     }
     View r = {}, dy = {}, dr = {}, dx = {};
     auto st = [&](int k) { return strides ? strides + 2 * k : nullptr; };

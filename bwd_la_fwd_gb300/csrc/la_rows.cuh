@@ -137,10 +137,10 @@ template <typename T> __device__ __forceinline__ T *rows_of(const Seqs &Q, const
     return (T *)o.p + (Q.off ? Q.off[seq] * o.sn : seq * o.sb);
 }
 
-// out[m] = sum over p of part[p M + m], p in a fixed order: `first` sums go to out0, the others to out1 (either may be
-// null).
-cudaError_t sum_parts(const float *part, int parts, long long M, long long first, float *out0, float *out1,
-                      cudaStream_t s);
+// out[m] = sum over p of part[p M + m], p in a fixed order: the first n0 sums go to out0, the next n1 to out1, the others to
+// out2 (any of which may be null).
+cudaError_t sum_parts(const float *part, int parts, long long M, float *out0, long long n0, float *out1, long long n1,
+                      float *out2, cudaStream_t s);
 
 // A [B,N,C] operand's view; strides: its (batch, row), or null for contiguous rows.
 inline int rows_view(View &v, const void *p, long long B, long long N, long long C, int elem, const long long *strides) {

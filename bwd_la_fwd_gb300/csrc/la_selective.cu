@@ -56,8 +56,8 @@ struct Params {
     const float *dlast;        // [nseq, C, S] or null
     float *dfirst;
     float *pbc;                // [groups of 64 channels, T, G, 2 S]
-    float *pa;                 // [walkers, C, S], then [walkers, C] of dD and of d(dt_bias)
-    int walkers;
+    float *pa;                 // [walkers][C S of dA, C of dD, C of d(dt_bias)]
+    int walkers, units;        // CTAs of a channel block, which walk all units
     uint32_t *valid;           // whether the offsets were in order, for the sums behind
 };
 
@@ -152,6 +152,24 @@ __device__ __forceinline__ bool unit_of(const Params &P, int unit, int &seq, int
     const int lo = P.seq.off[seq];
     j = unit - (seq + lo / P.part), len = P.seq.off[seq + 1] - lo;
     return true;
+}
+// The same where the offsets are known to be in order; by each thread itself.
+__device__ __forceinline__ void unit_at(const Params &P, int unit, int &seq, int &j, int &first, int &len) {
+    if (!P.seq.off) {
+        const int per = max(1, (P.seq.N + P.part - 1) / P.part);
+        seq = unit / per, j = unit - seq * per, first = seq * P.seq.N, len = P.seq.N;
+        return;
+    }
+    int lo = 0, hi = P.seq.nseq;  // units of sequences before lo begin at or before this one, those from hi on behind it
+    while (lo < hi) {
+        const int m = (lo + hi) / 2;
+        if (m + P.seq.off[m] / P.part <= unit) lo = m + 1;
+        else hi = m;
+    }
+    seq = lo - 1, j = first = len = 0;
+    if (seq < 0) return;
+    first = P.seq.off[seq], len = P.seq.off[seq + 1] - first;
+    j = unit - (seq + first / P.part);
 }
 __device__ __forceinline__ long long mark_slot(const Params &P, int seq, int row) {
     const long long lo = P.seq.off ? P.seq.off[seq] : (long long)seq * P.seq.N;
@@ -389,7 +407,9 @@ template <int S> struct Back {
     };
 };
 
-template <typename T, int S>
+// ENDS: where time is cut into parts, a first launch, which forms what leaves each part's first row (from zero behind its
+// last, the last part from dstate_out) and the sum of its d.
+template <typename T, int S, bool ENDS>
 __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_kernel(const __grid_constant__ Params P) {
     using K = Back<S>;
     constexpr int CH = K::CH, R = K::R, NB = K::NB, QW = K::QW, HELP = K::HELP;
@@ -402,7 +422,7 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
         int n;
         fine = offsets_in_order(P.seq, n, [](int, int) { return false; });
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) *P.valid = fine;
+    if (!ENDS && blockIdx.x == 0 && threadIdx.x == 0) *P.valid = fine;
     const int helper = (int)threadIdx.x - K::SCAN;
     if (helper >= 0) {
         const int row = helper / (CH / 4), col = helper % (CH / 4) * 4, n = nc - col;
@@ -417,8 +437,12 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
             Vec<T, 4> x, d, o, z;
         } in, out;  // on their way to d and g; to the gradients of rows
         Vec<T, 4> vb[NB];
-        for (int seq = walker; seq < P.seq.nseq && fine; seq += P.walkers) {
-            const int first = P.seq.off ? P.seq.off[seq] : seq * P.seq.N, len = P.seq.off ? P.seq.off[seq + 1] - first : P.seq.N;
+        for (int unit = walker; unit < P.units && fine; unit += P.walkers) {
+            int seq, j, first, all;
+            unit_at(P, unit, seq, j, first, all);
+            const long long t0 = (long long)j * P.part;
+            if (seq < 0 || (j > 0 && t0 >= all) || (ENDS && j == 0)) continue;
+            const int lo = (int)t0, len = (int)min(t0 + P.part, (long long)all);  // rows lo ... len - 1
             const T *x = rows_of<const T>(P.seq, P.x, seq) + c0 + col, *dt = rows_of<const T>(P.seq, P.dt, seq) + c0 + col;
             const T *z = P.z.p ? rows_of<const T>(P.seq, P.z, seq) + c0 + col : nullptr;
             const T *dO = rows_of<const T>(P.seq, P.dO, seq) + c0 + col;
@@ -426,17 +450,17 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
             T *dz = z ? rows_of<T>(P.seq, P.dz, seq) + c0 + col : nullptr;
             const T *Bp = (const T *)P.B.p + (P.seq.off ? first * P.B.sn : seq * P.B.sb) + g * P.B.sg;
             const T *Cp = (const T *)P.C.p + (P.seq.off ? first * P.C.sn : seq * P.C.sb) + g * P.C.sg;
-            const int tiles = (len + R - 1) / R;
+            const int tiles = (len - lo + R - 1) / R;
             auto fetch = [&](int k, Four &f) {
-                const int r = k * R + row;
+                const int r = lo + k * R + row;
                 const bool on = k >= 0 && r < len && n >= 4;
-                load_ahead(f.x, x + r * P.x.sn, on);
+                if (!ENDS) load_ahead(f.x, x + r * P.x.sn, on);
                 load_ahead(f.d, dt + r * P.dt.sn, on);
                 load_ahead(f.o, dO + r * P.dO.sn, on);
                 load_ahead(f.z, z + r * P.z.sn, on && z);
             };
             auto rest = [&](int k, Four &f) {  // the last channels, where they are no whole vector
-                const int r = k * R + row;
+                const int r = lo + k * R + row;
                 if (r >= len || n <= 0 || n >= 4) return;
                 f.x = load_vec<T, 4>(x + r * P.x.sn, n);
                 f.d = load_vec<T, 4>(dt + r * P.dt.sn, n);
@@ -446,13 +470,13 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
             auto fetch_bc = [&](int k) {
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
-                    const int v = i * HELP + helper, which = v / (R * S / 4), r = k * R + v % (R * S / 4) / (S / 4), s = v % (S / 4) * 4;
-                    load_ahead(vb[i], (which ? Cp + r * P.C.sn : Bp + r * P.B.sn) + s, which < 2 && k >= 0 && r < len);
+                    const int v = i * HELP + helper, which = v / (R * S / 4), r = lo + k * R + v % (R * S / 4) / (S / 4), s = v % (S / 4) * 4;
+                    load_ahead(vb[i], (which ? Cp + r * P.C.sn : Bp + r * P.B.sn) + s, which < 2 && (which || !ENDS) && k >= 0 && r < len);
                 }
             };
             auto produce = [&](int k) {
                 rest(k, in);
-                const bool live = k * R + row < len;
+                const bool live = lo + k * R + row < len;
                 float d[4], u[4], gr[4];
 #pragma unroll
                 for (int e = 0; e < 4; e += 2) {
@@ -461,7 +485,7 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    u[e] = d[e] * to_f(in.x.e[e]);
+                    u[e] = ENDS ? 0.f : d[e] * to_f(in.x.e[e]);
                     gr[e] = to_f(in.o.e[e]);
                     if (z) {
                         const float ze = to_f(in.z.e[e]);
@@ -470,14 +494,14 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
                     if (!live || e >= n) d[e] = u[e] = gr[e] = 0.f;  // no row: nothing happens
                 }
                 *(float4 *)&M.ds[k % 3][row][col] = make_float4(d[0], d[1], d[2], d[3]);
-                *(float4 *)&M.us[k & 1][row][col] = make_float4(u[0], u[1], u[2], u[3]);
+                if (!ENDS) *(float4 *)&M.us[k & 1][row][col] = make_float4(u[0], u[1], u[2], u[3]);
                 *(float4 *)&M.gs[k & 1][row][col] = make_float4(gr[0], gr[1], gr[2], gr[3]);
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
                     const int v = i * HELP + helper, which = v / (R * S / 4), r = v % (R * S / 4) / (S / 4), s = v % (S / 4) * 4;
                     if (which >= 2) continue;
                     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (k * R + r < len) f = make_float4(to_f(vb[i].e[0]), to_f(vb[i].e[1]), to_f(vb[i].e[2]), to_f(vb[i].e[3]));
+                    if (lo + k * R + r < len) f = make_float4(to_f(vb[i].e[0]), to_f(vb[i].e[1]), to_f(vb[i].e[2]), to_f(vb[i].e[3]));
                     *(float4 *)&M.bc[k & 1][which][r][s] = f;
                 }
             };
@@ -492,7 +516,7 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
             };
             auto finish = [&](int k) {
                 rest(k, out);
-                const int r = k * R + row;
+                const int r = lo + k * R + row;
                 if (r >= len || n <= 0) return;
                 float w[4], es[4], ys[4];
                 total(M.ws[k & 1], w), total(M.es[k & 1], es);
@@ -528,21 +552,24 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
                 __syncthreads();
                 if (k > 0) produce(k - 1);
                 fetch(k - 2, in), fetch_bc(k - 2);
+                if (ENDS) continue;
                 if (k + 1 < tiles) finish(k + 1);
                 fetch(k, out);
             }
             __syncthreads();  // the last tile's shared memory has been read
         }
-        // dD and the bias: over the tile's rows
+        if constexpr (!ENDS) {
+            // dD and the bias: over the tile's rows
 #pragma unroll
-        for (int e = 0; e < 4; ++e) M.us[0][row][col + e] = dD[e], M.gs[0][row][col + e] = dbias[e];
-        __syncthreads();
-        float *pd = P.pa + (long long)P.walkers * P.C_ * S + (long long)walker * 2 * P.C_;
-        for (int v = helper; v < nc; v += HELP) {
-            float s = 0.f, b = 0.f;
-            for (int r = 0; r < R; ++r) s += M.us[0][r][v], b += M.gs[0][r][v];
-            pd[c0 + v] = s;
-            pd[P.C_ + c0 + v] = b;
+            for (int e = 0; e < 4; ++e) M.us[0][row][col + e] = dD[e], M.gs[0][row][col + e] = dbias[e];
+            __syncthreads();
+            float *pd = P.pa + (long long)walker * P.C_ * (S + 2) + (long long)P.C_ * S;
+            for (int v = helper; v < nc; v += HELP) {
+                float s = 0.f, b = 0.f;
+                for (int r = 0; r < R; ++r) s += M.us[0][r][v], b += M.gs[0][r][v];
+                pd[c0 + v] = s;
+                pd[P.C_ + c0 + v] = b;
+            }
         }
         return;
     }
@@ -562,16 +589,30 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
             dA[i] = zero4();
         }
     };
-    for (int seq = walker; seq < P.seq.nseq && fine; seq += P.walkers) {
-        const int first = P.seq.off ? P.seq.off[seq] : seq * P.seq.N, len = P.seq.off ? P.seq.off[seq + 1] - first : P.seq.N;
-        const int tiles = (len + R - 1) / R;
+    for (int unit = walker; unit < P.units && fine; unit += P.walkers) {
+        int seq, j, first, all;
+        unit_at(P, unit, seq, j, first, all);
+        const long long t0 = (long long)j * P.part;
+        if (seq < 0 || (j > 0 && t0 >= all) || (ENDS && j == 0)) continue;
+        const int lo = (int)t0, len = (int)min(t0 + P.part, (long long)all);
+        const int tiles = (len - lo + R - 1) / R;
         F4 carry[2] = {zero4(), zero4()};  // a_{t+1} G_{t+1}
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (P.dlast && ch + i < nc) carry[i] = load4(P.dlast + ((long long)seq * P.C_ + c + i) * S + 4 * q);
+        for (int i = 0; i < 2; ++i) {
+            if (ch + i >= nc) continue;
+            const long long at = (long long)(c + i) * S + 4 * q;
+            if (P.dlast && len == all) carry[i] = load4(P.dlast + (long long)seq * P.C_ * S + at);
+            if (ENDS || len == all) continue;
+            const int last = unit + (all - lo - 1) / P.part;  // the sequence's last part, whose end has dstate_out in it
+            carry[i] = load4(P.ends + (long long)last * P.C_ * S + at);
+            for (int p = last - 1; p > unit; --p)
+                carry[i] = fma4(decay4(a2[i], P.sums[(long long)p * P.C_ + c + i]), carry[i], load4(P.ends + (long long)p * P.C_ * S + at));
+        }
+        float sum[2] = {0.f, 0.f};
         Vec<float, 4> mark[2] = {};
         auto fetch = [&](int k) {
-            const float *m = P.marks + (mark_slot(P, seq, k * R) * P.C_ + c) * S + 4 * q;
+            if (ENDS) return;
+            const float *m = P.marks + (mark_slot(P, seq, lo + k * R) * P.C_ + c) * S + 4 * q;
             load_ahead(mark[0], m, k >= 0 && ch < nc);
             load_ahead(mark[1], m + S, k >= 0 && ch + 1 < nc);
         };
@@ -584,67 +625,87 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
             if (k < 0) break;
             const int buf = k & 1;
             const auto &ds = M.ds[k % 3];
-            F4 h0[2];  // the tile's first state
+            if constexpr (ENDS) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) h0[i] = F4{make_float2(mark[i].e[0], mark[i].e[1]), make_float2(mark[i].e[2], mark[i].e[3])};
-            fetch(k - 1);
-            auto advance = [&](int r, const F4(&h)[2], F4(&to)[2]) {
-                const float2 d = *(const float2 *)&ds[r][ch], u = *(const float2 *)&M.us[buf][r][ch];
-                const F4 B = load4(&M.bc[buf][0][r][4 * q]);
-                to[0] = fma4(decay4(a2[0], d.x), h[0], mul4(B, u.x));
-                to[1] = fma4(decay4(a2[1], d.y), h[1], mul4(B, u.y));
-            };
-#pragma unroll
-            for (int half = R - 4; half >= 0; half -= 4) {
-                F4 hs[5][2];  // the states before each of four rows, and behind the last
-                hs[0][0] = h0[0], hs[0][1] = h0[1];
-#pragma unroll
-                for (int r = 0; r < half; ++r) advance(r, hs[0], hs[0]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) advance(half + r, hs[r], hs[r + 1]);
-                asm volatile("" ::: "memory");  // d, d x, B and the decays are not kept for the way back: registers are short
-                // Four rows' results are stored together: a store ends what may be loaded early.
-                float four[4];
-                float2 w[4], e[4], y[4];
-#pragma unroll
-                for (int i = 3; i >= 0; --i) {
-                    const int r = half + i;
-                    const float2 d = *(const float2 *)&ds[r][ch], u = *(const float2 *)&M.us[buf][r][ch], gr = *(const float2 *)&M.gs[buf][r][ch];
-                    const F4 B = load4(&M.bc[buf][0][r][4 * q]), C = load4(&M.bc[buf][1][r][4 * q]);
-                    if (P.z.p) y[i] = make_float2(dot4(C, hs[i + 1][0]), dot4(C, hs[i + 1][1]));
-                    const F4 G0 = fma4(C, gr.x, carry[0]), G1 = fma4(C, gr.y, carry[1]);
-                    const F4 dB = fma4(G1, u.y, mul4(G0, u.x)), dC = fma4(hs[i + 1][1], gr.y, mul4(hs[i + 1][0], gr.x));
-                    w[i] = make_float2(dot4(G0, B), dot4(G1, B));
-                    carry[0] = mul4(decay4(a2[0], d.x), G0);
-                    carry[1] = mul4(decay4(a2[1], d.y), G1);
-                    const F4 e0 = mul4(carry[0], hs[i][0]), e1 = mul4(carry[1], hs[i][1]);
-                    dA[0] = fma4(e0, d.x, dA[0]);
-                    dA[1] = fma4(e1, d.y, dA[1]);
-                    e[i] = make_float2(dot4(e0, a2[0]), dot4(e1, a2[1]));
-                    float v[8] = {dB.a.x, dB.a.y, dB.b.x, dB.b.y, dC.a.x, dC.a.y, dC.b.x, dC.b.y};
-                    four[i] = lanes_sum<8, 1>(v, lane & 7);
+                for (int r = R - 1; r >= 0; --r) {
+                    const float2 d = *(const float2 *)&ds[r][ch], gr = *(const float2 *)&M.gs[buf][r][ch];
+                    const F4 C = load4(&M.bc[buf][1][r][4 * q]);
+                    carry[0] = mul4(decay4(a2[0], d.x), fma4(C, gr.x, carry[0]));
+                    carry[1] = mul4(decay4(a2[1], d.y), fma4(C, gr.y, carry[1]));
+                    sum[0] += d.x, sum[1] += d.y;
                 }
-                const float s = lanes_sum<4, 8>(four, lane >> 3);
-                const int at = k * R + half + (lane >> 3);
-                if (at < len) pbc[(long long)at * P.G * 2 * S] = s;
+            } else {
+                F4 h0[2];  // the tile's first state
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    *(float2 *)&M.ws[buf][q][half + i][ch] = w[i];
-                    *(float2 *)&M.es[buf][q][half + i][ch] = e[i];
-                    if (P.z.p) *(float2 *)&M.ys[buf][q][half + i][ch] = y[i];
+                for (int i = 0; i < 2; ++i) h0[i] = F4{make_float2(mark[i].e[0], mark[i].e[1]), make_float2(mark[i].e[2], mark[i].e[3])};
+                fetch(k - 1);
+                auto advance = [&](int r, const F4(&h)[2], F4(&to)[2]) {
+                    const float2 d = *(const float2 *)&ds[r][ch], u = *(const float2 *)&M.us[buf][r][ch];
+                    const F4 B = load4(&M.bc[buf][0][r][4 * q]);
+                    to[0] = fma4(decay4(a2[0], d.x), h[0], mul4(B, u.x));
+                    to[1] = fma4(decay4(a2[1], d.y), h[1], mul4(B, u.y));
+                };
+#pragma unroll
+                for (int half = R - 4; half >= 0; half -= 4) {
+                    F4 hs[5][2];  // the states before each of four rows, and behind the last
+                    hs[0][0] = h0[0], hs[0][1] = h0[1];
+#pragma unroll
+                    for (int r = 0; r < half; ++r) advance(r, hs[0], hs[0]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) advance(half + r, hs[r], hs[r + 1]);
+                    asm volatile("" ::: "memory");  // d, d x, B and the decays are not kept for the way back: registers are short
+                    // Four rows' results are stored together: a store ends what may be loaded early.
+                    float four[4];
+                    float2 w[4], e[4], y[4];
+#pragma unroll
+                    for (int i = 3; i >= 0; --i) {
+                        const int r = half + i;
+                        const float2 d = *(const float2 *)&ds[r][ch], u = *(const float2 *)&M.us[buf][r][ch], gr = *(const float2 *)&M.gs[buf][r][ch];
+                        const F4 B = load4(&M.bc[buf][0][r][4 * q]), C = load4(&M.bc[buf][1][r][4 * q]);
+                        if (P.z.p) y[i] = make_float2(dot4(C, hs[i + 1][0]), dot4(C, hs[i + 1][1]));
+                        const F4 G0 = fma4(C, gr.x, carry[0]), G1 = fma4(C, gr.y, carry[1]);
+                        const F4 dB = fma4(G1, u.y, mul4(G0, u.x)), dC = fma4(hs[i + 1][1], gr.y, mul4(hs[i + 1][0], gr.x));
+                        w[i] = make_float2(dot4(G0, B), dot4(G1, B));
+                        carry[0] = mul4(decay4(a2[0], d.x), G0);
+                        carry[1] = mul4(decay4(a2[1], d.y), G1);
+                        const F4 e0 = mul4(carry[0], hs[i][0]), e1 = mul4(carry[1], hs[i][1]);
+                        dA[0] = fma4(e0, d.x, dA[0]);
+                        dA[1] = fma4(e1, d.y, dA[1]);
+                        e[i] = make_float2(dot4(e0, a2[0]), dot4(e1, a2[1]));
+                        float v[8] = {dB.a.x, dB.a.y, dB.b.x, dB.b.y, dC.a.x, dC.a.y, dC.b.x, dC.b.y};
+                        four[i] = lanes_sum<8, 1>(v, lane & 7);
+                    }
+                    const float s = lanes_sum<4, 8>(four, lane >> 3);
+                    const int at = lo + k * R + half + (lane >> 3);
+                    if (at < len) pbc[(long long)at * P.G * 2 * S] = s;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        *(float2 *)&M.ws[buf][q][half + i][ch] = w[i];
+                        *(float2 *)&M.es[buf][q][half + i][ch] = e[i];
+                        if (P.z.p) *(float2 *)&M.ys[buf][q][half + i][ch] = y[i];
+                    }
                 }
+                if (k % K::FLUSH == 0) flush();
             }
-            if (k % K::FLUSH == 0) flush();
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (P.dfirst && ch + i < nc) store4(P.dfirst + ((long long)seq * P.C_ + c + i) * S + 4 * q, carry[i]);
+        for (int i = 0; i < 2; ++i) {
+            if (ch + i >= nc) continue;
+            const long long at = (long long)(c + i) * S + 4 * q;
+            if (ENDS) {
+                store4(P.ends + (long long)unit * P.C_ * S + at, carry[i]);
+                if (q == 0) P.sums[(long long)unit * P.C_ + c + i] = sum[i];
+            } else if (P.dfirst && j == 0) {
+                store4(P.dfirst + (long long)seq * P.C_ * S + at, carry[i]);
+            }
+        }
         __syncthreads();
     }
+    if (ENDS) return;
     flush();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        if (ch + i < nc) *(float4 *)(P.pa + ((long long)walker * P.C_ + c + i) * S + 4 * q) = M.dA[i][threadIdx.x];
+        if (ch + i < nc) *(float4 *)(P.pa + (long long)walker * P.C_ * (S + 2) + (long long)(c + i) * S + 4 * q) = M.dA[i][threadIdx.x];
     __syncthreads();
 }
 
@@ -703,26 +764,30 @@ int forward_channels(int S) { return S == 8 ? Tile<8>::CH : S == 16 ? Tile<16>::
 int back_channels(int S) { return S == 8 ? Back<8>::CH : S == 16 ? Back<16>::CH : Back<32>::CH; }
 int blocks_per_group(int C, int G, int channels) { return (C / G + channels - 1) / channels; }
 
-// Rows of a part: all, where the sequences' channel blocks make kEnough CTAs, else as many parts of a sequence of the mean
-// length as make two CTAs to an SM and no more, of kLeastPart rows at least.
-constexpr int kEnough = 76, kLeastPart = 512;
+// Rows of a part: all, where the sequences' channel blocks make a CTA for every other SM, else as many parts of a sequence
+// of the mean length as stand on the SMs at once (two CTAs on each, one where S is 8 or 32), of kLeastPart rows at least.
+constexpr int kLeastPart = 512;
+static_assert(Tile<8>::CH == Back<8>::CH && Tile<16>::CH == Back<16>::CH && Tile<32>::CH == Back<32>::CH, "one rule for both");
 int part_rows(int T, int nseq, int C, int G, int S) {
     const long long n = nseq > 0 ? nseq : 1, ctas = n * G * blocks_per_group(C, G, forward_channels(S));
     const long long whole = ((long long)T + kTile) / kTile * kTile;
-    if (ctas >= kEnough || T / n < 2 * kLeastPart) return (int)whole;
-    long long want = 2 * kSMs / ctas;
+    if (ctas >= kSMs / 2 || T / n < 2 * kLeastPart) return (int)whole;
+    long long want = (S == 16 ? 2 : 1) * kSMs / ctas;
     if (want > kMaxParts) want = kMaxParts;
     long long part = ((T + n * want - 1) / (n * want) + kTile - 1) / kTile * kTile;
     if (part < kLeastPart) part = kLeastPart;
     return (int)(part < whole ? part : whole);
 }
 long long units_of(int T, int nseq, int N, int part, bool packed) {
-    if (packed) return nseq + T / part;
+    if (packed) return (long long)nseq + T / part;
     return (long long)nseq * (N > 0 ? (N + part - 1) / part : 1);
 }
-int walkers_of(int nseq, int C, int G, int S) {
+// CTAs of a channel block in the backward walk: four CTAs to an SM in all, or the units that there are at most (a batch has no
+// more than the same sequences packed).
+int walkers_of(int T, int nseq, int C, int G, int S) {
     const long long cblocks = (long long)G * blocks_per_group(C, G, back_channels(S)), want = (4 * kSMs + cblocks - 1) / cblocks;
-    return (int)(nseq < want ? nseq : want);
+    const long long units = units_of(T, nseq, 0, part_rows(T, nseq, C, G, S), true);
+    return (int)(units < want ? units : want);
 }
 struct Space {  // byte offsets of the workspace's arrays
     size_t ends, sums, pbc, pa, bytes;
@@ -735,17 +800,16 @@ Space space_of(int T, int nseq, int C, int G, int S, bool back) {
         at += (n + 255) & ~(size_t)255;
         return here;
     };
+    const int part = part_rows(T, nseq, C, G, S);
+    if (part < T) {
+        const size_t units = (size_t)units_of(T, nseq, 0, part, true) + 1;  // a batch has no more
+        w.ends = take(units * C * S * 4);
+        w.sums = take(units * C * 4);
+    }
     if (back) {
-        const size_t walkers = walkers_of(nseq, C, G, S);
+        const size_t walkers = walkers_of(T, nseq, C, G, S);
         w.pbc = take((size_t)blocks_per_group(C, G, back_channels(S)) * (back_channels(S) / 64) * T * G * 2 * S * 4);
         w.pa = take(walkers * C * (S + 2) * 4);
-    } else {
-        const int part = part_rows(T, nseq, C, G, S);
-        if (part < T) {
-            const size_t units = (size_t)nseq + T / part + 1;  // a batch has no more
-            w.ends = take(units * C * S * 4);
-            w.sums = take(units * C * 4);
-        }
     }
     w.bytes = at;
     return w;
@@ -836,18 +900,24 @@ template <typename T> cudaError_t forward(const Params &P, int S, long long unit
     return S == 8 ? forward<T, 8>(P, units, split, s) : S == 16 ? forward<T, 16>(P, units, split, s) : forward<T, 32>(P, units, split, s);
 }
 
-template <typename T, int S> cudaError_t backward(const Params &P, void *dB, void *dC, float *dA, float *dD, float *dbias, cudaStream_t s) {
+template <typename T, int S> cudaError_t backward(const Params &P, bool split, void *dB, void *dC, float *dA, float *dD, float *dbias, cudaStream_t s) {
     using M = typename Back<S>::Smem;
     static std::atomic<int> attr_state[kMaxDevices];
     if (!once_per_device(attr_state, [] {
-            return cudaFuncSetAttribute(backward_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(M)) == cudaSuccess;
+            return cudaFuncSetAttribute(backward_kernel<T, S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(M)) == cudaSuccess &&
+                   cudaFuncSetAttribute(backward_kernel<T, S, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(M)) == cudaSuccess;
         }))
         return cudaErrorInvalidValue;
     const long long blocks = (long long)P.walkers * P.G * P.bpg;
     if (blocks > 0) {
-        backward_kernel<T, S><<<(unsigned)blocks, Back<S>::THREADS, sizeof(M), s>>>(P);
-        cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
+        cudaError_t e;
+        if (split) {
+            backward_kernel<T, S, true><<<(unsigned)blocks, Back<S>::THREADS, sizeof(M), s>>>(P);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            count_launches(1);
+        }
+        backward_kernel<T, S, false><<<(unsigned)blocks, Back<S>::THREADS, sizeof(M), s>>>(P);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
         count_launches(1);
         const long long sums = ((long long)P.seq.T * P.G * 2 * S + 255) / 256;
         if (sums >= (1LL << 31)) return cudaErrorInvalidConfiguration;
@@ -857,12 +927,12 @@ template <typename T, int S> cudaError_t backward(const Params &P, void *dB, voi
             count_launches(1);
         }
     }
-    const cudaError_t e = sum_parts(P.pa, P.walkers, (long long)P.C_ * S, (long long)P.C_ * S, dA, nullptr, s);
-    return e != cudaSuccess ? e : sum_parts(P.pa + (size_t)P.walkers * P.C_ * S, P.walkers, 2LL * P.C_, P.C_, dD, dbias, s);
+    const long long n = (long long)P.C_ * S;
+    return sum_parts(P.pa, P.walkers, n + 2LL * P.C_, dA, n, dD, P.C_, dbias, s);
 }
-template <typename T> cudaError_t backward(const Params &P, int S, void *dB, void *dC, float *dA, float *dD, float *dbias, cudaStream_t s) {
-    return S == 8 ? backward<T, 8>(P, dB, dC, dA, dD, dbias, s) : S == 16 ? backward<T, 16>(P, dB, dC, dA, dD, dbias, s)
-                                                                       : backward<T, 32>(P, dB, dC, dA, dD, dbias, s);
+template <typename T> cudaError_t backward(const Params &P, int S, bool split, void *dB, void *dC, float *dA, float *dD, float *dbias, cudaStream_t s) {
+    return S == 8 ? backward<T, 8>(P, split, dB, dC, dA, dD, dbias, s) : S == 16 ? backward<T, 16>(P, split, dB, dC, dA, dD, dbias, s)
+                                                                       : backward<T, 32>(P, split, dB, dC, dA, dD, dbias, s);
 }
 
 template <typename T, int S> cudaError_t step(const Params &P, cudaStream_t s) {
@@ -973,11 +1043,15 @@ int la_selective_scan_backward(const void *X, const void *dt, const float *A, co
     P.dx = Op{dX, out[0].st[0], out[0].st[1]};
     P.ddt = Op{ddt, out[1].st[0], out[1].st[1]};
     P.dz = Op{dz, out[2].st[0], out[2].st[1]};
-    P.walkers = walkers_of(nseq, channels, G, S);
+    P.part = part_rows(T, nseq, channels, G, S);
+    const bool split = P.part < T && (packed || N > P.part);
+    P.units = (int)units_of(T, nseq, N, P.part, packed);
+    P.walkers = walkers_of(T, nseq, channels, G, S);
+    P.ends = (float *)((char *)workspace + w.ends), P.sums = (float *)((char *)workspace + w.sums);
     P.pbc = (float *)((char *)workspace + w.pbc), P.pa = (float *)((char *)workspace + w.pa);
     cudaStream_t s = (cudaStream_t)stream;
-    return status_of(dtype == LA_BF16 ? backward<__nv_bfloat16>(P, S, dB, dC, dA, dD, ddt_bias, s)
-                                      : backward<float>(P, S, dB, dC, dA, dD, ddt_bias, s));
+    return status_of(dtype == LA_BF16 ? backward<__nv_bfloat16>(P, S, split, dB, dC, dA, dD, ddt_bias, s)
+                                      : backward<float>(P, S, split, dB, dC, dA, dD, ddt_bias, s));
 }
 
 int la_selective_scan_step(const void *x, const void *dt, const float *A, const void *B, const void *C, const float *D,

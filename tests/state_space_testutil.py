@@ -146,19 +146,22 @@ def _states(x, d, ed, A, B, h, E, Hm, extra):
     """The states before and after each row, their bounds, and each row's decay with its relative bound.
 
     A decay is off by A's part of d's error, three roundings of the exponent and the 2 ulp (four half steps) of 2^x; the
-    input by d's error and two products; the step by one rounding.  `extra`: half steps of the state at a part's beginning
-    (of its sum of d, against x e^-x <= 0.4)."""
+    input by d's error and two products; the step by one rounding.  `extra`: where time is cut into parts, a
+    part's decay e^(A sum d) has a sum that is off by a half step for each of its n rows, so what stood before it by n half
+    steps of x e^-x <= 0.4, x = |A| sum d: 0.4 n half steps of the largest state so far, wherever in the part."""
+    Hx = Hm
     before, after, eb, ea, decay, rho = [], [], [], [], [], []
     for t in range(x.shape[0]):
         a = torch.exp(d[t][:, None] * A)
         r = A.abs() * ed[t][:, None] + U * (3 * (d[t][:, None] * A).abs() + 5)
         u = (d[t] * x[t])[:, None] * B[t]
-        before.append(h), eb.append(E), decay.append(a), rho.append(r)
+        before.append(h), eb.append(E + extra * U * Hx), decay.append(a), rho.append(r)
         E = a * E + a * Hm * (r + U) + (x[t].abs() * ed[t])[:, None] * B[t].abs() + 3 * U * u.abs()
         h = a * h + u
         Hm = a * Hm + u.abs()
-        after.append(h), ea.append(E + extra * U * Hm)
-    return before, after, eb, ea, decay, rho, h, E + extra * U * Hm, Hm
+        Hx = torch.maximum(Hx, Hm)
+        after.append(h), ea.append(E + extra * U * Hx)
+    return before, after, eb, ea, decay, rho, h, E + extra * U * Hx, Hm
 
 
 def scan(x, dt, A, B, C, D, z, bias, softplus, offsets, state, extra=0):
@@ -190,9 +193,9 @@ def scan(x, dt, A, B, C, D, z, bias, softplus, offsets, state, extra=0):
     return (Y, torch.stack(last) if last else empty), (tol + LOST, torch.stack(elast) + LOST if last else empty)
 
 
-def scan_backward(x, dt, A, B, C, dY, D, z, bias, softplus, offsets, state, dlast):
+def scan_backward(x, dt, A, B, C, dY, D, z, bias, softplus, offsets, state, dlast, extra=0):
     """-> dicts of the gradients and of their bounds (the states' bounds as in scan; G's in the same way, from g's (the gate's
-    |z| + 11 half steps) and the decays')."""
+    |z| + 11 half steps) and the decays'; `extra`: half steps of G behind a part's end, as of the state in scan)."""
     x, A, dY = x.double(), A.double(), dY.double()
     T, Ch = x.shape
     S, G = A.shape[1], B.shape[1]
@@ -207,19 +210,22 @@ def scan_backward(x, dt, A, B, C, dY, D, z, bias, softplus, offsets, state, dlas
     for i, (lo, hi) in enumerate(spans(offsets)):
         h = state[i].double() if state is not None else zero(Ch, S)
         s = slice(lo, hi)
-        before, after, eb, ea, decay, rho, _, _, _ = _states(x[s], d[s], ed[s], A, Bw[s], h, torch.zeros_like(h), h.abs(), 0)
+        before, after, eb, ea, decay, rho, _, _, _ = _states(x[s], d[s], ed[s], A, Bw[s], h, torch.zeros_like(h), h.abs(), extra)
         gate = silu(z.double()) if z is not None else torch.ones_like(x)
         P = dlast[i].double() if dlast is not None else zero(Ch, S)  # a_{t+1} G_{t+1}
-        EP, MP = torch.zeros_like(P), P.abs()
+        EP, MP, Gx = torch.zeros_like(P), P.abs(), P.abs()
         for t in range(hi - 1, lo - 1, -1):
             k = t - lo
             gt = dY[t] * gate[t]
             egt = U * ((z[t].double().abs() + 11) if z is not None else 0) * gt.abs()
             Gt, Gm = gt[:, None] * Cw[t] + P, (gt[:, None] * Cw[t]).abs() + MP
             EG = egt[:, None] * Cw[t].abs() + EP + U * Gm
+            carried = EG  # without what a part's end leaves, which does not grow
+            Gx = torch.maximum(Gx, Gm)
+            EG = EG + extra * U * Gx
             a, r = decay[k], rho[k]
             P, MP = a * Gt, a * Gm
-            EP = a * EG + MP * (r + U)
+            EP = a * carried + MP * (r + U)
             w, wm = (Gt * Bw[t]).sum(-1), (Gm * Bw[t].abs()).sum(-1)
             ew = (EG * Bw[t].abs()).sum(-1) + U * (S + 1) * wm
             g["dX"][t] = d[t] * w + Dv * gt
@@ -253,7 +259,7 @@ def scan_backward(x, dt, A, B, C, dY, D, z, bias, softplus, offsets, state, dlas
                 sg = silu_grad(zz)
                 g["dz"][t] = dY[t] * y * sg
                 e["dz"][t] = dY[t].abs() * (ey * sg.abs() + U * ((1 + zz.abs()) * (zz.abs() + 12) + 3) * M)
-        g["dstate_in"][i], e["dstate_in"][i] = P, EP
+        g["dstate_in"][i], e["dstate_in"][i] = P, EP + extra * U * Gx
     g["ddt_bias"] = g["ddt"].sum(0)
     e["ddt_bias"] = e["ddt"].sum(0) + U * (T + SUM) * m["ddt"].sum(0)
     e["dA"] += U * (T + SUM) * m["dA"]
