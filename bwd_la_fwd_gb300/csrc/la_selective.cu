@@ -336,6 +336,7 @@ __global__ void __launch_bounds__(Tile<S>::THREADS, S == 16 ? 2 : 1) forward_ker
         if (j == 0) {
             if (P.first) h[i] = load4(P.first + (long long)seq * P.C_ * S + at);
         } else if (!ENDS) {
+#pragma unroll 4
             for (int p = unit - j; p < unit; ++p) {
                 const F4 e = load4(P.ends + (long long)p * P.C_ * S + at);
                 h[i] = p == unit - j ? e : fma4(decay4(a2[i], P.sums[(long long)p * P.C_ + c + i]), h[i], e);
@@ -605,6 +606,7 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
             if (ENDS || len == all) continue;
             const int last = unit + (all - lo - 1) / P.part;  // the sequence's last part, whose end has dstate_out in it
             carry[i] = load4(P.ends + (long long)last * P.C_ * S + at);
+#pragma unroll 4
             for (int p = last - 1; p > unit; --p)
                 carry[i] = fma4(decay4(a2[i], P.sums[(long long)p * P.C_ + c + i]), carry[i], load4(P.ends + (long long)p * P.C_ * S + at));
         }
@@ -766,7 +768,7 @@ int blocks_per_group(int C, int G, int channels) { return (C / G + channels - 1)
 
 // Rows of a part: all, where the sequences' channel blocks make a CTA for every other SM, else as many parts of a sequence
 // of the mean length as stand on the SMs at once (two CTAs on each, one where S is 8 or 32), of kLeastPart rows at least.
-constexpr int kLeastPart = 512;
+constexpr int kLeastPart = 128;
 static_assert(Tile<8>::CH == Back<8>::CH && Tile<16>::CH == Back<16>::CH && Tile<32>::CH == Back<32>::CH, "one rule for both");
 int part_rows(int T, int nseq, int C, int G, int S) {
     const long long n = nseq > 0 ? nseq : 1, ctas = n * G * blocks_per_group(C, G, forward_channels(S));
