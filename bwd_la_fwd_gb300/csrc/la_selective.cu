@@ -120,14 +120,25 @@ template <int L, int STEP> __device__ __forceinline__ float lanes_sum(float (&v)
     return v[0];
 }
 
-template <int S> struct Tile {
-    static constexpr int R = kTile;                                       // rows
-    static constexpr int QW = S / 4, GW = QW > 4 ? 1 : 4 / QW;            // warps of a channel group, groups
-    static constexpr int CH = 64 * GW, HELP = CH == 64 ? 256 : 2 * CH;  // channels of a CTA, helping threads
-    static constexpr int THREADS = HELP + 32 * QW * GW;
-    static constexpr int NV = R * CH / 4 / HELP;                          // vectors of four channels to a helper
-    static constexpr int NB = (2 * R * S / 4 + HELP - 1) / HELP;          // of four of B and C
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// 16 bytes global -> shared; bytes past `n` are zero.
+__device__ __forceinline__ void copy16(void *dst, const void *src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// A forward CTA has 64 channels, CT of them to a scanning thread.
+template <typename T, int S, int CT> struct Tile {
+    static constexpr int R = kTile, CH = 64;
+    static constexpr int QW = S / 4, CW = 32 * CT;                       // warps of a channel group, channels of a warp
+    static constexpr int SCAN = 32 * QW * (CH / CW), HELP = R * CH / 4;  // threads; a vector of four channels to a helper
+    static constexpr int THREADS = SCAN + HELP;
+    static constexpr int PER_SM = THREADS <= 384 ? 2 : 1;
+    static constexpr int STAGES = 5;                                     // tiles on their way, or read for d, y or the outputs
     struct Smem {
+        T in[STAGES][3][R][CH];            // x, dt, z
+        T bc_in[STAGES][2][R][S];
         float ds[2][R][CH], us[2][R][CH];  // d and d x
         float bc[2][2][R][S];
         float ys[2][QW][R][CH];            // parts of y (the last member: a launch for ends has none)
@@ -177,10 +188,10 @@ __device__ __forceinline__ long long mark_slot(const Params &P, int seq, int row
 }
 
 // ENDS: the first launch, which forms the parts' last states only.
-template <typename T, int S, bool ENDS>
-__global__ void __launch_bounds__(Tile<S>::THREADS, S == 16 ? 2 : 1) forward_kernel(const __grid_constant__ Params P) {
-    using K = Tile<S>;
-    constexpr int CH = K::CH, R = K::R, NV = K::NV, NB = K::NB, QW = K::QW, HELP = K::HELP;
+template <typename T, int S, int CT, bool ENDS>
+__global__ void __launch_bounds__(Tile<T, S, CT>::THREADS, Tile<T, S, CT>::PER_SM) forward_kernel(const __grid_constant__ Params P) {
+    using K = Tile<T, S, CT>;
+    constexpr int CH = K::CH, R = K::R, QW = K::QW, HELP = K::HELP, ST = K::STAGES;
     extern __shared__ __align__(16) unsigned char raw[];
     typename K::Smem &M = *(typename K::Smem *)raw;
     const int cblocks = P.G * P.bpg, unit = blockIdx.x / cblocks, cb = blockIdx.x - unit * cblocks;
@@ -192,15 +203,13 @@ __global__ void __launch_bounds__(Tile<S>::THREADS, S == 16 ? 2 : 1) forward_ker
     const int lo = (int)t0, hi = (int)min(t0 + P.part, (long long)len);
     if (ENDS && hi == len) return;  // nothing follows
     const int g = cb / P.bpg, c0 = g * P.cpg + (cb - g * P.bpg) * CH, nc = min(CH, (g + 1) * P.cpg - c0);
-    const int tiles = (hi - lo + R - 1) / R, helper = (int)threadIdx.x - 32 * QW * K::GW;
+    const int tiles = (hi - lo + R - 1) / R, helper = (int)threadIdx.x - K::SCAN;
     if (helper >= 0) {
         const T *x = rows_of<const T>(P.seq, P.x, seq) + c0, *dt = rows_of<const T>(P.seq, P.dt, seq) + c0;
         const T *z = P.z.p ? rows_of<const T>(P.seq, P.z, seq) + c0 : nullptr;
         T *y = ENDS ? nullptr : rows_of<T>(P.seq, P.y, seq) + c0;
         const T *Bp = (const T *)P.B.p + (P.seq.off ? P.seq.off[seq] * P.B.sn : seq * P.B.sb) + g * P.B.sg;
         const T *Cp = (const T *)P.C.p + (P.seq.off ? P.seq.off[seq] * P.C.sn : seq * P.C.sb) + g * P.C.sg;
-        // vectors helper, helper + HELP, ... of a tile: the same channels in rows STEP apart
-        constexpr int STEP = HELP / (CH / 4);
         const int row = helper / (CH / 4), col = helper % (CH / 4) * 4, n = nc - col;
         float bias[4], D[4];
 #pragma unroll
@@ -208,128 +217,101 @@ __global__ void __launch_bounds__(Tile<S>::THREADS, S == 16 ? 2 : 1) forward_ker
             bias[k] = P.bias && k < n ? P.bias[c0 + col + k] : 0.f;
             D[k] = P.D && k < n ? P.D[c0 + col + k] : 0.f;
         }
-        // x, dt, B, C on their way to d, and x, z to the outputs: two tiles of each, so that a load has two steps' time
-        Vec<T, 4> px[2][NV], pd[2][NV], ex[2][NV], ez[2][NV], vb[2][NB];
-        auto fetch = [&](int k, Vec<T, 4>(&px)[NV], Vec<T, 4>(&pd)[NV], Vec<T, 4>(&vb)[NB]) {
-            const int t = lo + k * R;
+        // x, dt, z, B and C of a tile, 16 bytes a copy, zeros where there is no row or channel
+        auto copy = [&](int k) {
+            constexpr int E = 16 / (int)sizeof(T), VR = CH / E, VS = S / E, ROWS = R * VR, ALL = 3 * ROWS + 2 * R * VS;
+            const int t = lo + k * R, st = k % ST;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int r = t + row + i * STEP;
-                load_ahead(px[i], x + r * P.x.sn + col, r < hi && n >= 4);
-                load_ahead(pd[i], dt + r * P.dt.sn + col, r < hi && n >= 4);
+            for (int i = 0; i < (ALL + HELP - 1) / HELP; ++i) {
+                const int v = i * HELP + helper;
+                if (v < 3 * ROWS) {
+                    const int op = v / ROWS, r = v % ROWS / VR, e = v % VR * E;
+                    const T *p = op == 0 ? x : op == 1 ? dt : z;
+                    const long long sn = op == 0 ? P.x.sn : op == 1 ? P.dt.sn : P.z.sn;
+                    if (op == 2 && (ENDS || !z)) continue;
+                    const int have = t + r < hi ? max(0, min(16, (nc - e) * (int)sizeof(T))) : 0;
+                    copy16(&M.in[st][op][r][e], have ? p + (t + r) * sn + e : p, have);
+                } else if (v < ALL) {
+                    const int w = v - 3 * ROWS, op = w / (R * VS), r = w % (R * VS) / VS, e = w % VS * E;
+                    if (op == 1 && ENDS) continue;
+                    const bool have = t + r < hi;
+                    const T *p = op ? Cp : Bp;
+                    copy16(&M.bc_in[st][op][r][e], have ? p + (t + r) * (op ? P.C.sn : P.B.sn) + e : p, have ? 16 : 0);
+                }
             }
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int v = i * HELP + helper, which = v / (R * S / 4), r = t + v % (R * S / 4) / (S / 4), s = v % (S / 4) * 4;
-                load_ahead(vb[i], (which ? Cp + r * P.C.sn : Bp + r * P.B.sn) + s, which < (ENDS ? 1 : 2) && r < hi);
-            }
+            copy_commit();
         };
         const bool whole = nc == CH;
-        auto produce = [&](int k, Vec<T, 4>(&px)[NV], Vec<T, 4>(&pd)[NV], Vec<T, 4>(&vb)[NB]) {
-            const int t = lo + k * R, buf = k & 1;
-            const bool full = whole && t + R <= hi;  // no row or channel is missing
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int r = row + i * STEP;
-                if (full) {
-                    const float2 v = step_of(P, make_float2(to_f(pd[i].e[0]) + bias[0], to_f(pd[i].e[1]) + bias[1]));
-                    const float2 w = step_of(P, make_float2(to_f(pd[i].e[2]) + bias[2], to_f(pd[i].e[3]) + bias[3]));
-                    *(float4 *)&M.ds[buf][r][col] = make_float4(v.x, v.y, w.x, w.y);
-                    *(float4 *)&M.us[buf][r][col] = make_float4(v.x * to_f(px[i].e[0]), v.y * to_f(px[i].e[1]),
-                                                                w.x * to_f(px[i].e[2]), w.y * to_f(px[i].e[3]));
-                    continue;
-                }
-                const bool in = t + r < hi;
-                if (in && n > 0 && n < 4) {  // the last channels, where they are no whole vector
-                    px[i] = load_vec<T, 4>(x + (t + r) * P.x.sn + col, n);
-                    pd[i] = load_vec<T, 4>(dt + (t + r) * P.dt.sn + col, n);
-                }
-                float d[4], u[4];
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const float2 v = step_of(P, make_float2(to_f(pd[i].e[e]) + bias[e], to_f(pd[i].e[e + 1]) + bias[e + 1]));
-                    d[e] = in && e < n ? v.x : 0.f;  // no row: nothing happens
-                    d[e + 1] = in && e + 1 < n ? v.y : 0.f;
-                    u[e] = in && e < n ? v.x * to_f(px[i].e[e]) : 0.f;
-                    u[e + 1] = in && e + 1 < n ? v.y * to_f(px[i].e[e + 1]) : 0.f;
-                }
-                *(float4 *)&M.ds[buf][r][col] = make_float4(d[0], d[1], d[2], d[3]);
-                *(float4 *)&M.us[buf][r][col] = make_float4(u[0], u[1], u[2], u[3]);
+        auto produce = [&](int k) {
+            const int t = lo + k * R, buf = k & 1, st = k % ST;
+            const Vec<T, 4> vx = *(const Vec<T, 4> *)&M.in[st][0][row][col], vd = *(const Vec<T, 4> *)&M.in[st][1][row][col];
+            const float2 a = step_of(P, make_float2(to_f(vd.e[0]) + bias[0], to_f(vd.e[1]) + bias[1]));
+            const float2 b = step_of(P, make_float2(to_f(vd.e[2]) + bias[2], to_f(vd.e[3]) + bias[3]));
+            float4 d = make_float4(a.x, a.y, b.x, b.y);
+            if (!(whole && t + R <= hi)) {  // no row or channel: nothing happens
+                if (t + row >= hi || n < 1) d.x = 0.f;
+                if (t + row >= hi || n < 2) d.y = 0.f;
+                if (t + row >= hi || n < 3) d.z = 0.f;
+                if (t + row >= hi || n < 4) d.w = 0.f;
             }
+            *(float4 *)&M.ds[buf][row][col] = d;
+            *(float4 *)&M.us[buf][row][col] = make_float4(d.x * to_f(vx.e[0]), d.y * to_f(vx.e[1]), d.z * to_f(vx.e[2]), d.w * to_f(vx.e[3]));
+            constexpr int NB = (ENDS ? 1 : 2) * R * S / 4;
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int v = i * HELP + helper, which = v / (R * S / 4), r = v % (R * S / 4) / (S / 4), s = v % (S / 4) * 4;
-                if (which >= (ENDS ? 1 : 2)) continue;
-                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (t + r < hi) f = make_float4(to_f(vb[i].e[0]), to_f(vb[i].e[1]), to_f(vb[i].e[2]), to_f(vb[i].e[3]));
-                *(float4 *)&M.bc[buf][which][r][s] = f;
+            for (int i = 0; i < (NB + HELP - 1) / HELP; ++i) {
+                const int v = i * HELP + helper;
+                if (NB % HELP != 0 && v >= NB) break;
+                const Vec<T, 4> f = ((const Vec<T, 4> *)M.bc_in[st])[v];
+                ((float4 *)M.bc[buf])[v] = make_float4(to_f(f.e[0]), to_f(f.e[1]), to_f(f.e[2]), to_f(f.e[3]));
             }
         };
-        auto fetch_out = [&](int k, Vec<T, 4>(&ex)[NV], Vec<T, 4>(&ez)[NV]) {
+        auto finish = [&](int k) {
+            const int t = lo + k * R, buf = k & 1, st = k % ST;
+            const Vec<T, 4> vx = *(const Vec<T, 4> *)&M.in[st][0][row][col], vz = *(const Vec<T, 4> *)&M.in[st][2][row][col];
+            float4 s = *(const float4 *)&M.ys[buf][0][row][col];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int r = lo + k * R + row + i * STEP;
-                load_ahead(ex[i], x + r * P.x.sn + col, r < hi && n >= 4);
-                load_ahead(ez[i], z + r * P.z.sn + col, z && r < hi && n >= 4);
+            for (int w = 1; w < QW; ++w) {
+                const float4 o = *(const float4 *)&M.ys[buf][w][row][col];
+                s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
             }
-        };
-        auto finish = [&](int k, Vec<T, 4>(&ex)[NV], Vec<T, 4>(&ez)[NV]) {
-            const int t = lo + k * R, buf = k & 1;
+            const float v[4] = {s.x, s.y, s.z, s.w};
+            Vec<T, 4> out;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int r = row + i * STEP;
-                if (t + r >= hi || n <= 0) continue;
-                if (n < 4) {
-                    ex[i] = load_vec<T, 4>(x + (t + r) * P.x.sn + col, n);
-                    if (z) ez[i] = load_vec<T, 4>(z + (t + r) * P.z.sn + col, n);
+            for (int e = 0; e < 4; ++e) {
+                float f = fmaf(D[e], to_f(vx.e[e]), v[e]);
+                if (z) {
+                    const float ze = to_f(vz.e[e]);
+                    f *= ze * sigmoid(ze);
                 }
-                float4 s = *(const float4 *)&M.ys[buf][0][r][col];
-#pragma unroll
-                for (int w = 1; w < QW; ++w) {
-                    const float4 o = *(const float4 *)&M.ys[buf][w][r][col];
-                    s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
-                }
-                const float v[4] = {s.x, s.y, s.z, s.w};
-                Vec<T, 4> out;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float f = fmaf(D[e], to_f(ex[i].e[e]), v[e]);
-                    if (z) {
-                        const float ze = to_f(ez[i].e[e]);
-                        f *= ze * sigmoid(ze);
-                    }
-                    put(&out.e[e], f);
-                }
-                store_vec<T, 4>(y + (t + r) * P.y.sn + col, out, n);
+                put(&out.e[e], f);
             }
+            if (t + row < hi && n > 0) store_vec<T, 4>(y + (t + row) * P.y.sn + col, out, n);
         };
-        // Step k, while tile k is scanned: d of tile k + 1, the outputs of tile k - 1.
-        auto step = [&](int k, auto parity) {
-            constexpr int a = decltype(parity)::value, b = 1 - a;  // of k, of its neighbours
+        copy(0), copy(1), copy(2);
+        copy_wait<2>();
+        __syncthreads();
+        if (tiles > 0) produce(0);
+        copy_wait<1>();
+        // Step k, while tile k is scanned: d of tile k + 1, the outputs of tile k - 1, and tile k + 3 on its way into the
+        // place of tile k - 2.  Tile k + 2 is there when the next step begins.
+        for (int k = 0; k <= tiles; ++k) {
             __syncthreads();
-            if (k + 1 < tiles) produce(k + 1, px[b], pd[b], vb[b]);
-            fetch(k + 3, px[b], pd[b], vb[b]);
-            if (ENDS) return;
-            if (k > 0) finish(k - 1, ex[b], ez[b]);
-            fetch_out(k + 1, ex[b], ez[b]);
-        };
-        fetch(0, px[0], pd[0], vb[0]);
-        fetch(1, px[1], pd[1], vb[1]);
-        if (!ENDS) fetch_out(0, ex[0], ez[0]);
-        if (tiles > 0) produce(0, px[0], pd[0], vb[0]);
-        fetch(2, px[0], pd[0], vb[0]);
-        for (int k = 0; k <= tiles; k += 2) {
-            step(k, std::integral_constant<int, 0>());
-            if (k < tiles) step(k + 1, std::integral_constant<int, 1>());
+            if (k + 1 < tiles) produce(k + 1);
+            copy(k + 3);
+            if (!ENDS && k > 0) finish(k - 1);
+            copy_wait<1>();
         }
+        copy_wait<0>();
         return;
     }
-    // four states of two neighbouring channels
-    const int warp = threadIdx.x >> 5, q = warp % QW, ch = warp / QW * 64 + (threadIdx.x & 31) * 2, c = c0 + ch;
-    F4 a2[2] = {zero4(), zero4()}, h[2] = {zero4(), zero4()};
-    float sum[2] = {0.f, 0.f};
+    // four states of CT neighbouring channels
+    const int warp = threadIdx.x >> 5, q = warp % QW, ch = warp / QW * K::CW + (threadIdx.x & 31) * CT, c = c0 + ch;
+    F4 a2[CT], h[CT];
+    float sum[CT];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < CT; ++i) {
+        a2[i] = h[i] = zero4();
+        sum[i] = 0.f;
         if (ch + i >= nc) continue;
         const long long at = (long long)(c + i) * S + 4 * q;
         a2[i] = mul4(load4(P.A + at), kLog2e);
@@ -343,6 +325,7 @@ __global__ void __launch_bounds__(Tile<S>::THREADS, S == 16 ? 2 : 1) forward_ker
             }
         }
     }
+    __syncthreads();
     for (int k = 0; k <= tiles; ++k) {
         __syncthreads();
         if (k == tiles) break;
@@ -351,11 +334,16 @@ __global__ void __launch_bounds__(Tile<S>::THREADS, S == 16 ? 2 : 1) forward_ker
         // A row's operands are loaded a row ahead of it, before the parts of y of the row between are stored (which the
         // compiler has to take for stores to them).
         struct Row {
-            float2 d, u;
+            float d[CT], u[CT];
             F4 B, C;
         } ahead[2];
         auto load = [&](int r, Row &o) {
-            o.d = *(const float2 *)&M.ds[buf][r][ch], o.u = *(const float2 *)&M.us[buf][r][ch];
+            if constexpr (CT == 2) {
+                const float2 d = *(const float2 *)&M.ds[buf][r][ch], u = *(const float2 *)&M.us[buf][r][ch];
+                o.d[0] = d.x, o.d[1] = d.y, o.u[0] = u.x, o.u[1] = u.y;
+            } else {
+                o.d[0] = M.ds[buf][r][ch], o.u[0] = M.us[buf][r][ch];
+            }
             o.B = load4(&M.bc[buf][0][r][4 * q]);
             if (!ENDS) o.C = load4(&M.bc[buf][1][r][4 * q]);
         };
@@ -366,17 +354,23 @@ __global__ void __launch_bounds__(Tile<S>::THREADS, S == 16 ? 2 : 1) forward_ker
             const Row &o = ahead[r % 2];
             if (r % kMark == 0 && mark && lo + k * R + r < hi) {
                 float *m = mark + (long long)(r / kMark) * P.C_ * S;
-                if (ch < nc) store4(m, h[0]);
-                if (ch + 1 < nc) store4(m + S, h[1]);
+#pragma unroll
+                for (int i = 0; i < CT; ++i)
+                    if (ch + i < nc) store4(m + i * S, h[i]);
             }
-            h[0] = fma4(decay4(a2[0], o.d.x), h[0], mul4(o.B, o.u.x));
-            h[1] = fma4(decay4(a2[1], o.d.y), h[1], mul4(o.B, o.u.y));
-            if (ENDS) sum[0] += o.d.x, sum[1] += o.d.y;
-            else *(float2 *)&M.ys[buf][q][r][ch] = make_float2(dot4(o.C, h[0]), dot4(o.C, h[1]));
+#pragma unroll
+            for (int i = 0; i < CT; ++i) {
+                h[i] = fma4(decay4(a2[i], o.d[i]), h[i], mul4(o.B, o.u[i]));
+                if (ENDS) sum[i] += o.d[i];
+            }
+            if constexpr (!ENDS) {
+                if constexpr (CT == 2) *(float2 *)&M.ys[buf][q][r][ch] = make_float2(dot4(o.C, h[0]), dot4(o.C, h[CT - 1]));
+                else M.ys[buf][q][r][ch] = dot4(o.C, h[0]);
+            }
         }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < CT; ++i) {
         if (ch + i >= nc) continue;
         const long long at = (long long)(c + i) * S + 4 * q;
         if (ENDS) {
@@ -762,19 +756,18 @@ template <typename T, int S> __global__ void __launch_bounds__(kThreads) step_ke
 }
 
 // ----------------------------------------------------------------------------------------------------------- host
-int forward_channels(int S) { return S == 8 ? Tile<8>::CH : S == 16 ? Tile<16>::CH : Tile<32>::CH; }
+constexpr int kForwardChannels = 64;
 int back_channels(int S) { return S == 8 ? Back<8>::CH : S == 16 ? Back<16>::CH : Back<32>::CH; }
 int blocks_per_group(int C, int G, int channels) { return (C / G + channels - 1) / channels; }
 
 // Rows of a part: all, where the sequences' channel blocks make a CTA for every other SM, else as many parts of a sequence
-// of the mean length as stand on the SMs at once (two CTAs on each, one where S is 8 or 32), of kLeastPart rows at least.
+// of the mean length as stand on the SMs at once (two CTAs on each), of kLeastPart rows at least.
 constexpr int kLeastPart = 128;
-static_assert(Tile<8>::CH == Back<8>::CH && Tile<16>::CH == Back<16>::CH && Tile<32>::CH == Back<32>::CH, "one rule for both");
 int part_rows(int T, int nseq, int C, int G, int S) {
-    const long long n = nseq > 0 ? nseq : 1, ctas = n * G * blocks_per_group(C, G, forward_channels(S));
+    const long long n = nseq > 0 ? nseq : 1, ctas = n * G * blocks_per_group(C, G, kForwardChannels);
     const long long whole = ((long long)T + kTile) / kTile * kTile;
     if (ctas >= kSMs / 2 || T / n < 2 * kLeastPart) return (int)whole;
-    long long want = (S == 16 ? 2 : 1) * kSMs / ctas;
+    long long want = 2 * kSMs / ctas;
     if (want > kMaxParts) want = kMaxParts;
     long long part = ((T + n * want - 1) / (n * want) + kTile - 1) / kTile * kTile;
     if (part < kLeastPart) part = kLeastPart;
@@ -876,27 +869,32 @@ int take_inputs(Call &K, const void *X, const void *dt, const float *A, const vo
     return LA_OK;
 }
 
-template <typename T, int S> cudaError_t forward(const Params &P, long long units, bool split, cudaStream_t s) {
-    using K = Tile<S>;
+template <typename T, int S, int CT> cudaError_t launch_forward(const Params &P, long long blocks, bool split, cudaStream_t s) {
+    using K = Tile<T, S, CT>;
     constexpr int all = (int)sizeof(typename K::Smem), some = (int)offsetof(typename K::Smem, ys);
     static std::atomic<int> attr_state[kMaxDevices];
     if (!once_per_device(attr_state, [] {
-            return cudaFuncSetAttribute(forward_kernel<T, S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, some) == cudaSuccess &&
-                   cudaFuncSetAttribute(forward_kernel<T, S, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, all) == cudaSuccess;
+            return cudaFuncSetAttribute(forward_kernel<T, S, CT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, some) == cudaSuccess &&
+                   cudaFuncSetAttribute(forward_kernel<T, S, CT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, all) == cudaSuccess;
         }))
         return cudaErrorInvalidValue;
-    const long long blocks = units * P.G * P.bpg;
-    if (blocks >= (1LL << 31)) return cudaErrorInvalidConfiguration;
     if (split) {
-        forward_kernel<T, S, true><<<(unsigned)blocks, K::THREADS, some, s>>>(P);
+        forward_kernel<T, S, CT, true><<<(unsigned)blocks, K::THREADS, some, s>>>(P);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         count_launches(1);
     }
-    forward_kernel<T, S, false><<<(unsigned)blocks, K::THREADS, all, s>>>(P);
+    forward_kernel<T, S, CT, false><<<(unsigned)blocks, K::THREADS, all, s>>>(P);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) count_launches(1);
     return e;
+}
+// One channel to a scanning thread where each SM has one CTA at most, whose warps then are too few; else two.
+template <typename T, int S> cudaError_t forward(const Params &P, long long units, bool split, cudaStream_t s) {
+    const long long blocks = units * P.G * P.bpg;
+    if (blocks >= (1LL << 31)) return cudaErrorInvalidConfiguration;
+    if (S <= 16 && blocks <= kSMs) return launch_forward<T, S, S <= 16 ? 1 : 2>(P, blocks, split, s);
+    return launch_forward<T, S, 2>(P, blocks, split, s);
 }
 template <typename T> cudaError_t forward(const Params &P, int S, long long units, bool split, cudaStream_t s) {
     return S == 8 ? forward<T, 8>(P, units, split, s) : S == 16 ? forward<T, 16>(P, units, split, s) : forward<T, 32>(P, units, split, s);
@@ -992,7 +990,7 @@ int la_selective_scan(const void *X, const void *dt, const float *A, const void 
     if (nseq == 0) return LA_OK;
     Params &P = K.P;
     P.last = state_out, P.marks = marks;
-    P.bpg = blocks_per_group(channels, G, forward_channels(S));
+    P.bpg = blocks_per_group(channels, G, kForwardChannels);
     P.seq.status = (uint32_t *)workspace;
     P.part = part_rows(T, nseq, channels, G, S);
     const long long units = units_of(T, nseq, N, P.part, packed);
