@@ -389,12 +389,14 @@ __global__ void __launch_bounds__(Tile<T, S, CT>::THREADS, Tile<T, S, CT>::PER_S
 // summed over the warp's 64 channels, in the thread and then by butterflies of shuffles that hand each lane a value of its
 // own (8 values over 8 lanes, then four rows of them over the four groups of lanes), and over the channel blocks by a launch
 // of its own.  Bound by shared memory and issue slots alike: some 190 clocks of an SM for a row of 64 channels.
-template <int S> struct Back {
+template <typename T, int S> struct Back {
     static constexpr int R = kMark, QW = S / 4, GW = QW > 4 ? 1 : 4 / QW, CH = 64 * GW;
     static constexpr int HELP = R * CH / 4, SCAN = 32 * QW * GW, THREADS = HELP + SCAN;  // a vector of four channels to a helper
-    static constexpr int NB = (2 * R * S / 4 + HELP - 1) / HELP;
+    static constexpr int STAGES = 4;  // tiles on their way, or read for d and g, or for the gradients of rows
     static constexpr int FLUSH = 8;  // tiles between additions to dA's sums, which so pass fewer roundings
     struct Smem {
+        T in[STAGES][4][R][CH];                          // x, dt, dO, z
+        T bc_in[STAGES][2][R][S];
         float ds[3][R][CH], us[2][R][CH], gs[2][R][CH];  // d, d x, g
         float bc[2][2][R][S];
         float ys[2][QW][R][CH], ws[2][QW][R][CH], es[2][QW][R][CH];
@@ -405,9 +407,9 @@ template <int S> struct Back {
 // ENDS: where time is cut into parts, a first launch, which forms what leaves each part's first row (from zero behind its
 // last, the last part from dstate_out) and the sum of its d.
 template <typename T, int S, bool ENDS>
-__global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_kernel(const __grid_constant__ Params P) {
-    using K = Back<S>;
-    constexpr int CH = K::CH, R = K::R, NB = K::NB, QW = K::QW, HELP = K::HELP;
+__global__ void __launch_bounds__(Back<T, S>::THREADS, S == 16 ? 2 : 1) backward_kernel(const __grid_constant__ Params P) {
+    using K = Back<T, S>;
+    constexpr int CH = K::CH, R = K::R, QW = K::QW, HELP = K::HELP, ST = K::STAGES;
     extern __shared__ __align__(16) unsigned char raw[];
     typename K::Smem &M = *(typename K::Smem *)raw;
     const int cblocks = P.G * P.bpg, walker = blockIdx.x / cblocks, cb = blockIdx.x - walker * cblocks;
@@ -428,76 +430,74 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
             D[e] = P.D && e < n ? P.D[c0 + col + e] : 0.f;
             dD[e] = dbias[e] = 0.f;
         }
-        struct Four {
-            Vec<T, 4> x, d, o, z;
-        } in, out;  // on their way to d and g; to the gradients of rows
-        Vec<T, 4> vb[NB];
         for (int unit = walker; unit < P.units && fine; unit += P.walkers) {
             int seq, j, first, all;
             unit_at(P, unit, seq, j, first, all);
             const long long t0 = (long long)j * P.part;
             if (seq < 0 || (j > 0 && t0 >= all) || (ENDS && j == 0)) continue;
             const int lo = (int)t0, len = (int)min(t0 + P.part, (long long)all);  // rows lo ... len - 1
-            const T *x = rows_of<const T>(P.seq, P.x, seq) + c0 + col, *dt = rows_of<const T>(P.seq, P.dt, seq) + c0 + col;
-            const T *z = P.z.p ? rows_of<const T>(P.seq, P.z, seq) + c0 + col : nullptr;
-            const T *dO = rows_of<const T>(P.seq, P.dO, seq) + c0 + col;
+            const T *x = rows_of<const T>(P.seq, P.x, seq) + c0, *dt = rows_of<const T>(P.seq, P.dt, seq) + c0;
+            const T *z = P.z.p ? rows_of<const T>(P.seq, P.z, seq) + c0 : nullptr, *dO = rows_of<const T>(P.seq, P.dO, seq) + c0;
             T *dx = rows_of<T>(P.seq, P.dx, seq) + c0 + col, *ddt = rows_of<T>(P.seq, P.ddt, seq) + c0 + col;
             T *dz = z ? rows_of<T>(P.seq, P.dz, seq) + c0 + col : nullptr;
             const T *Bp = (const T *)P.B.p + (P.seq.off ? first * P.B.sn : seq * P.B.sb) + g * P.B.sg;
             const T *Cp = (const T *)P.C.p + (P.seq.off ? first * P.C.sn : seq * P.C.sb) + g * P.C.sg;
             const int tiles = (len - lo + R - 1) / R;
-            auto fetch = [&](int k, Four &f) {
-                const int r = lo + k * R + row;
-                const bool on = k >= 0 && r < len && n >= 4;
-                if (!ENDS) load_ahead(f.x, x + r * P.x.sn, on);
-                load_ahead(f.d, dt + r * P.dt.sn, on);
-                load_ahead(f.o, dO + r * P.dO.sn, on);
-                load_ahead(f.z, z + r * P.z.sn, on && z);
-            };
-            auto rest = [&](int k, Four &f) {  // the last channels, where they are no whole vector
-                const int r = lo + k * R + row;
-                if (r >= len || n <= 0 || n >= 4) return;
-                f.x = load_vec<T, 4>(x + r * P.x.sn, n);
-                f.d = load_vec<T, 4>(dt + r * P.dt.sn, n);
-                f.o = load_vec<T, 4>(dO + r * P.dO.sn, n);
-                if (z) f.z = load_vec<T, 4>(z + r * P.z.sn, n);
-            };
-            auto fetch_bc = [&](int k) {
+            // as in the forward: 16 bytes a copy, zeros where there is no row or channel
+            auto copy = [&](int k) {
+                constexpr int E = 16 / (int)sizeof(T), VR = CH / E, VS = S / E, ROWS = R * VR, ALL = 4 * ROWS + 2 * R * VS;
+                if (k >= 0) {
+                    const int t = lo + k * R, st = k % ST;
 #pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    const int v = i * HELP + helper, which = v / (R * S / 4), r = lo + k * R + v % (R * S / 4) / (S / 4), s = v % (S / 4) * 4;
-                    load_ahead(vb[i], (which ? Cp + r * P.C.sn : Bp + r * P.B.sn) + s, which < 2 && (which || !ENDS) && k >= 0 && r < len);
+                    for (int i = 0; i < (ALL + HELP - 1) / HELP; ++i) {
+                        const int v = i * HELP + helper;
+                        if (v < 4 * ROWS) {
+                            const int op = v / ROWS, r = v % ROWS / VR, e = v % VR * E;
+                            const T *p = op == 0 ? x : op == 1 ? dt : op == 2 ? dO : z;
+                            const long long sn = op == 0 ? P.x.sn : op == 1 ? P.dt.sn : op == 2 ? P.dO.sn : P.z.sn;
+                            if ((op == 3 && !z) || (op == 0 && ENDS)) continue;
+                            const int have = t + r < len ? max(0, min(16, (nc - e) * (int)sizeof(T))) : 0;
+                            copy16(&M.in[st][op][r][e], have ? p + (t + r) * sn + e : p, have);
+                        } else if (v < ALL) {
+                            const int w = v - 4 * ROWS, op = w / (R * VS), r = w % (R * VS) / VS, e = w % VS * E;
+                            if (op == 0 && ENDS) continue;
+                            const bool have = t + r < len;
+                            const T *p = op ? Cp : Bp;
+                            copy16(&M.bc_in[st][op][r][e], have ? p + (t + r) * (op ? P.C.sn : P.B.sn) + e : p, have ? 16 : 0);
+                        }
+                    }
                 }
+                copy_commit();
             };
             auto produce = [&](int k) {
-                rest(k, in);
-                const bool live = lo + k * R + row < len;
-                float d[4], u[4], gr[4];
+                const int t = lo + k * R, st = k % ST;
+                auto at = [&](int op) { return *(const Vec<T, 4> *)&M.in[st][op][row][col]; };
+                const Vec<T, 4> vx = at(0), vd = at(1), vo = at(2), vz = at(3);
+                const float2 a = step_of(P, make_float2(to_f(vd.e[0]) + bias[0], to_f(vd.e[1]) + bias[1]));
+                const float2 b = step_of(P, make_float2(to_f(vd.e[2]) + bias[2], to_f(vd.e[3]) + bias[3]));
+                float d[4] = {a.x, a.y, b.x, b.y}, gr[4];
+                if (!(nc == CH && t + R <= len))  // no row or channel: nothing happens (what was copied there is zero)
 #pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const float2 v = step_of(P, make_float2(to_f(in.d.e[e]) + bias[e], to_f(in.d.e[e + 1]) + bias[e + 1]));
-                    d[e] = v.x, d[e + 1] = v.y;
-                }
+                    for (int e = 0; e < 4; ++e)
+                        if (t + row >= len || e >= n) d[e] = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    u[e] = ENDS ? 0.f : d[e] * to_f(in.x.e[e]);
-                    gr[e] = to_f(in.o.e[e]);
+                    gr[e] = to_f(vo.e[e]);
                     if (z) {
-                        const float ze = to_f(in.z.e[e]);
+                        const float ze = to_f(vz.e[e]);
                         gr[e] *= ze * sigmoid(ze);
                     }
-                    if (!live || e >= n) d[e] = u[e] = gr[e] = 0.f;  // no row: nothing happens
                 }
                 *(float4 *)&M.ds[k % 3][row][col] = make_float4(d[0], d[1], d[2], d[3]);
-                if (!ENDS) *(float4 *)&M.us[k & 1][row][col] = make_float4(u[0], u[1], u[2], u[3]);
                 *(float4 *)&M.gs[k & 1][row][col] = make_float4(gr[0], gr[1], gr[2], gr[3]);
+                if (!ENDS) *(float4 *)&M.us[k & 1][row][col] = make_float4(d[0] * to_f(vx.e[0]), d[1] * to_f(vx.e[1]), d[2] * to_f(vx.e[2]), d[3] * to_f(vx.e[3]));
+                constexpr int NB = 2 * R * S / 4;
 #pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    const int v = i * HELP + helper, which = v / (R * S / 4), r = v % (R * S / 4) / (S / 4), s = v % (S / 4) * 4;
-                    if (which >= 2) continue;
-                    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (lo + k * R + r < len) f = make_float4(to_f(vb[i].e[0]), to_f(vb[i].e[1]), to_f(vb[i].e[2]), to_f(vb[i].e[3]));
-                    *(float4 *)&M.bc[k & 1][which][r][s] = f;
+                for (int i = 0; i < (NB + HELP - 1) / HELP; ++i) {
+                    const int v = i * HELP + helper;
+                    if (NB % HELP != 0 && v >= NB) break;
+                    const Vec<T, 4> f = ((const Vec<T, 4> *)M.bc_in[st])[v];
+                    ((float4 *)M.bc[k & 1])[v] = make_float4(to_f(f.e[0]), to_f(f.e[1]), to_f(f.e[2]), to_f(f.e[3]));
                 }
             };
             auto total = [&](const float (&parts)[QW][R][CH], float (&s)[4]) {
@@ -510,9 +510,10 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
                 s[0] = a.x, s[1] = a.y, s[2] = a.z, s[3] = a.w;
             };
             auto finish = [&](int k) {
-                rest(k, out);
-                const int r = lo + k * R + row;
+                const int r = lo + k * R + row, st = k % ST;
                 if (r >= len || n <= 0) return;
+                auto in = [&](int op) { return *(const Vec<T, 4> *)&M.in[st][op][row][col]; };
+                const Vec<T, 4> vx = in(0), vd = in(1), vo = in(2), vz = in(3);
                 float w[4], es[4], ys[4];
                 total(M.ws[k & 1], w), total(M.es[k & 1], es);
                 if (z) total(M.ys[k & 1], ys);
@@ -521,16 +522,16 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
                 Vec<T, 4> ox, od, oz;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float xe = to_f(out.x.e[e]), oe = to_f(out.o.e[e]);
+                    const float xe = to_f(vx.e[e]), oe = to_f(vo.e[e]);
                     float gr = oe;
                     if (z) {
-                        const float ze = to_f(out.z.e[e]), sg = sigmoid(ze);
+                        const float ze = to_f(vz.e[e]), sg = sigmoid(ze);
                         gr *= ze * sg;
                         put(&oz.e[e], oe * fmaf(D[e], xe, ys[e]) * silu_grad(ze, sg));
                     }
                     put(&ox.e[e], fmaf(d[e], w[e], D[e] * gr));
                     float s = fmaf(es[e], kLn2, xe * w[e]);
-                    if (P.softplus) s *= sigmoid(to_f(out.d.e[e]) + bias[e]);
+                    if (P.softplus) s *= sigmoid(to_f(vd.e[e]) + bias[e]);
                     put(&od.e[e], s);
                     dbias[e] += s;
                     dD[e] = fmaf(gr, xe, dD[e]);
@@ -539,17 +540,19 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
                 store_vec<T, 4>(ddt + r * P.ddt.sn, od, n);
                 if (z) store_vec<T, 4>(dz + r * P.dz.sn, oz, n);
             };
-            fetch(tiles - 1, in), fetch_bc(tiles - 1);
+            copy(tiles - 1), copy(tiles - 2);
+            copy_wait<1>();
+            __syncthreads();
             if (tiles > 0) produce(tiles - 1);
-            fetch(tiles - 2, in), fetch_bc(tiles - 2);
-            // while tile k is walked: d and g of tile k - 1, the gradients of tile k + 1
+            copy_wait<0>();
+            // while tile k is walked: d and g of tile k - 1, the gradients of tile k + 1, and tile k - 2 on its way into the place
+            // of tile k + 2
             for (int k = tiles - 1; k >= -1; --k) {
                 __syncthreads();
                 if (k > 0) produce(k - 1);
-                fetch(k - 2, in), fetch_bc(k - 2);
-                if (ENDS) continue;
-                if (k + 1 < tiles) finish(k + 1);
-                fetch(k, out);
+                copy(k - 2);
+                if (!ENDS && k + 1 < tiles) finish(k + 1);
+                copy_wait<0>();
             }
             __syncthreads();  // the last tile's shared memory has been read
         }
@@ -613,6 +616,7 @@ __global__ void __launch_bounds__(Back<S>::THREADS, S == 16 ? 2 : 1) backward_ke
             load_ahead(mark[1], m + S, k >= 0 && ch + 1 < nc);
         };
         fetch(tiles - 1);
+        __syncthreads();
         // sums of dB (values 0 ... 3) and dC (4 ... 7) of the warp's states: a lane's value of a row of four
         float *pbc = P.pbc + ((long long)((cb - g * P.bpg) * K::GW + group) * P.seq.T + first) * P.G * 2 * S + g * 2 * S +
                      (lane & 4 ? S : 0) + 4 * q + (lane & 3);
@@ -714,7 +718,7 @@ template <typename T, int S> __global__ void __launch_bounds__(256) sum_bc_kerne
     if (P.seq.off && (row < P.seq.off[0] || row >= P.seq.off[P.seq.nseq])) return;
     float s = 0.f;
 #pragma unroll 4
-    for (int b = 0; b < P.bpg * Back<S>::GW; ++b) s += P.pbc[(long long)b * P.seq.T * row_w + i];
+    for (int b = 0; b < P.bpg * Back<T, S>::GW; ++b) s += P.pbc[(long long)b * P.seq.T * row_w + i];
     const int g = at / (2 * S), n = at % (2 * S);
     put((n < S ? dB : dC) + (row * P.G + g) * S + n % S, s);
 }
@@ -757,7 +761,7 @@ template <typename T, int S> __global__ void __launch_bounds__(kThreads) step_ke
 
 // ----------------------------------------------------------------------------------------------------------- host
 constexpr int kForwardChannels = 64;
-int back_channels(int S) { return S == 8 ? Back<8>::CH : S == 16 ? Back<16>::CH : Back<32>::CH; }
+int back_channels(int S) { return S == 8 ? Back<float, 8>::CH : S == 16 ? Back<float, 16>::CH : Back<float, 32>::CH; }
 int blocks_per_group(int C, int G, int channels) { return (C / G + channels - 1) / channels; }
 
 // Rows of a part: all, where the sequences' channel blocks make a CTA for every other SM, else as many parts of a sequence
@@ -901,7 +905,7 @@ template <typename T> cudaError_t forward(const Params &P, int S, long long unit
 }
 
 template <typename T, int S> cudaError_t backward(const Params &P, bool split, void *dB, void *dC, float *dA, float *dD, float *dbias, cudaStream_t s) {
-    using M = typename Back<S>::Smem;
+    using M = typename Back<T, S>::Smem;
     static std::atomic<int> attr_state[kMaxDevices];
     if (!once_per_device(attr_state, [] {
             return cudaFuncSetAttribute(backward_kernel<T, S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(M)) == cudaSuccess &&
@@ -912,11 +916,11 @@ template <typename T, int S> cudaError_t backward(const Params &P, bool split, v
     if (blocks > 0) {
         cudaError_t e;
         if (split) {
-            backward_kernel<T, S, true><<<(unsigned)blocks, Back<S>::THREADS, sizeof(M), s>>>(P);
+            backward_kernel<T, S, true><<<(unsigned)blocks, Back<T, S>::THREADS, sizeof(M), s>>>(P);
             if ((e = cudaGetLastError()) != cudaSuccess) return e;
             count_launches(1);
         }
-        backward_kernel<T, S, false><<<(unsigned)blocks, Back<S>::THREADS, sizeof(M), s>>>(P);
+        backward_kernel<T, S, false><<<(unsigned)blocks, Back<T, S>::THREADS, sizeof(M), s>>>(P);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         count_launches(1);
         const long long sums = ((long long)P.seq.T * P.G * 2 * S + 255) / 256;
