@@ -70,7 +70,7 @@ template <typename T> __device__ __forceinline__ void widen(float2 (&to)[kV / 2]
 template <typename T> __device__ __forceinline__ Vec<T, kV> narrow(const float2 (&x)[kV / 2]) {
     Vec<T, kV> r;
 #pragma unroll
-    for (int k = 0; k < kV / 2; ++k) put(&r.e[2 * k], x[k].x), put(&r.e[2 * k + 1], x[k].y);
+    for (int k = 0; k < kV / 2; ++k) put2(r.e + 2 * k, x[k].x, x[k].y);
     return r;
 }
 __device__ __forceinline__ float2 sigmoid2(float2 p) { return make_float2(sigmoid(p.x), sigmoid(p.y)); }

@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(Shape<T, TPR, NV>::THREADS, per_sm<TPR>()) for
                     if (n <= 0) continue;
                     Vec<T, V> o;
 #pragma unroll
-                    for (int k = 0; k < V; ++k) put(&o.e[k], r[j][i][k]);
+                    for (int k = 0; k < V; k += 2) put2(o.e + k, r[j][i][k], r[j][i][k + 1]);
                     store_vec<T, V>(row_of<T>(P.r, first + j, P.N) + c, o, n);
                 }
         combine<TPR, S::THREADS, R, false>(ss, sm);
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(Shape<T, TPR, NV>::THREADS, per_sm<TPR>()) for
                     if (n <= 0) continue;
                     Vec<T, V> o;
 #pragma unroll
-                    for (int k = 0; k < V; ++k) put(&o.e[k], r[j][i][k]);
+                    for (int k = 0; k < V; k += 2) put2(o.e + k, r[j][i][k], r[j][i][k + 1]);
                     store_vec<T, V>(row_of<T>(P.y, first + j, P.N) + c, o, n);
                 } else {
                     float a = top[j];

@@ -67,6 +67,16 @@ template <typename T, int V> __device__ __forceinline__ void store_vec(T *p, con
         if (k < n) p[k] = x.e[k];
 }
 
+// Two values rounded together, four to a vector.
+__device__ __forceinline__ void put2(float *p, float x, float y) { p[0] = x, p[1] = y; }
+__device__ __forceinline__ void put2(__nv_bfloat16 *p, float x, float y) { *(__nv_bfloat162 *)p = __floats2bfloat162_rn(x, y); }
+template <typename T> __device__ __forceinline__ Vec<T, 4> rounded4(const float (&x)[4]) {
+    Vec<T, 4> r;
+    put2(r.e, x[0], x[1]);
+    put2(r.e + 2, x[2], x[3]);
+    return r;
+}
+
 // e^x by the hardware's 2^x: within 2 ulp, and half a step of the product x log2 e, which is |x| half steps of the result.
 __device__ __forceinline__ float exp_fast(float x) {
     float y;

@@ -274,18 +274,16 @@ __global__ void __launch_bounds__(Tile<T, S, CT>::THREADS, Tile<T, S, CT>::PER_S
                 const float4 o = *(const float4 *)&M.ys[buf][w][row][col];
                 s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
             }
-            const float v[4] = {s.x, s.y, s.z, s.w};
-            Vec<T, 4> out;
+            float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float f = fmaf(D[e], to_f(vx.e[e]), v[e]);
+                v[e] = fmaf(D[e], to_f(vx.e[e]), v[e]);
                 if (z) {
                     const float ze = to_f(vz.e[e]);
-                    f *= ze * sigmoid(ze);
+                    v[e] *= ze * sigmoid(ze);
                 }
-                put(&out.e[e], f);
             }
-            if (t + row < hi && n > 0) store_vec<T, 4>(y + (t + row) * P.y.sn + col, out, n);
+            if (t + row < hi && n > 0) store_vec<T, 4>(y + (t + row) * P.y.sn + col, rounded4<T>(v), n);
         };
         copy(0), copy(1), copy(2);
         copy_wait<2>();
@@ -519,7 +517,7 @@ __global__ void __launch_bounds__(Back<T, S>::THREADS, S == 16 ? 2 : 1) backward
                 if (z) total(M.ys[k & 1], ys);
                 const float4 d4 = *(const float4 *)&M.ds[k % 3][row][col];
                 const float d[4] = {d4.x, d4.y, d4.z, d4.w};
-                Vec<T, 4> ox, od, oz;
+                float fx[4], fd[4], fz[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float xe = to_f(vx.e[e]), oe = to_f(vo.e[e]);
@@ -527,18 +525,18 @@ __global__ void __launch_bounds__(Back<T, S>::THREADS, S == 16 ? 2 : 1) backward
                     if (z) {
                         const float ze = to_f(vz.e[e]), sg = sigmoid(ze);
                         gr *= ze * sg;
-                        put(&oz.e[e], oe * fmaf(D[e], xe, ys[e]) * silu_grad(ze, sg));
+                        fz[e] = oe * fmaf(D[e], xe, ys[e]) * silu_grad(ze, sg);
                     }
-                    put(&ox.e[e], fmaf(d[e], w[e], D[e] * gr));
+                    fx[e] = fmaf(d[e], w[e], D[e] * gr);
                     float s = fmaf(es[e], kLn2, xe * w[e]);
                     if (P.softplus) s *= sigmoid(to_f(vd.e[e]) + bias[e]);
-                    put(&od.e[e], s);
+                    fd[e] = s;
                     dbias[e] += s;
                     dD[e] = fmaf(gr, xe, dD[e]);
                 }
-                store_vec<T, 4>(dx + r * P.dx.sn, ox, n);
-                store_vec<T, 4>(ddt + r * P.ddt.sn, od, n);
-                if (z) store_vec<T, 4>(dz + r * P.dz.sn, oz, n);
+                store_vec<T, 4>(dx + r * P.dx.sn, rounded4<T>(fx), n);
+                store_vec<T, 4>(ddt + r * P.ddt.sn, rounded4<T>(fd), n);
+                if (z) store_vec<T, 4>(dz + r * P.dz.sn, rounded4<T>(fz), n);
             };
             copy(tiles - 1), copy(tiles - 2);
             copy_wait<1>();
@@ -733,28 +731,41 @@ template <typename T, int S> __global__ void __launch_bounds__(kThreads) step_ke
     const F4 a2 = mul4(load4(P.A + (long long)cc * S + 4 * q), kLog2e);
     const float bias = P.bias ? P.bias[cc] : 0.f, D = P.D ? P.D[cc] : 0.f;
     const int b1 = min((int)(blockIdx.y + 1) * per, P.seq.nseq);
-#pragma unroll 4
-    for (int b = blockIdx.y * per; b < b1; ++b) {
-        float *st = P.last + ((long long)b * P.C_ + cc) * S + 4 * q;
-        const F4 h0 = load4(st);
-        const float x = to_f(((const T *)P.x.p)[b * P.x.sb + cc]);
-        const float d = step_of(P, both(to_f(((const T *)P.dt.p)[b * P.dt.sb + cc]) + bias)).x;
-        const Vec<T, 4> vb = *(const Vec<T, 4> *)((const T *)P.B.p + b * P.B.sb + g * P.B.sg + 4 * q);
-        const Vec<T, 4> vc = *(const Vec<T, 4> *)((const T *)P.C.p + b * P.C.sb + g * P.C.sg + 4 * q);
-        const F4 B{make_float2(to_f(vb.e[0]), to_f(vb.e[1])), make_float2(to_f(vb.e[2]), to_f(vb.e[3]))};
-        const F4 C{make_float2(to_f(vc.e[0]), to_f(vc.e[1])), make_float2(to_f(vc.e[2]), to_f(vc.e[3]))};
-        const F4 h = fma4(decay4(a2, d), h0, mul4(B, d * x));
-        if (mine) store4(st, h);
-        float y = dot4(C, h);
+    constexpr int U = 4;  // sequences whose states are on their way together
+    for (int b0 = blockIdx.y * per; b0 < b1; b0 += U) {
+        Vec<float, 4> h0[U];
+        Vec<T, 4> vb[U], vc[U];
+        T x[U], dt[U], z[U];
 #pragma unroll
-        for (int k = L / 2; k > 0; k /= 2) y += __shfl_xor_sync(0xffffffffu, y, k);
-        if (q == 0 && mine) {
-            y = fmaf(D, x, y);
-            if (P.z.p) {
-                const float z = to_f(((const T *)P.z.p)[b * P.z.sb + cc]);
-                y *= z * sigmoid(z);
+        for (int i = 0; i < U; ++i) {
+            const long long b = min(b0 + i, b1 - 1);
+            h0[i] = *(const Vec<float, 4> *)(P.last + (b * P.C_ + cc) * S + 4 * q);
+            vb[i] = *(const Vec<T, 4> *)((const T *)P.B.p + b * P.B.sb + g * P.B.sg + 4 * q);
+            vc[i] = *(const Vec<T, 4> *)((const T *)P.C.p + b * P.C.sb + g * P.C.sg + 4 * q);
+            x[i] = ((const T *)P.x.p)[b * P.x.sb + cc];
+            dt[i] = ((const T *)P.dt.p)[b * P.dt.sb + cc];
+            if (P.z.p) z[i] = ((const T *)P.z.p)[b * P.z.sb + cc];
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (b0 + i >= b1) break;  // the same for the block
+            const long long b = b0 + i;
+            const float xv = to_f(x[i]), d = step_of(P, both(to_f(dt[i]) + bias)).x;
+            const F4 B{make_float2(to_f(vb[i].e[0]), to_f(vb[i].e[1])), make_float2(to_f(vb[i].e[2]), to_f(vb[i].e[3]))};
+            const F4 C{make_float2(to_f(vc[i].e[0]), to_f(vc[i].e[1])), make_float2(to_f(vc[i].e[2]), to_f(vc[i].e[3]))};
+            const F4 h = fma4(decay4(a2, d), F4{make_float2(h0[i].e[0], h0[i].e[1]), make_float2(h0[i].e[2], h0[i].e[3])}, mul4(B, d * xv));
+            if (mine) store4(P.last + (b * P.C_ + cc) * S + 4 * q, h);
+            float y = dot4(C, h);
+#pragma unroll
+            for (int k = L / 2; k > 0; k /= 2) y += __shfl_xor_sync(0xffffffffu, y, k);
+            if (q == 0 && mine) {
+                y = fmaf(D, xv, y);
+                if (P.z.p) {
+                    const float zv = to_f(z[i]);
+                    y *= zv * sigmoid(zv);
+                }
+                put((T *)P.y.p + b * P.y.sb + cc, y);
             }
-            put((T *)P.y.p + b * P.y.sb + cc, y);
         }
     }
 }
