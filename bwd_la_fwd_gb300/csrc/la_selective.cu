@@ -121,10 +121,20 @@ template <int L, int STEP> __device__ __forceinline__ float lanes_sum(float (&v)
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-// 16 bytes global -> shared; bytes past `n` are zero.
-__device__ __forceinline__ void copy16(void *dst, const void *src, int n) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n) : "memory");
-}
+// A thread's share of a tile's copies: 16 bytes of a row, `bytes` of them there (the others zero), or none (-1).
+template <typename T> struct Copy {
+    const T *src;         // of tile 0
+    long long step;       // elements to the next tile
+    uint32_t dst;         // of stage 0
+    int stage, row, bytes;
+    // `live`: the tile has the row; else zeros, and nothing is read
+    __device__ __forceinline__ void issue(int tile, int st, bool live) const {
+        if (bytes < 0) return;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + st * stage), "l"(src + (live ? tile * step : 0)),
+                     "r"(live ? bytes : 0)
+                     : "memory");
+    }
+};
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
@@ -218,27 +228,27 @@ __global__ void __launch_bounds__(Tile<T, S, CT>::THREADS, Tile<T, S, CT>::PER_S
             D[k] = P.D && k < n ? P.D[c0 + col + k] : 0.f;
         }
         // x, dt, z, B and C of a tile, 16 bytes a copy, zeros where there is no row or channel
-        auto copy = [&](int k) {
-            constexpr int E = 16 / (int)sizeof(T), VR = CH / E, VS = S / E, ROWS = R * VR, ALL = 3 * ROWS + 2 * R * VS;
-            const int t = lo + k * R, st = k % ST;
+        constexpr int E = 16 / (int)sizeof(T), VR = CH / E, VS = S / E, ROWS = R * VR, ALL = 3 * ROWS + 2 * R * VS;
+        Copy<T> mine[(ALL + HELP - 1) / HELP];
 #pragma unroll
-            for (int i = 0; i < (ALL + HELP - 1) / HELP; ++i) {
-                const int v = i * HELP + helper;
-                if (v < 3 * ROWS) {
-                    const int op = v / ROWS, r = v % ROWS / VR, e = v % VR * E;
-                    const T *p = op == 0 ? x : op == 1 ? dt : z;
-                    const long long sn = op == 0 ? P.x.sn : op == 1 ? P.dt.sn : P.z.sn;
-                    if (op == 2 && (ENDS || !z)) continue;
-                    const int have = t + r < hi ? max(0, min(16, (nc - e) * (int)sizeof(T))) : 0;
-                    copy16(&M.in[st][op][r][e], have ? p + (t + r) * sn + e : p, have);
-                } else if (v < ALL) {
-                    const int w = v - 3 * ROWS, op = w / (R * VS), r = w % (R * VS) / VS, e = w % VS * E;
-                    if (op == 1 && ENDS) continue;
-                    const bool have = t + r < hi;
-                    const T *p = op ? Cp : Bp;
-                    copy16(&M.bc_in[st][op][r][e], have ? p + (t + r) * (op ? P.C.sn : P.B.sn) + e : p, have ? 16 : 0);
-                }
+        for (int i = 0; i < (ALL + HELP - 1) / HELP; ++i) {
+            const int v = i * HELP + helper;
+            if (v < 3 * ROWS) {
+                const int op = v / ROWS, r = v % ROWS / VR, e = v % VR * E;
+                const T *p = op == 0 ? x : op == 1 ? dt : z;
+                const long long sn = op == 0 ? P.x.sn : op == 1 ? P.dt.sn : P.z.sn;
+                mine[i] = Copy<T>{p + (lo + r) * sn + e, R * sn, smem_addr(&M.in[0][op][r][e]), (int)sizeof(M.in[0]), r,
+                                  op == 2 && (ENDS || !z) ? -1 : max(0, min(16, (nc - e) * (int)sizeof(T)))};
+            } else {
+                const int w = v - 3 * ROWS, op = w / (R * VS) & 1, r = w % (R * VS) / VS, e = w % VS * E;
+                const long long sn = op ? P.C.sn : P.B.sn;
+                mine[i] = Copy<T>{(op ? Cp : Bp) + (lo + r) * sn + e, R * sn, smem_addr(&M.bc_in[0][op][r][e]), (int)sizeof(M.bc_in[0]), r,
+                                  v < ALL && !(op && ENDS) ? 16 : -1};
             }
+        }
+        auto copy = [&](int k) {
+#pragma unroll
+            for (int i = 0; i < (ALL + HELP - 1) / HELP; ++i) mine[i].issue(k, k % ST, lo + k * R < hi - mine[i].row);
             copy_commit();
         };
         const bool whole = nc == CH;
@@ -441,30 +451,30 @@ __global__ void __launch_bounds__(Back<T, S>::THREADS, S == 16 ? 2 : 1) backward
             const T *Bp = (const T *)P.B.p + (P.seq.off ? first * P.B.sn : seq * P.B.sb) + g * P.B.sg;
             const T *Cp = (const T *)P.C.p + (P.seq.off ? first * P.C.sn : seq * P.C.sb) + g * P.C.sg;
             const int tiles = (len - lo + R - 1) / R;
-            // as in the forward: 16 bytes a copy, zeros where there is no row or channel
-            auto copy = [&](int k) {
-                constexpr int E = 16 / (int)sizeof(T), VR = CH / E, VS = S / E, ROWS = R * VR, ALL = 4 * ROWS + 2 * R * VS;
-                if (k >= 0) {
-                    const int t = lo + k * R, st = k % ST;
+            // x, dt, dO, z, B and C of a tile, 16 bytes a copy, zeros where there is no row or channel
+            constexpr int E = 16 / (int)sizeof(T), VR = CH / E, VS = S / E, ROWS = R * VR, ALL = 4 * ROWS + 2 * R * VS;
+            Copy<T> mine[(ALL + HELP - 1) / HELP];
 #pragma unroll
-                    for (int i = 0; i < (ALL + HELP - 1) / HELP; ++i) {
-                        const int v = i * HELP + helper;
-                        if (v < 4 * ROWS) {
-                            const int op = v / ROWS, r = v % ROWS / VR, e = v % VR * E;
-                            const T *p = op == 0 ? x : op == 1 ? dt : op == 2 ? dO : z;
-                            const long long sn = op == 0 ? P.x.sn : op == 1 ? P.dt.sn : op == 2 ? P.dO.sn : P.z.sn;
-                            if ((op == 3 && !z) || (op == 0 && ENDS)) continue;
-                            const int have = t + r < len ? max(0, min(16, (nc - e) * (int)sizeof(T))) : 0;
-                            copy16(&M.in[st][op][r][e], have ? p + (t + r) * sn + e : p, have);
-                        } else if (v < ALL) {
-                            const int w = v - 4 * ROWS, op = w / (R * VS), r = w % (R * VS) / VS, e = w % VS * E;
-                            if (op == 0 && ENDS) continue;
-                            const bool have = t + r < len;
-                            const T *p = op ? Cp : Bp;
-                            copy16(&M.bc_in[st][op][r][e], have ? p + (t + r) * (op ? P.C.sn : P.B.sn) + e : p, have ? 16 : 0);
-                        }
-                    }
+            for (int i = 0; i < (ALL + HELP - 1) / HELP; ++i) {
+                const int v = i * HELP + helper;
+                if (v < 4 * ROWS) {
+                    const int op = v / ROWS, r = v % ROWS / VR, e = v % VR * E;
+                    const T *p = op == 0 ? x : op == 1 ? dt : op == 2 ? dO : z;
+                    const long long sn = op == 0 ? P.x.sn : op == 1 ? P.dt.sn : op == 2 ? P.dO.sn : P.z.sn;
+                    const bool on = !((op == 3 && !z) || (op == 0 && ENDS));
+                    mine[i] = Copy<T>{p + (lo + r) * sn + e, R * sn, smem_addr(&M.in[0][op][r][e]), (int)sizeof(M.in[0]), r,
+                                      on ? max(0, min(16, (nc - e) * (int)sizeof(T))) : -1};
+                } else {
+                    const int w = v - 4 * ROWS, op = w / (R * VS) & 1, r = w % (R * VS) / VS, e = w % VS * E;
+                    const long long sn = op ? P.C.sn : P.B.sn;
+                    mine[i] = Copy<T>{(op ? Cp : Bp) + (lo + r) * sn + e, R * sn, smem_addr(&M.bc_in[0][op][r][e]), (int)sizeof(M.bc_in[0]), r,
+                                      v < ALL && (op || !ENDS) ? 16 : -1};
                 }
+            }
+            auto copy = [&](int k) {
+                if (k >= 0)
+#pragma unroll
+                    for (int i = 0; i < (ALL + HELP - 1) / HELP; ++i) mine[i].issue(k, k % ST, lo + k * R < len - mine[i].row);
                 copy_commit();
             };
             auto produce = [&](int k) {
@@ -723,7 +733,7 @@ template <typename T, int S> __global__ void __launch_bounds__(256) sum_bc_kerne
 
 // ----------------------------------------------------------------------------------------------------------- step
 // S / 4 lanes to a channel, as above; a block keeps its channels' A and walks `rows` sequences.  Bound by the state's bytes.
-template <typename T, int S> __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Params P, int per) {
+template <typename T, int S> __global__ void __launch_bounds__(kThreads, 4) step_kernel(const __grid_constant__ Params P, int per) {
     constexpr int L = S / 4;
     const int q = threadIdx.x % L, c = (int)((blockIdx.x * (long long)kThreads + threadIdx.x) / L);
     const bool mine = c < P.C_;
@@ -731,7 +741,7 @@ template <typename T, int S> __global__ void __launch_bounds__(kThreads) step_ke
     const F4 a2 = mul4(load4(P.A + (long long)cc * S + 4 * q), kLog2e);
     const float bias = P.bias ? P.bias[cc] : 0.f, D = P.D ? P.D[cc] : 0.f;
     const int b1 = min((int)(blockIdx.y + 1) * per, P.seq.nseq);
-    constexpr int U = 4;  // sequences whose states are on their way together
+    constexpr int U = 2;  // sequences whose states are on their way together
     for (int b0 = blockIdx.y * per; b0 < b1; b0 += U) {
         Vec<float, 4> h0[U];
         Vec<T, 4> vb[U], vc[U];
@@ -954,7 +964,7 @@ template <typename T, int S> cudaError_t step(const Params &P, cudaStream_t s) {
     const long long across = ((long long)P.C_ * (S / 4) + kThreads - 1) / kThreads;
     // Sequences to a block, which read A once: as many as leave 8 blocks to an SM.
     int per = 1;
-    while (per < 16 && across * ((P.seq.nseq + 2 * per - 1) / (2 * per)) >= 8 * kSMs) per *= 2;
+    while (per < 16 && across * ((P.seq.nseq + 2 * per - 1) / (2 * per)) >= 16 * kSMs) per *= 2;
     while ((P.seq.nseq + per - 1) / per > 65535) per *= 2;
     step_kernel<T, S><<<dim3((unsigned)across, (unsigned)((P.seq.nseq + per - 1) / per)), kThreads, 0, s>>>(P, per);
     return cudaGetLastError();
