@@ -272,7 +272,7 @@ int run_rows(int T, int across, int per_sm) {
 int check_sizes(int nseq, int N, int C, int K, int act, int dtype, bool packed) {
     if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
     if (act != LA_CONV_NONE && act != LA_CONV_SILU) return LA_ERR_INVALID_ARG;
-    if (nseq < 0 || N < 0 || C < 1 || K < 1) return LA_ERR_INVALID_ARG;
+    if (nseq < 0 || N < 0 || C < 1 || C >= 1 << 24 || K < 1) return LA_ERR_INVALID_ARG;
     const long long T = packed ? N : (long long)nseq * N;
     if (T > kMaxRows || T >= (1LL << 40) / C || (long long)nseq * kMaxK >= (1LL << 40) / C || nseq > kMaxRows) return LA_ERR_INVALID_ARG;
     if (K < 2 || K > kMaxK) return LA_ERR_UNSUPPORTED;
@@ -329,7 +329,7 @@ int la_short_conv(const void *X, const float *W, const float *bias, const void *
 }
 
 size_t la_short_conv_workspace_bytes(int C, int K) {
-    if (C < 1 || K < 2 || K > la::conv::kMaxK) return 0;
+    if (C < 1 || C >= 1 << 24 || K < 2 || K > la::conv::kMaxK) return 0;
     return 256 + (size_t)la::conv::kMaxParts * C * (K + 1) * sizeof(float);
 }
 

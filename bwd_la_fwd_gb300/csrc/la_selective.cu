@@ -33,7 +33,7 @@ constexpr int kThreads = 256;  // of a step's block
 constexpr int kMark = 8;       // rows between the states that a forward keeps for its backward, and of its tile
 constexpr int kTile = 16;      // rows of a forward tile
 constexpr int kSMs = 152;
-constexpr int kMaxParts = 64;  // of a sequence
+constexpr int kMaxParts = 64;  // of a sequence of the mean length
 
 struct GOp {                   // B, C: [.., G, S]
     const void *p;
@@ -785,17 +785,21 @@ constexpr int kForwardChannels = 64;
 int back_channels(int S) { return S == 8 ? Back<float, 8>::CH : S == 16 ? Back<float, 16>::CH : Back<float, 32>::CH; }
 int blocks_per_group(int C, int G, int channels) { return (C / G + channels - 1) / channels; }
 
-// Rows of a part: all, where the sequences' channel blocks make a CTA for every other SM, else as many parts of a sequence
-// of the mean length as stand on the SMs at once (two CTAs on each), of kLeastPart rows at least.
+// Rows of a part.  Where the sequences' channel blocks make fewer CTAs than one for two SMs, as many parts of a sequence of the
+// mean length as stand on the SMs at once (two CTAs on each), of kLeastPart rows at least (1 x 65536 x 2048: 9 parts 1.14 ms,
+// one 9 ms).  Else eight mean lengths: only packed sequences that are far longer than the others are cut.
 constexpr int kLeastPart = 128;
-int part_rows(int T, int nseq, int C, int G, int S) {
+int part_rows(int T, int nseq, int C, int G) {
     const long long n = nseq > 0 ? nseq : 1, ctas = n * G * blocks_per_group(C, G, kForwardChannels);
     const long long whole = ((long long)T + kTile) / kTile * kTile;
-    if (ctas >= kSMs / 2 || T / n < 2 * kLeastPart) return (int)whole;
-    long long want = 2 * kSMs / ctas;
-    if (want > kMaxParts) want = kMaxParts;
-    long long part = ((T + n * want - 1) / (n * want) + kTile - 1) / kTile * kTile;
+    long long part = 8 * ((T + n - 1) / n);
+    if (ctas < kSMs / 2 && T / n >= 2 * kLeastPart) {
+        long long want = 2 * kSMs / ctas;
+        if (want > kMaxParts) want = kMaxParts;
+        part = (T + n * want - 1) / (n * want);
+    }
     if (part < kLeastPart) part = kLeastPart;
+    part = (part + kTile - 1) / kTile * kTile;
     return (int)(part < whole ? part : whole);
 }
 long long units_of(int T, int nseq, int N, int part, bool packed) {
@@ -806,7 +810,7 @@ long long units_of(int T, int nseq, int N, int part, bool packed) {
 // more than the same sequences packed).
 int walkers_of(int T, int nseq, int C, int G, int S) {
     const long long cblocks = (long long)G * blocks_per_group(C, G, back_channels(S)), want = (4 * kSMs + cblocks - 1) / cblocks;
-    const long long units = units_of(T, nseq, 0, part_rows(T, nseq, C, G, S), true);
+    const long long units = units_of(T, nseq, 0, part_rows(T, nseq, C, G), true);
     return (int)(units < want ? units : want);
 }
 struct Space {  // byte offsets of the workspace's arrays
@@ -820,7 +824,7 @@ Space space_of(int T, int nseq, int C, int G, int S, bool back) {
         at += (n + 255) & ~(size_t)255;
         return here;
     };
-    const int part = part_rows(T, nseq, C, G, S);
+    const int part = part_rows(T, nseq, C, G);
     if (part < T) {
         const size_t units = (size_t)units_of(T, nseq, 0, part, true) + 1;  // a batch has no more
         w.ends = take(units * C * S * 4);
@@ -837,7 +841,7 @@ Space space_of(int T, int nseq, int C, int G, int S, bool back) {
 
 int check_sizes(int nseq, int N, int C, int G, int S, int dtype, bool packed) {
     if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
-    if (nseq < 0 || N < 0 || C < 1 || G < 1 || S < 1 || C % G != 0) return LA_ERR_INVALID_ARG;
+    if (nseq < 0 || N < 0 || C < 1 || C >= 1 << 24 || G < 1 || S < 1 || C % G != 0) return LA_ERR_INVALID_ARG;
     const long long T = packed ? N : (long long)nseq * N;
     if (T > kMaxRows || nseq > kMaxRows || T >= (1LL << 40) / C || (long long)nseq * S >= (1LL << 40) / C ||
         (long long)G * S >= (1LL << 31) / 2 || T >= (1LL << 40) / ((long long)G * S))
@@ -1017,7 +1021,7 @@ int la_selective_scan(const void *X, const void *dt, const float *A, const void 
     P.last = state_out, P.marks = marks;
     P.bpg = blocks_per_group(channels, G, kForwardChannels);
     P.seq.status = (uint32_t *)workspace;
-    P.part = part_rows(T, nseq, channels, G, S);
+    P.part = part_rows(T, nseq, channels, G);
     const long long units = units_of(T, nseq, N, P.part, packed);
     const bool split = P.part < T && (packed || N > P.part);
     P.ends = (float *)((char *)workspace + w.ends), P.sums = (float *)((char *)workspace + w.sums);
@@ -1068,7 +1072,7 @@ int la_selective_scan_backward(const void *X, const void *dt, const float *A, co
     P.dx = Op{dX, out[0].st[0], out[0].st[1]};
     P.ddt = Op{ddt, out[1].st[0], out[1].st[1]};
     P.dz = Op{dz, out[2].st[0], out[2].st[1]};
-    P.part = part_rows(T, nseq, channels, G, S);
+    P.part = part_rows(T, nseq, channels, G);
     const bool split = P.part < T && (packed || N > P.part);
     P.units = (int)units_of(T, nseq, N, P.part, packed);
     P.walkers = walkers_of(T, nseq, channels, G, S);

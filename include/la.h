@@ -348,7 +348,8 @@ int la_gated_scan_step(const void *x, const void *w, void *h, float *state, int 
  *   strides    in : host array, (batch, row) element strides of X, residual, sum, Y (8 values; the rules of the strided
  *              passes), or NULL for contiguous tensors
  * A row is read before it is written: an output may be an input itself (same pointer and strides; sum = residual, Y = X).
- * Squares are summed in fp32: rows beyond some 1e18 overflow (rstd = 0).  B = 0 or N = 0 does nothing.
+ * Squares are summed in fp32: rows beyond some 1e18 overflow (rstd = 0); a row of zeros is 0 with eps > 0 and NaN with 0.
+ * B = 0 or N = 0 does nothing.
  */
 int la_rms_norm(const void *X, const void *residual, const float *weight, void *sum, void *Y, int B, int N, int C,
                 float eps, int dtype, const long long *strides, void *stream);
@@ -427,7 +428,7 @@ int la_short_conv_step(const void *x, const float *W, const float *bias, void *s
  *   y = sum_n C_t[g,n] h_t[c,n] + D x,   Y = y z / (1 + e^-z)   (y without z)
  *   X, dt, z, Y  in, in, in, out: [nseq,N,C] of `dtype`; with seq_offsets N rows of nseq sequences end to end, [N,C], as in
  *                la_prompt (rows outside every sequence are neither read into a result nor written; offsets out of order
- *                compute nothing and LA_ERR_BOUNDS is reported).  z may be NULL.  All rows together < 2^31 - 1024.
+ *                compute nothing and LA_ERR_BOUNDS is reported).  z may be NULL.  All rows together < 2^31 - 1024, C < 2^24.
  *   B, C         in : [nseq,N,G,S] (packed [N,G,S]) of `dtype`;  S = 8, 16 or 32;  with G > 1 C / G a multiple of 8
  *   A, D, dt_bias  in : float [C,S], [C], [C]; D and dt_bias may be NULL for 0.  A is finite (negative for states that fade).
  *   state_in     in : float [nseq,C,S], or NULL for 0;  state_out out: the same of each sequence's end, or NULL.  Not the
@@ -437,7 +438,7 @@ int la_short_conv_step(const void *x, const float *W, const float *bias, void *s
  *   strides      in : host array, (batch, row) element strides of X, dt, z, Y and (batch, row, group) of B, C (14 values;
  *                the rules of the strided passes; packed, the batch's are not used), or NULL for contiguous tensors
  *   workspace    workspace_bytes >= la_selective_scan_workspace_bytes(T, ...), T = all rows together, under the workspace
- *                rules above; one for the largest T and nseq may be too small for other shapes: ask for each
+ *                rules above (fewer rows or sequences may need more: they are cut into parts)
  * The states and sums are held in fp32.  A sequence's rows do not depend on other sequences, whatever those hold; an
  * infinity or a NaN of its own may reach every later row of it.
  */
@@ -451,7 +452,7 @@ int la_selective_scan(const void *X, const void *dt, const float *A, const void 
 
 /*
  * Gradients of sum dY . Y + sum dstate_out . state_out, from the marks that the forward left for the same inputs:
- *   dX, ddt, dz  out: contiguous [nseq,N,C] (packed [N,C]) of `dtype`; dz with z only
+ *   dX, ddt, dz  out: contiguous [nseq,N,C] (packed [N,C]) of `dtype`, rows of whole 16-byte vectors; dz with z only
  *   dB, dC       out: contiguous [nseq,N,G,S] (packed [N,G,S]) of `dtype`, summed in fp32 and rounded once
  *   dA, dD, ddt_bias  out: float [C,S], [C], [C] (the last two may be NULL; 0 without rows)
  *   dstate_out   in : float [nseq,C,S], or NULL for 0;  dstate_in out: the same for state_in, or NULL

@@ -209,6 +209,26 @@ def test_strided_views_odd_channels_and_in_place(kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_batches_with_rows_between_them(kind):
+    """Entries whose rows do not follow one another evenly: as the packed call on copies, forward and backward."""
+    from bwd_la_fwd_gb300 import la
+    gen = torch.Generator().manual_seed(8)
+    big = [normal(gen, 3, 12, 72, kind=kind).cuda() for _ in range(3)]
+    w = torch.randn(72, generator=gen).cuda()
+    x, res, dy = (t[:, 1:11] for t in big)
+    a = la.la_rms_norm(x, w, residual=res)
+    b = la.la_rms_norm(x.contiguous(), w, residual=res.contiguous())
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    a, b = la.la_rms_norm_8bit(x, w), la.la_rms_norm_8bit(x.contiguous(), w)
+    assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8)) and torch.equal(a[1], b[1])
+    a, b = la.la_rms_norm_backward(x, w, dy, dR=res), la.la_rms_norm_backward(x.contiguous(), w, dy.contiguous(), dR=res.contiguous())
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    one = la.la_rms_norm(big[0][:, 5:6], w)[0]  # a row from each entry
+    assert torch.equal(one, la.la_rms_norm(big[0], w)[0][:, 5:6])
+
+
+@pytest.mark.gpu
 def test_rows_of_zeros_infinities_and_nan():
     """A zero row stays zero (eps > 0), its scale the least; a row with an infinity or NaN spoils itself alone."""
     from bwd_la_fwd_gb300 import la

@@ -48,7 +48,7 @@ def test_refuses_on_the_host():
         return lib.la_short_conv(x, w, b, first, o, last, off, nseq, N, C, K, act, dtype, st, ws, size, None)
 
     assert call(dtype=2) == 1 and call(act=2) == 1 and call(nseq=-1) == 1 and call(N=-1) == 1 and call(C=0) == 1 and call(K=0) == 1
-    assert call(K=1) == 2 and call(K=5) == 2
+    assert call(K=1) == 2 and call(K=5) == 2 and call(C=2 ** 24) == 1
     assert call(x=None) == 1 and call(w=None) == 1 and call(o=None) == 1 and call(o=(3 << 20) + 8) == 1 and call(b=5) == 1
     assert call(C=33) == 1 and call(strides=[256, 32, 256, 64]) == 1
     assert call(o=1 << 20) == 1 and call(o=2 << 20) == 1                       # no form in place
