@@ -5,9 +5,11 @@
 //   backward, at r as stored: g = w dy,  dx = dr + rstd (g - r rstd^2 mean(g r)),  dw = sum over rows of dy r rstd
 //
 // A row is read once into registers: TPR threads with NV 16-byte vectors each.  What bounds it is HBM (forward x, residual,
-// r, y; backward r, dy, dr, dx).  A block walks rows RPI at a time for each group of TPR threads, so that their loads are on
-// their way together and two barriers serve all of them, with the weights in registers.  r is normed as the fp32 sum, not
-// as rounded to the tokens' type: y then passes one rounding.
+// r, y; backward r, dy, dr, dx).  The blocks stand on all SMs at once and walk the rows, one or two at a time for each group of
+// TPR threads, the next ones' loads on their way meanwhile and the weights in registers (4 x 4096 x 2048 with a residual, bf16:
+// 45.1 us, 5.9 TB/s; without loads ahead and with eight blocks to an SM 94; four blocks for three change nothing).  The
+// gradient of 8 x 2048 x 2048 takes 60 us (4.5 TB/s): two sums a row and the parts of dw, 304 rows of them, added by a second
+// launch.  r is normed as the fp32 sum, not as rounded to the tokens' type: y then passes one rounding.
 #include <math.h>
 
 #include <type_traits>

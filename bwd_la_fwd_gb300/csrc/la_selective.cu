@@ -9,11 +9,13 @@
 //
 // A scanning thread holds four states of two channels in registers, a warp four states of 64 channels, and the warps of the
 // other states stand beside it.  They walk rows in tiles of 16, reading d, d x, B and C from shared memory and leaving each
-// row's part of y there, while four helping warps form d and d x of the next tile from dt and x and write the outputs of the
-// tile before; one barrier a tile.  Everything is held in fp32.
-// T C S exponentials and 4 T C S multiply-adds bind it, and more than these what a row brings through shared memory: a warp's
-// 16-byte load of B (the same for all lanes) takes two clocks of the SM, one of d two for 32 channels.  Two channels to a
-// thread share the loads of B and C.
+// row's part of y there, while helping warps form d and d x of the next tile and write the outputs of the tile before; one
+// barrier a tile.  x, dt, z, B and C come by asynchronous copies into a ring of tiles: loaded ahead into registers, behind
+// branches, each waited for its own arrival (4 x 4096 x 2048, bf16: 1209 us; predicated 332; copies 287).  All is held in fp32.
+// T C S exponentials (32 an SM and clock) and 4 T C S multiply-adds are 60 us there; what binds it are issue slots (some 260
+// instructions for a row of 64 channels) and shared memory, whose 16-byte loads of B and C take two clocks of the SM each
+// though all lanes ask for the same.  Two channels to a thread share them (1 x 65536 x 2048: 1.14 ms, one channel 1.33); one
+// channel to a thread gives twice the warps where an SM has one CTA (4 x 4096 x 2048: 250 us, two channels 287).
 // Where there are few channels time is cut into parts: a first launch forms each part's last state, started from zero (the
 // first part of a sequence: from its state), and the sum of its d, whose e^(A sum) is the part's decay; the second launch
 // folds them into the state that each part starts from.
@@ -396,7 +398,10 @@ __global__ void __launch_bounds__(Tile<T, S, CT>::THREADS, Tile<T, S, CT>::PER_S
 // sum G B and sum a h G A in shared memory, where the helping warps add them up and form the gradients of rows; dB and dC are
 // summed over the warp's 64 channels, in the thread and then by butterflies of shuffles that hand each lane a value of its
 // own (8 values over 8 lanes, then four rows of them over the four groups of lanes), and over the channel blocks by a launch
-// of its own.  Bound by shared memory and issue slots alike: some 190 clocks of an SM for a row of 64 channels.
+// of its own.  Bound by issue slots (870 instructions for a row of 64 channels, 65 % of the slots of the SMs that have two
+// CTAs) and by the scanning warps' latencies; shared memory takes 190 clocks for such a row.  8 x 2048 x 2048, bf16: 751 us.
+// Values kept from the way forth to the way back (decays, d, B) spill: 1713 us where forming them again takes 778.  Components
+// turned so that lanes need not choose what they exchange save 6 % of the instructions and cost as much in shared memory.
 template <typename T, int S> struct Back {
     static constexpr int R = kMark, QW = S / 4, GW = QW > 4 ? 1 : 4 / QW, CH = 64 * GW;
     static constexpr int HELP = R * CH / 4, SCAN = 32 * QW * GW, THREADS = HELP + SCAN;  // a vector of four channels to a helper
@@ -732,7 +737,8 @@ template <typename T, int S> __global__ void __launch_bounds__(256) sum_bc_kerne
 }
 
 // ----------------------------------------------------------------------------------------------------------- step
-// S / 4 lanes to a channel, as above; a block keeps its channels' A and walks `rows` sequences.  Bound by the state's bytes.
+// S / 4 lanes to a channel; a block keeps its channels' A and walks `per` sequences, two states to a lane on their way.  Bound by
+// the state's bytes: 256 x 4096 x 16, bf16: 31.5 us, 4.5 TB/s (one state on its way 37, four 37 with fewer blocks).
 template <typename T, int S> __global__ void __launch_bounds__(kThreads, 4) step_kernel(const __grid_constant__ Params P, int per) {
     constexpr int L = S / 4;
     const int q = threadIdx.x % L, c = (int)((blockIdx.x * (long long)kThreads + threadIdx.x) / L);
@@ -787,7 +793,7 @@ int blocks_per_group(int C, int G, int channels) { return (C / G + channels - 1)
 
 // Rows of a part.  Where the sequences' channel blocks make fewer CTAs than one for two SMs, as many parts of a sequence of the
 // mean length as stand on the SMs at once (two CTAs on each), of kLeastPart rows at least (1 x 65536 x 2048: 9 parts 1.14 ms,
-// one 9 ms).  Else eight mean lengths: only packed sequences that are far longer than the others are cut.
+// one 3.51 ms).  Else eight mean lengths: only packed sequences that are far longer than the others are cut.
 constexpr int kLeastPart = 128;
 int part_rows(int T, int nseq, int C, int G) {
     const long long n = nseq > 0 ? nseq : 1, ctas = n * G * blocks_per_group(C, G, kForwardChannels);
