@@ -15,7 +15,8 @@
 // T C S exponentials (32 an SM and clock) and 4 T C S multiply-adds are 60 us there; what binds it are issue slots (some 260
 // instructions for a row of 64 channels) and shared memory, whose 16-byte loads of B and C take two clocks of the SM each
 // though all lanes ask for the same.  Two channels to a thread share them (1 x 65536 x 2048: 1.14 ms, one channel 1.33); one
-// channel to a thread gives twice the warps where an SM has one CTA (4 x 4096 x 2048: 250 us, two channels 287).
+// channel to a thread gives twice the warps where an SM has one CTA, and registers for operands three rows ahead (4 x 4096 x
+// 2048: 240 us, one row ahead 250, two channels 287).
 // Where there are few channels time is cut into parts: a first launch forms each part's last state, started from zero (the
 // first part of a sequence: from its state), and the sum of its d, whose e^(A sum) is the part's decay; the second launch
 // folds them into the state that each part starts from.
@@ -341,12 +342,13 @@ __global__ void __launch_bounds__(Tile<T, S, CT>::THREADS, Tile<T, S, CT>::PER_S
         if (k == tiles) break;
         const int buf = k & 1;
         float *mark = !ENDS && P.marks ? P.marks + (mark_slot(P, seq, lo + k * R) * P.C_ + c) * S + 4 * q : nullptr;
-        // A row's operands are loaded a row ahead of it, before the parts of y of the row between are stored (which the
-        // compiler has to take for stores to them).
+        // A row's operands are loaded ahead of it, before the parts of y of the rows between are stored (which the compiler has
+        // to take for stores to them); as many rows as registers allow.
+        constexpr int DEPTH = CT == 1 ? 4 : 2;
         struct Row {
             float d[CT], u[CT];
             F4 B, C;
-        } ahead[2];
+        } ahead[DEPTH];
         auto load = [&](int r, Row &o) {
             if constexpr (CT == 2) {
                 const float2 d = *(const float2 *)&M.ds[buf][r][ch], u = *(const float2 *)&M.us[buf][r][ch];
@@ -357,11 +359,12 @@ __global__ void __launch_bounds__(Tile<T, S, CT>::THREADS, Tile<T, S, CT>::PER_S
             o.B = load4(&M.bc[buf][0][r][4 * q]);
             if (!ENDS) o.C = load4(&M.bc[buf][1][r][4 * q]);
         };
-        load(0, ahead[0]);
+#pragma unroll
+        for (int r = 0; r < DEPTH - 1; ++r) load(r, ahead[r]);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (r + 1 < R) load(r + 1, ahead[(r + 1) % 2]);
-            const Row &o = ahead[r % 2];
+            if (r + DEPTH - 1 < R) load(r + DEPTH - 1, ahead[(r + DEPTH - 1) % DEPTH]);
+            const Row &o = ahead[r % DEPTH];
             if (r % kMark == 0 && mark && lo + k * R + r < hi) {
                 float *m = mark + (long long)(r / kMark) * P.C_ * S;
 #pragma unroll
@@ -1080,7 +1083,9 @@ int la_selective_scan_backward(const void *X, const void *dt, const float *A, co
     P.dz = Op{dz, out[2].st[0], out[2].st[1]};
     P.part = part_rows(T, nseq, channels, G);
     const bool split = P.part < T && (packed || N > P.part);
-    P.units = (int)units_of(T, nseq, N, P.part, packed);
+    const long long units = units_of(T, nseq, N, P.part, packed);
+    if (units >= (1LL << 31)) return LA_ERR_INVALID_ARG;
+    P.units = (int)units;
     P.walkers = walkers_of(T, nseq, channels, G, S);
     P.ends = (float *)((char *)workspace + w.ends), P.sums = (float *)((char *)workspace + w.sums);
     P.pbc = (float *)((char *)workspace + w.pbc), P.pa = (float *)((char *)workspace + w.pa);

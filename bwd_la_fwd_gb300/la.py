@@ -1036,14 +1036,14 @@ def la_selective_scan_backward(X, dt, A, B, C, dY, marks, D=None, z=None, dt_bia
         got.dB, got.dC = (new(B.shape, dtype=B.dtype, device=X.device) for _ in range(2))
         got.dA = torch.empty((channels, S), dtype=torch.float32, device=X.device)
         got.dD, got.ddt_bias = (torch.empty((channels,), dtype=torch.float32, device=X.device) for _ in range(2))
-        got.dstate_in = torch.zeros((nseq, channels, S), dtype=torch.float32, device=X.device) if dstate_out is not None else None
+        got.dstate_in = new((nseq, channels, S), dtype=torch.float32, device=X.device)
         if workspace is None:
             workspace = new_selective_scan_workspace(T, nseq, channels, G, S, code, backward=True, device=X.device)
         st = load_library().la_selective_scan_backward(
             X.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _raw(D), _raw(z), _raw(dt_bias),
             int(bool(softplus)), dY.data_ptr(), marks.data_ptr(), _raw(dstate_out), got.dX.data_ptr(), got.ddt.data_ptr(),
             got.dA.data_ptr(), got.dB.data_ptr(), got.dC.data_ptr(), got.dD.data_ptr(), _raw(got.dz), got.ddt_bias.data_ptr(),
-            _raw(got.dstate_in), _raw(seq_offsets), nseq, N, channels, G, S, code, _ARRAYS[14](*strides),
+            got.dstate_in.data_ptr(), _raw(seq_offsets), nseq, N, channels, G, S, code, _ARRAYS[14](*strides),
             workspace.data_ptr(), workspace.numel() * workspace.element_size(), sp)
     if st != 0:
         raise LAError(st, "la_selective_scan_backward")
