@@ -402,21 +402,20 @@ __global__ void __launch_bounds__(Tile<T, S, CT>::THREADS, Tile<T, S, CT>::PER_S
 // summed over the warp's 64 channels, in the thread and then by butterflies of shuffles that hand each lane a value of its
 // own (8 values over 8 lanes, then four rows of them over the four groups of lanes), and over the channel blocks by a launch
 // of its own.  Bound by issue slots (870 instructions for a row of 64 channels, 65 % of the slots of the SMs that have two
-// CTAs) and by the scanning warps' latencies; shared memory takes 190 clocks for such a row.  8 x 2048 x 2048, bf16: 751 us.
+// CTAs) and by the scanning warps' latencies; shared memory takes 190 clocks for such a row.  8 x 2048 x 2048, bf16: 736 us.
 // Values kept from the way forth to the way back (decays, d, B) spill: 1713 us where forming them again takes 778.  Components
 // turned so that lanes need not choose what they exchange save 6 % of the instructions and cost as much in shared memory.
 template <typename T, int S> struct Back {
     static constexpr int R = kMark, QW = S / 4, GW = QW > 4 ? 1 : 4 / QW, CH = 64 * GW;
     static constexpr int HELP = R * CH / 4, SCAN = 32 * QW * GW, THREADS = HELP + SCAN;  // a vector of four channels to a helper
     static constexpr int STAGES = 4;  // tiles on their way, or read for d and g, or for the gradients of rows
-    static constexpr int FLUSH = 8;  // tiles between additions to dA's sums, which so pass fewer roundings
     struct Smem {
         T in[STAGES][4][R][CH];                          // x, dt, dO, z
         T bc_in[STAGES][2][R][S];
         float ds[3][R][CH], us[2][R][CH], gs[2][R][CH];  // d, d x, g
         float bc[2][2][R][S];
         float ys[2][QW][R][CH], ws[2][QW][R][CH], es[2][QW][R][CH];
-        float4 dA[2][SCAN];
+        float4 dA[2][SCAN];                              // each scanning thread's sums
     };
 };
 
@@ -701,7 +700,7 @@ __global__ void __launch_bounds__(Back<T, S>::THREADS, S == 16 ? 2 : 1) backward
                         if (P.z.p) *(float2 *)&M.ys[buf][q][half + i][ch] = y[i];
                     }
                 }
-                if (k % K::FLUSH == 0) flush();
+                flush();  // (once in eight tiles 752 us: registers)
             }
         }
 #pragma unroll
