@@ -124,7 +124,8 @@ template <int L, int STEP> __device__ __forceinline__ float lanes_sum(float (&v)
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-// A thread's share of a tile's copies: 16 bytes of a row, `bytes` of them there (the others zero), or none (-1).
+// A thread's share of a tile's copies: 16 bytes of a row, `bytes` of them there (the others zero), or none (-1).  The source has
+// to lie at a multiple of 16 bytes even where nothing is read of it.
 template <typename T> struct Copy {
     const T *src;         // of tile 0
     long long step;       // elements to the next tile
@@ -879,7 +880,10 @@ int take_inputs(Call &K, const void *X, const void *dt, const float *A, const vo
     const int elem = dtype == LA_BF16 ? 2 : 4, batch = packed ? 1 : nseq, T = packed ? N : nseq * N;
     if (!A || ((uintptr_t)A & 15) || ((uintptr_t)D & 15) || ((uintptr_t)bias & 15) || ((uintptr_t)state & 15) || ((uintptr_t)off & 3))
         return LA_ERR_INVALID_ARG;
+    // Operands that have one row at most are never stepped, and the rows of a tile behind the last one are addressed, though not
+    // read: their row stride is 0, as the width of one row need not be whole vectors.  Without rows A stands for them.
     const void *ptr[4] = {X, dt, z, other};
+    if (T == 0) ptr[0] = ptr[1] = ptr[3] = B = C = A, ptr[2] = z ? A : nullptr;
     int rc;
     for (int k = 0; k < 4 && T > 0; ++k) {
         if (k == 2 && !z) continue;
@@ -890,10 +894,12 @@ int take_inputs(Call &K, const void *X, const void *dt, const float *A, const vo
         if ((rc = group_view(K.v[5], C, batch, N, G, S, elem, strides ? strides + 11 : nullptr))) return rc;
     }
     Params &P = K.P;
-    auto op = [&](int k) { return Op{ptr[k], K.v[k].st[0], K.v[k].st[1]}; };
+    const bool stepped = (packed ? T : N) > 1;
+    auto op = [&](int k) { return Op{ptr[k], K.v[k].st[0], stepped ? K.v[k].st[1] : 0}; };
     P.x = op(0), P.dt = op(1), P.z = op(2), P.y = P.dO = op(3);
-    P.B = GOp{B, K.v[4].st[0], K.v[4].st[1], K.v[4].st[2]};
-    P.C = GOp{C, K.v[5].st[0], K.v[5].st[1], K.v[5].st[2]};
+    P.y.p = other;
+    auto group_op = [&](int k, const void *p) { return GOp{p, K.v[k].st[0], stepped ? K.v[k].st[1] : 0, K.v[k].st[2]}; };
+    P.B = group_op(4, B), P.C = group_op(5, C);
     P.A = A, P.D = D, P.bias = bias, P.first = state;
     P.seq = Seqs{off, nseq, N, T, nullptr};
     P.C_ = Cn, P.G = G, P.cpg = Cn / G;
