@@ -721,7 +721,11 @@ __global__ void __launch_bounds__(Back<T, S>::THREADS, S == 16 ? 2 : 1) backward
     flush();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        if (ch + i < nc) *(float4 *)(P.pa + (long long)walker * P.C_ * (S + 2) + (long long)(c + i) * S + 4 * q) = M.dA[i][threadIdx.x];
+        if (ch + i < nc) {  // (a walker's sums begin at 16 bytes where the channels are even)
+            const float4 f = M.dA[i][threadIdx.x];
+            store_vec(P.pa + (long long)walker * P.C_ * (S + 2) + (long long)(c + i) * S + 4 * q, Vec<float, 4>{{f.x, f.y, f.z, f.w}}, 4,
+                      P.C_ % 2 == 0);
+        }
     __syncthreads();
 }
 

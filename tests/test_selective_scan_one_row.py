@@ -40,6 +40,13 @@ def test_one_row(C, S, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_one_row_and_sequences_without_rows(kind):
+    c, dy, st, _ = _case(1, 75, 1, 16, 4, kind, 7)
+    off = [0, 0, 1, 1, 1]
+    _check(c, dy, st, off, kind, lambda t: t, torch.tensor(off, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_a_batch_of_one_row_each(kind):
     """The sequences lie 80 channels apart."""
     B, C = 3, 75
@@ -53,3 +60,14 @@ def test_a_batch_of_one_row_each(kind):
         return wide[:, :, :C]
 
     _check(c, dy, st, list(range(B + 1)), kind, view, None)
+
+
+def test_no_rows_of_odd_channels():
+    from bwd_la_fwd_gb300 import la
+    A = -torch.ones(75, 16, device="cuda")
+    e, b = torch.empty(2, 0, 75, device="cuda"), torch.empty(2, 0, 1, 16, device="cuda")
+    st, last = torch.randn(2, 75, 16, device="cuda"), torch.empty(2, 75, 16, device="cuda")
+    marks = la.new_selective_scan_marks(0, 2, 75, 16)
+    la.la_selective_scan(e, e, A, b, b, z=e, state_in=st, state_out=last, marks=marks)
+    got = la.la_selective_scan_backward(e, e, A, b, b, e, marks, z=e, dstate_out=st)
+    assert torch.equal(st, last) and torch.equal(got.dstate_in, st) and not got.dA.any()
