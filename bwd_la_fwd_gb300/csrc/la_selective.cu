@@ -35,6 +35,7 @@ using namespace rows;
 constexpr int kThreads = 256;  // of a step's block
 constexpr int kMark = 8;       // rows between the states that a forward keeps for its backward, and of its tile
 constexpr int kTile = 16;      // rows of a forward tile
+constexpr int kGroup = 16;     // tiles whose sums of dA are added up by themselves
 constexpr int kSMs = 152;
 constexpr int kMaxParts = 64;  // of a sequence of the mean length
 
@@ -107,7 +108,7 @@ __device__ __forceinline__ float dot4(const F4 &x, const F4 &y) {
 // 2^(a2 d).  The hardware's 2^x is on the average too small, by 0.6 to 2.6e-8 for exponents between -2^-17 and -1/2, and a state
 // that fades slowly gathers that of all rows it remembers.  So exponents are made kLift larger, within the one multiply-add that
 // forms them: means between -1.1 and 1.0e-8, the same rms; 2^kLift is 1, so rows that are not there still leave a state as it
-// is.  8 x 2048 x 2048: dA off by 0.94e-6 of its norm, 2.0e-6 without.
+// is.  8 x 2048 x 2048: dA off by 0.90e-6 of its norm, 2.0e-6 without.
 constexpr float kLift = 2.2351742e-8f;  // 3 2^-27
 __device__ __forceinline__ F4 decay4(const F4 &a2, float d) {
     const F4 e = fma4(a2, d, F4{both(kLift), both(kLift)});
@@ -421,7 +422,7 @@ template <typename T, int S> struct Back {
         float ds[3][R][CH], us[2][R][CH], gs[2][R][CH];  // d, d x, g
         float bc[2][2][R][S];
         float ys[2][QW][R][CH], ws[2][QW][R][CH], es[2][QW][R][CH];
-        float4 dA[2][SCAN];                              // each scanning thread's sums
+        float4 dA[2][2][SCAN];                           // each scanning thread's sums: of a group of tiles, of all groups
     };
 };
 
@@ -598,14 +599,17 @@ __global__ void __launch_bounds__(Back<T, S>::THREADS, S == 16 ? 2 : 1) backward
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         if (ch + i < nc) a2[i] = mul4(load4(P.A + (long long)(c + i) * S + 4 * q), kLog2e);
-        M.dA[i][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        M.dA[0][i][threadIdx.x] = M.dA[1][i][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    auto flush = [&] {
+    auto flush = [&](bool group_ends) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float4 &s = M.dA[i][threadIdx.x];
+            float4 &s = M.dA[0][i][threadIdx.x], &all = M.dA[1][i][threadIdx.x];
             s = make_float4(s.x + dA[i].a.x, s.y + dA[i].a.y, s.z + dA[i].b.x, s.w + dA[i].b.y);
             dA[i] = zero4();
+            if (!group_ends) continue;
+            all = make_float4(all.x + s.x, all.y + s.y, all.z + s.z, all.w + s.w);
+            s = make_float4(0.f, 0.f, 0.f, 0.f);
         }
     };
     for (int unit = walker; unit < P.units && fine; unit += P.walkers) {
@@ -706,7 +710,7 @@ __global__ void __launch_bounds__(Back<T, S>::THREADS, S == 16 ? 2 : 1) backward
                         if (P.z.p) *(float2 *)&M.ys[buf][q][half + i][ch] = y[i];
                     }
                 }
-                flush();  // (once in eight tiles 752 us: registers)
+                flush(k % kGroup == 0);  // (registers added to shared memory once in eight tiles: 752 us)
             }
         }
 #pragma unroll
@@ -723,11 +727,10 @@ __global__ void __launch_bounds__(Back<T, S>::THREADS, S == 16 ? 2 : 1) backward
         __syncthreads();
     }
     if (ENDS) return;
-    flush();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         if (ch + i < nc) {  // (a walker's sums begin at 16 bytes where the channels are even)
-            const float4 f = M.dA[i][threadIdx.x];
+            const float4 f = M.dA[1][i][threadIdx.x];
             store_vec(P.pa + (long long)walker * P.C_ * (S + 2) + (long long)(c + i) * S + 4 * q, Vec<float, 4>{{f.x, f.y, f.z, f.w}}, 4,
                       P.C_ % 2 == 0);
         }
