@@ -115,6 +115,14 @@ __device__ __forceinline__ F4 decay4(const F4 &a2, float d) {
     return F4{make_float2(ex2(e.a.x), ex2(e.a.y)), make_float2(ex2(e.b.x), ex2(e.b.y))};
 }
 
+// 2^(a2 d) h + x, d a part's sum, by four factors: a part's growth, or its fading, may be beyond fp32's range where the state that
+// it reaches is not.  A factor counts as the largest number at most, so what is 0 stays 0, as it does row by row.
+__device__ __forceinline__ float finite(float f) { return fminf(f, 3.40282347e38f); }
+__device__ __forceinline__ F4 over_part(const F4 &a2, float d, const F4 &h, const F4 &x) {
+    const F4 e = decay4(a2, 0.25f * d), f{make_float2(finite(e.a.x), finite(e.a.y)), make_float2(finite(e.b.x), finite(e.b.y))};
+    return fma4(f, mul4(f, mul4(f, mul4(f, h))), x);
+}
+
 // Sums over L lanes (q of them this one's number, lanes STEP apart) of L values each; lane q gets value q's.
 template <int L, int STEP> __device__ __forceinline__ float lanes_sum(float (&v)[L], int q) {
 #pragma unroll
@@ -336,11 +344,10 @@ __global__ void __launch_bounds__(Tile<T, S, CT>::THREADS, Tile<T, S, CT>::PER_S
         if (j == 0) {
             if (P.first) h[i] = load4(P.first + (long long)seq * P.C_ * S + at);
         } else if (!ENDS) {
+            h[i] = load4(P.ends + (long long)(unit - j) * P.C_ * S + at);
 #pragma unroll 4
-            for (int p = unit - j; p < unit; ++p) {
-                const F4 e = load4(P.ends + (long long)p * P.C_ * S + at);
-                h[i] = p == unit - j ? e : fma4(decay4(a2[i], P.sums[(long long)p * P.C_ + c + i]), h[i], e);
-            }
+            for (int p = unit - j + 1; p < unit; ++p)
+                h[i] = over_part(a2[i], P.sums[(long long)p * P.C_ + c + i], h[i], load4(P.ends + (long long)p * P.C_ * S + at));
         }
     }
     __syncthreads();
@@ -630,7 +637,7 @@ __global__ void __launch_bounds__(Back<T, S>::THREADS, S == 16 ? 2 : 1) backward
             carry[i] = load4(P.ends + (long long)last * P.C_ * S + at);
 #pragma unroll 4
             for (int p = last - 1; p > unit; --p)
-                carry[i] = fma4(decay4(a2[i], P.sums[(long long)p * P.C_ + c + i]), carry[i], load4(P.ends + (long long)p * P.C_ * S + at));
+                carry[i] = over_part(a2[i], P.sums[(long long)p * P.C_ + c + i], carry[i], load4(P.ends + (long long)p * P.C_ * S + at));
         }
         float sum[2] = {0.f, 0.f};
         Vec<float, 4> mark[2] = {};
