@@ -65,7 +65,7 @@ struct Params {
     uint32_t *valid;           // whether the offsets were in order, for the sums behind
 };
 
-constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+constexpr float kLn2 = 0.693147181f, kLargest = 3.40282347e38f;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -105,10 +105,17 @@ __device__ __forceinline__ float dot4(const F4 &x, const F4 &y) {
     const float2 s = fma2(x.b, y.b, mul2(x.a, y.a));
     return s.x + s.y;
 }
+// A log2 e, rounded towards zero: never infinite, so that a row with d = 0, or one that is not there, changes no state.  The
+// constant is the float above log2 e, 1.2 half steps too large, so that the product is off by as much at most either way.
+__device__ __forceinline__ float log2_rate(float a) { return __fmul_rz(a, 1.44269514f); }
+__device__ __forceinline__ F4 rates4(const float *A) {
+    const F4 a = load4(A);
+    return F4{make_float2(log2_rate(a.a.x), log2_rate(a.a.y)), make_float2(log2_rate(a.b.x), log2_rate(a.b.y))};
+}
 // 2^(a2 d).  The hardware's 2^x is on the average too small, by 0.6 to 2.6e-8 for exponents between -2^-17 and -1/2, and a state
 // that fades slowly gathers that of all rows it remembers.  So exponents are made kLift larger, within the one multiply-add that
 // forms them: means between -1.1 and 1.0e-8, the same rms; 2^kLift is 1, so rows that are not there still leave a state as it
-// is.  8 x 2048 x 2048: dA off by 0.90e-6 of its norm, 2.0e-6 without.
+// is.  8 x 2048 x 2048: dA off by 0.92e-6 of its norm, 2.0e-6 without.
 constexpr float kLift = 2.2351742e-8f;  // 3 2^-27
 __device__ __forceinline__ F4 decay4(const F4 &a2, float d) {
     const F4 e = fma4(a2, d, F4{both(kLift), both(kLift)});
@@ -117,7 +124,7 @@ __device__ __forceinline__ F4 decay4(const F4 &a2, float d) {
 
 // 2^(a2 d) h + x, d a part's sum, by four factors: a part's growth, or its fading, may be beyond fp32's range where the state that
 // it reaches is not.  A factor counts as the largest number at most, so what is 0 stays 0, as it does row by row.
-__device__ __forceinline__ float finite(float f) { return fminf(f, 3.40282347e38f); }
+__device__ __forceinline__ float finite(float f) { return fminf(f, kLargest); }
 __device__ __forceinline__ F4 over_part(const F4 &a2, float d, const F4 &h, const F4 &x) {
     const F4 e = decay4(a2, 0.25f * d), f{make_float2(finite(e.a.x), finite(e.a.y)), make_float2(finite(e.b.x), finite(e.b.y))};
     return fma4(f, mul4(f, mul4(f, mul4(f, h))), x);
@@ -340,7 +347,7 @@ __global__ void __launch_bounds__(Tile<T, S, CT>::THREADS, Tile<T, S, CT>::PER_S
         sum[i] = 0.f;
         if (ch + i >= nc) continue;
         const long long at = (long long)(c + i) * S + 4 * q;
-        a2[i] = mul4(load4(P.A + at), kLog2e);
+        a2[i] = rates4(P.A + at);
         if (j == 0) {
             if (P.first) h[i] = load4(P.first + (long long)seq * P.C_ * S + at);
         } else if (!ENDS) {
@@ -605,7 +612,7 @@ __global__ void __launch_bounds__(Back<T, S>::THREADS, S == 16 ? 2 : 1) backward
     F4 a2[2] = {zero4(), zero4()}, dA[2] = {zero4(), zero4()};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        if (ch + i < nc) a2[i] = mul4(load4(P.A + (long long)(c + i) * S + 4 * q), kLog2e);
+        if (ch + i < nc) a2[i] = rates4(P.A + (long long)(c + i) * S + 4 * q);
         M.dA[0][i][threadIdx.x] = M.dA[1][i][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     auto flush = [&](bool group_ends) {
@@ -766,7 +773,7 @@ template <typename T, int S> __global__ void __launch_bounds__(kThreads, 4) step
     const int q = threadIdx.x % L, c = (int)((blockIdx.x * (long long)kThreads + threadIdx.x) / L);
     const bool mine = c < P.C_;
     const int cc = mine ? c : 0, g = cc / P.cpg;
-    const F4 a2 = mul4(load4(P.A + (long long)cc * S + 4 * q), kLog2e);
+    const F4 a2 = rates4(P.A + (long long)cc * S + 4 * q);
     const float bias = P.bias ? P.bias[cc] : 0.f, D = P.D ? P.D[cc] : 0.f;
     const int b1 = min((int)(blockIdx.y + 1) * per, P.seq.nseq);
     constexpr int U = 2;  // sequences whose states are on their way together

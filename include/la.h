@@ -430,7 +430,8 @@ int la_short_conv_step(const void *x, const float *W, const float *bias, void *s
  *                la_prompt (rows outside every sequence are neither read into a result nor written; offsets out of order
  *                compute nothing and LA_ERR_BOUNDS is reported).  z may be NULL.  All rows together < 2^31 - 1024, C < 2^24.
  *   B, C         in : [nseq,N,G,S] (packed [N,G,S]) of `dtype`;  S = 8, 16 or 32;  with G > 1 C / G a multiple of 8
- *   A, D, dt_bias  in : float [C,S], [C], [C]; D and dt_bias may be NULL for 0.  A is finite (negative for states that fade).
+ *   A, D, dt_bias  in : float [C,S], [C], [C]; D and dt_bias may be NULL for 0.  A is finite (negative for states that fade; sizes
+ *                beyond 2.35e38 count as that).
  *   state_in     in : float [nseq,C,S], or NULL for 0;  state_out out: the same of each sequence's end, or NULL.  Not the
  *                same array.
  *   marks        out: la_selective_scan_marks_bytes() of states for la_selective_scan_backward, or NULL
