@@ -93,7 +93,7 @@ __device__ __forceinline__ Vec<T, V> row_at(const Params &P, const T *x, int seq
 template <typename T, int K, bool SILU> __global__ void __launch_bounds__(kThreads, kPerSM) forward_kernel(const __grid_constant__ Params P) {
     constexpr int V = kV, A = kFwdAhead;
     const int c = (blockIdx.x * kThreads + threadIdx.x) * V, n = P.C - c;
-    const int r0 = blockIdx.y * P.run, r1 = min(r0 + P.run, P.seq.T);
+    const int r0 = blockIdx.y * P.run, r1 = r0 + min(P.run, P.seq.T - r0);
     const Taps<K> taps(P, c);
     for_stretches(P.seq, r0, r1, [&](int seq, int t0, int t1, int len, bool begins) {
         if (n <= 0) return;
@@ -141,7 +141,7 @@ template <typename T, int K, bool SILU> __global__ void __launch_bounds__(kThrea
 template <typename T, int K, bool SILU> __global__ void __launch_bounds__(kThreads, kBackPerSM) backward_kernel(const __grid_constant__ Params P) {
     constexpr int V = kV, A = kAhead;
     const int c = (blockIdx.x * kThreads + threadIdx.x) * V, n = P.C - c;
-    const int r0 = blockIdx.y * P.run, r1 = min(r0 + P.run, P.seq.T);
+    const int r0 = blockIdx.y * P.run, r1 = r0 + min(P.run, P.seq.T - r0);
     const Taps<K> taps(P, c);
     float2 dw[K][V / 2] = {}, db[V / 2] = {};
     for_stretches(P.seq, r0, r1, [&](int seq, int t0, int t1, int len, bool) {
@@ -262,12 +262,14 @@ template <int WHAT> int run(const Params &P, int K, int act, int dtype, dim3 gri
     return LA_OK;
 }
 
+int runs_of(int T, int rows) { return (int)(((long long)T + rows - 1) / rows); }
+
 // Rows of a run: as many as let all blocks stand on the SMs at once, and kRun at least.
 int run_rows(int T, int across, int per_sm) {
     const int runs = across < per_sm * kSMs ? per_sm * kSMs / across : 1;
     int rows = (int)(((long long)T + runs - 1) / runs);
     if (rows < kRun) rows = kRun;
-    while (((long long)T + rows - 1) / rows > 65535) rows *= 2;
+    while (runs_of(T, rows) > 65535) rows *= 2;
     return rows;
 }
 
@@ -327,7 +329,7 @@ int la_short_conv(const void *X, const float *W, const float *bias, const void *
     P.C = C;
     const unsigned across = (unsigned)((C + kThreads * kV - 1) / (kThreads * kV));
     P.run = run_rows(T, (int)across, kPerSM);
-    const int runs = T > 0 ? (T + P.run - 1) / P.run : 1;
+    const int runs = T > 0 ? runs_of(T, P.run) : 1;
     return run<kForward>(P, K, activation, dtype, dim3(across, (unsigned)runs), stream);
 }
 
@@ -373,8 +375,8 @@ int la_short_conv_backward(const void *X, const float *W, const float *bias, con
     int parts = 0;
     if (nseq > 0 && T > 0) {
         P.run = run_rows(T, (int)across, kBackPerSM);
-        if ((T + P.run - 1) / P.run > kMaxParts) P.run = (T + kMaxParts - 1) / kMaxParts;
-        parts = (T + P.run - 1) / P.run;
+        if (runs_of(T, P.run) > kMaxParts) P.run = runs_of(T, kMaxParts);
+        parts = runs_of(T, P.run);
         if ((rc = run<kBackward>(P, K, activation, dtype, dim3(across, (unsigned)parts), stream))) return rc;
     }
     const long long M = (long long)C * (K + 1);
