@@ -180,10 +180,12 @@ template <typename T, int S, int CT> struct Tile {
     };
 };
 
+// Parts of a sequence of N rows in a batch: one at least.
+__host__ __device__ __forceinline__ int parts_of(int N, int part) { return (N - 1) / part + 1; }
 // The unit's sequence and part.  A sequence's parts are units i + off[i] / part onwards: there are as many as it needs.
 __device__ __forceinline__ bool unit_of(const Params &P, int unit, int &seq, int &j, int &len) {
     if (!P.seq.off) {
-        const int per = max(1, (P.seq.N + P.part - 1) / P.part);
+        const int per = parts_of(P.seq.N, P.part);
         seq = unit / per, j = unit - seq * per, len = P.seq.N;
         return true;
     }
@@ -202,7 +204,7 @@ __device__ __forceinline__ bool unit_of(const Params &P, int unit, int &seq, int
 // The same where the offsets are known to be in order; by each thread itself.
 __device__ __forceinline__ void unit_at(const Params &P, int unit, int &seq, int &j, int &first, int &len) {
     if (!P.seq.off) {
-        const int per = max(1, (P.seq.N + P.part - 1) / P.part);
+        const int per = parts_of(P.seq.N, P.part);
         seq = unit / per, j = unit - seq * per, first = seq * P.seq.N, len = P.seq.N;
         return;
     }
@@ -839,7 +841,7 @@ int part_rows(int T, int nseq, int C, int G) {
 }
 long long units_of(int T, int nseq, int N, int part, bool packed) {
     if (packed) return (long long)nseq + T / part;
-    return (long long)nseq * (N > 0 ? (N + part - 1) / part : 1);
+    return (long long)nseq * parts_of(N, part);
 }
 // CTAs of a channel block in the backward walk: four CTAs to an SM in all, or the units that there are at most (a batch has no
 // more than the same sequences packed).

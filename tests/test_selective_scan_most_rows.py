@@ -1,0 +1,31 @@
+"""The selective scan over nearly as many rows as an int numbers (140 GB on the device), one sequence in parts of millions."""
+import pytest
+import torch
+
+from ops_testutil import U
+
+pytestmark = pytest.mark.gpu
+
+
+def test_most_rows():
+    """Tokens in the last rows only, in a sequence that forgets: what a call on these rows alone gives.  A state remembers some 2.5
+    rows (decays of e^-0.5 and less), each of them within 20 half steps; outputs are rounded to bf16, where a difference in
+    fp32 may be a step."""
+    from bwd_la_fwd_gb300 import la
+    if torch.cuda.get_device_properties(0).total_memory < 200 * 2 ** 30:
+        pytest.skip("needs 200 GB")
+    T, C, S, last = 2 ** 31 - 1100, 8, 8, 1000
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    new = lambda v, *s: torch.full((1, T, *s), v, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    x, dt, b, y = new(0.0, C), new(0.5, C), new(0.0, 1, S), new(3.0, C)
+    for t in (x, b):
+        t[:, -last:] = torch.randn(t[:, -last:].shape, generator=gen, device="cuda").bfloat16()
+    A = -torch.arange(1, S + 1, device="cuda").float().repeat(C, 1)
+    h, few = (torch.empty(1, C, S, device="cuda") for _ in range(2))
+    la.la_selective_scan(x, dt, A, b, b, softplus=False, state_out=h, Y=y)
+    z = la.la_selective_scan(*(t[:, -last:] for t in (x, dt)), A, b[:, -last:], b[:, -last:], softplus=False, state_out=few)
+    assert float((h - few).abs().max()) <= 2 * 2.5 * 20 * U * 16  # inputs are under 4, their products under 16
+    assert ((y[:, -last:].float() - z.float()).abs() <= 2.0 ** -7 * z.float().abs() + 2 * 2.5 * 20 * U * 16 * 4 * S).all()
+    assert not y[:, :-last:100003].any() and not y[:, :1000].any()
+    del x, dt, b, y
+    torch.cuda.empty_cache()
