@@ -180,7 +180,7 @@ template <typename T, int S, int CT> struct Tile {
     };
 };
 
-// Parts of a sequence of N rows in a batch: one at least.
+// Parts of `part` that N rows (or sequences) have: one at least.
 __host__ __device__ __forceinline__ int parts_of(int N, int part) { return (N - 1) / part + 1; }
 // The unit's sequence and part.  A sequence's parts are units i + off[i] / part onwards: there are as many as it needs.
 __device__ __forceinline__ bool unit_of(const Params &P, int unit, int &seq, int &j, int &len) {
@@ -777,7 +777,7 @@ template <typename T, int S> __global__ void __launch_bounds__(kThreads, 4) step
     const int cc = mine ? c : 0, g = cc / P.cpg;
     const F4 a2 = rates4(P.A + (long long)cc * S + 4 * q);
     const float bias = P.bias ? P.bias[cc] : 0.f, D = P.D ? P.D[cc] : 0.f;
-    const int b1 = min((int)(blockIdx.y + 1) * per, P.seq.nseq);
+    const int b1 = (int)min((blockIdx.y + 1) * (unsigned)per, (unsigned)P.seq.nseq);
     constexpr int U = 2;  // sequences whose states are on their way together
     for (int b0 = blockIdx.y * per; b0 < b1; b0 += U) {
         Vec<float, 4> h0[U];
@@ -1010,9 +1010,9 @@ template <typename T, int S> cudaError_t step(const Params &P, cudaStream_t s) {
     const long long across = ((long long)P.C_ * (S / 4) + kThreads - 1) / kThreads;
     // Sequences to a block, which read A once: as many as leave 8 blocks to an SM.
     int per = 1;
-    while (per < 16 && across * ((P.seq.nseq + 2 * per - 1) / (2 * per)) >= 16 * kSMs) per *= 2;
-    while ((P.seq.nseq + per - 1) / per > 65535) per *= 2;
-    step_kernel<T, S><<<dim3((unsigned)across, (unsigned)((P.seq.nseq + per - 1) / per)), kThreads, 0, s>>>(P, per);
+    while (per < 16 && across * parts_of(P.seq.nseq, 2 * per) >= 16 * kSMs) per *= 2;
+    while (parts_of(P.seq.nseq, per) > 65535) per *= 2;
+    step_kernel<T, S><<<dim3((unsigned)across, (unsigned)parts_of(P.seq.nseq, per)), kThreads, 0, s>>>(P, per);
     return cudaGetLastError();
 }
 template <typename T> cudaError_t step(const Params &P, int S, cudaStream_t s) {
