@@ -5,9 +5,10 @@ parallel, then linked into ``bwd_la_fwd_gb300/libla_gb300.so``.  No CMake, no to
 machinery: the library is a plain C-ABI shared object.
 
 ``checked=True`` builds the same sources with ``-DLA_CHECKED`` into ``libla_gb300_checked.so``: every
-global-memory index that a kernel computes itself for a workspace array or the normaliser is checked
-against the array's extent, and a violation is recorded as LA_ERR_BOUNDS in the workspace status word
-instead of being performed.  It is a test build (the product loads ``libla_gb300.so``).
+global-memory index that a kernel of the LA passes computes itself for a workspace array or the
+normaliser is checked against the array's extent, and a violation is recorded as LA_ERR_BOUNDS in the
+workspace status word instead of being performed.  The kernels of the operators around the head (rotary,
+prompts, gated recurrence, norm, short convolution, selective scan) have no such checks.  It is a test build (the product loads ``libla_gb300.so``).
 """
 from __future__ import annotations
 

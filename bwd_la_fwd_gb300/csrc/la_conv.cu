@@ -7,9 +7,9 @@
 //
 // A thread has four channels and walks a run of rows, the last K - 1 of them in registers as fp32 pairs and the next ones on
 // their way, so each row is read once (and K - 1 rows again at a run's start).  Runs are as long as lets all blocks stand on the
-// SMs at once.  HBM and issue slots bound it alike: 12,000 x 4096, bf16, four taps: 45 us, 4.4 TB/s (runs of 32 rows 53 us, each
+// SMs at once.  HBM and issue slots (56 %) bound it alike: 12,000 x 4096, bf16, four taps: 45 us, 4.4 TB/s (runs of 32 rows 53 us, each
 // tap's conversion by itself 47).  The backward walk is the same with a second window, of dp: dx of a row is complete K - 1
-// rows later, so a run computes dp of the K - 1 rows behind it again (2 x 2047 x 2048, fp32: 34 us, of which the sums of the runs'
+// rows later, so a run computes dp of the K - 1 rows behind it again (2 x 2047 x 2048, fp32: 32 us, of which the sums of the runs'
 // dw are a second launch).  Sums are fp32.
 #include "la_f32x2.cuh"
 #include "la_rows.cuh"

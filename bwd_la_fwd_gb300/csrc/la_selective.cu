@@ -12,9 +12,9 @@
 // row's part of y there, while helping warps form d and d x of the next tile and write the outputs of the tile before; one
 // barrier a tile.  x, dt, z, B and C come by asynchronous copies into a ring of tiles: loaded ahead into registers, behind
 // branches, each waited for its own arrival (4 x 4096 x 2048, bf16: 1209 us; predicated 332; copies 287).  All is held in fp32.
-// T C S exponentials (32 an SM and clock) and 4 T C S multiply-adds are 60 us there; what binds it are issue slots (some 260
+// T C S exponentials (32 an SM and clock) and 4 T C S multiply-adds are 60 us there; what binds it are issue slots (some 270
 // instructions for a row of 64 channels) and shared memory, whose 16-byte loads of B and C take two clocks of the SM each
-// though all lanes ask for the same.  Two channels to a thread share them (1 x 65536 x 2048: 1.14 ms, one channel 1.33); one
+// though all lanes ask for the same.  Two channels to a thread share them (1 x 65536 x 2048: 1.13 ms, one channel 1.33); one
 // channel to a thread gives twice the warps where an SM has one CTA, and registers for operands three rows ahead (4 x 4096 x
 // 2048: 240 us, one row ahead 250, two channels 287).
 // Where there are few channels time is cut into parts: a first launch forms each part's last state, started from zero (the
@@ -37,7 +37,7 @@ constexpr int kMark = 8;       // rows between the states that a forward keeps f
 constexpr int kTile = 16;      // rows of a forward tile
 constexpr int kGroup = 16;     // tiles whose sums of dA are added up by themselves
 constexpr int kSMs = 152;
-constexpr int kMaxParts = 64;  // of a sequence of the mean length
+constexpr int kMaxParts = 64;  // of a sequence of the mean length (each folds in all before it, one by one)
 
 struct GOp {                   // B, C: [.., G, S]
     const void *p;
@@ -424,8 +424,8 @@ __global__ void __launch_bounds__(Tile<T, S, CT>::THREADS, Tile<T, S, CT>::PER_S
 // sum G B and sum a h G A in shared memory, where the helping warps add them up and form the gradients of rows; dB and dC are
 // summed over the warp's 64 channels, in the thread and then by butterflies of shuffles that hand each lane a value of its
 // own (8 values over 8 lanes, then four rows of them over the four groups of lanes), and over the channel blocks by a launch
-// of its own.  Bound by issue slots (870 instructions for a row of 64 channels, 65 % of the slots of the SMs that have two
-// CTAs) and by the scanning warps' latencies; shared memory takes 190 clocks for such a row.  8 x 2048 x 2048, bf16: 736 us.
+// of its own.  Bound by issue slots (834 instructions for a row of 64 channels, 65 % of the slots of the SMs that have two
+// CTAs) and by the scanning warps' latencies; shared memory takes 190 clocks for such a row.  8 x 2048 x 2048, bf16: 743 us.
 // Values kept from the way forth to the way back (decays, d, B) spill: 1713 us where forming them again takes 778.  Components
 // turned so that lanes need not choose what they exchange save 6 % of the instructions and cost as much in shared memory.
 template <typename T, int S> struct Back {
@@ -823,8 +823,11 @@ int back_channels(int S) { return S == 8 ? Back<float, 8>::CH : S == 16 ? Back<f
 int blocks_per_group(int C, int G, int channels) { return (C / G + channels - 1) / channels; }
 
 // Rows of a part.  Where the sequences' channel blocks make fewer CTAs than one for two SMs, as many parts of a sequence of the
-// mean length as stand on the SMs at once (two CTAs on each), of kLeastPart rows at least (1 x 65536 x 2048: 9 parts 1.14 ms,
-// one 3.51 ms).  Else eight mean lengths: only packed sequences that are far longer than the others are cut.
+// mean length as stand on the SMs at once, two CTAs on each, of kLeastPart rows at least (1 x 65536 x 2048, bf16: 9 parts 1.13 ms,
+// one 3.51 ms).  That is what fits with 8 states and with 16 in bf16; with 16 in fp32 (124,928 bytes of shared memory) and with 32
+// (131,072 and 172,032) one CTA fits, and such parts stand in two rounds; these were not measured.  Else eight mean lengths: only
+// packed sequences that are far longer than the others are cut, but a packed call of more than that in all makes the launch for
+// the parts' last states in any case, as the host does not know the lengths.
 constexpr int kLeastPart = 128;
 int part_rows(int T, int nseq, int C, int G) {
     const long long n = nseq > 0 ? nseq : 1, ctas = n * G * blocks_per_group(C, G, kForwardChannels);
@@ -1008,7 +1011,7 @@ template <typename T> cudaError_t backward(const Params &P, int S, bool split, v
 
 template <typename T, int S> cudaError_t step(const Params &P, cudaStream_t s) {
     const long long across = ((long long)P.C_ * (S / 4) + kThreads - 1) / kThreads;
-    // Sequences to a block, which read A once: as many as leave 8 blocks to an SM.
+    // Sequences to a block, which read A once: as many as leave 16 blocks to an SM.
     int per = 1;
     while (per < 16 && across * parts_of(P.seq.nseq, 2 * per) >= 16 * kSMs) per *= 2;
     while (parts_of(P.seq.nseq, per) > 65535) per *= 2;
