@@ -348,7 +348,8 @@ int la_gated_scan_step(const void *x, const void *w, void *h, float *state, int 
  *   strides    in : host array, (batch, row) element strides of X, residual, sum, Y (8 values; the rules of the strided
  *              passes), or NULL for contiguous tensors
  * A row is read before it is written: an output may be an input itself (same pointer and strides; sum = residual, Y = X).
- * Squares are summed in fp32: rows beyond some 1e18 overflow (rstd = 0); a row of zeros is 0 with eps > 0 and NaN with 0.
+ * Squares are summed in fp32: rows beyond some 1e18 overflow (rstd = 0), those of rows under some 1e-19 are lost (with eps = 0
+ * rstd is infinite); a row of zeros is 0 with eps > 0 and NaN with 0.
  * B = 0 or N = 0 does nothing.
  */
 int la_rms_norm(const void *X, const void *residual, const float *weight, void *sum, void *Y, int B, int N, int C,
